@@ -281,6 +281,185 @@ ssd_status ssd_fwd_static_scratch(const ssd_shape* shape, const void* x, const f
                                   const void* Bm, const void* Cm, const float* D, const float* init_state,
                                   void* y, float* final_state, ssd_stream_t stream);
 
+/* ===========================================================================
+ * The layer around ssd_fwd, for serving: the short causal convolution in front
+ * of it, the selective scan (a decay per channel and state instead of one per
+ * head), the single-token form of both recurrences, products of a few tokens
+ * with 4-bit weights, and beam search's selection and reordering of states.
+ * The pages describe none of these; the formulas are stated with each call.
+ *
+ * Each call takes one argument struct.  Its first field is the struct's own
+ * size (a caller compiled against another layout gets SSD_ERR_INVALID_ARG).
+ * Strides are in elements.  "rows" are tensors whose innermost dimension is
+ * contiguous and whose other strides are free (a slice of a projection's
+ * output); every other tensor is contiguous.  Tensors are aligned to their
+ * element; 16-byte alignment of data and strides is faster, never required
+ * (except where a call says so).  The conventions above hold otherwise:
+ * device pointers, work enqueued on `stream`, argument errors before anything
+ * is enqueued, nothing allocated or kept.
+ *
+ * State caches hold `nslots` rows; sequence b uses row slots[b] (row b where
+ * slots is NULL).  The rows of one call must differ.  A sequence whose row
+ * lies outside [0, nslots) is idle: its outputs are 0 and no cache row is
+ * read or written for it.
+ *
+ * A convolution's cache is a ring of `width` tokens: [nslots][width][channels],
+ * where slot q holds the input of the sequence's newest token t with
+ * t mod width == q.  Tokens before a sequence's first are 0 whatever the ring
+ * holds, so a ring needs no clearing. */
+
+typedef enum { SSD_ACT_NONE = 0, SSD_ACT_SILU = 1 } ssd_activation;
+
+/* y[b][t][c] = act(bias[c] + sum_{j < width} weight[c][j] * u[b][t - width + 1 + j][c])
+ * for the tokens t < lengths[b], 0 for those after them; inputs before the
+ * call's first token come from the ring.  The output is split by channel over
+ * up to three tensors, so that x, Bm and Cm land where ssd_fwd reads them. */
+typedef struct {
+  int64_t size;              /* sizeof(ssd_conv_args) */
+  int64_t batch, seqlen;     /* >= 0; batch <= 65535 */
+  int64_t nslots;            /* rows of the ring; >= batch where slots is NULL */
+  int32_t channels, width;   /* width 2, 3 or 4 */
+  int32_t dtype, activation; /* of u, ring and out; ssd_activation */
+  int32_t nout;              /* 1..3 */
+  int32_t out_channels[3];   /* channels of each output; they add up to `channels` */
+  const void* u;             /* rows [batch][seqlen][channels] */
+  int64_t u_batch, u_token;  /* strides */
+  const float* weight;       /* [channels][width] */
+  const float* bias;         /* [channels] or NULL */
+  const void* ring;          /* or NULL: nothing came before, nothing is kept */
+  void* new_ring;            /* the ring after the call; NULL: `ring` is updated in place */
+  const int32_t* positions;  /* [batch] tokens before this call; NULL: 0 */
+  const int32_t* lengths;    /* [batch] tokens of this call, taken into [0, seqlen]; NULL: seqlen */
+  const int32_t* slots;      /* [batch] or NULL */
+  void* out[3];              /* [batch][seqlen][out_channels[i]] */
+} ssd_conv_args;
+
+ssd_status ssd_conv_fwd(const ssd_conv_args* args, ssd_stream_t stream);
+
+/* The selective scan.  With d = delta + delta_bias, put through softplus where
+ * `softplus` is set, and channel c in group g = c / (channels / ngroups):
+ *     h_t[c][n] = exp(d_t[c] * A[c][n]) * h_{t-1}[c][n] + d_t[c] * u_t[c] * Bm_t[g][n]
+ *     y_t[c] = (sum_n h_t[c][n] * Cm_t[g][n] + D[c] * u_t[c]) * silu(z_t[c])
+ * for t < lengths[b]; y is 0 after that and the state stays.  State, decay and
+ * sums are 32 bits.  seqlen 1 is the single-token form; final_state may be
+ * init_state (updated in place).  Long sequences with few channels are cut
+ * into segments that run side by side, which takes the workspace. */
+typedef struct {
+  int64_t size;
+  int64_t batch, seqlen; /* batch <= 65535 */
+  int32_t channels, dstate, ngroups, dtype; /* dstate 1..64; ngroups divides channels */
+  int32_t softplus, reserved;
+  const void *u, *delta, *z, *Bm, *Cm; /* rows [batch][seqlen][...]; z may be NULL */
+  int64_t u_batch, u_token, delta_batch, delta_token, z_batch, z_token;
+  int64_t B_batch, B_token, C_batch, C_token; /* Bm, Cm [..][ngroups][dstate], the last two contiguous */
+  const float* A;          /* [channels][dstate] */
+  const float* D;          /* [channels] or NULL (0) */
+  const float* delta_bias; /* [channels] or NULL (0) */
+  const float* init_state; /* [batch][channels][dstate] or NULL (0) */
+  float* final_state;      /* the same shape, or NULL */
+  void* y;                 /* [batch][seqlen][channels] */
+  const int32_t* lengths;  /* [batch] or NULL */
+  void* workspace;         /* 16-byte aligned */
+  size_t workspace_bytes;
+} ssd_selective_scan_args;
+
+/* Bytes of workspace (0 where none is needed or the sizes are refused); only
+ * batch, seqlen, channels, dstate and ngroups are read. */
+size_t ssd_selective_scan_workspace_size(const ssd_selective_scan_args* args);
+ssd_status ssd_selective_scan(const ssd_selective_scan_args* args, ssd_stream_t stream);
+
+/* One token of a Mamba-2 layer's convolution and recurrence, for every
+ * sequence of a batch: x, Bm, Cm = silu(convolution of u and the ring), the
+ * ring takes u, and with d = dt + dt_bias (through softplus where set)
+ *     h = exp(d * A_h) * h + d * x b^T,   y = (h c + D_h * x) * silu(z).
+ * The continuation of ssd_conv_fwd and ssd_fwd: state is ssd_fwd's final_state. */
+typedef struct {
+  int64_t size;
+  int64_t batch, nslots; /* batch <= 65535 */
+  int32_t nheads, headdim, ngroups, dstate; /* headdim 64; dstate 64, 128 or 256 */
+  int32_t width, dtype;  /* of u, z, ring and y */
+  int32_t dt_dtype, softplus;
+  const void *u, *z, *dt; /* rows [batch][nheads*headdim + 2*ngroups*dstate], [batch][nheads*headdim] or NULL, [batch][nheads] */
+  int64_t u_batch, z_batch, dt_batch;
+  const float* weight;  /* [nheads*headdim + 2*ngroups*dstate][width] */
+  const float* bias;    /* or NULL */
+  const float* A;       /* [nheads] */
+  const float* D;       /* [nheads] */
+  const float* dt_bias; /* [nheads] or NULL */
+  void* ring;           /* [nslots][width][...], updated in place */
+  const float* state;   /* [nslots][nheads][headdim][dstate], 16-byte aligned */
+  float* new_state;     /* the state after the token; NULL: updated in place */
+  const int32_t* positions; /* [batch] tokens before this one */
+  const int32_t* slots;     /* [batch] or NULL */
+  void* y;                  /* [batch][nheads][headdim] */
+} ssd_step_args;
+
+ssd_status ssd_step(const ssd_step_args* args, ssd_stream_t stream);
+
+/* y[m][n] = sum_k x[m][k] * (q[n][k] - 8) * scales[n][k / group] (+ add[m][n]),
+ * q the 4-bit codes, for a few tokens m.  Codes are packed in tiles of 16 rows
+ * and 64 columns, [ceil(n/16)][ceil(k/64)][32 lanes][4 words], codes outside
+ * the matrix 8: lane 4 r + c, word 2 h + i holds, at bit 4 (a + 2 e) + 16 p,
+ * row 8 a + r and column 32 h + 8 c + 4 i + 2 e + p of its tile
+ * (r < 8, c < 4, h, i, a, e, p < 2).  Products and sums are 32 bits: bf16 x
+ * enters exactly, fp32 x as the exact sum of three bf16 parts. */
+typedef struct {
+  int64_t size;
+  int64_t tokens; /* >= 0 */
+  int32_t n, k, group, dtype; /* group 32, 64 or 128; dtype of x, add and y */
+  const void* x;  /* rows [tokens][k] */
+  int64_t x_token;
+  const void* packed; /* 16-byte aligned */
+  const float* scales; /* [n][ceil(k/group)] */
+  const void* add;     /* rows [tokens][n] or NULL */
+  int64_t add_token;
+  void* y; /* [tokens][n] */
+} ssd_w4_matvec_args;
+
+ssd_status ssd_w4_matvec(const ssd_w4_matvec_args* args, ssd_stream_t stream);
+
+/* Beam search's choice.  Candidate (w, v) has the score
+ *     scores[b][w] + (logits[b][w][v] - log sum_v' exp(logits[b][w][v'])),
+ * a NaN counting as -infinity; a finished beam has one candidate that is not
+ * -infinity, (w, eos), at scores[b][w].  Writes the k best per b in falling
+ * order, equal scores by rising w * vocab + v: their scores, beams and tokens.
+ * k in 1..64, k <= beams * vocab, beams in 1..64, beams * vocab < 2^31. */
+typedef struct {
+  int64_t size;
+  int64_t batch; /* <= 65535 */
+  int32_t beams, vocab, k, dtype; /* of logits */
+  int32_t eos, reserved;
+  const void* logits; /* rows [batch][beams][vocab] */
+  int64_t logits_batch, logits_beam;
+  const float* scores;     /* [batch][beams] */
+  const uint8_t* finished; /* [batch][beams], not 0: finished; or NULL */
+  float* out_scores;       /* [batch][k] */
+  int32_t *parents, *tokens;
+  void* workspace; /* 16-byte aligned */
+  size_t workspace_bytes;
+} ssd_beam_select_args;
+
+/* Only batch, beams, vocab, k are read. */
+size_t ssd_beam_select_workspace_size(const ssd_beam_select_args* args);
+ssd_status ssd_beam_select(const ssd_beam_select_args* args, ssd_stream_t stream);
+
+/* new row (b, i) = old row (b, parents[b][i]) of every tensor: dst[j] is
+ * [batch][k][row_bytes[j]], src[j] [batch][beams][row_bytes[j]].  dst[j] may
+ * be src[j] (then k == beams, and rows that stay are not moved); they must not
+ * overlap otherwise.  A parent outside [0, beams) leaves its row unwritten. */
+#define SSD_REORDER_MAX 16
+typedef struct {
+  int64_t size;
+  int64_t batch;
+  int32_t beams, k, count, reserved; /* k, beams in 1..64; count <= SSD_REORDER_MAX */
+  const int32_t* parents; /* [batch][k] */
+  const void* src[SSD_REORDER_MAX];
+  void* dst[SSD_REORDER_MAX];
+  int64_t row_bytes[SSD_REORDER_MAX];
+} ssd_beam_reorder_args;
+
+ssd_status ssd_beam_reorder(const ssd_beam_reorder_args* args, ssd_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -26,7 +26,9 @@ STATUS = {0: "SSD_OK", 1: "SSD_ERR_INVALID_ARG", 2: "SSD_ERR_UNSUPPORTED", 3: "S
 EXPORTS = ("ssd_status_string", "ssd_validate_shape", "ssd_fwd_workspace_layout", "ssd_fwd_workspace_size",
            "ssd_fwd", "ssd_fwd_check", "ssd_chunk_cumsum", "ssd_chunk_state", "ssd_state_passing",
            "ssd_compute_out", "ssd_debug_timeout_probe", "ssd_fwd_kernel_count", "ssd_fwd_static_scratch",
-           "ssd_fwd_fused", "ssd_fused_pass", "ssd_fwd_range", "ssd_causal_cb")
+           "ssd_fwd_fused", "ssd_fused_pass", "ssd_fwd_range", "ssd_causal_cb",
+           "ssd_conv_fwd", "ssd_selective_scan", "ssd_selective_scan_workspace_size", "ssd_step", "ssd_w4_matvec",
+           "ssd_beam_select", "ssd_beam_select_workspace_size", "ssd_beam_reorder")
 
 # Size of the library's own workspace array used by ssd_fwd_static_scratch.
 SSD_STATIC_SCRATCH_BYTES = 32 << 20
@@ -98,6 +100,13 @@ def _load() -> ctypes.CDLL:
     lib.ssd_debug_timeout_probe.argtypes = [vp, ctypes.c_uint32, vp]
     lib.ssd_fwd_static_scratch.restype = c_int
     lib.ssd_fwd_static_scratch.argtypes = [sp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    for name in ("ssd_conv_fwd", "ssd_selective_scan", "ssd_step", "ssd_w4_matvec", "ssd_beam_select",
+                 "ssd_beam_reorder"):  # (argument struct, stream)
+        getattr(lib, name).restype = c_int
+        getattr(lib, name).argtypes = [ctypes.c_char_p, vp]
+    for name in ("ssd_selective_scan_workspace_size", "ssd_beam_select_workspace_size"):
+        getattr(lib, name).restype = sz
+        getattr(lib, name).argtypes = [ctypes.c_char_p]
     return lib
 
 
@@ -491,3 +500,9 @@ def ssd_fwd_static_scratch(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B
     code = lib.ssd_fwd_static_scratch(ctypes.byref(shape), _ptr(x), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm),
                                       _ptr(D), _ptr(init_state), _ptr(y), _ptr(final_state), _stream(stream))
     _check(code, "ssd_fwd_static_scratch")
+
+
+# The layer around ssd_fwd (convolution, selective scan, single tokens, 4-bit products, beam search).
+from .layer import (ssd_beam_reorder, ssd_beam_select, ssd_beam_select_workspace_size, ssd_conv_fwd,  # noqa: E402
+                    ssd_selective_scan, ssd_selective_scan_workspace_size, ssd_step, ssd_w4_matvec, w4_pack,
+                    w4_quantize)
