@@ -4,14 +4,20 @@
 //   y_t[c] = (sum_n h_t[c][n] C_t[n] + D[c] u_t[c]) silu(z_t[c]).
 //
 // Work and split.  Per token and state one exponential and three multiply-adds:
-// at 16 states the special-function unit and the issue slots bound it, not
-// memory.  A block takes 32 channels, four lanes a channel, each lane a quarter
-// of the states, and walks down the tokens in tiles of 32: the tile's u, delta,
-// z, B and C come by 16-byte loads one tile ahead (in registers while the tile
-// before is computed), the steps are put through softplus once and kept with
-// d u in shared memory, the states stay in registers, multiply-adds go two at a
-// time (f32x2).  Four tokens' sums are joined over the four lanes together:
-// three shuffles for four tokens, and every lane ends with one token's sum.
+// at 16 states the issue slots and the filling of registers from shared memory
+// bound it, not memory.  A block of 16 channels (32 for up to 8 states) walks
+// down the tokens in tiles of 32, and has two sides that meet once a tile:
+//  - the recurrence: a lane keeps four states of two channels in registers (so
+//    a token's B and C are read once for both), T lanes share a channel,
+//    multiply-adds go two at a time (f32x2).  Four tokens' sums are joined over
+//    a channel's lanes together: with four lanes three shuffles for four tokens,
+//    and every lane ends with one token's sum;
+//  - the memory side (two warps): 16-byte loads one tile ahead, the steps put
+//    through softplus once and kept with d u in shared memory, and the outputs
+//    of the tile before (skip term, gate, 16-byte stores).
+// With both sides' work in one warp a block's latency, not its work, set the
+// pace (2 x 2048 x 5120, 16 states, bf16: 304 us); one warp for the memory side
+// 194, two 171.
 //
 // Segments.  With few channels a sequence is cut into segments that run side by
 // side: a first launch computes every segment's state from zero and its sum of
@@ -24,11 +30,8 @@
 namespace ssd {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kLanes = 4;      // lanes a channel
-constexpr int kChannels = kThreads / kLanes;
-constexpr int kTile = 32;      // tokens a tile
-constexpr int kYRow = 40;      // floats a row of sums: four rows of 8 channels fall into different banks
+constexpr int kNS = 4;    // states a lane keeps of each of its two channels
+constexpr int kTile = 32;  // tokens a tile
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct ScanParams {
@@ -54,6 +57,7 @@ struct Raw<__nv_bfloat16> {
   uint4 v;
   __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = v; }
   __device__ __forceinline__ void set(int i, __nv_bfloat16 x) {
     const uint32_t bits = __bfloat16_as_ushort(x);
     uint32_t* w = &v.x;
@@ -72,6 +76,10 @@ struct Raw<float> {
     a = __ldg(reinterpret_cast<const float4*>(p));
     b = __ldg(reinterpret_cast<const float4*>(p) + 1);
   }
+  __device__ __forceinline__ void store(float* p) const {
+    reinterpret_cast<float4*>(p)[0] = a;
+    reinterpret_cast<float4*>(p)[1] = b;
+  }
   __device__ __forceinline__ void set(int i, float x) { (i < 4 ? &a.x : &b.x)[i % 4] = x; }
   __device__ __forceinline__ float get(int i) const { return (i < 4 ? &a.x : &b.x)[i % 4]; }
 };
@@ -87,22 +95,6 @@ __device__ __forceinline__ void load8(Raw<T>& r, const T* p, int n) {
     for (int i = 0; i < 8; ++i)
       if (i < n) r.set(i, p[i]);
   }
-}
-
-// log(1 + exp(v)) = max(v, 0) + log(1 + e), e = exp(-|v|), and with s = e / (2 + e) <= 1/3
-// log(1 + e) = 2 atanh(s) = 2 (s + s^3/3 + s^5/5 + ...): no digits are lost for small e, as they
-// are in log(1 + e) itself.  Seven terms leave 2 s^15/15 < 2^-26 s.
-__device__ __forceinline__ float softplus_exact(float v) {
-  const float e = expf(-fabsf(v));
-  const float s = __fdividef(e, 2.f + e);
-  const float q = s * s;
-  float r = fmaf(q, 1.f / 13.f, 1.f / 11.f);
-  r = fmaf(q, r, 1.f / 9.f);
-  r = fmaf(q, r, 1.f / 7.f);
-  r = fmaf(q, r, 1.f / 5.f);
-  r = fmaf(q, r, 1.f / 3.f);
-  r = fmaf(q * s, r, s);
-  return fmaxf(v, 0.f) + 2.f * r;
 }
 
 __device__ __forceinline__ float exp2_fast(float v) {
@@ -131,20 +123,53 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   return r;
 }
 
+// log(1 + exp(v)) = max(v, 0) + log(1 + e), e = exp(-|v|), and with s = e / (2 + e) <= 1/3
+// log(1 + e) = 2 atanh(s) = 2 (s + s^3/3 + s^5/5 + ...): no digits are lost for small e, as they
+// are in log(1 + e) itself.  Six terms leave 2 s^13/13 < 2^-22 s, and less the smaller e is.
+__device__ __forceinline__ void softplus2(float& v0, float& v1) {
+  const float e0 = expf(-fabsf(v0)), e1 = expf(-fabsf(v1));
+  const uint64_t s = pack2(__fdividef(e0, 2.f + e0), __fdividef(e1, 2.f + e1));
+  const uint64_t q = mul2(s, s);
+  auto both = [](float c) { return pack2(c, c); };
+  uint64_t r = fma2(q, both(1.f / 11.f), both(1.f / 9.f));
+  r = fma2(q, r, both(1.f / 7.f));
+  r = fma2(q, r, both(1.f / 5.f));
+  r = fma2(q, r, both(1.f / 3.f));
+  r = fma2(mul2(q, s), r, s);
+  float r0, r1;
+  unpack2(r, r0, r1);
+  v0 = fmaf(2.f, r0, fmaxf(v0, 0.f));
+  v1 = fmaf(2.f, r1, fmaxf(v1, 0.f));
+}
+
+// Sizes that follow from T, the lanes of a channel (T * kNS states).
+template <int T>
+struct Shape {
+  static constexpr int kN = T * kNS;
+  static constexpr int kChannels = T == 2 ? 32 : 16;       // of a block
+  static constexpr int kThreads = kChannels / 2 * T;       // of the recurrence
+  static constexpr int kHelp = T == 16 ? 128 : 64;         // of the memory side
+  static constexpr int kCols = kChannels / 8;              // vectors of eight channels in a row
+  static constexpr int kIO = kTile * kCols;                // and in a tile
+  static constexpr int kIOEach = (kIO + kHelp - 1) / kHelp;
+  static constexpr int kBC = kTile * kN / 8;               // vectors of eight in a tile of B (or C)
+  static constexpr int kBCEach = (2 * kBC + kHelp - 1) / kHelp;
+  // rows in floats, padded so that neighbouring rows fall into different banks
+  static constexpr int kStepRow = 2 * kChannels + 4, kYRow = kChannels + 8;
+};
+
 // kState: only the segment's state from zero and its sum of steps (the first of two launches).
-template <typename T, int NS, bool kVec, bool kState>
-__global__ void __launch_bounds__(kThreads) scan_kernel(ScanParams p) {
-  constexpr int kN = kLanes * NS;  // states, padded
-  constexpr int kBC = kTile * kN / 8;             // vectors of eight in a tile of B (or C)
-  constexpr int kBCEach = (2 * kBC + kThreads - 1) / kThreads;
-  __shared__ __align__(16) float2 s_step[kTile][kChannels];  // (d, d u)
-  __shared__ __align__(16) float s_B[kTile][kN], s_C[kTile][kN];
-  __shared__ __align__(16) float s_y[kTile][kYRow];
+template <typename V, int T, bool kVec, bool kState>
+__global__ void __launch_bounds__(Shape<T>::kThreads + Shape<T>::kHelp) scan_kernel(ScanParams p) {
+  using S = Shape<T>;
+  __shared__ __align__(16) float s_step[2][kTile][S::kStepRow];  // (d, d u) of each channel
+  __shared__ __align__(16) float s_B[2][kTile][S::kN], s_C[2][kTile][S::kN];
+  __shared__ __align__(16) float s_y[2][kTile][S::kYRow];
 
   const int group = blockIdx.x / p.tiles;
-  const int in_group = (blockIdx.x % p.tiles) * kChannels;
+  const int in_group = (blockIdx.x % p.tiles) * S::kChannels;
   const int c0 = group * p.per + in_group;
-  const int nc = p.per - in_group < kChannels ? p.per - in_group : kChannels;
+  const int nc = p.per - in_group < S::kChannels ? p.per - in_group : S::kChannels;
   const int64_t b = blockIdx.z;
   const int seg = blockIdx.y;
   int64_t len = p.L;
@@ -152,201 +177,269 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(ScanParams p) {
   const int64_t begin = seg * p.segment;
   const int64_t stop = seg + 1 < p.segments && begin + p.segment < p.L ? begin + p.segment : p.L;  // of the outputs
   const int64_t end = len < stop ? len : stop;                                 // of the recurrence
+  const int tiles = end > begin ? static_cast<int>((end - begin + kTile - 1) / kTile) : 0;
 
-  const int tid = threadIdx.x;
-  const int row = tid / 4, col = (tid % 4) * 8;  // loads and stores: a token, eight channels
-  const int valid = nc - col;
-  const int ch = tid / kLanes, part = tid % kLanes;  // recurrence: a channel, a quarter of its states
-  const bool live = ch < nc;
-
-  const T* u = static_cast<const T*>(p.u) + b * p.ub + c0 + col;
-  const T* delta = static_cast<const T*>(p.delta) + b * p.db + c0 + col;
-  const T* z = static_cast<const T*>(p.z) + b * p.zb + c0 + col;
-  const T* Bm = static_cast<const T*>(p.Bm) + b * p.Bb + static_cast<int64_t>(group) * p.N;
-  const T* Cm = static_cast<const T*>(p.Cm) + b * p.Cb + static_cast<int64_t>(group) * p.N;
-
-  Raw<T> ru, rd, rz, rbc[kBCEach];
-  auto fetch = [&](int64_t t0) {
-    const int64_t t = t0 + row;
-    const int n = t < end ? valid : 0;
-    load8<T, kVec>(ru, u + t * p.ut, n);
-    load8<T, kVec>(rd, delta + t * p.dt, n);
-    if constexpr (!kState) {
-      if (p.z) load8<T, kVec>(rz, z + t * p.zt, n);
-    }
-#pragma unroll
-    for (int i = 0; i < kBCEach; ++i) {
-      const int v = tid + i * kThreads;
-      const bool is_c = v >= kBC;
-      const int at = is_c ? v - kBC : v;
-      const int64_t tt = t0 + at / (kN / 8);
-      const int n0 = at % (kN / 8) * 8;
-      if (v < (kState ? kBC : 2 * kBC))
-        load8<T, kVec>(rbc[i], (is_c ? Cm + tt * p.Ct : Bm + tt * p.Bt) + n0, tt < end ? p.N - n0 : 0);
-    }
-  };
-  fetch(begin);
-
-  uint64_t a2[NS / 2], h2[NS / 2];
-  const int64_t state_row = (b * p.D + c0 + ch) * p.N;
-  const int n0 = part * NS;
-#pragma unroll
-  for (int i = 0; i < NS / 2; ++i) {
-    float a[2], h[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int n = n0 + 2 * i + e;
-      const bool in = live && n < p.N;
-      a[e] = in ? p.A[static_cast<int64_t>(c0 + ch) * p.N + n] * kLog2e : 0.f;
-      h[e] = in && p.init && p.segments == 1 ? p.init[state_row + n] : 0.f;
-      // final_state may be init_state, and the last segment's block may end before another reads
-      // its state: in segments all read a copy
-      if (kState && seg == 0 && in)
-        p.seg_state[((b * p.segments) * p.D + c0 + ch) * p.N + n] = p.init ? p.init[state_row + n] : 0.f;
-    }
-    a2[i] = pack2(a[0], a[1]);
-    h2[i] = pack2(h[0], h[1]);
-  }
-  if (!kState && p.segments > 1) {
-    grid_dep_wait();
-#pragma unroll 4
-    for (int j = 0; j <= seg; ++j) {  // the state entering this segment
-      const int64_t at = (b * p.segments + j) * p.D + c0 + ch;
-      const float sum = live && j > 0 ? p.seg_sum[at - p.D] : 0.f;
-      const uint64_t sum2 = pack2(sum, sum);
-#pragma unroll
-      for (int i = 0; i < NS / 2; ++i) {
-        const int n = n0 + 2 * i;
-        const float lo = live && n < p.N ? p.seg_state[at * p.N + n] : 0.f;
-        const float hi = live && n + 1 < p.N ? p.seg_state[at * p.N + n + 1] : 0.f;
-        float x, y;
-        unpack2(mul2(sum2, a2[i]), x, y);
-        h2[i] = fma2(pack2(exp2_fast(x), exp2_fast(y)), h2[i], pack2(lo, hi));
-      }
-    }
-  }
-  float bias[8], skip[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    bias[i] = p.delta_bias && i < valid ? p.delta_bias[c0 + col + i] : 0.f;
-    skip[i] = !kState && p.skip && i < valid ? p.skip[c0 + col + i] : 0.f;
-  }
-
-  float total = 0.f;
-  for (int64_t t0 = begin; t0 < end; t0 += kTile) {
-    // the tile's steps and rows of B and C
-    const bool there = t0 + row < end;
+  if (threadIdx.x >= S::kThreads) {
+    // ---- memory side: loads, steps, and the outputs of the tile before ----
+    const int tid = threadIdx.x - S::kThreads;
+    const V* u = static_cast<const V*>(p.u) + b * p.ub + c0;
+    const V* delta = static_cast<const V*>(p.delta) + b * p.db + c0;
+    const V* z = static_cast<const V*>(p.z) + b * p.zb + c0;
+    const V* Bm = static_cast<const V*>(p.Bm) + b * p.Bb + static_cast<int64_t>(group) * p.N;
+    const V* Cm = static_cast<const V*>(p.Cm) + b * p.Cb + static_cast<int64_t>(group) * p.N;
+    // a thread's vectors all lie in the same eight channels (kHelp is a multiple of kCols)
+    const int col0 = tid % S::kCols * 8;
+    float bias[8], skip[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      float d = rd.get(i) + bias[i];
-      if (p.softplus) d = softplus_exact(d);
-      if (!there) d = 0.f;  // past the end the state stays
-      s_step[row][col + i] = make_float2(d, d * ru.get(i));
+      bias[i] = p.delta_bias && col0 + i < nc ? p.delta_bias[c0 + col0 + i] : 0.f;
+      skip[i] = !kState && p.skip && col0 + i < nc ? p.skip[c0 + col0 + i] : 0.f;
     }
+    struct Tile {
+      Raw<V> u[S::kIOEach], d[S::kIOEach], z[S::kIOEach], bc[S::kBCEach];
+    } r;                                                                    // the tile on its way
+    Raw<V> u1[S::kIOEach], z1[S::kIOEach], u2[S::kIOEach], z2[S::kIOEach];  // the two staged last
+    auto fetch = [&](int64_t t0) {
 #pragma unroll
-    for (int i = 0; i < kBCEach; ++i) {
-      const int v = tid + i * kThreads;
-      const bool is_c = v >= kBC;
-      const int at = is_c ? v - kBC : v;
-      if (v < (kState ? kBC : 2 * kBC)) {
-        float* dst = (is_c ? s_C : s_B)[at / (kN / 8)] + at % (kN / 8) * 8;
-#pragma unroll
-        for (int e = 0; e < 8; e += 4)
-          *reinterpret_cast<float4*>(dst + e) =
-              make_float4(rbc[i].get(e), rbc[i].get(e + 1), rbc[i].get(e + 2), rbc[i].get(e + 3));
-      }
-    }
-    const Raw<T> cu = ru, cz = rz;
-    __syncthreads();
-    if (t0 + kTile < end) fetch(t0 + kTile);
-
-    const int nt = end - t0 < kTile ? static_cast<int>(end - t0) : kTile;
-    for (int t = 0; t < nt; t += 4) {
-      float acc[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 st = s_step[t + k][ch];
-        const uint64_t d2 = pack2(st.x, st.x), du2 = pack2(st.y, st.y);
-        if (kState) total += st.x;
-        uint64_t sum2 = 0;
-        const uint64_t* B2 = reinterpret_cast<const uint64_t*>(&s_B[t + k][n0]);
-        const uint64_t* C2 = reinterpret_cast<const uint64_t*>(&s_C[t + k][n0]);
-#pragma unroll
-        for (int i = 0; i < NS / 2; ++i) {
-          float x, y;
-          unpack2(mul2(d2, a2[i]), x, y);
-          h2[i] = fma2(pack2(exp2_fast(x), exp2_fast(y)), h2[i], mul2(du2, B2[i]));
-          if constexpr (!kState) sum2 = fma2(h2[i], C2[i], sum2);
-        }
+      for (int i = 0; i < S::kIOEach; ++i) {
+        const int v = tid + i * S::kHelp;
+        const int64_t t = t0 + v / S::kCols;
+        const int n = v < S::kIO && t < end ? nc - col0 : 0;
+        load8<V, kVec>(r.u[i], u + t * p.ut + col0, n);
+        load8<V, kVec>(r.d[i], delta + t * p.dt + col0, n);
         if constexpr (!kState) {
-          float lo, hi;
-          unpack2(sum2, lo, hi);
-          acc[k] = lo + hi;
+          if (p.z) load8<V, kVec>(r.z[i], z + t * p.zt + col0, n);
         }
       }
-      if constexpr (!kState) {
-        // lanes with bit 0 keep tokens 1 and 3, then those with bit 1 the later of the two left
-        const bool b0 = part & 1, b1 = part & 2;
-        float k0 = b0 ? acc[1] : acc[0], k1 = b0 ? acc[3] : acc[2];
-        k0 += __shfl_xor_sync(0xffffffffu, b0 ? acc[0] : acc[1], 1);
-        k1 += __shfl_xor_sync(0xffffffffu, b0 ? acc[2] : acc[3], 1);
-        const float sum = (b1 ? k1 : k0) + __shfl_xor_sync(0xffffffffu, b1 ? k0 : k1, 2);
-        s_y[t + (part & 1) + (part & 2)][ch] = sum;
+#pragma unroll
+      for (int i = 0; i < S::kBCEach; ++i) {
+        const int v = tid + i * S::kHelp;
+        const bool is_c = v >= S::kBC;
+        const int at = is_c ? v - S::kBC : v;
+        const int64_t t = t0 + at / (S::kN / 8);
+        const int n = at % (S::kN / 8) * 8;
+        if (v < (kState ? S::kBC : 2 * S::kBC))
+          load8<V, kVec>(r.bc[i], (is_c ? Cm + t * p.Ct : Bm + t * p.Bt) + n, t < end ? p.N - n : 0);
       }
-    }
-    __syncthreads();
-    if constexpr (!kState) {
-      if (there && valid > 0) {
-        T* y = static_cast<T*>(p.y) + (b * p.L + t0 + row) * p.D + c0 + col;
-        float v[8];
+    };
+    auto stage = [&](int64_t t0, int buf) {  // the tile's steps and rows of B and C
+#pragma unroll
+      for (int j = 0; j < S::kIOEach; ++j) {
+        const int v = tid + j * S::kHelp;
+        const int row = v / S::kCols;
+        if (v < S::kIO) {
+          const bool there = t0 + row < end;
+          float4* dst = reinterpret_cast<float4*>(&s_step[buf][row][2 * col0]);
+#pragma unroll
+          for (int i = 0; i < 8; i += 2) {
+            float d0 = r.d[j].get(i) + bias[i], d1 = r.d[j].get(i + 1) + bias[i + 1];
+            if (p.softplus) softplus2(d0, d1);
+            if (!there) d0 = d1 = 0.f;  // past the end the state stays
+            dst[i / 2] = make_float4(d0, d0 * r.u[j].get(i), d1, d1 * r.u[j].get(i + 1));
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < S::kBCEach; ++i) {
+        const int v = tid + i * S::kHelp;
+        const bool is_c = v >= S::kBC;
+        const int at = is_c ? v - S::kBC : v;
+        if (v < (kState ? S::kBC : 2 * S::kBC)) {
+          float* dst = (is_c ? s_C : s_B)[buf][at / (S::kN / 8)] + at % (S::kN / 8) * 8;
+#pragma unroll
+          for (int e = 0; e < 8; e += 4)
+            *reinterpret_cast<float4*>(dst + e) =
+                make_float4(r.bc[i].get(e), r.bc[i].get(e + 1), r.bc[i].get(e + 2), r.bc[i].get(e + 3));
+        }
+      }
+    };
+    auto put = [&](int64_t t0, int buf) {  // the outputs, with the inputs of two tiles ago
+#pragma unroll
+      for (int j = 0; j < S::kIOEach; ++j) {
+        const int v = tid + j * S::kHelp;
+        const int row = v / S::kCols;
+        if (v >= S::kIO || t0 + row >= end || col0 >= nc) continue;
+        V* y = static_cast<V*>(p.y) + (b * p.L + t0 + row) * p.D + c0 + col0;
+        float out[8];
+#pragma unroll
+        for (int i = 0; i < 8; i += 4) {
+          const float4 sum = *reinterpret_cast<const float4*>(&s_y[buf][row][col0 + i]);
+          out[i] = sum.x, out[i + 1] = sum.y, out[i + 2] = sum.z, out[i + 3] = sum.w;
+        }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          v[i] = fmaf(skip[i], cu.get(i), s_y[row][col + i]);
-          if (p.z) v[i] *= silu(cz.get(i));
+          out[i] = fmaf(skip[i], u2[j].get(i), out[i]);
+          if (p.z) out[i] *= silu(z2[j].get(i));
         }
         if constexpr (kVec) {
-          Raw<T> out;
+          Raw<V> r;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) out.set(i, from_f32<T>(v[i]));
-          if constexpr (sizeof(T) == 2) {
-            *reinterpret_cast<uint4*>(y) = out.v;
-          } else {
-            reinterpret_cast<float4*>(y)[0] = out.a;
-            reinterpret_cast<float4*>(y)[1] = out.b;
-          }
+          for (int i = 0; i < 8; ++i) r.set(i, from_f32<V>(out[i]));
+          r.store(y);
         } else {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            if (i < valid) y[i] = from_f32<T>(v[i]);
+            if (col0 + i < nc) y[i] = from_f32<V>(out[i]);
+        }
+      }
+    };
+    fetch(begin);
+    for (int i = 0; i <= tiles; ++i) {  // stage tile i, put tile i - 2, load tile i + 1
+      const int64_t t0 = begin + static_cast<int64_t>(i) * kTile;
+      if (i < tiles) stage(t0, i & 1);
+      if constexpr (!kState) {
+        if (i >= 2) put(t0 - 2 * kTile, i & 1);
+#pragma unroll
+        for (int j = 0; j < S::kIOEach; ++j) u2[j] = u1[j], z2[j] = z1[j], u1[j] = r.u[j], z1[j] = r.z[j];
+      }
+      if (i + 1 < tiles) fetch(t0 + kTile);
+      __syncthreads();
+    }
+    if constexpr (!kState) {
+      if (tiles > 0) put(begin + static_cast<int64_t>(tiles - 1) * kTile, (tiles - 1) & 1);
+      for (int64_t t = (end > begin ? end : begin) + tid / S::kCols; t < stop; t += S::kHelp / S::kCols) {
+        V* y = static_cast<V*>(p.y) + (b * p.L + t) * p.D + c0 + col0;  // after the sequence's end
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (col0 + i < nc) y[i] = from_f32<V>(0.f);
+      }
+    }
+    return;
+  }
+
+  // ---- the recurrence: two channels a lane, a share of their states ----
+  const int tid = threadIdx.x;
+  const int ch = tid / T * 2, part = tid % T;
+  const int n0 = part * kNS;
+  uint64_t a2[2][kNS / 2], h2[2][kNS / 2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int64_t state_row = (b * p.D + c0 + ch + k) * p.N;
+#pragma unroll
+    for (int i = 0; i < kNS / 2; ++i) {
+      float a[2], h[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int n = n0 + 2 * i + e;
+        const bool in = ch + k < nc && n < p.N;
+        a[e] = in ? p.A[static_cast<int64_t>(c0 + ch + k) * p.N + n] * kLog2e : 0.f;
+        h[e] = in && p.init && p.segments == 1 ? p.init[state_row + n] : 0.f;
+        // final_state may be init_state, and the last segment's block may end before another reads
+        // its state: in segments all read a copy
+        if (kState && seg == 0 && in)
+          p.seg_state[(b * p.segments * p.D + c0 + ch + k) * p.N + n] = p.init ? p.init[state_row + n] : 0.f;
+      }
+      a2[k][i] = pack2(a[0], a[1]);
+      h2[k][i] = pack2(h[0], h[1]);
+    }
+  }
+  if (!kState && p.segments > 1) {
+    grid_dep_wait();
+#pragma unroll 2
+    for (int j = 0; j <= seg; ++j) {  // the state entering this segment
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const bool live = ch + k < nc;
+        const int64_t at = (b * p.segments + j) * p.D + c0 + ch + k;
+        const float sum = live && j > 0 ? p.seg_sum[at - p.D] : 0.f;
+        const uint64_t sum2 = pack2(sum, sum);
+#pragma unroll
+        for (int i = 0; i < kNS / 2; ++i) {
+          const int n = n0 + 2 * i;
+          const float lo = live && n < p.N ? p.seg_state[at * p.N + n] : 0.f;
+          const float hi = live && n + 1 < p.N ? p.seg_state[at * p.N + n + 1] : 0.f;
+          float x, y;
+          unpack2(mul2(sum2, a2[k][i]), x, y);
+          h2[k][i] = fma2(pack2(exp2_fast(x), exp2_fast(y)), h2[k][i], pack2(lo, hi));
         }
       }
     }
   }
+  float total[2] = {0.f, 0.f};
+  __syncthreads();
+  for (int i = 0; i < tiles; ++i) {
+    const int buf = i & 1;
+    // all tokens of a tile, whatever the tile holds (steps past the end are 0): one straight run, in which the
+    // joining of four tokens' sums overlaps the next four
+#pragma unroll 2
+    for (int t = 0; t < kTile; t += 4) {
+      float acc[2][4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float4 st = *reinterpret_cast<const float4*>(&s_step[buf][t + q][2 * ch]);
+        const ulonglong2 B4 = *reinterpret_cast<const ulonglong2*>(&s_B[buf][t + q][n0]);
+        ulonglong2 C4;
+        if constexpr (!kState) C4 = *reinterpret_cast<const ulonglong2*>(&s_C[buf][t + q][n0]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float d = k ? st.z : st.x, du = k ? st.w : st.y;
+          const uint64_t d2 = pack2(d, d), du2 = pack2(du, du);
+          if (kState) total[k] += d;
+          uint64_t sum2 = 0;
+#pragma unroll
+          for (int j = 0; j < kNS / 2; ++j) {
+            float x, y;
+            unpack2(mul2(d2, a2[k][j]), x, y);
+            h2[k][j] = fma2(pack2(exp2_fast(x), exp2_fast(y)), h2[k][j], mul2(du2, j ? B4.y : B4.x));
+            if constexpr (!kState) sum2 = j ? fma2(h2[k][j], C4.y, sum2) : mul2(h2[k][j], C4.x);
+          }
+          if constexpr (!kState) {
+            float lo, hi;
+            unpack2(sum2, lo, hi);
+            acc[k][q] = lo + hi;
+          }
+        }
+      }
+      if constexpr (!kState) {
+        // lanes with bit 0 keep tokens 1 and 3, then those with bit 1 the later of the two left; over
+        // higher bits the sums are added
+        const bool b0 = part & 1, b1 = part & 2;
+        float one[2], two[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          one[k] = (b0 ? acc[k][1] : acc[k][0]) + __shfl_xor_sync(0xffffffffu, b0 ? acc[k][0] : acc[k][1], 1);
+          two[k] = (b0 ? acc[k][3] : acc[k][2]) + __shfl_xor_sync(0xffffffffu, b0 ? acc[k][2] : acc[k][3], 1);
+        }
+        if constexpr (T == 2) {
+          *reinterpret_cast<float2*>(&s_y[buf][t + part][ch]) = make_float2(one[0], one[1]);
+          *reinterpret_cast<float2*>(&s_y[buf][t + 2 + part][ch]) = make_float2(two[0], two[1]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            one[k] = (b1 ? two[k] : one[k]) + __shfl_xor_sync(0xffffffffu, b1 ? one[k] : two[k], 2);
+#pragma unroll
+            for (int o = 4; o < T; o *= 2) one[k] += __shfl_xor_sync(0xffffffffu, one[k], o);
+          }
+          if (part < 4) *reinterpret_cast<float2*>(&s_y[buf][t + part][ch]) = make_float2(one[0], one[1]);
+        }
+      }
+    }
+    __syncthreads();
+  }
   if constexpr (kState) {
     grid_dep_launch();
-    const int64_t at = (b * p.segments + seg + 1) * p.D + c0 + ch;
-    if (live) {
-      if (part == 0) p.seg_sum[at - p.D] = total;
 #pragma unroll
-      for (int i = 0; i < NS / 2; ++i) {
+    for (int k = 0; k < 2; ++k) {
+      if (ch + k >= nc) continue;
+      const int64_t at = (b * p.segments + seg + 1) * p.D + c0 + ch + k;
+      if (part == 0) p.seg_sum[at - p.D] = total[k];
+#pragma unroll
+      for (int i = 0; i < kNS / 2; ++i) {
         float lo, hi;
-        unpack2(h2[i], lo, hi);
+        unpack2(h2[k][i], lo, hi);
         if (n0 + 2 * i < p.N) p.seg_state[at * p.N + n0 + 2 * i] = lo;
         if (n0 + 2 * i + 1 < p.N) p.seg_state[at * p.N + n0 + 2 * i + 1] = hi;
       }
     }
-  } else {
-    for (int64_t t = (end > begin ? end : begin) + row; t < stop; t += kThreads / 4) {  // after the sequence's end
-      T* y = static_cast<T*>(p.y) + (b * p.L + t) * p.D + c0 + col;
+  } else if (p.final_state && seg + 1 == p.segments) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < valid) y[i] = from_f32<T>(0.f);
-    }
-    if (p.final_state && seg + 1 == p.segments && live) {
+    for (int k = 0; k < 2; ++k) {
+      if (ch + k >= nc) continue;
+      const int64_t state_row = (b * p.D + c0 + ch + k) * p.N;
 #pragma unroll
-      for (int i = 0; i < NS / 2; ++i) {
+      for (int i = 0; i < kNS / 2; ++i) {
         float lo, hi;
-        unpack2(h2[i], lo, hi);
+        unpack2(h2[k][i], lo, hi);
         if (n0 + 2 * i < p.N) p.final_state[state_row + n0 + 2 * i] = lo;
         if (n0 + 2 * i + 1 < p.N) p.final_state[state_row + n0 + 2 * i + 1] = hi;
       }
@@ -354,40 +447,47 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(ScanParams p) {
   }
 }
 
-// Segments a sequence is cut into: enough blocks for `kFill` on every multiprocessor, but no
-// segment below kLeast tokens.
-constexpr int64_t kFill = 6, kLeast = 128;
+// Segments a sequence is cut into: enough recurrence warps for kFill on every multiprocessor, but no
+// segment below kLeast tokens.  Measured: 16384 x 2048 fp32 with 8, 12, 16 and 24 warps 362, 370,
+// 364 and 381 us (whole: 1550 us); 2 x 2048 x 5120 whole 171 us, in segments (24 warps) 205.
+constexpr int64_t kFill = 16, kLeast = 128;
 
-int segment_count(int64_t batch, int64_t L, int blocks) {
-  const int64_t all = batch * blocks;
+int segment_count(int64_t batch, int64_t L, int64_t blocks, int warps) {
+  const int64_t all = batch * blocks * warps;
   const int64_t want = kFill * layer_sm_count();
-  if (2 * all > want) return 1;
+  if (4 * all > want) return 1;
   int64_t s = want / all;
   const int64_t most = L / kLeast;
   if (s > most) s = most;
   return s < 3 ? 1 : static_cast<int>(s);  // two segments pay for one in the first launch and gain nothing
 }
 
-template <typename T, int NS, bool kVec>
-cudaError_t launch_ns(const ScanParams& p, int64_t batch, cudaStream_t stream) {
+template <typename V, int T, bool kVec>
+cudaError_t launch_lanes(ScanParams p, int64_t batch, cudaStream_t stream) {
+  constexpr int kThreads = Shape<T>::kThreads + Shape<T>::kHelp;
   const unsigned blocks = static_cast<unsigned>(p.G * p.tiles);
   if (p.segments > 1) {
-    const cudaError_t e = launch_k(scan_kernel<T, NS, kVec, true>,
+    const cudaError_t e = launch_k(scan_kernel<V, T, kVec, true>,
                                    dim3(blocks, static_cast<unsigned>(p.segments - 1), static_cast<unsigned>(batch)),
                                    dim3(kThreads), 0, stream, false, p);
     if (e != cudaSuccess) return e;
   }
-  return launch_k(scan_kernel<T, NS, kVec, false>,
-                  dim3(blocks, static_cast<unsigned>(p.segments), static_cast<unsigned>(batch)), dim3(kThreads), 0,
-                  stream, p.segments > 1, p);
+  return launch_k(scan_kernel<V, T, kVec, false>,
+                  dim3(blocks, static_cast<unsigned>(p.segments), static_cast<unsigned>(batch)), dim3(kThreads),
+                  0, stream, p.segments > 1, p);
 }
 
-template <typename T, bool kVec>
+// Lanes a channel's states are spread over.
+int lanes_of(int N) { return N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }
+
+template <typename V, bool kVec>
 cudaError_t launch_vec(const ScanParams& p, int64_t batch, cudaStream_t stream) {
-  if (p.N <= 8) return launch_ns<T, 2, kVec>(p, batch, stream);
-  if (p.N <= 16) return launch_ns<T, 4, kVec>(p, batch, stream);
-  if (p.N <= 32) return launch_ns<T, 8, kVec>(p, batch, stream);
-  return launch_ns<T, 16, kVec>(p, batch, stream);
+  switch (lanes_of(p.N)) {
+    case 2: return launch_lanes<V, 2, kVec>(p, batch, stream);
+    case 4: return launch_lanes<V, 4, kVec>(p, batch, stream);
+    case 8: return launch_lanes<V, 8, kVec>(p, batch, stream);
+    default: return launch_lanes<V, 16, kVec>(p, batch, stream);
+  }
 }
 
 template <typename T>
@@ -409,8 +509,11 @@ ssd_status check_sizes(const ssd_selective_scan_args* a) {
   return SSD_OK;
 }
 
-int blocks_of(const ssd_selective_scan_args* a) {
-  return a->ngroups * static_cast<int>(ceil_div(a->channels / a->ngroups, kChannels));
+int channels_of_block(int N) { return lanes_of(N) == 2 ? Shape<2>::kChannels : Shape<4>::kChannels; }
+
+int segments_of(const ssd_selective_scan_args* a) {
+  const int64_t blocks = ceil_div(a->channels / a->ngroups, channels_of_block(a->dstate)) * a->ngroups;
+  return segment_count(a->batch, a->seqlen, blocks, lanes_of(a->dstate) < 4 ? 1 : lanes_of(a->dstate) / 4);
 }
 
 }  // namespace
@@ -419,7 +522,7 @@ int blocks_of(const ssd_selective_scan_args* a) {
 extern "C" size_t ssd_selective_scan_workspace_size(const ssd_selective_scan_args* a) {
   using namespace ssd;
   if (check_sizes(a) != SSD_OK || a->batch == 0) return 0;
-  const int s = segment_count(a->batch, a->seqlen, blocks_of(a));
+  const int s = segments_of(a);
   return s == 1 ? 0 : static_cast<size_t>(s) * a->batch * a->channels * (a->dstate + 1) * sizeof(float);
 }
 
@@ -442,7 +545,7 @@ extern "C" ssd_status ssd_selective_scan(const ssd_selective_scan_args* a, ssd_s
     return SSD_OK;
   }
   ScanParams p{};
-  p.segments = segment_count(a->batch, a->seqlen, blocks_of(a));
+  p.segments = segments_of(a);
   if (p.segments > 1) {
     if (!a->workspace || !aligned_to(a->workspace, 16)) return SSD_ERR_INVALID_ARG;
     if (a->workspace_bytes < ssd_selective_scan_workspace_size(a)) return SSD_ERR_WORKSPACE;
@@ -455,7 +558,7 @@ extern "C" ssd_status ssd_selective_scan(const ssd_selective_scan_args* a, ssd_s
   p.N = a->dstate;
   p.G = a->ngroups;
   p.per = a->channels / a->ngroups;
-  p.tiles = static_cast<int>(ceil_div(p.per, kChannels));
+  p.tiles = static_cast<int>(ceil_div(p.per, channels_of_block(p.N)));
   p.softplus = a->softplus != 0;
   p.u = a->u, p.delta = a->delta, p.z = a->z, p.Bm = a->Bm, p.Cm = a->Cm;
   p.ub = a->u_batch, p.ut = a->u_token, p.db = a->delta_batch, p.dt = a->delta_token;
