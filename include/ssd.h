@@ -316,7 +316,7 @@ typedef enum { SSD_ACT_NONE = 0, SSD_ACT_SILU = 1 } ssd_activation;
  * up to three tensors, so that x, Bm and Cm land where ssd_fwd reads them. */
 typedef struct {
   int64_t size;              /* sizeof(ssd_conv_args) */
-  int64_t batch, seqlen;     /* >= 0; batch <= 65535 */
+  int64_t batch, seqlen;     /* >= 0; batch <= 65535, seqlen <= 2^30 */
   int64_t nslots;            /* rows of the ring; >= batch where slots is NULL */
   int32_t channels, width;   /* width 2, 3 or 4 */
   int32_t dtype, activation; /* of u, ring and out; ssd_activation */

@@ -2,8 +2,11 @@
 //   y[t][c] = act(bias[c] + sum_{j<W} w[c][j] u[t - W + 1 + j][c]).
 //
 // Each input element is used by W outputs of its own channel only, so the work
-// is one pass over memory: a thread walks down a run of tokens of its channel
-// with the last W - 1 inputs in registers.
+// is one pass over memory, and HBM bounds it.  A thread takes four channels (8 or
+// 16 bytes) and walks down a run of tokens with the last W - 1 inputs in
+// registers; the next eight tokens are on their way while eight are computed.
+// Runs of one channel group start W - 1 tokens early, which costs 3/32 more
+// reads (from L2, mostly) at runs of 32.
 //
 // The ring may be read and updated in place: the thread that owns a channel's
 // first run is the only one that reads the ring, and it writes it too, after
@@ -14,11 +17,11 @@ namespace ssd {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kRun = 32;  // tokens per block
+constexpr int kStep = 8;  // tokens loaded together
 
 struct ConvParams {
   int64_t L, u_batch, u_token, nslots;
-  int C, silu;
+  int C, silu, run;  // run: tokens a thread walks down, a multiple of kStep
   const void* u;
   const float *weight, *bias;
   const void* ring;
@@ -28,69 +31,158 @@ struct ConvParams {
   int begin[4];  // first channel of each output; begin[nout] = C
 };
 
-template <typename T, int W>
+// kC consecutive channels of one token, as they lie in memory.
+template <typename T, int kC>
+struct Chans;
+template <typename T>
+struct Chans<T, 1> {
+  T v;
+  __device__ __forceinline__ void load(const T* p) { v = *p; }
+  __device__ __forceinline__ void store(T* p) const { *p = v; }
+  __device__ __forceinline__ float get(int) const { return to_f32(v); }
+  __device__ __forceinline__ void set(const float (&f)[1]) { v = from_f32<T>(f[0]); }
+};
+template <>
+struct Chans<float, 4> {
+  float4 v;
+  __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float4*>(p); }
+  __device__ __forceinline__ void store(float* p) const { *reinterpret_cast<float4*>(p) = v; }
+  __device__ __forceinline__ float get(int i) const { return (&v.x)[i]; }
+  __device__ __forceinline__ void set(const float (&f)[4]) { v = make_float4(f[0], f[1], f[2], f[3]); }
+};
+template <>
+struct Chans<__nv_bfloat16, 4> {
+  uint2 v;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint2*>(p); }
+  __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint2*>(p) = v; }
+  __device__ __forceinline__ float get(int i) const {
+    const uint32_t w = i < 2 ? v.x : v.y;
+    return __uint_as_float(i % 2 ? w & 0xFFFF0000u : w << 16);
+  }
+  __device__ __forceinline__ void set(const float (&f)[4]) {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(f[0], f[1]), hi = __floats2bfloat162_rn(f[2], f[3]);
+    v = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  }
+};
+
+template <typename T, int W, int kC>
 __global__ void __launch_bounds__(kThreads) conv_kernel(ConvParams p) {
-  const int c = blockIdx.x * kThreads + threadIdx.x;
-  const int b = blockIdx.z;
-  if (c >= p.C) return;
-  const int64_t t0 = static_cast<int64_t>(blockIdx.y) * kRun;
-  const int64_t t1 = t0 + kRun < p.L ? t0 + kRun : p.L;
+  using Ch = Chans<T, kC>;
+  const int groups = p.C / kC;
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  const int64_t t0 = id / groups * p.run;
+  const int c = static_cast<int>(id % groups) * kC;
+  const int b = blockIdx.y;
+  if (t0 >= p.L && t0 > 0) return;
+  const int64_t t1 = t0 + p.run < p.L ? t0 + p.run : p.L;
   const int64_t slot = p.slots ? p.slots[b] : b;
-  const bool idle = slot < 0 || slot >= p.nslots;
+  const bool idle = p.ring && (slot < 0 || slot >= p.nslots);
   int64_t len = p.L;
   if (p.lengths) len = p.lengths[b] < 0 ? 0 : p.lengths[b] < p.L ? p.lengths[b] : p.L;
-  if (idle && p.ring) len = 0;
+  if (idle) len = 0;
+  const int64_t end = len < t1 ? len : t1;
   const int64_t pos = p.positions && p.positions[b] > 0 ? p.positions[b] : 0;
   const T* u = static_cast<const T*>(p.u) + b * p.u_batch + c;
-  const T* ring = static_cast<const T*>(p.ring);
-  if (ring && !idle) ring += slot * W * p.C + c;
+  const T* ring = p.ring && !idle ? static_cast<const T*>(p.ring) + slot * W * p.C + c : nullptr;
 
-  float w[W], win[W];  // win[j]: input of token t - W + 1 + j
+  Ch next[kStep];
+  auto fetch = [&](int64_t t) {
 #pragma unroll
-  for (int j = 0; j < W; ++j) w[j] = p.weight[static_cast<int64_t>(c) * W + j];
-  const float bias = p.bias ? p.bias[c] : 0.f;
+    for (int k = 0; k < kStep; ++k)
+      if (t + k < end) next[k].load(u + (t + k) * p.u_token);
+  };
+  fetch(t0);
+
+  float w[W][kC], win[W][kC], bias[kC];  // win[j]: input of token t - W + 1 + j
+  if constexpr (W == 4) {
+    static_assert(sizeof(float4) == W * sizeof(float), "a channel's taps are one vector");
+    const bool vec = (reinterpret_cast<uintptr_t>(p.weight) & 15) == 0;
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j) {
-    const int64_t t = t0 - (W - 1) + j;
-    win[j + 1] = 0.f;
-    if (t >= 0) {
-      if (t < len) win[j + 1] = to_f32(u[t * p.u_token]);
-    } else if (ring && !idle && pos + t >= 0) {
-      win[j + 1] = to_f32(ring[((pos + t) % W) * p.C]);
+    for (int i = 0; i < kC; ++i) {
+      const float* row = p.weight + static_cast<int64_t>(c + i) * W;
+      float4 f;
+      if (vec) f = *reinterpret_cast<const float4*>(row);
+      else f = make_float4(row[0], row[1], row[2], row[3]);
+      w[0][i] = f.x, w[1][i] = f.y, w[2][i] = f.z, w[3][i] = f.w;
     }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kC; ++i)
+#pragma unroll
+      for (int j = 0; j < W; ++j) w[j][i] = p.weight[static_cast<int64_t>(c + i) * W + j];
   }
-  if (t0 == 0 && ring && !idle) {
-    T* nr = p.new_ring ? static_cast<T*>(p.new_ring) + slot * W * p.C + c : const_cast<T*>(ring);
-    if (p.new_ring && len < W) {
 #pragma unroll
-      for (int q = 0; q < W; ++q) nr[q * p.C] = ring[q * p.C];
+  for (int i = 0; i < kC; ++i) bias[i] = p.bias ? p.bias[c + i] : 0.f;
+#pragma unroll
+  for (int j = 1; j < W; ++j) {
+    const int64_t t = t0 - W + j;
+    Ch before;
+    const bool in_call = t >= 0 && t < len, in_ring = t < 0 && ring && pos + t >= 0;
+    if (in_call) before.load(u + t * p.u_token);
+    else if (in_ring) before.load(ring + (pos + t) % W * p.C);
+#pragma unroll
+    for (int i = 0; i < kC; ++i) win[j][i] = in_call || in_ring ? before.get(i) : 0.f;
+  }
+  if (t0 == 0 && ring) {
+    T* keep = p.new_ring ? static_cast<T*>(p.new_ring) + slot * W * p.C + c : const_cast<T*>(ring);
+    Ch v;
+    if (p.new_ring && len < W) {  // slots that no token of this call takes
+#pragma unroll
+      for (int q = 0; q < W; ++q) {
+        v.load(ring + q * p.C);
+        v.store(keep + q * p.C);
+      }
     }
-    for (int64_t t = len > W ? len - W : 0; t < len; ++t) nr[((pos + t) % W) * p.C] = u[t * p.u_token];
+    for (int64_t t = len > W ? len - W : 0; t < len; ++t) {
+      v.load(u + t * p.u_token);
+      v.store(keep + (pos + t) % W * p.C);
+    }
   }
   int part = 0;
   while (c >= p.begin[part + 1]) ++part;
   const int64_t width = p.begin[part + 1] - p.begin[part];
   T* out = static_cast<T*>(p.out[part]) + static_cast<int64_t>(b) * p.L * width + (c - p.begin[part]);
-  for (int64_t t = t0; t < t1; ++t) {
-    if (t >= len) {
-      out[t * width] = from_f32<T>(0.f);
-      continue;
+  for (int64_t t = t0; t < t1; t += kStep) {
+    Ch now[kStep];
+#pragma unroll
+    for (int k = 0; k < kStep; ++k) now[k] = next[k];
+    fetch(t + kStep);
+#pragma unroll
+    for (int k = 0; k < kStep; ++k) {
+      if (t + k >= t1) break;
+      float acc[kC];
+#pragma unroll
+      for (int i = 0; i < kC; ++i) {
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) win[j][i] = win[j + 1][i];
+        win[W - 1][i] = now[k].get(i);
+        acc[i] = bias[i];
+#pragma unroll
+        for (int j = 0; j < W; ++j) acc[i] = fmaf(w[j][i], win[j][i], acc[i]);
+        if (p.silu) acc[i] = silu(acc[i]);
+        if (t + k >= len) acc[i] = 0.f;
+      }
+      Ch y;
+      y.set(acc);
+      y.store(out + (t + k) * width);
     }
-#pragma unroll
-    for (int j = 0; j < W - 1; ++j) win[j] = win[j + 1];
-    win[W - 1] = to_f32(u[t * p.u_token]);
-    float acc = bias;
-#pragma unroll
-    for (int j = 0; j < W; ++j) acc = fmaf(w[j], win[j], acc);
-    out[t * width] = from_f32<T>(p.silu ? silu(acc) : acc);
   }
 }
 
 template <typename T>
-cudaError_t launch(const ConvParams& p, int width, int64_t batch, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(ceil_div(p.C, kThreads)),
-                  static_cast<unsigned>(p.L > 0 ? ceil_div(p.L, kRun) : 1), static_cast<unsigned>(batch));
-  auto k = width == 2 ? conv_kernel<T, 2> : width == 3 ? conv_kernel<T, 3> : conv_kernel<T, 4>;
+cudaError_t launch(ConvParams p, int width, int64_t batch, cudaStream_t stream) {
+  // four channels at a time where they start on a whole vector in every row
+  const size_t bytes = 4 * sizeof(T);
+  bool vec = p.C % 4 == 0 && aligned_to(p.u, bytes) && p.u_token % 4 == 0 && p.u_batch % 4 == 0 &&
+             aligned_to(p.ring, bytes) && aligned_to(p.new_ring, bytes);
+  for (int i = 0; i < 3; ++i) vec = vec && p.begin[i] % 4 == 0 && aligned_to(p.out[i], bytes);
+  const int64_t groups = vec ? p.C / 4 : p.C;
+  // long runs re-read least; short ones where the threads would not fill the GPU otherwise
+  p.run = batch * groups * ceil_div(p.L, 32) >= 1024 * static_cast<int64_t>(layer_sm_count()) ? 32 : kStep;
+  const int64_t runs = p.L > 0 ? ceil_div(p.L, p.run) : 1;
+  const dim3 grid(static_cast<unsigned>(ceil_div(groups * runs, kThreads)), static_cast<unsigned>(batch));
+  auto k = vec ? (width == 2 ? conv_kernel<T, 2, 4> : width == 3 ? conv_kernel<T, 3, 4> : conv_kernel<T, 4, 4>)
+               : (width == 2 ? conv_kernel<T, 2, 1> : width == 3 ? conv_kernel<T, 3, 1> : conv_kernel<T, 4, 1>);
   return launch_k(k, grid, dim3(kThreads), 0, stream, false, p);
 }
 
@@ -112,7 +204,7 @@ extern "C" ssd_status ssd_conv_fwd(const ssd_conv_args* a, ssd_stream_t stream) 
   if (a->batch < 0 || a->seqlen < 0 || a->channels <= 0 || a->nslots < 0) return SSD_ERR_INVALID_ARG;
   if (!known_dtype(a->dtype) || a->width < 2 || a->width > 4) return SSD_ERR_UNSUPPORTED;
   if (a->activation != SSD_ACT_NONE && a->activation != SSD_ACT_SILU) return SSD_ERR_UNSUPPORTED;
-  if (a->batch > 65535 || ceil_div(a->seqlen, kRun) > 65535) return SSD_ERR_UNSUPPORTED;
+  if (a->batch > 65535 || a->seqlen > (int64_t(1) << 30)) return SSD_ERR_UNSUPPORTED;
   if (a->nout < 1 || a->nout > 3) return SSD_ERR_INVALID_ARG;
   const size_t es = elem_size(a->dtype);
   ConvParams p{};

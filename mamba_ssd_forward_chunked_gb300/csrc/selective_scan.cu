@@ -447,9 +447,103 @@ __global__ void __launch_bounds__(Shape<T>::kThreads + Shape<T>::kHelp) scan_ker
   }
 }
 
+// One token: every state is read and written once and there is nothing to walk along, so memory
+// bounds it.  A thread takes four states of a channel, T neighbouring lanes share the channel (its
+// step is formed by each of them), and runs over kRows sequences, whose loads are all on their way
+// before the first is used; A and the channel's constants are read once for them.
+constexpr int kTokenThreads = 256, kRows = 4;
+
+template <typename V, int T, bool kVec>
+__global__ void __launch_bounds__(kTokenThreads) scan_token_kernel(ScanParams p, int batch) {
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * kTokenThreads + threadIdx.x;
+  const int part = static_cast<int>(id % T), n0 = 4 * part;
+  const bool live = id / T < p.D;
+  const int c = live ? static_cast<int>(id / T) : p.D - 1;  // lanes past the end repeat the last channel
+  const int g = c / p.per;
+  const int b0 = blockIdx.y * kRows;
+
+  auto load4 = [&](const float* t, float (&v)[4]) {  // four states from t, 0 past N
+    if constexpr (kVec) {
+      float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (n0 < p.N) f = *reinterpret_cast<const float4*>(t);
+      v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = n0 + e < p.N ? t[e] : 0.f;
+    }
+  };
+  auto load_bc = [&](const V* t, float (&v)[4]) {
+    if constexpr (kVec && sizeof(V) == 2) {
+      uint2 w = make_uint2(0, 0);
+      if (n0 < p.N) w = *reinterpret_cast<const uint2*>(t);
+      v[0] = __uint_as_float(w.x << 16), v[1] = __uint_as_float(w.x & 0xFFFF0000u);
+      v[2] = __uint_as_float(w.y << 16), v[3] = __uint_as_float(w.y & 0xFFFF0000u);
+    } else if constexpr (kVec) {
+      load4(reinterpret_cast<const float*>(t), v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = n0 + e < p.N ? to_f32(t[e]) : 0.f;
+    }
+  };
+
+  float a[4], h[kRows][4], Bv[kRows][4], Cv[kRows][4], u[kRows], d[kRows], z[kRows];
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    const int64_t b = b0 + r < batch ? b0 + r : batch - 1;
+    const bool on = !p.lengths || p.lengths[b] > 0;
+    u[r] = d[r] = z[r] = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[r][e] = Bv[r][e] = Cv[r][e] = 0.f;
+    if (p.init) load4(p.init + (b * p.D + c) * p.N + n0, h[r]);
+    if (on) {  // a sequence without a token keeps its state, and its inputs are not looked at
+      u[r] = to_f32(static_cast<const V*>(p.u)[b * p.ub + c]);
+      d[r] = to_f32(static_cast<const V*>(p.delta)[b * p.db + c]);
+      if (p.z) z[r] = to_f32(static_cast<const V*>(p.z)[b * p.zb + c]);
+      load_bc(static_cast<const V*>(p.Bm) + b * p.Bb + static_cast<int64_t>(g) * p.N + n0, Bv[r]);
+      load_bc(static_cast<const V*>(p.Cm) + b * p.Cb + static_cast<int64_t>(g) * p.N + n0, Cv[r]);
+    }
+  }
+  load4(p.A + static_cast<int64_t>(c) * p.N + n0, a);
+  const float bias = p.delta_bias ? p.delta_bias[c] : 0.f, skip = p.skip ? p.skip[c] : 0.f;
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    const int64_t b = b0 + r;
+    if (b >= batch) break;
+    const bool on = !p.lengths || p.lengths[b] > 0;
+    float step = d[r] + bias, other = 0.f;
+    if (p.softplus) softplus2(step, other);
+    if (!on) step = 0.f;
+    const float du = step * u[r];
+    float sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      h[r][e] = fmaf(exp2_fast(step * (a[e] * kLog2e)), h[r][e], du * Bv[r][e]);
+      sum = fmaf(h[r][e], Cv[r][e], sum);
+    }
+#pragma unroll
+    for (int o = 1; o < T; o *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (!live) continue;
+    if (part == 0) {
+      float y = fmaf(skip, u[r], sum);
+      if (p.z) y *= silu(z[r]);
+      static_cast<V*>(p.y)[b * p.D + c] = from_f32<V>(on ? y : 0.f);
+    }
+    if (p.final_state) {
+      float* out = p.final_state + (b * p.D + c) * p.N + n0;
+      if constexpr (kVec) {
+        if (n0 < p.N) *reinterpret_cast<float4*>(out) = make_float4(h[r][0], h[r][1], h[r][2], h[r][3]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (n0 + e < p.N) out[e] = h[r][e];
+      }
+    }
+  }
+}
+
 // Segments a sequence is cut into: enough recurrence warps for kFill on every multiprocessor, but no
 // segment below kLeast tokens.  Measured: 16384 x 2048 fp32 with 8, 12, 16 and 24 warps 362, 370,
-// 364 and 381 us (whole: 1550 us); 2 x 2048 x 5120 whole 171 us, in segments (24 warps) 205.
+// 364 and 381 us; 2 x 2048 x 5120 whole 171 us, in segments (24 warps) 205.
 constexpr int64_t kFill = 16, kLeast = 128;
 
 int segment_count(int64_t batch, int64_t L, int64_t blocks, int warps) {
@@ -460,6 +554,19 @@ int segment_count(int64_t batch, int64_t L, int64_t blocks, int warps) {
   const int64_t most = L / kLeast;
   if (s > most) s = most;
   return s < 3 ? 1 : static_cast<int>(s);  // two segments pay for one in the first launch and gain nothing
+}
+
+template <typename V, int T>
+cudaError_t launch_token(const ScanParams& p, int64_t batch, cudaStream_t stream) {
+  const int64_t es = sizeof(V);
+  // four states at a time where they start on 16 bytes (B and C: on four elements) everywhere
+  const bool vec = p.N % 4 == 0 && aligned_to(p.A, 16) && aligned_to(p.init, 16) && aligned_to(p.final_state, 16) &&
+                   aligned_to(p.Bm, 4 * es) && aligned_to(p.Cm, 4 * es) &&
+                   (batch == 1 || (p.Bb % 4 == 0 && p.Cb % 4 == 0));
+  const dim3 grid(static_cast<unsigned>(ceil_div(static_cast<int64_t>(p.D) * T, kTokenThreads)),
+                  static_cast<unsigned>(ceil_div(batch, kRows)));
+  return launch_k(vec ? scan_token_kernel<V, T, true> : scan_token_kernel<V, T, false>, grid, dim3(kTokenThreads), 0,
+                  stream, false, p, static_cast<int>(batch));
 }
 
 template <typename V, int T, bool kVec>
@@ -492,10 +599,18 @@ cudaError_t launch_vec(const ScanParams& p, int64_t batch, cudaStream_t stream) 
 
 template <typename T>
 cudaError_t launch(const ScanParams& p, int64_t batch, cudaStream_t stream) {
+  if (p.L == 1) {
+    switch (lanes_of(p.N)) {
+      case 2: return launch_token<T, 2>(p, batch, stream);
+      case 4: return launch_token<T, 4>(p, batch, stream);
+      case 8: return launch_token<T, 8>(p, batch, stream);
+      default: return launch_token<T, 16>(p, batch, stream);
+    }
+  }
   // 16-byte loads where every row of eight channels (of eight states) starts on 16 bytes and is whole
   const int64_t es = sizeof(T);
   auto row16 = [&](const void* t, int64_t s0, int64_t s1) {
-    return aligned_to(t, 16) && (batch == 1 || s0 * es % 16 == 0) && (p.L <= 1 || s1 * es % 16 == 0);
+    return aligned_to(t, 16) && (batch == 1 || s0 * es % 16 == 0) && s1 * es % 16 == 0;
   };
   const bool vec = p.per % 8 == 0 && p.N % 8 == 0 && row16(p.u, p.ub, p.ut) && row16(p.delta, p.db, p.dt) &&
                    row16(p.z, p.zb, p.zt) && row16(p.Bm, p.Bb, p.Bt) && row16(p.Cm, p.Cb, p.Ct) && aligned_to(p.y, 16);

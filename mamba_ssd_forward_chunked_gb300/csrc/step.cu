@@ -2,11 +2,15 @@
 // the token's x, B, C channels with its ring, then per head
 //   h = exp(d A) h + d x b^T,   y = (h c + D x) silu(z).
 //
-// One block per (sequence, head).  It forms the head's x and its group's B and
-// C itself, so the whole layer step is one launch: B and C are formed again by
-// every head of a group, a few hundred multiplications against the head's
-// 2 x 32 KB of state.  The ring has one slot more than the taps reach back, so
-// the slot that takes the new token is read by nobody in this launch.
+// Every state is read and written once, so HBM bounds it (one sequence: the
+// latency of one launch).  A block takes a head of a sequence, or a quarter of
+// its rows where there are few heads in the batch.  Its states are on their way,
+// 16 bytes a load and up to 16 loads a thread, before it forms the head's x and
+// its group's B and C by itself, so that the whole layer step is one launch: B
+// and C are formed again by every head of a group, a few hundred multiplications
+// against the head's 2 x 32 KB of state.  The ring has one slot more than the
+// taps reach back, so the slot that takes the new token is read by nobody in
+// this launch, and B's and C's are written by one block of the group alone.
 #include "layer.cuh"
 
 namespace ssd {
@@ -27,63 +31,111 @@ struct StepParams {
   void* y;
 };
 
-template <typename T>
+// kRows: rows of the head's 64 that a block takes.
+template <typename T, int N, int kRows>
 __global__ void __launch_bounds__(kThreads) step_kernel(StepParams p) {
-  __shared__ float xbc[kP + 2 * 256];
-  const int h = blockIdx.x;
+  constexpr int kLanes = N >= 128 ? 32 : 16;           // lanes that share a row
+  constexpr int kVecs = N / (4 * kLanes);              // float4 a lane has of a row
+  constexpr int kPerPass = kThreads / kLanes;          // rows the block takes in one pass
+  constexpr int kPasses = kRows / kPerPass;
+  __shared__ __align__(16) float s_x[kRows], s_B[N], s_C[N];
+  __shared__ float s_y[kRows];
+  const int row0 = blockIdx.x % (kP / kRows) * kRows;
+  const int h = blockIdx.x / (kP / kRows);
   const int64_t b = blockIdx.y;
   const int g = h / (p.H / p.G);
-  const bool writes_group = h % (p.H / p.G) == 0;  // the group's first head keeps its B and C in the ring
+  const bool writes_group = h % (p.H / p.G) == 0 && row0 == 0;  // keeps the group's B and C in the ring
   const int64_t slot = p.slots ? p.slots[b] : b;
-  T* y = static_cast<T*>(p.y) + (b * p.H + h) * kP;
+  const int tid = threadIdx.x;
+  T* y = static_cast<T*>(p.y) + (b * p.H + h) * kP + row0;
   if (slot < 0 || slot >= p.nslots) {
-    if (threadIdx.x < kP) y[threadIdx.x] = from_f32<T>(0.f);
+    if (tid < kRows) y[tid] = from_f32<T>(0.f);
     return;
   }
-  const int64_t pos = p.positions[b] > 0 ? p.positions[b] : 0;
-  const int inner = p.H * kP;
-  const int64_t C = inner + 2 * p.G * p.N;
-  const T* u = static_cast<const T*>(p.u) + b * p.u_batch;
-  T* ring = static_cast<T*>(p.ring) + slot * p.W * C;
-  for (int i = threadIdx.x; i < kP + 2 * p.N; i += kThreads) {
-    const int c = i < kP ? h * kP + i
-                         : inner + (i < kP + p.N ? g * p.N + (i - kP) : p.G * p.N + g * p.N + (i - kP - p.N));
-    const float* w = p.weight + static_cast<int64_t>(c) * p.W;
-    float acc = p.bias ? p.bias[c] : 0.f;
-    for (int j = 0; j < p.W - 1; ++j) {
-      const int64_t t = pos - (p.W - 1) + j;
-      if (t >= 0) acc = fmaf(w[j], to_f32(ring[(t % p.W) * C + c]), acc);
-    }
-    acc = fmaf(w[p.W - 1], to_f32(u[c]), acc);
-    xbc[i] = silu(acc);
-    if (i < kP || writes_group) ring[(pos % p.W) * C + c] = u[c];
-  }
-  __syncthreads();
+
+  const int lane = tid % kLanes, row_in = tid / kLanes;
+  const int64_t base = ((slot * p.H + h) * kP + row0 + row_in) * N + 4 * lane;
+  float4 st[kPasses][kVecs];
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i)
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v)
+      st[i][v] = __ldcs(reinterpret_cast<const float4*>(p.state + base + i * kPerPass * N + v * 4 * kLanes));
+
   float d = p.dt_f32 ? static_cast<const float*>(p.dt)[b * p.dt_batch + h]
                      : to_f32(static_cast<const T*>(p.dt)[b * p.dt_batch + h]);
   if (p.dt_bias) d += p.dt_bias[h];
-  if (p.softplus) d = softplus(d);
-  const float decay = expf(d * p.A[h]);
-  const float skip = p.D[h];
-  const int64_t base = (slot * p.H + h) * kP * p.N;
-  float* out = p.new_state ? p.new_state : const_cast<float*>(p.state);
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  for (int r = warp; r < kP; r += kThreads / 32) {
-    const float dx = d * xbc[r];
-    float acc = 0.f;
-    for (int n = lane; n < p.N; n += 32) {
-      const int64_t i = base + r * p.N + n;
-      const float v = fmaf(decay, p.state[i], dx * xbc[kP + n]);
-      out[i] = v;
-      acc = fmaf(v, xbc[kP + p.N + n], acc);
+  const float rate = p.A[h], skip = p.D[h];
+  float z = 0.f;
+  if (p.z && tid < kRows) z = to_f32(static_cast<const T*>(p.z)[b * p.z_batch + h * kP + row0 + tid]);
+
+  const int64_t pos = p.positions[b] > 0 ? p.positions[b] : 0;
+  const int inner = p.H * kP;
+  const int64_t C = inner + 2 * p.G * N;
+  const T* u = static_cast<const T*>(p.u) + b * p.u_batch;
+  T* ring = static_cast<T*>(p.ring) + slot * p.W * C;
+  const int newest = static_cast<int>(pos % p.W);
+#pragma unroll
+  for (int i = tid; i < kRows + 2 * N; i += kThreads) {
+    const int c = i < kRows ? h * kP + row0 + i
+                            : inner + (i < kRows + N ? g * N + (i - kRows) : (p.G + g) * N + (i - kRows - N));
+    const float* w = p.weight + static_cast<int64_t>(c) * p.W;
+    const T now = u[c];
+    float acc = p.bias ? p.bias[c] : 0.f;
+    acc = fmaf(w[p.W - 1], to_f32(now), acc);
+#pragma unroll
+    for (int j = 1; j < 4; ++j) {  // the token j before this one
+      if (j >= p.W || j > pos) break;
+      const int q = newest >= j ? newest - j : newest - j + p.W;
+      acc = fmaf(w[p.W - 1 - j], to_f32(ring[q * C + c]), acc);
     }
-    for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-    if (lane == 0) {
-      acc = fmaf(skip, xbc[r], acc);
-      if (p.z) acc *= silu(to_f32(static_cast<const T*>(p.z)[b * p.z_batch + h * kP + r]));
-      y[r] = from_f32<T>(acc);
-    }
+    if (i < kRows || writes_group) ring[newest * C + c] = now;
+    (i < kRows ? s_x[i] : i < kRows + N ? s_B[i - kRows] : s_C[i - kRows - N]) = silu(acc);
   }
+  __syncthreads();
+  if (p.softplus) d = softplus(d);
+  const float decay = expf(d * rate);
+  float* out = (p.new_state ? p.new_state : const_cast<float*>(p.state)) + base;
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const float dx = d * s_x[row_in + i * kPerPass];
+    float sum = 0.f;
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) {
+      const float4 B4 = *reinterpret_cast<const float4*>(&s_B[4 * lane + v * 4 * kLanes]);
+      const float4 C4 = *reinterpret_cast<const float4*>(&s_C[4 * lane + v * 4 * kLanes]);
+      float4 s = st[i][v];
+      s.x = fmaf(decay, s.x, dx * B4.x);
+      s.y = fmaf(decay, s.y, dx * B4.y);
+      s.z = fmaf(decay, s.z, dx * B4.z);
+      s.w = fmaf(decay, s.w, dx * B4.w);
+      sum = fmaf(s.x, C4.x, fmaf(s.y, C4.y, fmaf(s.z, C4.z, fmaf(s.w, C4.w, sum))));
+      __stcs(reinterpret_cast<float4*>(out + i * kPerPass * N + v * 4 * kLanes), s);
+    }
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) s_y[row_in + i * kPerPass] = sum;
+  }
+  __syncthreads();
+  if (tid < kRows) {
+    float v = fmaf(skip, s_x[tid], s_y[tid]);
+    if (p.z) v *= silu(z);
+    y[tid] = from_f32<T>(v);
+  }
+}
+
+template <typename T, int N>
+cudaError_t launch(const StepParams& p, int64_t batch, cudaStream_t stream) {
+  // a head a block, or quarters of heads while those leave the GPU room
+  const bool few = batch * p.H < 2 * static_cast<int64_t>(layer_sm_count());
+  const dim3 grid(static_cast<unsigned>(p.H * (few ? 4 : 1)), static_cast<unsigned>(batch));
+  return launch_k(few ? step_kernel<T, N, 16> : step_kernel<T, N, 64>, grid, dim3(kThreads), 0, stream, false, p);
+}
+
+template <typename T>
+cudaError_t launch_n(const StepParams& p, int64_t batch, cudaStream_t stream) {
+  return p.N == 64 ? launch<T, 64>(p, batch, stream) : p.N == 128 ? launch<T, 128>(p, batch, stream)
+                                                                  : launch<T, 256>(p, batch, stream);
 }
 
 }  // namespace
@@ -117,8 +169,6 @@ extern "C" ssd_status ssd_step(const ssd_step_args* a, ssd_stream_t stream) {
   p.ring = a->ring, p.state = a->state, p.new_state = a->new_state;
   p.positions = a->positions, p.slots = a->slots;
   p.y = a->y;
-  const dim3 grid(static_cast<unsigned>(p.H), static_cast<unsigned>(a->batch));
-  return launched(a->dtype == SSD_BF16
-                      ? launch_k(step_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, stream, false, p)
-                      : launch_k(step_kernel<float>, grid, dim3(kThreads), 0, stream, false, p));
+  return launched(a->dtype == SSD_BF16 ? launch_n<__nv_bfloat16>(p, a->batch, stream)
+                                       : launch_n<float>(p, a->batch, stream));
 }
