@@ -1,10 +1,24 @@
 // Beam search: the k best of beams x vocab candidates, and the reordering of
 // the states that the choice decides.
 //
-// Selection in two launches: each beam's log-sum-exp, then per request k rounds
-// over all candidates, each taking the largest key below the last one taken.  A
-// key holds a score in the order of unsigned integers and the complement of the
-// candidate's index, so keys differ and equal scores fall by rising index.
+// Selection reads the logits once; HBM bounds it.  Within a beam the score
+// s + (x - lse) never falls as the logit x rises, so a block that holds a piece
+// of a row in registers can name its best by logit before the row's log-sum-exp
+// is known: it writes the k + 1 best and the piece's maximum and sum of
+// exponentials.  A second launch joins the sums in a fixed order and picks the k
+// best scores of a request among its pieces' candidates.
+//
+// A key holds a value in the order of unsigned integers and the complement of
+// the candidate's index, so keys differ and equal values fall by rising index.
+// The n best of a block: every group of four (or two) threads has a largest key;
+// no key below the n-th largest of those can be among the n best, few keys reach
+// it, and those are ranked by counting.
+//
+// Rounding can give different logits of a beam one score, and then the lower
+// index goes first although its logit is smaller.  Such a candidate may be
+// missing from its piece's list, but only if the piece's (k + 1)-th still has
+// the k-th best score; then the second launch looks through the pieces that
+// reach this score once more, in the order of indexes.
 //
 // Reordering moves bytes: a thread owns a few bytes' position in all rows of a
 // request, reads them all, then writes, so that it may work in place.
@@ -17,26 +31,35 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxBeams = 64;
+constexpr int kMaxGroups = 128;
+constexpr int kMergeKeys = 1024;  // candidates the second launch ranks at once
+using Key = unsigned long long;
 
 struct SelectParams {
   int64_t logits_batch, logits_beam;
-  int beams, vocab, k, eos;
+  int beams, vocab, k, eos, pieces, keep;  // keep: keys of a piece, k + 1
   const void* logits;
   const float* scores;
   const uint8_t* finished;
   float* out_scores;
   int32_t *parents, *tokens;
-  float* lse;  // [batch][beams]
+  Key* keys;      // [batch][beams][pieces][keep]: best logits of a piece, 0 where it has fewer
+  float2* sums;   // [batch][beams][pieces]: (maximum, sum of exp(x - maximum))
 };
 
-// Scores in the order of unsigned integers; -0 and +0 are one score.
+// Values in the order of unsigned integers; -0 and +0 are one value, and a NaN counts as -infinity.
 __device__ __forceinline__ uint32_t order_of(float v) {
-  const uint32_t b = __float_as_uint(v + 0.f);
+  const uint32_t b = __float_as_uint(v == v ? v + 0.f : -INFINITY);
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 __device__ __forceinline__ float value_of(uint32_t o) {
   return __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o);
 }
+__device__ __forceinline__ Key key_of(float v, uint32_t index) {
+  return (static_cast<Key>(order_of(v)) << 32) | static_cast<uint32_t>(~index);
+}
+__device__ __forceinline__ float key_value(Key k) { return value_of(static_cast<uint32_t>(k >> 32)); }
+__device__ __forceinline__ uint32_t key_index(Key k) { return ~static_cast<uint32_t>(k); }
 
 // A candidate's score; a NaN counts as -infinity.
 __device__ __forceinline__ float score_of(float beam, float x, float lse) {
@@ -44,73 +67,294 @@ __device__ __forceinline__ float score_of(float beam, float x, float lse) {
   return s == s ? s : -INFINITY;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) lse_kernel(SelectParams p) {
-  __shared__ float red[kThreads];
-  const int64_t b = blockIdx.y;
-  const int w = blockIdx.x;
-  const T* x = static_cast<const T*>(p.logits) + b * p.logits_batch + w * p.logits_beam;
-  float top = -INFINITY;
-  bool nan = false;
-  for (int v = threadIdx.x; v < p.vocab; v += kThreads) {
-    const float f = to_f32(x[v]);
-    nan |= f != f;
-    top = fmaxf(top, f);
+// Threads that share a group where the n best are wanted: at least n groups.
+__host__ __device__ constexpr int share_of(int n) { return 4 * n <= kThreads ? 4 : 2; }
+
+// The n-th largest of the block's groups' largest keys: no smaller key is among the n best.  0 where
+// fewer than n groups have any.
+__device__ __forceinline__ Key bound_of(Key mine, int n, Key (&s_group)[kMaxGroups], Key& s_bound) {
+  const int share = share_of(n), groups = kThreads / share;
+  for (int o = 1; o < share; o *= 2) {
+    const Key other = __shfl_xor_sync(0xffffffffu, mine, o);
+    mine = other > mine ? other : mine;
   }
-  nan = __syncthreads_or(nan);
-  red[threadIdx.x] = top;
+  if (threadIdx.x % share == 0) s_group[threadIdx.x / share] = mine;
+  if (threadIdx.x == 0) s_bound = 0;
   __syncthreads();
-  for (int o = kThreads / 2; o > 0; o >>= 1) {
-    if (threadIdx.x < o) red[threadIdx.x] = fmaxf(red[threadIdx.x], red[threadIdx.x + o]);
-    __syncthreads();
+  if (threadIdx.x < groups) {
+    const Key key = s_group[threadIdx.x];
+    int rank = 0;
+#pragma unroll 16
+    for (int i = 0; i < groups; ++i) rank += s_group[i] > key;
+    if (rank == n - 1 && key) s_bound = key;  // keys differ: one thread at most
   }
-  top = red[0];
   __syncthreads();
-  float sum = 0.f;
-  for (int v = threadIdx.x; v < p.vocab; v += kThreads) sum += expf(to_f32(x[v]) - top);
-  red[threadIdx.x] = sum;
-  __syncthreads();
-  for (int o = kThreads / 2; o > 0; o >>= 1) {
-    if (threadIdx.x < o) red[threadIdx.x] += red[threadIdx.x + o];
-    __syncthreads();
+  return s_bound;
+}
+
+// Writes the k largest of the n different keys in order (0 where there are fewer).
+__device__ __forceinline__ void rank_keys(const Key* keys, int n, int k, Key* out) {
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const Key key = keys[i];
+    int rank = 0;
+    for (int j = 0; j < n; ++j) rank += keys[j] > key;
+    if (rank < k) out[rank] = key;
   }
-  if (threadIdx.x == 0) p.lse[b * p.beams + w] = nan ? NAN : top + logf(red[0]);
+  for (int i = n + threadIdx.x; i < k; i += kThreads) out[i] = 0;
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) select_kernel(SelectParams p) {
-  __shared__ unsigned long long red[kThreads];
-  const int64_t b = blockIdx.x;
-  unsigned long long last = ~0ull;
-  for (int i = 0; i < p.k; ++i) {
-    unsigned long long best = 0;
-    for (int w = 0; w < p.beams; ++w) {
-      const T* x = static_cast<const T*>(p.logits) + b * p.logits_batch + w * p.logits_beam;
-      const float s = p.scores[b * p.beams + w], lse = p.lse[b * p.beams + w];
-      const bool done = p.finished && p.finished[b * p.beams + w];
-      for (int v = threadIdx.x; v < p.vocab; v += kThreads) {
-        float f = done ? (v == p.eos ? s : -INFINITY) : score_of(s, to_f32(x[v]), lse);
-        if (f != f) f = -INFINITY;
-        const uint32_t flat = static_cast<uint32_t>(w) * p.vocab + v;
-        const unsigned long long key = (static_cast<unsigned long long>(order_of(f)) << 32) | (~flat);
-        if (key < last && key > best) best = key;
-      }
-    }
-    red[threadIdx.x] = best;
-    __syncthreads();
-    for (int o = kThreads / 2; o > 0; o >>= 1) {
-      if (threadIdx.x < o && red[threadIdx.x + o] > red[threadIdx.x]) red[threadIdx.x] = red[threadIdx.x + o];
-      __syncthreads();
-    }
-    last = red[0];
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      const uint32_t flat = ~static_cast<uint32_t>(last);
-      p.out_scores[b * p.k + i] = value_of(static_cast<uint32_t>(last >> 32));
-      p.parents[b * p.k + i] = static_cast<int32_t>(flat / p.vocab);
-      p.tokens[b * p.k + i] = static_cast<int32_t>(flat % p.vocab);
+struct Eight;
+template <>
+struct Eight<float> {
+  static __device__ __forceinline__ void load(const float* p, float* v) {
+    const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+};
+template <>
+struct Eight<__nv_bfloat16> {
+  static __device__ __forceinline__ void load(const __nv_bfloat16* p, float* v) {
+    const uint4 w = __ldcs(reinterpret_cast<const uint4*>(p));
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(u[i] << 16);
+      v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
     }
   }
+};
+
+// One piece of a row: kEach logits a thread.  kVec: rows are 16-byte aligned.
+template <typename T, int kEach, bool kVec>
+__global__ void __launch_bounds__(kThreads) piece_kernel(SelectParams p) {
+  extern __shared__ __align__(16) unsigned char raw[];
+  Key* s_keys = reinterpret_cast<Key*>(raw);  // `keep` groups' worth: no more keys reach the bound
+  __shared__ Key s_group[kMaxGroups], s_bound;
+  __shared__ float s_red[2][kThreads / 32];
+  __shared__ int s_count;
+  grid_dep_launch();
+  const int piece = blockIdx.x, w = blockIdx.y, tid = threadIdx.x;
+  const int64_t b = blockIdx.z, row = b * p.beams + w;
+  const int v0 = piece * kThreads * kEach;
+  if (tid == 0) s_count = 0;
+
+  // element e of the thread: index at(e), rising with e
+  auto at = [&](int e) { return kVec ? v0 + e / 8 * (8 * kThreads) + 8 * tid + e % 8 : v0 + e * kThreads + tid; };
+  float x[kEach];
+  if (p.finished && p.finished[row]) {
+    // one candidate, whose score is the beam's: logits of 0 and -infinity, whose log-sum-exp is 0
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) x[e] = at(e) == p.eos ? 0.f : -INFINITY;
+  } else {
+    const T* src = static_cast<const T*>(p.logits) + b * p.logits_batch + w * p.logits_beam;
+    if constexpr (kVec) {
+#pragma unroll
+      for (int e = 0; e < kEach; e += 8) {
+        if (at(e) + 8 <= p.vocab) {
+          Eight<T>::load(src + at(e), x + e);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[e + i] = at(e + i) < p.vocab ? to_f32(src[at(e + i)]) : -INFINITY;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) x[e] = at(e) < p.vocab ? to_f32(src[at(e)]) : -INFINITY;
+    }
+  }
+
+  // maximum and sum of exponentials (places past the row's end add nothing)
+  float top = -INFINITY;
+  int first = -1;  // the thread's largest logit, the first of equals
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    if (x[e] > top || (first < 0 && at(e) < p.vocab)) {
+      first = e;
+      top = fmaxf(top, x[e]);
+    }
+  }
+  Key mine = 0;
+  if (first >= 0) mine = key_of(top, static_cast<uint32_t>(at(first)));
+  float piece_top = top;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) piece_top = fmaxf(piece_top, __shfl_xor_sync(0xffffffffu, piece_top, o));
+  if (tid % 32 == 0) s_red[0][tid / 32] = piece_top;
+  const Key bound = bound_of(mine, p.keep, s_group, s_bound);
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i) piece_top = fmaxf(piece_top, s_red[0][i]);
+  float sum = 0.f;
+  const float shift = piece_top > -INFINITY ? piece_top : 0.f;  // a piece with nothing left sums to 0
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) sum += __expf(x[e] - shift);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (tid % 32 == 0) s_red[1][tid / 32] = sum;
+
+  const float least = key_value(bound);
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    if (bound && x[e] < least) continue;  // (a NaN goes on, as -infinity)
+    const Key key = key_of(x[e], static_cast<uint32_t>(at(e)));
+    if (key >= bound && at(e) < p.vocab) s_keys[atomicAdd(&s_count, 1)] = key;
+  }
+  __syncthreads();
+  rank_keys(s_keys, s_count, p.keep, p.keys + (row * p.pieces + piece) * p.keep);
+  if (tid == 0) {
+    sum = 0.f;
+    for (int i = 0; i < kThreads / 32; ++i) sum += s_red[1][i];
+    p.sums[row * p.pieces + piece] = make_float2(piece_top, sum);
+  }
+}
+
+// The k best of a request's candidates.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) merge_kernel(SelectParams p, int piece_size) {
+  __shared__ Key s_keys[kMergeKeys], s_best[kMaxBeams], s_group[kMaxGroups], s_bound;
+  __shared__ float s_lse[kMaxBeams], s_score[kMaxBeams];
+  __shared__ int s_count;
+  grid_dep_wait();
+  const int64_t b = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid % 32;
+  const float2* sums = p.sums + b * p.beams * p.pieces;
+  for (int w = tid / 32; w < p.beams; w += kThreads / 32) {  // a warp a beam
+    float top = -INFINITY, sum = 0.f;
+    for (int i = lane; i < p.pieces; i += 32) top = fmaxf(top, sums[w * p.pieces + i].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    for (int i = lane; i < p.pieces; i += 32) {
+      const float2 v = sums[w * p.pieces + i];
+      sum += v.x > -INFINITY || v.y != v.y ? v.y * expf(v.x - top) : 0.f;  // a NaN in the sum stays
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) {
+      s_lse[w] = top + logf(sum);
+      s_score[w] = p.scores[b * p.beams + w];
+    }
+  }
+  if (tid == 0) s_count = 0;
+  __syncthreads();
+
+  const int per = p.pieces * p.keep, all = p.beams * per;
+  const Key* keys = p.keys + b * all;
+  auto candidate = [&](int i) -> Key {
+    const Key key = keys[i];
+    if (!key) return 0;
+    const int w = i / per;
+    return key_of(score_of(s_score[w], key_value(key), s_lse[w]), static_cast<uint32_t>(w) * p.vocab + key_index(key));
+  };
+  Key mine = 0;
+  for (int i = tid; i < all; i += kThreads) {
+    const Key key = candidate(i);
+    mine = key > mine ? key : mine;
+  }
+  const Key bound = bound_of(mine, p.k, s_group, s_bound);
+  for (int i = tid; i < all; i += kThreads) {
+    const Key key = candidate(i);
+    if (key && key >= bound) {
+      const int n = atomicAdd(&s_count, 1);
+      if (n < kMergeKeys) s_keys[n] = key;
+    }
+  }
+  __syncthreads();
+  if (s_count <= kMergeKeys) {
+    rank_keys(s_keys, s_count, p.k, s_best);
+    __syncthreads();
+  } else {
+    // too many reach the bound (as with rows of equal logits and a large k): k rounds over them
+    Key last = ~0ull;
+    for (int i = 0; i < p.k; ++i) {
+      mine = 0;
+      for (int j = tid; j < all; j += kThreads) {
+        const Key key = candidate(j);
+        if (key < last && key > mine) mine = key;
+      }
+      last = bound_of(mine, 1, s_group, s_bound);
+      if (tid == 0) s_best[i] = last;
+      __syncthreads();
+    }
+  }
+
+  // equal scores below a piece's list
+  const uint32_t worst = static_cast<uint32_t>(s_best[p.k - 1] >> 32);
+  bool hidden = false;
+  for (int i = tid; i < p.beams * p.pieces; i += kThreads) {
+    const Key key = keys[static_cast<int64_t>(i) * p.keep + p.k];
+    const int w = i / p.pieces;
+    // (behind a last key of -infinity there is nothing but -infinity at higher indexes)
+    if (key && key_value(key) > -INFINITY &&
+        order_of(score_of(s_score[w], key_value(key), s_lse[w])) == worst)
+      hidden = true;
+  }
+  if (__syncthreads_or(hidden)) {
+    int found = 0;  // the candidates above the k-th score stay; those at it are gathered by rising index
+    while (static_cast<uint32_t>(s_best[found] >> 32) != worst) ++found;
+    for (int i = 0; i < p.beams * p.pieces && found < p.k; ++i) {
+      const int w = i / p.pieces, piece = i % p.pieces;
+      const bool done = p.finished && p.finished[b * p.beams + w];
+      if (order_of(score_of(s_score[w], sums[i].x, s_lse[w])) < worst) continue;  // (a NaN is in no maximum)
+      const T* src = static_cast<const T*>(p.logits) + b * p.logits_batch + w * p.logits_beam;
+      const int stop = p.vocab - piece * piece_size < piece_size ? p.vocab : (piece + 1) * piece_size;
+      for (int v0 = piece * piece_size; v0 < stop && found < p.k; v0 += kThreads) {
+        const int v = v0 + tid;
+        bool hit = false;
+        if (v < stop) {
+          const float x = done ? (v == p.eos ? 0.f : -INFINITY) : to_f32(src[v]);
+          hit = order_of(score_of(s_score[w], x, s_lse[w])) == worst;
+        }
+        const unsigned votes = __ballot_sync(0xffffffffu, hit);
+        if (lane == 0) s_group[tid / 32] = __popc(votes);
+        __syncthreads();
+        int before = found, total = 0;
+        for (int j = 0; j < kThreads / 32; ++j) {
+          if (j < tid / 32) before += static_cast<int>(s_group[j]);
+          total += static_cast<int>(s_group[j]);
+        }
+        before += __popc(votes & ((1u << lane) - 1u));
+        if (hit && before < p.k)
+          s_best[before] = (static_cast<Key>(worst) << 32) |
+                           static_cast<uint32_t>(~(static_cast<uint32_t>(w) * p.vocab + v));
+        found += total;
+        __syncthreads();
+      }
+    }
+    __syncthreads();
+  }
+  if (tid < p.k) {
+    const Key key = s_best[tid];
+    p.out_scores[b * p.k + tid] = key_value(key);
+    p.parents[b * p.k + tid] = static_cast<int32_t>(key_index(key) / p.vocab);
+    p.tokens[b * p.k + tid] = static_cast<int32_t>(key_index(key) % p.vocab);
+  }
+}
+
+// Logits a thread holds: 32, or 8 where pieces of 32 a thread would be fewer than two a multiprocessor.
+int each_of(int64_t batch, int beams, int vocab) {
+  return batch * beams * ceil_div(vocab, 32 * kThreads) < 2 * static_cast<int64_t>(layer_sm_count()) ? 8 : 32;
+}
+
+template <typename T, int kEach>
+cudaError_t launch_pieces(const SelectParams& p, bool vec, int64_t batch, cudaStream_t stream) {
+  const size_t smem = static_cast<size_t>(p.keep) * share_of(p.keep) * kEach * sizeof(Key);
+  auto k = vec ? piece_kernel<T, kEach, true> : piece_kernel<T, kEach, false>;
+  if (smem > 40 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  const dim3 grid(static_cast<unsigned>(p.pieces), static_cast<unsigned>(p.beams), static_cast<unsigned>(batch));
+  return launch_k(k, grid, dim3(kThreads), smem, stream, false, p);
+}
+
+template <typename T>
+cudaError_t launch_select(const SelectParams& p, int64_t batch, cudaStream_t stream) {
+  const int64_t es = sizeof(T);
+  const bool vec = aligned_to(p.logits, 16) && p.logits_beam * es % 16 == 0 && p.logits_batch * es % 16 == 0;
+  const int each = each_of(batch, p.beams, p.vocab);
+  const cudaError_t e = each == 8 ? launch_pieces<T, 8>(p, vec, batch, stream) : launch_pieces<T, 32>(p, vec, batch, stream);
+  if (e != cudaSuccess) return e;
+  return launch_k(merge_kernel<T>, dim3(static_cast<unsigned>(batch)), dim3(kThreads), 0, stream, true, p,
+                  each * kThreads);
 }
 
 struct ReorderParams {
@@ -121,31 +365,52 @@ struct ReorderParams {
   int64_t row_bytes[SSD_REORDER_MAX];
 };
 
-template <typename V>
-__global__ void __launch_bounds__(kThreads) reorder_kernel(ReorderParams p, int j) {
+// kK: an upper limit of the rows of a request.
+template <typename V, int kK>
+__global__ void __launch_bounds__(kThreads) reorder_kernel(ReorderParams p) {
+  __shared__ int s_parent[kK];
+  const int j = blockIdx.z;
+  const int64_t b = blockIdx.y;
   const int64_t units = p.row_bytes[j] / static_cast<int64_t>(sizeof(V));
   const int64_t at = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const int64_t b = blockIdx.y;
+  const bool in_place = p.src[j] == p.dst[j];
+  if (threadIdx.x < p.k) {
+    const int from = p.parents[b * p.k + threadIdx.x];
+    s_parent[threadIdx.x] = from < 0 || from >= p.beams || (in_place && from == static_cast<int>(threadIdx.x)) ? -1 : from;
+  }
+  __syncthreads();
   if (at >= units) return;
   const V* src = static_cast<const V*>(p.src[j]) + b * p.beams * units + at;
   V* dst = static_cast<V*>(p.dst[j]) + b * p.k * units + at;
-  const bool in_place = p.src[j] == p.dst[j];
-  V v[kMaxBeams];
-  for (int i = 0; i < p.k; ++i) {
-    const int from = p.parents[b * p.k + i];
-    if (from >= 0 && from < p.beams && !(in_place && from == i)) v[i] = src[from * units];
-  }
-  for (int i = 0; i < p.k; ++i) {
-    const int from = p.parents[b * p.k + i];
-    if (from >= 0 && from < p.beams && !(in_place && from == i)) dst[i * units] = v[i];
-  }
+  V v[kK];
+#pragma unroll
+  for (int i = 0; i < kK; ++i)
+    if (i < p.k && s_parent[i] >= 0) v[i] = src[s_parent[i] * units];
+#pragma unroll
+  for (int i = 0; i < kK; ++i)
+    if (i < p.k && s_parent[i] >= 0) dst[i * units] = v[i];
 }
 
+// One launch for all tensors that move in units of V.
 template <typename V>
-cudaError_t launch_reorder(const ReorderParams& p, int j, int64_t batch, cudaStream_t stream) {
-  const int64_t units = p.row_bytes[j] / static_cast<int64_t>(sizeof(V));
-  const dim3 grid(static_cast<unsigned>(ceil_div(units, kThreads)), static_cast<unsigned>(batch));
-  return launch_k(reorder_kernel<V>, grid, dim3(kThreads), 0, stream, false, p, j);
+cudaError_t launch_reorder(const ReorderParams& all, int unit, int64_t batch, cudaStream_t stream) {
+  ReorderParams p = all;
+  int64_t most = 0;
+  p.count = 0;
+  for (int j = 0; j < all.count; ++j) {
+    const uintptr_t bits = reinterpret_cast<uintptr_t>(all.src[j]) | reinterpret_cast<uintptr_t>(all.dst[j]) |
+                           static_cast<uintptr_t>(all.row_bytes[j]);
+    if (all.row_bytes[j] == 0 || ((bits & 15) == 0 ? 16 : (bits & 3) == 0 ? 4 : 1) != unit) continue;
+    p.src[p.count] = all.src[j], p.dst[p.count] = all.dst[j], p.row_bytes[p.count] = all.row_bytes[j];
+    ++p.count;
+    if (all.row_bytes[j] / unit > most) most = all.row_bytes[j] / unit;
+  }
+  if (p.count == 0) return cudaSuccess;
+  const dim3 grid(static_cast<unsigned>(ceil_div(most, kThreads)), static_cast<unsigned>(batch),
+                  static_cast<unsigned>(p.count));
+  auto k = p.k <= 4 ? reorder_kernel<V, 4> : p.k <= 8 ? reorder_kernel<V, 8> : p.k <= 16 ? reorder_kernel<V, 16>
+                                                                                         : reorder_kernel<V, 64>;
+  return launch_k(k, grid, dim3(kThreads), 0, stream, false, p);
 }
 
 ssd_status check_select(const ssd_beam_select_args* a) {
@@ -162,8 +427,10 @@ ssd_status check_select(const ssd_beam_select_args* a) {
 }  // namespace ssd
 
 extern "C" size_t ssd_beam_select_workspace_size(const ssd_beam_select_args* a) {
-  if (ssd::check_select(a) != SSD_OK) return 0;
-  return static_cast<size_t>(a->batch) * a->beams * sizeof(float);
+  using namespace ssd;
+  if (check_select(a) != SSD_OK) return 0;
+  const size_t pieces = ceil_div(a->vocab, each_of(a->batch, a->beams, a->vocab) * kThreads);
+  return static_cast<size_t>(a->batch) * a->beams * pieces * ((a->k + 1) * sizeof(Key) + sizeof(float2));
 }
 
 extern "C" ssd_status ssd_beam_select(const ssd_beam_select_args* a, ssd_stream_t stream) {
@@ -183,16 +450,12 @@ extern "C" ssd_status ssd_beam_select(const ssd_beam_select_args* a, ssd_stream_
   p.beams = a->beams, p.vocab = a->vocab, p.k = a->k, p.eos = a->eos;
   p.logits = a->logits, p.scores = a->scores, p.finished = a->finished;
   p.out_scores = a->out_scores, p.parents = a->parents, p.tokens = a->tokens;
-  p.lse = static_cast<float*>(a->workspace);
-  const unsigned batch = static_cast<unsigned>(a->batch);
-  const dim3 rows(static_cast<unsigned>(p.beams), batch);
-  const bool bf16 = a->dtype == SSD_BF16;
-  cudaError_t e = bf16 ? launch_k(lse_kernel<__nv_bfloat16>, rows, dim3(kThreads), 0, stream, false, p)
-                       : launch_k(lse_kernel<float>, rows, dim3(kThreads), 0, stream, false, p);
-  if (e != cudaSuccess) return SSD_ERR_CUDA;
-  e = bf16 ? launch_k(select_kernel<__nv_bfloat16>, dim3(batch), dim3(kThreads), 0, stream, false, p)
-           : launch_k(select_kernel<float>, dim3(batch), dim3(kThreads), 0, stream, false, p);
-  return launched(e);
+  p.pieces = static_cast<int>(ceil_div(p.vocab, each_of(a->batch, p.beams, p.vocab) * kThreads));
+  p.keep = p.k + 1;
+  p.keys = static_cast<Key*>(a->workspace);
+  p.sums = reinterpret_cast<float2*>(p.keys + a->batch * p.beams * p.pieces * p.keep);
+  return launched(a->dtype == SSD_BF16 ? launch_select<__nv_bfloat16>(p, a->batch, stream)
+                                       : launch_select<float>(p, a->batch, stream));
 }
 
 extern "C" ssd_status ssd_beam_reorder(const ssd_beam_reorder_args* a, ssd_stream_t stream) {
@@ -210,14 +473,8 @@ extern "C" ssd_status ssd_beam_reorder(const ssd_beam_reorder_args* a, ssd_strea
   }
   if (a->batch == 0 || a->count == 0) return SSD_OK;
   if (!a->parents || !aligned_to(a->parents, 4)) return SSD_ERR_INVALID_ARG;
-  for (int j = 0; j < a->count; ++j) {
-    if (p.row_bytes[j] == 0) continue;
-    const uintptr_t bits = reinterpret_cast<uintptr_t>(p.src[j]) | reinterpret_cast<uintptr_t>(p.dst[j]) |
-                           static_cast<uintptr_t>(p.row_bytes[j]);
-    const cudaError_t e = (bits & 15) == 0 ? launch_reorder<uint4>(p, j, a->batch, stream)
-                          : (bits & 3) == 0 ? launch_reorder<uint32_t>(p, j, a->batch, stream)
-                                            : launch_reorder<uint8_t>(p, j, a->batch, stream);
-    if (e != cudaSuccess) return SSD_ERR_CUDA;
-  }
-  return SSD_OK;
+  cudaError_t e = launch_reorder<uint4>(p, 16, a->batch, stream);
+  if (e == cudaSuccess) e = launch_reorder<uint32_t>(p, 4, a->batch, stream);
+  if (e == cudaSuccess) e = launch_reorder<uint8_t>(p, 1, a->batch, stream);
+  return launched(e);
 }
