@@ -103,10 +103,10 @@ def _load() -> ctypes.CDLL:
     for name in ("ssd_conv_fwd", "ssd_selective_scan", "ssd_step", "ssd_w4_matvec", "ssd_beam_select",
                  "ssd_beam_reorder"):  # (argument struct, stream)
         getattr(lib, name).restype = c_int
-        getattr(lib, name).argtypes = [ctypes.c_char_p, vp]
+        getattr(lib, name).argtypes = [vp, vp]
     for name in ("ssd_selective_scan_workspace_size", "ssd_beam_select_workspace_size"):
         getattr(lib, name).restype = sz
-        getattr(lib, name).argtypes = [ctypes.c_char_p]
+        getattr(lib, name).argtypes = [vp]
     return lib
 
 

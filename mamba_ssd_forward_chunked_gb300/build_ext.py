@@ -5,22 +5,29 @@ static CUDA runtime into one shared library next to this file.  The library
 has a plain C ABI (include/ssd.h) and no link-time dependency on libcuda (the
 driver entry point for tensor-map encoding is looked up at run time).
 
+csrc/binding.cpp (the layer operators on torch tensors) is compiled beside it
+into the Python module _layer_binding.so, against the installed torch and the
+library.
+
 Run as a script (``python mamba_ssd_forward_chunked_gb300/build_ext.py``) or
 load it by path: importing the package itself needs the library it builds.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(HERE, "libssd_gb300.so")
+BINDING = os.path.join(HERE, "_layer_binding.so")
 BUILD = os.path.join(ROOT, "_build")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -37,6 +44,28 @@ def _nvcc() -> str:
 
 def sources():
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
+
+
+def _binding_compile(src: str, obj: str):
+    """The host compiler's command for the binding (torch is only located, not imported)."""
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-Wno-deprecated-declarations",
+            "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(torch, "include"),
+            "-isystem", os.path.join(cuda, "include"), "-c", src, "-o", obj]
+
+
+def _binding_link(obj: str, out: str):
+    lib = os.path.join(os.path.dirname(importlib.util.find_spec("torch").origin), "lib")
+    return [os.environ.get("CXX", "g++"), "-shared", "-o", out, obj, "-L", HERE, "-l:" + os.path.basename(OUT),
+            "-Wl,-rpath,$ORIGIN", "-L", lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+
+
+def _run(cmd, what: str) -> None:
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError(what + " failed")
 
 
 def _stale(out: str, deps) -> bool:
@@ -59,6 +88,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
         objs.append(obj)
         if force or _stale(obj, [src] + headers):
             jobs.append([nvcc, *ARCH, *flags, "-I", INCLUDE, "-I", CSRC, "-c", src, "-o", obj])
+    binding_src = os.path.join(CSRC, "binding.cpp")
+    binding_obj = os.path.join(BUILD, "binding.o")
+    if force or _stale(binding_obj, [binding_src, os.path.join(INCLUDE, "ssd.h")]):
+        jobs.append(_binding_compile(binding_src, binding_obj))
     if jobs:
         with cf.ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
             results = list(ex.map(lambda c: subprocess.run(c, capture_output=True, text=True), jobs))
@@ -66,14 +99,13 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
             if verbose or r.returncode != 0:
                 sys.stderr.write(r.stdout + r.stderr)
             if r.returncode != 0:
-                raise RuntimeError("nvcc failed: " + " ".join(cmd))
+                raise RuntimeError("compilation failed: " + " ".join(cmd))
     if force or jobs or _stale(OUT, objs):
-        cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", OUT + ".tmp", *objs]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            sys.stderr.write(r.stdout + r.stderr)
-            raise RuntimeError("link failed")
+        _run([nvcc, *ARCH, "-shared", "-cudart", "static", "-o", OUT + ".tmp", *objs], "link")
         os.replace(OUT + ".tmp", OUT)
+    if force or _stale(BINDING, [binding_obj, OUT]):
+        _run(_binding_link(binding_obj, BINDING + ".tmp"), "link of the binding")
+        os.replace(BINDING + ".tmp", BINDING)
     return OUT
 
 

@@ -4,12 +4,21 @@ fails its checks, or has nothing to do, before any CUDA call)."""
 import os
 import re
 import shutil
+import struct
 import subprocess
 
 import pytest
 import torch
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+# the argument structs of include/ssd.h, in native layout
+REORDER_MAX = 16
+CONV_ARGS = struct.Struct("@4q8iP2q10P")
+SCAN_ARGS = struct.Struct("@3q6i5P10q8PN")
+STEP_ARGS = struct.Struct("@3q8i3P3q11P")
+W4_ARGS = struct.Struct("@2q4iPq3PqP")
+SELECT_ARGS = struct.Struct("@2q6iP2q6PN")
+REORDER_ARGS = struct.Struct("@2q4iP%dP%dP%dq" % ((REORDER_MAX,) * 3))
 FAKE = 1 << 20  # an aligned address that no call here reads
 
 
@@ -22,7 +31,6 @@ def ext():
 
 
 def test_struct_sizes_match_the_header(ext, tmp_path):
-    from mamba_ssd_forward_chunked_gb300 import layer
     cc = shutil.which("gcc") or shutil.which("cc")
     if cc is None:
         pytest.skip("no C compiler")
@@ -33,10 +41,10 @@ def test_struct_sizes_match_the_header(ext, tmp_path):
     exe = tmp_path / "s"
     subprocess.run([cc, "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe)], check=True)
     got = [int(v) for v in subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()]
-    assert got == [s.size for s in (layer.CONV_ARGS, layer.SCAN_ARGS, layer.STEP_ARGS, layer.W4_ARGS,
-                                    layer.SELECT_ARGS, layer.REORDER_ARGS)]
+    assert got == [s.size for s in (CONV_ARGS, SCAN_ARGS, STEP_ARGS, W4_ARGS,
+                                    SELECT_ARGS, REORDER_ARGS)]
     text = open(os.path.join(ROOT, "include", "ssd.h")).read()
-    assert int(re.search(r"#define SSD_REORDER_MAX (\d+)", text).group(1)) == layer.REORDER_MAX
+    assert int(re.search(r"#define SSD_REORDER_MAX (\d+)", text).group(1)) == REORDER_MAX
 
 
 @pytest.mark.parametrize("n,k", [(16, 64), (1, 1), (17, 65), (40, 200)])
@@ -77,12 +85,11 @@ def test_quantize_keeps_weights_within_half_a_step(ext):
 
 
 def conv_args(ext, **kw):
-    from mamba_ssd_forward_chunked_gb300 import layer
-    v = dict(size=layer.CONV_ARGS.size, batch=2, seqlen=5, nslots=0, channels=12, width=4, dtype=0, act=1, nout=3,
+    v = dict(size=CONV_ARGS.size, batch=2, seqlen=5, nslots=0, channels=12, width=4, dtype=0, act=1, nout=3,
              c0=4, c1=4, c2=4, u=FAKE, ub=60, ut=12, weight=FAKE, bias=0, ring=0, new_ring=0, positions=0, lengths=0,
              slots=0, o0=FAKE, o1=FAKE, o2=FAKE)
     v.update(kw)
-    return layer.CONV_ARGS.pack(*v.values())
+    return CONV_ARGS.pack(*v.values())
 
 
 @pytest.mark.parametrize("want,kw", [
@@ -99,12 +106,11 @@ def test_conv_refusals(ext, want, kw):
 
 
 def scan_args(ext, **kw):
-    from mamba_ssd_forward_chunked_gb300 import layer
-    v = dict(size=layer.SCAN_ARGS.size, batch=2, seqlen=5, channels=12, dstate=16, ngroups=1, dtype=1, softplus=1,
+    v = dict(size=SCAN_ARGS.size, batch=2, seqlen=5, channels=12, dstate=16, ngroups=1, dtype=1, softplus=1,
              reserved=0, u=FAKE, delta=FAKE, z=0, Bm=FAKE, Cm=FAKE, ub=60, ut=12, db=60, dt=12, zb=0, zt=0, Bb=80, Bt=16,
              Cb=80, Ct=16, A=FAKE, D=0, bias=0, init=0, final=0, y=FAKE, lengths=0, ws=0, nbytes=0)
     v.update(kw)
-    return layer.SCAN_ARGS.pack(*v.values())
+    return SCAN_ARGS.pack(*v.values())
 
 
 @pytest.mark.parametrize("want,kw", [
@@ -119,12 +125,11 @@ def test_scan_refusals(ext, want, kw):
 
 
 def step_args(ext, **kw):
-    from mamba_ssd_forward_chunked_gb300 import layer
-    v = dict(size=layer.STEP_ARGS.size, batch=2, nslots=2, nheads=4, headdim=64, ngroups=2, dstate=64, width=4, dtype=1,
+    v = dict(size=STEP_ARGS.size, batch=2, nslots=2, nheads=4, headdim=64, ngroups=2, dstate=64, width=4, dtype=1,
              dt_dtype=1, softplus=1, u=FAKE, z=0, dt=FAKE, us=512, zs=0, ts=4, weight=FAKE, bias=0, A=FAKE, D=FAKE,
              dt_bias=0, ring=FAKE, state=FAKE, new_state=0, positions=FAKE, slots=0, y=FAKE)
     v.update(kw)
-    return layer.STEP_ARGS.pack(*v.values())
+    return STEP_ARGS.pack(*v.values())
 
 
 @pytest.mark.parametrize("want,kw", [
@@ -141,11 +146,10 @@ def test_step_refusals(ext, want, kw):
 
 
 def w4_args(ext, **kw):
-    from mamba_ssd_forward_chunked_gb300 import layer
-    v = dict(size=layer.W4_ARGS.size, tokens=1, n=16, k=64, group=32, dtype=1, x=FAKE, xs=64, packed=FAKE, scales=FAKE,
+    v = dict(size=W4_ARGS.size, tokens=1, n=16, k=64, group=32, dtype=1, x=FAKE, xs=64, packed=FAKE, scales=FAKE,
              add=0, adds=0, y=FAKE)
     v.update(kw)
-    return layer.W4_ARGS.pack(*v.values())
+    return W4_ARGS.pack(*v.values())
 
 
 @pytest.mark.parametrize("want,kw", [
@@ -159,11 +163,10 @@ def test_w4_refusals(ext, want, kw):
 
 
 def select_args(ext, **kw):
-    from mamba_ssd_forward_chunked_gb300 import layer
-    v = dict(size=layer.SELECT_ARGS.size, batch=2, beams=4, vocab=100, k=4, dtype=0, eos=2, reserved=0, logits=FAKE,
+    v = dict(size=SELECT_ARGS.size, batch=2, beams=4, vocab=100, k=4, dtype=0, eos=2, reserved=0, logits=FAKE,
              lb=400, lw=100, scores=FAKE, finished=0, out=FAKE, parents=FAKE, tokens=FAKE, ws=FAKE, nbytes=1 << 30)
     v.update(kw)
-    return layer.SELECT_ARGS.pack(*v.values())
+    return SELECT_ARGS.pack(*v.values())
 
 
 @pytest.mark.parametrize("want,kw", [
@@ -178,13 +181,12 @@ def test_select_refusals(ext, want, kw):
 
 
 def reorder_args(ext, **kw):
-    from mamba_ssd_forward_chunked_gb300 import layer
-    n = layer.REORDER_MAX
-    v = dict(size=layer.REORDER_ARGS.size, batch=2, beams=4, k=4, count=1, reserved=0, parents=FAKE, src=FAKE,
+    n = REORDER_MAX
+    v = dict(size=REORDER_ARGS.size, batch=2, beams=4, k=4, count=1, reserved=0, parents=FAKE, src=FAKE,
              dst=2 * FAKE, row=64)
     v.update(kw)
     lists = [[v[key]] + [0] * (n - 1) for key in ("src", "dst", "row")]
-    return layer.REORDER_ARGS.pack(*[v[key] for key in ("size", "batch", "beams", "k", "count", "reserved", "parents")],
+    return REORDER_ARGS.pack(*[v[key] for key in ("size", "batch", "beams", "k", "count", "reserved", "parents")],
                                    *lists[0], *lists[1], *lists[2])
 
 
