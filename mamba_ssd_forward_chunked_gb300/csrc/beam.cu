@@ -165,17 +165,21 @@ __global__ void __launch_bounds__(kThreads) piece_kernel(SelectParams p) {
   }
 
   // maximum and sum of exponentials (places past the row's end add nothing)
-  float top = -INFINITY;
-  int first = -1;  // the thread's largest logit, the first of equals
+  float top8[kEach / 8];
 #pragma unroll
-  for (int e = 0; e < kEach; ++e) {
-    if (x[e] > top || (first < 0 && at(e) < p.vocab)) {
-      first = e;
-      top = fmaxf(top, x[e]);
-    }
+  for (int e = 0; e < kEach; e += 8) {
+    top8[e / 8] = x[e];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) top8[e / 8] = fmaxf(top8[e / 8], x[e + i]);
   }
+  float top = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kEach / 8; ++i) top = fmaxf(top, top8[i]);
+  int first = 0;  // the first of the thread's largest logits
+#pragma unroll
+  for (int e = kEach - 1; e >= 0; --e) first = x[e] == top ? e : first;
   Key mine = 0;
-  if (first >= 0) mine = key_of(top, static_cast<uint32_t>(at(first)));
+  if (at(0) < p.vocab) mine = key_of(top, static_cast<uint32_t>(at(first)));
   float piece_top = top;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) piece_top = fmaxf(piece_top, __shfl_xor_sync(0xffffffffu, piece_top, o));
@@ -186,17 +190,20 @@ __global__ void __launch_bounds__(kThreads) piece_kernel(SelectParams p) {
   float sum = 0.f;
   const float shift = piece_top > -INFINITY ? piece_top : 0.f;  // a piece with nothing left sums to 0
 #pragma unroll
-  for (int e = 0; e < kEach; ++e) sum += __expf(x[e] - shift);
+  for (int e = 0; e < kEach; ++e) sum += exp2_fast((x[e] - shift) * kLog2e);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (tid % 32 == 0) s_red[1][tid / 32] = sum;
 
   const float least = key_value(bound);
 #pragma unroll
-  for (int e = 0; e < kEach; ++e) {
-    if (bound && x[e] < least) continue;  // (a NaN goes on, as -infinity)
-    const Key key = key_of(x[e], static_cast<uint32_t>(at(e)));
-    if (key >= bound && at(e) < p.vocab) s_keys[atomicAdd(&s_count, 1)] = key;
+  for (int e = 0; e < kEach; e += 8) {
+    if (bound && top8[e / 8] < least) continue;  // (NaN go on, as -infinity)
+#pragma unroll
+    for (int i = e; i < e + 8; ++i) {
+      const Key key = key_of(x[i], static_cast<uint32_t>(at(i)));
+      if (key >= bound && at(i) < p.vocab) s_keys[atomicAdd(&s_count, 1)] = key;
+    }
   }
   __syncthreads();
   rank_keys(s_keys, s_count, p.keep, p.keys + (row * p.pieces + piece) * p.keep);

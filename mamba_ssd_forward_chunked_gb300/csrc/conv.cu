@@ -66,7 +66,7 @@ struct Chans<__nv_bfloat16, 4> {
 };
 
 template <typename T, int W, int kC>
-__global__ void __launch_bounds__(kThreads) conv_kernel(ConvParams p) {
+__global__ void __launch_bounds__(kThreads, 6) conv_kernel(ConvParams p) {
   using Ch = Chans<T, kC>;
   const int groups = p.C / kC;
   const int64_t id = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
@@ -85,13 +85,22 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(ConvParams p) {
   const T* u = static_cast<const T*>(p.u) + b * p.u_batch + c;
   const T* ring = p.ring && !idle ? static_cast<const T*>(p.ring) + slot * W * p.C + c : nullptr;
 
+  // token t0 + n of the run lies at u + n * step (a run is short: 32-bit offsets)
+  const int n1 = static_cast<int>(t1 - t0), nend = end > t0 ? static_cast<int>(end - t0) : 0;
+  const T* in = u + t0 * p.u_token;
   Ch next[kStep];
-  auto fetch = [&](int64_t t) {
+  auto fetch = [&](int n) {
+    const T* from = in + n * p.u_token;
+    if (n + kStep <= nend) {
 #pragma unroll
-    for (int k = 0; k < kStep; ++k)
-      if (t + k < end) next[k].load(u + (t + k) * p.u_token);
+      for (int k = 0; k < kStep; ++k, from += p.u_token) next[k].load(from);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kStep; ++k, from += p.u_token)
+        if (n + k < nend) next[k].load(from);
+    }
   };
-  fetch(t0);
+  fetch(0);
 
   float w[W][kC], win[W][kC], bias[kC];  // win[j]: input of token t - W + 1 + j
   if constexpr (W == 4) {
@@ -142,14 +151,13 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(ConvParams p) {
   while (c >= p.begin[part + 1]) ++part;
   const int64_t width = p.begin[part + 1] - p.begin[part];
   T* out = static_cast<T*>(p.out[part]) + static_cast<int64_t>(b) * p.L * width + (c - p.begin[part]);
-  for (int64_t t = t0; t < t1; t += kStep) {
+  out += t0 * width;
+  for (int n = 0; n < n1; n += kStep) {
     Ch now[kStep];
 #pragma unroll
     for (int k = 0; k < kStep; ++k) now[k] = next[k];
-    fetch(t + kStep);
-#pragma unroll
-    for (int k = 0; k < kStep; ++k) {
-      if (t + k >= t1) break;
+    fetch(n + kStep);
+    auto put = [&](int k, bool live) {
       float acc[kC];
 #pragma unroll
       for (int i = 0; i < kC; ++i) {
@@ -160,11 +168,20 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(ConvParams p) {
 #pragma unroll
         for (int j = 0; j < W; ++j) acc[i] = fmaf(w[j][i], win[j][i], acc[i]);
         if (p.silu) acc[i] = silu(acc[i]);
-        if (t + k >= len) acc[i] = 0.f;
+        if (!live) acc[i] = 0.f;
       }
       Ch y;
       y.set(acc);
-      y.store(out + (t + k) * width);
+      y.store(out);
+      out += width;
+    };
+    if (n + kStep <= nend) {
+#pragma unroll
+      for (int k = 0; k < kStep; ++k) put(k, true);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kStep; ++k)
+        if (n + k < n1) put(k, n + k < nend);
     }
   }
 }

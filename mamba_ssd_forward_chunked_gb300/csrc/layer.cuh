@@ -21,11 +21,36 @@ __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// v / (1 + exp(-v)).  Below about -88 exp(-v) is infinite and the quotient -0, the limit.
-__device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.f + __expf(-v)); }
+// 2^v and 1/v by the special-function unit, to about 2^-22 of the value; results below the normal
+// numbers are 0, which spares the instructions that would keep them.
+__device__ __forceinline__ float exp2_fast(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float rcp_fast(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
 
-// log(1 + exp(v)); above 20 it equals v in 32 bits.
-__device__ __forceinline__ float softplus(float v) { return v > 20.f ? v : log1pf(__expf(v)); }
+// v / (1 + exp(-v)).  Where exp(-v) is infinite (v below -88) the quotient is -0, the limit.
+__device__ __forceinline__ float silu(float v) { return v * rcp_fast(1.f + exp2_fast(-kLog2e * v)); }
+
+// log(1 + exp(v)) = max(v, 0) + log(1 + e), e = exp(-|v|), and with s = e / (2 + e) <= 1/3
+// log(1 + e) = 2 atanh(s) = 2 (s + s^3/3 + s^5/5 + ...): no digits are lost for small e, as they
+// are in log(1 + e) itself.  Six terms leave 2 s^13/13 < 2^-22 s, and less the smaller e is.
+__device__ __forceinline__ float softplus(float v) {
+  const float e = expf(-fabsf(v));
+  const float s = e * rcp_fast(2.f + e);
+  const float q = s * s;
+  float r = fmaf(q, 1.f / 11.f, 1.f / 9.f);
+  r = fmaf(q, r, 1.f / 7.f);
+  r = fmaf(q, r, 1.f / 5.f);
+  r = fmaf(q, r, 1.f / 3.f);
+  r = fmaf(q * s, r, s);
+  return fmaf(2.f, r, fmaxf(v, 0.f));
+}
 
 // ------------------------------------------------------------------ host side
 inline bool aligned_to(const void* p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }

@@ -32,7 +32,6 @@ namespace {
 
 constexpr int kNS = 4;    // states a lane keeps of each of its two channels
 constexpr int kTile = 32;  // tokens a tile
-constexpr float kLog2e = 1.4426950408889634f;
 
 struct ScanParams {
   int64_t L;
@@ -97,12 +96,6 @@ __device__ __forceinline__ void load8(Raw<T>& r, const T* p, int n) {
   }
 }
 
-__device__ __forceinline__ float exp2_fast(float v) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
-}
-
 // Two 32-bit numbers in one 64-bit register, for the packed multiply-adds.
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
   uint64_t r;
@@ -123,12 +116,10 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   return r;
 }
 
-// log(1 + exp(v)) = max(v, 0) + log(1 + e), e = exp(-|v|), and with s = e / (2 + e) <= 1/3
-// log(1 + e) = 2 atanh(s) = 2 (s + s^3/3 + s^5/5 + ...): no digits are lost for small e, as they
-// are in log(1 + e) itself.  Six terms leave 2 s^13/13 < 2^-22 s, and less the smaller e is.
+// softplus of two numbers, its polynomial two at a time.
 __device__ __forceinline__ void softplus2(float& v0, float& v1) {
   const float e0 = expf(-fabsf(v0)), e1 = expf(-fabsf(v1));
-  const uint64_t s = pack2(__fdividef(e0, 2.f + e0), __fdividef(e1, 2.f + e1));
+  const uint64_t s = pack2(e0 * rcp_fast(2.f + e0), e1 * rcp_fast(2.f + e1));
   const uint64_t q = mul2(s, s);
   auto both = [](float c) { return pack2(c, c); };
   uint64_t r = fma2(q, both(1.f / 11.f), both(1.f / 9.f));
@@ -451,10 +442,10 @@ __global__ void __launch_bounds__(Shape<T>::kThreads + Shape<T>::kHelp) scan_ker
 // bounds it.  A thread takes four states of a channel, T neighbouring lanes share the channel (its
 // step is formed by each of them), and runs over kRows sequences, whose loads are all on their way
 // before the first is used; A and the channel's constants are read once for them.
-constexpr int kTokenThreads = 256, kRows = 4;
+constexpr int kTokenThreads = 128, kRows = 2;
 
 template <typename V, int T, bool kVec>
-__global__ void __launch_bounds__(kTokenThreads) scan_token_kernel(ScanParams p, int batch) {
+__global__ void __launch_bounds__(kTokenThreads, 8) scan_token_kernel(ScanParams p, int batch) {
   const int64_t id = static_cast<int64_t>(blockIdx.x) * kTokenThreads + threadIdx.x;
   const int part = static_cast<int>(id % T), n0 = 4 * part;
   const bool live = id / T < p.D;
@@ -510,8 +501,8 @@ __global__ void __launch_bounds__(kTokenThreads) scan_token_kernel(ScanParams p,
     const int64_t b = b0 + r;
     if (b >= batch) break;
     const bool on = !p.lengths || p.lengths[b] > 0;
-    float step = d[r] + bias, other = 0.f;
-    if (p.softplus) softplus2(step, other);
+    float step = d[r] + bias;
+    if (p.softplus) step = softplus(step);
     if (!on) step = 0.f;
     const float du = step * u[r];
     float sum = 0.f;
