@@ -5,8 +5,7 @@
 // is one pass over memory, and HBM bounds it.  A thread takes four channels (8 or
 // 16 bytes) and walks down a run of tokens with the last W - 1 inputs in
 // registers; the next eight tokens are on their way while eight are computed.
-// Runs of one channel group start W - 1 tokens early, which costs 3/32 more
-// reads (from L2, mostly) at runs of 32.
+// A run reads the W - 1 tokens before it again (from L2, mostly).
 //
 // The ring may be read and updated in place: the thread that owns a channel's
 // first run is the only one that reads the ring, and it writes it too, after
@@ -66,7 +65,7 @@ struct Chans<__nv_bfloat16, 4> {
 };
 
 template <typename T, int W, int kC>
-__global__ void __launch_bounds__(kThreads, 6) conv_kernel(ConvParams p) {
+__global__ void __launch_bounds__(kThreads) conv_kernel(ConvParams p) {
   using Ch = Chans<T, kC>;
   const int groups = p.C / kC;
   const int64_t id = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
@@ -194,8 +193,11 @@ cudaError_t launch(ConvParams p, int width, int64_t batch, cudaStream_t stream) 
              aligned_to(p.ring, bytes) && aligned_to(p.new_ring, bytes);
   for (int i = 0; i < 3; ++i) vec = vec && p.begin[i] % 4 == 0 && aligned_to(p.out[i], bytes);
   const int64_t groups = vec ? p.C / 4 : p.C;
-  // long runs re-read least; short ones where the threads would not fill the GPU otherwise
-  p.run = batch * groups * ceil_div(p.L, 32) >= 1024 * static_cast<int64_t>(layer_sm_count()) ? 32 : kStep;
+  // Long runs re-read least, and the longest that still gives 1024 threads a multiprocessor is taken,
+  // or runs of 8.  4 x 4096 x 5376 bf16 with runs of 16, 32, 64 and 128: 84, 69, 65 and 63 us.
+  p.run = kStep;
+  for (int run : {32, 64, 128})
+    if (batch * groups * ceil_div(p.L, run) >= 1024 * static_cast<int64_t>(layer_sm_count())) p.run = run;
   const int64_t runs = p.L > 0 ? ceil_div(p.L, p.run) : 1;
   const dim3 grid(static_cast<unsigned>(ceil_div(groups * runs, kThreads)), static_cast<unsigned>(batch));
   auto k = vec ? (width == 2 ? conv_kernel<T, 2, 4> : width == 3 ? conv_kernel<T, 3, 4> : conv_kernel<T, 4, 4>)
