@@ -2,9 +2,9 @@
 // the states that the choice decides.
 //
 // Selection reads the logits once; HBM bounds it.  Within a beam the score
-// s + (x - lse) never falls as the logit x rises, so a block that holds a piece
-// of a row in registers can name its best by logit before the row's log-sum-exp
-// is known: it writes the k + 1 best and the piece's maximum and sum of
+// s + (x - lse) never falls as the logit x rises, so a block that reads a piece
+// of a row can name its best by logit before the row's log-sum-exp is known: it
+// writes the k + 1 best and the piece's maximum and sum of
 // exponentials.  A second launch joins the sums in a fixed order and picks the k
 // best scores of a request among its pieces' candidates.
 //
@@ -81,12 +81,13 @@ __device__ __forceinline__ Key bound_of(Key mine, int n, Key (&s_group)[kMaxGrou
   if (threadIdx.x % share == 0) s_group[threadIdx.x / share] = mine;
   if (threadIdx.x == 0) s_bound = 0;
   __syncthreads();
-  if (threadIdx.x < groups) {
-    const Key key = s_group[threadIdx.x];
+  {  // each thread counts a share of the groups that are above its own
+    const int part = threadIdx.x % share;
     int rank = 0;
-#pragma unroll 16
-    for (int i = 0; i < groups; ++i) rank += s_group[i] > key;
-    if (rank == n - 1 && key) s_bound = key;  // keys differ: one thread at most
+#pragma unroll 8
+    for (int i = part; i < groups; i += share) rank += s_group[i] > mine;
+    for (int o = 1; o < share; o *= 2) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+    if (part == 0 && rank == n - 1 && mine) s_bound = mine;  // keys differ: one group at most
   }
   __syncthreads();
   return s_bound;
@@ -103,110 +104,171 @@ __device__ __forceinline__ void rank_keys(const Key* keys, int n, int k, Key* ou
   for (int i = n + threadIdx.x; i < k; i += kThreads) out[i] = 0;
 }
 
+// Eight consecutive logits (16 or 32 bytes) as they lie in memory.
 template <typename T>
 struct Eight;
 template <>
 struct Eight<float> {
-  static __device__ __forceinline__ void load(const float* p, float* v) {
-    const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = *reinterpret_cast<const float4*>(p), b = *(reinterpret_cast<const float4*>(p) + 1);
   }
+  __device__ __forceinline__ float get(int i) const { return (i < 4 ? &a.x : &b.x)[i % 4]; }
 };
 template <>
 struct Eight<__nv_bfloat16> {
-  static __device__ __forceinline__ void load(const __nv_bfloat16* p, float* v) {
-    const uint4 w = __ldcs(reinterpret_cast<const uint4*>(p));
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(u[i] << 16);
-      v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-    }
+  uint4 q;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { q = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ float get(int i) const {
+    const uint32_t w = (&q.x)[i / 2];
+    return __uint_as_float(i % 2 ? w & 0xFFFF0000u : w << 16);
   }
 };
 
-// One piece of a row: kEach logits a thread.  kVec: rows are 16-byte aligned.
-template <typename T, int kEach, bool kVec>
+// One piece of a row: kEights times eight logits a thread.  They are read once; of each eight a
+// thread keeps the maximum, and the few eights that reach the bound are read again, from cache.
+// kVec: rows are 16-byte aligned.
+template <typename T, int kEights, bool kVec>
 __global__ void __launch_bounds__(kThreads) piece_kernel(SelectParams p) {
   extern __shared__ __align__(16) unsigned char raw[];
-  Key* s_keys = reinterpret_cast<Key*>(raw);  // `keep` groups' worth: no more keys reach the bound
+  Key* s_keys = reinterpret_cast<Key*>(raw);
   __shared__ Key s_group[kMaxGroups], s_bound;
   __shared__ float s_red[2][kThreads / 32];
   __shared__ int s_count;
   grid_dep_launch();
   const int piece = blockIdx.x, w = blockIdx.y, tid = threadIdx.x;
   const int64_t b = blockIdx.z, row = b * p.beams + w;
-  const int v0 = piece * kThreads * kEach;
+  const int v0 = piece * kThreads * 8 * kEights;
   if (tid == 0) s_count = 0;
 
-  // element e of the thread: index at(e), rising with e
-  auto at = [&](int e) { return kVec ? v0 + e / 8 * (8 * kThreads) + 8 * tid + e % 8 : v0 + e * kThreads + tid; };
-  float x[kEach];
-  if (p.finished && p.finished[row]) {
-    // one candidate, whose score is the beam's: logits of 0 and -infinity, whose log-sum-exp is 0
+  // element i of the thread's eight g: its index rises with g and i
+  auto at = [&](int g, int i) { return v0 + g * (8 * kThreads) + (kVec ? 8 * tid + i : kThreads * i + tid); };
+  const T* src = static_cast<const T*>(p.logits) + b * p.logits_batch + w * p.logits_beam;
+  const bool done = p.finished && p.finished[row];
+  const bool plain = kVec && !done && p.vocab - v0 >= kThreads * 8 * kEights;
+  auto read = [&](int g, float (&v)[8]) {
+    if (plain) {
+      Eight<T> x;
+      x.load(src + at(g, 0));
 #pragma unroll
-    for (int e = 0; e < kEach; ++e) x[e] = at(e) == p.eos ? 0.f : -INFINITY;
-  } else {
-    const T* src = static_cast<const T*>(p.logits) + b * p.logits_batch + w * p.logits_beam;
-    if constexpr (kVec) {
-#pragma unroll
-      for (int e = 0; e < kEach; e += 8) {
-        if (at(e) + 8 <= p.vocab) {
-          Eight<T>::load(src + at(e), x + e);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[e + i] = at(e + i) < p.vocab ? to_f32(src[at(e + i)]) : -INFINITY;
-        }
-      }
+      for (int i = 0; i < 8; ++i) v[i] = x.get(i);
     } else {
 #pragma unroll
-      for (int e = 0; e < kEach; ++e) x[e] = at(e) < p.vocab ? to_f32(src[at(e)]) : -INFINITY;
+      for (int i = 0; i < 8; ++i) {
+        v[i] = -INFINITY;  // past the row's end; adds nothing
+        // a finished beam's one candidate, at the beam's score: logits of 0 and -infinity, whose
+        // log-sum-exp is 0
+        if (done) v[i] = at(g, i) == p.eos ? 0.f : -INFINITY;
+        else if (at(g, i) < p.vocab) v[i] = to_f32(src[at(g, i)]);
+      }
+    }
+  };
+
+  // maximum and sum of exponentials, the sum for the thread's maximum so far
+  float top8[kEights], top = -INFINITY, sum = 0.f;
+  auto add = [&](int g, const float (&v)[8]) {
+    float m = v[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = fmaxf(m, v[i]);
+    top8[g] = m;
+    const float before = top;
+    top = fmaxf(top, m);
+    const float shift = top > -INFINITY ? top : 0.f;  // nothing but -infinity sums to 0
+    const uint64_t minus2 = pack2(-shift, -shift), scale2 = pack2(kLog2e, kLog2e);
+    uint64_t sum2 = pack2(sum * exp2_fast((before - shift) * kLog2e), 0.f);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      float lo, hi;
+      unpack2(mul2(add2(pack2(v[i], v[i + 1]), minus2), scale2), lo, hi);
+      sum2 = add2(sum2, pack2(exp2_fast(lo), exp2_fast(hi)));
+    }
+    float hi;
+    unpack2(sum2, sum, hi);
+    sum += hi;
+  };
+  if (plain) {
+    Eight<T> x[kEights];
+#pragma unroll
+    for (int g = 0; g < kEights; ++g) x[g].load(src + at(g, 0));
+#pragma unroll
+    for (int g = 0; g < kEights; ++g) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = x[g].get(i);
+      add(g, v);
+    }
+  } else {
+#pragma unroll
+    for (int g = 0; g < kEights; ++g) {
+      float v[8];
+      read(g, v);
+      add(g, v);
     }
   }
 
-  // maximum and sum of exponentials (places past the row's end add nothing)
-  float top8[kEach / 8];
+  // The thread's largest key or a little less: the index is that of the last of the eight that hold
+  // the first of its largest logits, so `keep` keys reach the bound all the same (more, with ties).
+  int best = kEights - 1;  // the first eight that hold the largest logit
 #pragma unroll
-  for (int e = 0; e < kEach; e += 8) {
-    top8[e / 8] = x[e];
-#pragma unroll
-    for (int i = 1; i < 8; ++i) top8[e / 8] = fmaxf(top8[e / 8], x[e + i]);
-  }
-  float top = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < kEach / 8; ++i) top = fmaxf(top, top8[i]);
-  int first = 0;  // the first of the thread's largest logits
-#pragma unroll
-  for (int e = kEach - 1; e >= 0; --e) first = x[e] == top ? e : first;
+  for (int g = kEights - 1; g >= 0; --g) best = top8[g] == top ? g : best;
   Key mine = 0;
-  if (at(0) < p.vocab) mine = key_of(top, static_cast<uint32_t>(at(first)));
+  if (at(0, 0) < p.vocab) mine = key_of(top, static_cast<uint32_t>(at(best, 7)));
   float piece_top = top;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) piece_top = fmaxf(piece_top, __shfl_xor_sync(0xffffffffu, piece_top, o));
   if (tid % 32 == 0) s_red[0][tid / 32] = piece_top;
-  const Key bound = bound_of(mine, p.keep, s_group, s_bound);
+
+  // The keys from the bound up.  Where the groups' keys are exact they lie in `keep` groups at most,
+  // for which there is room; with ties the first round may overrun it, and a second takes exact keys.
+  const int room = p.keep * share_of(p.keep) * 8 * kEights;
+#pragma unroll 1
+  for (int round = 0;; ++round) {
+    const Key bound = bound_of(mine, p.keep, s_group, s_bound);
+    const float least = key_value(bound);
+    unsigned hits = 0;
+#pragma unroll
+    for (int g = 0; g < kEights; ++g)
+      if (!bound || !(top8[g] < least)) hits |= 1u << g;  // (NaN go on, as -infinity)
+    for (; hits; hits &= hits - 1) {
+      if (*static_cast<volatile int*>(&s_count) > room) break;
+      const int g = __ffs(static_cast<int>(hits)) - 1;
+      float v[8];
+      read(g, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if ((bound && v[i] < least) || at(g, i) >= p.vocab) continue;
+        const Key key = key_of(v[i], static_cast<uint32_t>(at(g, i)));
+        if (key < bound) continue;
+        const int n = atomicAdd(&s_count, 1);
+        if (n < room) s_keys[n] = key;
+      }
+    }
+    __syncthreads();
+    if (s_count <= room || round == 1) break;
+    // (a NaN counts as -infinity and is in no maximum, so a thread without more starts at its first)
+    mine = 0;
+    for (int g = top > -INFINITY ? best : 0; g < kEights; ++g) {
+      float v[8];
+      read(g, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const Key key = at(g, i) < p.vocab ? key_of(v[i], static_cast<uint32_t>(at(g, i))) : 0;
+        mine = key > mine ? key : mine;
+      }
+      if (mine) break;
+    }
+    __syncthreads();
+    if (tid == 0) s_count = 0;
+  }
+
 #pragma unroll
   for (int i = 0; i < kThreads / 32; ++i) piece_top = fmaxf(piece_top, s_red[0][i]);
-  float sum = 0.f;
-  const float shift = piece_top > -INFINITY ? piece_top : 0.f;  // a piece with nothing left sums to 0
-#pragma unroll
-  for (int e = 0; e < kEach; ++e) sum += exp2_fast((x[e] - shift) * kLog2e);
+  if (top > -INFINITY) sum *= exp2_fast((top - piece_top) * kLog2e);  // (else it is 0, or lost)
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (tid % 32 == 0) s_red[1][tid / 32] = sum;
-
-  const float least = key_value(bound);
-#pragma unroll
-  for (int e = 0; e < kEach; e += 8) {
-    if (bound && top8[e / 8] < least) continue;  // (NaN go on, as -infinity)
-#pragma unroll
-    for (int i = e; i < e + 8; ++i) {
-      const Key key = key_of(x[i], static_cast<uint32_t>(at(i)));
-      if (key >= bound && at(i) < p.vocab) s_keys[atomicAdd(&s_count, 1)] = key;
-    }
-  }
   __syncthreads();
-  rank_keys(s_keys, s_count, p.keep, p.keys + (row * p.pieces + piece) * p.keep);
+  rank_keys(s_keys, s_count < room ? s_count : room, p.keep, p.keys + (row * p.pieces + piece) * p.keep);
   if (tid == 0) {
     sum = 0.f;
     for (int i = 0; i < kThreads / 32; ++i) sum += s_red[1][i];
@@ -336,15 +398,16 @@ __global__ void __launch_bounds__(kThreads) merge_kernel(SelectParams p, int pie
   }
 }
 
-// Logits a thread holds: 32, or 8 where pieces of 32 a thread would be fewer than two a multiprocessor.
-int each_of(int64_t batch, int beams, int vocab) {
-  return batch * beams * ceil_div(vocab, 32 * kThreads) < 2 * static_cast<int64_t>(layer_sm_count()) ? 8 : 32;
+// Times eight logits that a thread reads: eight, or one where that would leave fewer than four pieces a
+// multiprocessor.
+int eights_of(int64_t batch, int beams, int vocab) {
+  return batch * beams * ceil_div(vocab, 64 * kThreads) >= 4 * static_cast<int64_t>(layer_sm_count()) ? 8 : 1;
 }
 
-template <typename T, int kEach>
+template <typename T, int kEights>
 cudaError_t launch_pieces(const SelectParams& p, bool vec, int64_t batch, cudaStream_t stream) {
-  const size_t smem = static_cast<size_t>(p.keep) * share_of(p.keep) * kEach * sizeof(Key);
-  auto k = vec ? piece_kernel<T, kEach, true> : piece_kernel<T, kEach, false>;
+  const size_t smem = static_cast<size_t>(p.keep) * share_of(p.keep) * 8 * kEights * sizeof(Key);
+  auto k = vec ? piece_kernel<T, kEights, true> : piece_kernel<T, kEights, false>;
   if (smem > 40 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
@@ -357,11 +420,11 @@ template <typename T>
 cudaError_t launch_select(const SelectParams& p, int64_t batch, cudaStream_t stream) {
   const int64_t es = sizeof(T);
   const bool vec = aligned_to(p.logits, 16) && p.logits_beam * es % 16 == 0 && p.logits_batch * es % 16 == 0;
-  const int each = each_of(batch, p.beams, p.vocab);
-  const cudaError_t e = each == 8 ? launch_pieces<T, 8>(p, vec, batch, stream) : launch_pieces<T, 32>(p, vec, batch, stream);
+  const int eights = eights_of(batch, p.beams, p.vocab);
+  const cudaError_t e = eights == 8 ? launch_pieces<T, 8>(p, vec, batch, stream) : launch_pieces<T, 1>(p, vec, batch, stream);
   if (e != cudaSuccess) return e;
   return launch_k(merge_kernel<T>, dim3(static_cast<unsigned>(batch)), dim3(kThreads), 0, stream, true, p,
-                  each * kThreads);
+                  eights * 8 * kThreads);
 }
 
 struct ReorderParams {
@@ -436,7 +499,7 @@ ssd_status check_select(const ssd_beam_select_args* a) {
 extern "C" size_t ssd_beam_select_workspace_size(const ssd_beam_select_args* a) {
   using namespace ssd;
   if (check_select(a) != SSD_OK) return 0;
-  const size_t pieces = ceil_div(a->vocab, each_of(a->batch, a->beams, a->vocab) * kThreads);
+  const size_t pieces = ceil_div(a->vocab, eights_of(a->batch, a->beams, a->vocab) * 8 * kThreads);
   return static_cast<size_t>(a->batch) * a->beams * pieces * ((a->k + 1) * sizeof(Key) + sizeof(float2));
 }
 
@@ -457,7 +520,7 @@ extern "C" ssd_status ssd_beam_select(const ssd_beam_select_args* a, ssd_stream_
   p.beams = a->beams, p.vocab = a->vocab, p.k = a->k, p.eos = a->eos;
   p.logits = a->logits, p.scores = a->scores, p.finished = a->finished;
   p.out_scores = a->out_scores, p.parents = a->parents, p.tokens = a->tokens;
-  p.pieces = static_cast<int>(ceil_div(p.vocab, each_of(a->batch, p.beams, p.vocab) * kThreads));
+  p.pieces = static_cast<int>(ceil_div(p.vocab, eights_of(a->batch, p.beams, p.vocab) * 8 * kThreads));
   p.keep = p.k + 1;
   p.keys = static_cast<Key*>(a->workspace);
   p.sums = reinterpret_cast<float2*>(p.keys + a->batch * p.beams * p.pieces * p.keep);

@@ -410,6 +410,39 @@ def test_beam_ties_and_masks(ssd, dtype):
         same_choice(ssd.ssd_beam_select(x.cuda(), s.cuda(), 8, finished=done.cuda(), eos=eos), ref.beam(x, s, 8, done, eos))
 
 
+@both_types
+def test_beam_low_logits_beside_masked_ones(ssd, dtype):
+    """Logits far below 0 beside whole stretches of minus infinity or of the
+    type's lowest value: the sums must neither overflow nor lose them."""
+    g = gen(31)
+    V = 40000
+    x = (torch.randn(4, 3, V, generator=g) - 1000.0).to(dtype)
+    x[1, :, 100:39000] = -float("inf")
+    x[2, :, 100:39000] = torch.finfo(dtype).min
+    x[3, 1:] = torch.finfo(dtype).min
+    s = torch.tensor([-1.0, -2.5, -4.0]).repeat(4, 1)
+    for k in (1, 6):
+        same_choice(ssd.ssd_beam_select(x.cuda(), s.cuda(), k), ref.beam(x, s, k), k)
+
+
+@both_types
+def test_beam_many_requests_of_ties(ssd, dtype):
+    """Enough rows for the long pieces, with ties, masks and finished beams."""
+    g = gen(32)
+    x = (torch.randint(0, 4, (40, 4, 70000), generator=g)).to(dtype)
+    x[::3] = 0.0
+    x[1::3, :, :69990] = -float("inf")
+    s = torch.tensor([-1.0, -1.0, -1.5, -9.0]).repeat(40, 1)
+    done = torch.zeros(40, 4, dtype=torch.bool)
+    done[5:9, 1] = True
+    done[7] = True
+    # equal sums in every beam of a request whose rows are equal
+    x[:, 1] = x[:, 0]
+    for k in (4, 64):
+        same_choice(ssd.ssd_beam_select(x.cuda(), s.cuda(), k, finished=done.cuda(), eos=69999),
+                    ref.beam(x, s, k, done, 69999), k)
+
+
 def test_beam_scores_that_swallow_small_differences(ssd):
     """A beam at -2^23 (units of 1): logits that differ by less are equal scores,
     and fall by index, not by logit.  All beams share one row, hence one sum."""
