@@ -23,7 +23,7 @@
 namespace ssd {
 namespace {
 
-constexpr int kMaxWarps = 16;
+constexpr int kMaxWarps = 16;  // of a block
 
 struct W4Params {
   int64_t x_token, add_token;
@@ -125,32 +125,42 @@ __global__ void __launch_bounds__(kMaxWarps * 32) w4_kernel(W4Params p) {
   const uint4* packed = p.packed + static_cast<int64_t>(blockIdx.x) * p.ktiles * 32 + lane;
 
   float total[kCols][4] = {};
-  // a warp's unit: 64 columns, or 128 where a scale holds for 128
-  constexpr int kUnit = kGroup == 128 ? 2 : 1;
-  const int units = (p.ktiles + kUnit - 1) / kUnit;
-#pragma unroll 4
-  for (int unit = warp; unit < units; unit += warps) {
-    float sum[kCols][4] = {};
+  // a warp's unit: two tiles, 128 columns; its next kAhead units' codes are on their way together
+  constexpr int kAhead = kCols * kParts == 1 ? 4 : 2;
+  const int units = (p.ktiles + 1) / 2;
+  for (int base = warp; base < units; base += kAhead * warps) {
+    uint4 q[kAhead][2];
 #pragma unroll
-    for (int half = 0; half < 2 * kUnit; ++half) {  // 32 columns: two products
-      const int kt = unit * kUnit + half / 2;
-      if (kUnit == 2 && kt >= p.ktiles) break;
-      const uint4 q = __ldg(packed + static_cast<int64_t>(kt) * 32);
-      const int k0 = kt * 64 + half % 2 * 32 + c * 8;
-      uint32_t xw[kCols][4];
+    for (int u = 0; u < kAhead; ++u)
 #pragma unroll
-      for (int t = 0; t < kCols; ++t) load_x<kVec>(x[t] + k0, part[t], x[t] ? p.k - k0 : 0, xw[t]);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t w = half % 2 ? (i ? q.w : q.z) : (i ? q.y : q.x);
-        const uint32_t a[4] = {codes<0>(w), codes<1>(w), codes<2>(w), codes<3>(w)};
-#pragma unroll
-        for (int t = 0; t < kCols; ++t) mma_bf16(sum[t], a, xw[t][2 * i], xw[t][2 * i + 1]);
+      for (int h = 0; h < 2; ++h) {
+        const int kt = 2 * (base + u * warps) + h;
+        q[u][h] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);  // zeros past the end
+        if (kt < p.ktiles) q[u][h] = __ldg(packed + static_cast<int64_t>(kt) * 32);
       }
-      if (kGroup == 32 || half == 2 * kUnit - 1 || (kUnit == 2 && half % 2 == 1 && kt + 1 == p.ktiles)) {
-        const int g = kGroup == 32 ? kt * 2 + half % 2 : unit;
-        if (g < p.ngroups) {  // (a last group's columns past k are all 0)
-          const float f0 = __ldg(s0 + g), f1 = __ldg(s1 + g);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int unit = base + u * warps;
+      if (unit >= units) break;
+      float sum[kCols][4] = {};
+#pragma unroll
+      for (int part4 = 0; part4 < 4; ++part4) {  // 32 columns: two products
+        const int k0 = unit * 128 + part4 * 32 + c * 8;
+        uint32_t xw[kCols][4];
+#pragma unroll
+        for (int t = 0; t < kCols; ++t) load_x<kVec>(x[t] + k0, part[t], x[t] ? p.k - k0 : 0, xw[t]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint4& v = q[u][part4 / 2];
+          const uint32_t w = part4 % 2 ? (i ? v.w : v.z) : (i ? v.y : v.x);
+          const uint32_t a[4] = {codes<0>(w), codes<1>(w), codes<2>(w), codes<3>(w)};
+#pragma unroll
+          for (int t = 0; t < kCols; ++t) mma_bf16(sum[t], a, xw[t][2 * i], xw[t][2 * i + 1]);
+        }
+        constexpr int kParts32 = kGroup / 32;  // 32-column parts a scale holds for
+        if (part4 % kParts32 == kParts32 - 1) {
+          const int g = unit * (4 / kParts32) + part4 / kParts32;
+          const float f0 = g < p.ngroups ? __ldg(s0 + g) : 0.f, f1 = g < p.ngroups ? __ldg(s1 + g) : 0.f;
 #pragma unroll
           for (int t = 0; t < kCols; ++t) {
             total[t][0] = fmaf(f0, sum[t][0], total[t][0]);
@@ -192,15 +202,17 @@ template <typename T, int kCols, int kGroup>
 cudaError_t launch_cols(const W4Params& p, cudaStream_t stream) {
   constexpr int kTokens = kCols * 8 / (sizeof(T) == 4 ? 3 : 1);
   const bool vec = p.k % 8 == 0 && aligned_to(p.x, 16) && p.x_token * static_cast<int64_t>(sizeof(T)) % 16 == 0;
-  const int64_t units = ceil_div(p.ktiles, kGroup == 128 ? 2 : 1);
+  const int64_t units = ceil_div(p.ktiles, 2);
   const dim3 grid(static_cast<unsigned>(ceil_div(p.n, 16)), static_cast<unsigned>(ceil_div(p.M, kTokens)));
-  // warps for about two units each, fewer where there are many blocks anyway
-  int warps = static_cast<int>(ceil_div(units, 2));
-  const int64_t enough = ceil_div(32 * static_cast<int64_t>(layer_sm_count()), static_cast<int64_t>(grid.x) * grid.y);
-  if (warps > enough) warps = static_cast<int>(enough < 4 ? (warps < 4 ? warps : 4) : enough);
-  if (warps > kMaxWarps) warps = kMaxWarps;
+  // as many warps as give every multiprocessor kWarps, at least 4, and no more than there are units
+  // (2560 -> 10576, one token, with 16, 24, 32, 48 and 64: 6.3, 6.3, 6.0, 6.9 and 7.5 us)
+  constexpr int64_t kWarps = 32;
+  int64_t warps = ceil_div(kWarps * layer_sm_count(), static_cast<int64_t>(grid.x) * grid.y);
+  warps = warps < 4 ? 4 : warps > kMaxWarps ? kMaxWarps : warps;
+  if (warps > units) warps = units;
   const size_t smem = static_cast<size_t>(warps) * kCols * 4 * 32 * sizeof(float);
-  return launch_k(vec ? w4_kernel<T, kCols, kGroup, true> : w4_kernel<T, kCols, kGroup, false>, grid, dim3(warps * 32),
+  return launch_k(vec ? w4_kernel<T, kCols, kGroup, true> : w4_kernel<T, kCols, kGroup, false>, grid,
+                  dim3(static_cast<unsigned>(warps) * 32),
                   smem, stream, false, p);
 }
 
