@@ -414,8 +414,14 @@ typedef struct {
   const void* add;     /* rows [tokens][n] or NULL */
   int64_t add_token;
   void* y; /* [tokens][n] */
+  void* workspace; /* 16-byte aligned */
+  size_t workspace_bytes;
 } ssd_w4_matvec_args;
 
+/* Bytes of workspace: for 32-bit x and for rows of x that are not 16-byte
+ * vectors (0 otherwise, or where the sizes are refused); tokens, k, n, group,
+ * dtype, x and x_token are read. */
+size_t ssd_w4_matvec_workspace_size(const ssd_w4_matvec_args* args);
 ssd_status ssd_w4_matvec(const ssd_w4_matvec_args* args, ssd_stream_t stream);
 
 /* Beam search's choice.  Candidate (w, v) has the score

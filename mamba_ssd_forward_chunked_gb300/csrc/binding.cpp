@@ -321,7 +321,7 @@ PyObject* step(PyObject* const* p) {
   return wrap(y);
 }
 
-// x, packed, scales, group, add, y
+// x, packed, scales, group, add, y, workspace
 PyObject* w4_matvec(PyObject* const* p) {
   const First x = first(p[0], "x", 2);
   const int64_t M = x.t.size(0), K = x.t.size(1), group = whole(p[3], "group");
@@ -343,6 +343,16 @@ PyObject* w4_matvec(PyObject* const* p) {
   dense<void>(p[5], "y", x.dev, x.type, {M, n});
   const at::Tensor y = p[5] != Py_None ? tensor(p[5], "y") : empty({M, n}, x.type, x.t);
   a.y = y.data_ptr();
+  a.size = sizeof(a);
+  at::Tensor space;
+  if (p[6] != Py_None) {
+    const int64_t bytes = tensor(p[6], "workspace").numel();
+    a.workspace = dense<void>(p[6], "workspace", x.dev, at::kByte, {bytes});
+    a.workspace_bytes = static_cast<size_t>(bytes);
+  } else if (const size_t need = ssd_w4_matvec_workspace_size(&a)) {
+    space = empty({static_cast<int64_t>(need)}, at::kByte, x.t);
+    a.workspace = space.data_ptr(), a.workspace_bytes = need;
+  }
   call(ssd_w4_matvec, "ssd_w4_matvec", a, x.dev);
   return wrap(y);
 }
@@ -477,7 +487,7 @@ PyMODINIT_FUNC PyInit__layer_binding() {
       method<conv_fwd, 11>("conv_fwd"),
       method<selective_scan, 15>("selective_scan"),
       method<step, 16>("step"),
-      method<w4_matvec, 6>("w4_matvec"),
+      method<w4_matvec, 7>("w4_matvec"),
       method<beam_select, 6>("beam_select"),
       method<beam_reorder, 3>("beam_reorder"),
       method<scan_workspace, 5>("scan_workspace"),

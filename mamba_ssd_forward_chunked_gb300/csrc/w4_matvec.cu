@@ -14,10 +14,13 @@
 //
 // x enters exactly: bf16 as it is, a 32-bit x as three bf16 parts
 // x = hi + mid + lo in three columns of the product, added in 32 bits at the
-// end.  A group's sum is scaled in 32 bits when its columns are done.
+// end.  The parts (and bf16 rows that are not 16-byte vectors) are laid out by a
+// small launch in front, in the workspace; the product's launch overlaps it and
+// has its first codes on their way before it waits for it.  A group's sum is
+// scaled in 32 bits when its columns are done.
 //
-// A block takes 16 rows; its warps take column tiles in turn and their sums are
-// joined in shared memory in a fixed order.
+// A block takes 16 rows; its warps take pairs of column tiles in turn and their
+// sums are joined in shared memory in a fixed order.
 #include "layer.cuh"
 
 namespace ssd {
@@ -26,9 +29,9 @@ namespace {
 constexpr int kMaxWarps = 16;  // of a block
 
 struct W4Params {
-  int64_t x_token, add_token;
+  int64_t x_token, add_token;  // x_token: of the columns
   int M, n, k, ktiles, ngroups;
-  const void* x;
+  const __nv_bfloat16* x;  // the product's columns: [tokens * parts][..], 16-byte rows
   const uint4* packed;
   const float* scales;
   const void* add;
@@ -49,58 +52,38 @@ __device__ __forceinline__ uint32_t codes(uint32_t w) {
   return *reinterpret_cast<uint32_t*>(&r);
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
+// The top 16 bits of a 32-bit number as a number; cut, not rounded, so that no part overflows.
+__device__ __forceinline__ float cut(float v) { return __uint_as_float(__float_as_uint(v) & 0xFFFF0000u); }
+
+// The product's columns of x [tokens][k]: zeros from k to the row's end; of a 32-bit x its three parts
+// of 8 bits (24 in all).  An infinity or NaN is its own first part.
+constexpr int kColumnThreads = 256;
+__global__ void __launch_bounds__(kColumnThreads) columns_kernel(const __nv_bfloat16* x, int64_t x_token, int k, int row,
+                                                                 __nv_bfloat16* out) {
+  grid_dep_launch();
+  const int at = blockIdx.x * kColumnThreads + threadIdx.x;
+  const int64_t m = blockIdx.y;
+  if (at < row) out[m * row + at] = at < k ? x[m * x_token + at] : __float2bfloat16_rn(0.f);
+}
+__global__ void __launch_bounds__(kColumnThreads) columns_kernel(const float* x, int64_t x_token, int k, int row,
+                                                                 __nv_bfloat16* out) {
+  grid_dep_launch();
+  const int at = blockIdx.x * kColumnThreads + threadIdx.x;
+  const int64_t m = blockIdx.y;
+  if (at >= row) return;
+  const float v = at < k ? x[m * x_token + at] : 0.f;
+  const bool finite = fabsf(v) < INFINITY;
+  const float hi = finite ? cut(v) : v, mid = finite ? cut(v - hi) : 0.f, lo = finite ? v - hi - mid : 0.f;
+  out += 3 * m * row + at;
+  out[0] = __float2bfloat16_rn(hi);
+  out[row] = __float2bfloat16_rn(mid);
+  out[2 * row] = __float2bfloat16_rn(lo);
 }
 
-// A lane's eight columns (k0 ..) of its token, as the four operand words of two products.
-template <bool kVec>
-__device__ __forceinline__ void load_x(const __nv_bfloat16* x, int, int left, uint32_t (&w)[4]) {
-  w[0] = w[1] = w[2] = w[3] = 0;
-  if constexpr (kVec) {
-    if (left > 0) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(x));
-      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < left) w[i / 2] |= static_cast<uint32_t>(__bfloat16_as_ushort(x[i])) << (16 * (i % 2));
-  }
-}
-template <bool kVec>
-__device__ __forceinline__ void load_x(const float* x, int part, int left, uint32_t (&w)[4]) {
-  float f[8];
-  if constexpr (kVec) {
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-    if (left > 0) a = __ldg(reinterpret_cast<const float4*>(x)), b = __ldg(reinterpret_cast<const float4*>(x) + 1);
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = i < left ? x[i] : 0.f;
-  }
-  // the part'th eight bits of x (cut, not rounded, so that no part overflows): 3 x 8 = 24 bits are all
-  // of it.  An infinity or NaN is its own first part.
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    auto cut = [](float v) { return __uint_as_float(__float_as_uint(v) & 0xFFFF0000u); };
-    if (fabsf(f[i]) < INFINITY) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        if (j < part) f[i] -= cut(f[i]);
-      f[i] = cut(f[i]);
-    } else if (part > 0) {
-      f[i] = 0.f;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = pack_bf16(f[2 * i], f[2 * i + 1]);
-}
-
-// kCols: products' token columns in blocks of 8.  kGroup: columns a scale holds for.  kVec: k is a
-// multiple of 8 and x's rows are 16-byte aligned.
-template <typename T, int kCols, int kGroup, bool kVec>
+// kCols: products' columns in blocks of 8.  kGroup: columns of weights a scale holds for.  kDirect: the
+// columns are x itself, read through the read-only cache path (5120 -> 2560, eight tokens: 5.6 us against
+// 7.1 without); columns that the launch in front writes are read by ordinary loads.
+template <typename T, int kCols, int kGroup, bool kDirect>
 __global__ void __launch_bounds__(kMaxWarps * 32) w4_kernel(W4Params p) {
   constexpr int kParts = sizeof(T) == 4 ? 3 : 1;        // columns of a token
   constexpr int kTokens = kCols * 8 / kParts;           // tokens of a block (fp32: 2 in 8 columns)
@@ -110,14 +93,12 @@ __global__ void __launch_bounds__(kMaxWarps * 32) w4_kernel(W4Params p) {
   const int m0 = blockIdx.y * kTokens;
   const int row = blockIdx.x * 16 + r;
 
-  const T* x[kCols];
-  int part[kCols];
+  const __nv_bfloat16* x[kCols];
 #pragma unroll
   for (int t = 0; t < kCols; ++t) {
     const int col = t * 8 + r;
-    const int m = m0 + col / kParts;
-    part[t] = col % kParts;
-    x[t] = col / kParts < kTokens && m < p.M ? static_cast<const T*>(p.x) + m * p.x_token : nullptr;
+    const bool in = col / kParts < kTokens && m0 + col / kParts < p.M;
+    x[t] = in ? p.x + (static_cast<int64_t>(m0) * kParts + col) * p.x_token : nullptr;
   }
   // rows past the matrix hold codes of 8 and any scale will do
   const float* s0 = p.scales + static_cast<int64_t>(row < p.n ? row : p.n - 1) * p.ngroups;
@@ -126,8 +107,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32) w4_kernel(W4Params p) {
 
   float total[kCols][4] = {};
   // a warp's unit: two tiles, 128 columns; its next kAhead units' codes are on their way together
-  constexpr int kAhead = kCols * kParts == 1 ? 4 : 2;
+  constexpr int kAhead = kCols == 1 ? 4 : 2;
   const int units = (p.ktiles + 1) / 2;
+  bool waited = false;
   for (int base = warp; base < units; base += kAhead * warps) {
     uint4 q[kAhead][2];
 #pragma unroll
@@ -138,6 +120,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32) w4_kernel(W4Params p) {
         q[u][h] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);  // zeros past the end
         if (kt < p.ktiles) q[u][h] = __ldg(packed + static_cast<int64_t>(kt) * 32);
       }
+    if (!kDirect && !waited) grid_dep_wait();
+    waited = true;
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int unit = base + u * warps;
@@ -146,16 +130,22 @@ __global__ void __launch_bounds__(kMaxWarps * 32) w4_kernel(W4Params p) {
 #pragma unroll
       for (int part4 = 0; part4 < 4; ++part4) {  // 32 columns: two products
         const int k0 = unit * 128 + part4 * 32 + c * 8;
-        uint32_t xw[kCols][4];
+        uint4 xw[kCols];
 #pragma unroll
-        for (int t = 0; t < kCols; ++t) load_x<kVec>(x[t] + k0, part[t], x[t] ? p.k - k0 : 0, xw[t]);
+        for (int t = 0; t < kCols; ++t) {
+          xw[t] = make_uint4(0, 0, 0, 0);
+          if (x[t] && k0 < p.k) {
+            const uint4* from = reinterpret_cast<const uint4*>(x[t] + k0);
+            xw[t] = kDirect ? __ldg(from) : *from;
+          }
+        }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const uint4& v = q[u][part4 / 2];
           const uint32_t w = part4 % 2 ? (i ? v.w : v.z) : (i ? v.y : v.x);
           const uint32_t a[4] = {codes<0>(w), codes<1>(w), codes<2>(w), codes<3>(w)};
 #pragma unroll
-          for (int t = 0; t < kCols; ++t) mma_bf16(sum[t], a, xw[t][2 * i], xw[t][2 * i + 1]);
+          for (int t = 0; t < kCols; ++t) mma_bf16(sum[t], a, i ? xw[t].z : xw[t].x, i ? xw[t].w : xw[t].y);
         }
         constexpr int kParts32 = kGroup / 32;  // 32-column parts a scale holds for
         if (part4 % kParts32 == kParts32 - 1) {
@@ -198,10 +188,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32) w4_kernel(W4Params p) {
   }
 }
 
-template <typename T, int kCols, int kGroup>
+template <typename T, int kCols, int kGroup, bool kDirect>
 cudaError_t launch_cols(const W4Params& p, cudaStream_t stream) {
   constexpr int kTokens = kCols * 8 / (sizeof(T) == 4 ? 3 : 1);
-  const bool vec = p.k % 8 == 0 && aligned_to(p.x, 16) && p.x_token * static_cast<int64_t>(sizeof(T)) % 16 == 0;
   const int64_t units = ceil_div(p.ktiles, 2);
   const dim3 grid(static_cast<unsigned>(ceil_div(p.n, 16)), static_cast<unsigned>(ceil_div(p.M, kTokens)));
   // as many warps as give every multiprocessor kWarps, at least 4, and no more than there are units
@@ -211,43 +200,87 @@ cudaError_t launch_cols(const W4Params& p, cudaStream_t stream) {
   warps = warps < 4 ? 4 : warps > kMaxWarps ? kMaxWarps : warps;
   if (warps > units) warps = units;
   const size_t smem = static_cast<size_t>(warps) * kCols * 4 * 32 * sizeof(float);
-  return launch_k(vec ? w4_kernel<T, kCols, kGroup, true> : w4_kernel<T, kCols, kGroup, false>, grid,
-                  dim3(static_cast<unsigned>(warps) * 32),
-                  smem, stream, false, p);
+  return launch_k(w4_kernel<T, kCols, kGroup, kDirect>, grid, dim3(static_cast<unsigned>(warps) * 32), smem, stream,
+                  !kDirect, p);
 }
 
-template <typename T, int kGroup>
+template <typename T, int kGroup, bool kDirect>
 cudaError_t launch(const W4Params& p, cudaStream_t stream) {
-  // one block of eight columns where all tokens fit, else two (twice the tokens for the codes' price)
-  constexpr int kOne = 8 / (sizeof(T) == 4 ? 3 : 1);
-  return p.M <= kOne ? launch_cols<T, 1, kGroup>(p, stream) : launch_cols<T, 2, kGroup>(p, stream);
+  // the fewest blocks of eight columns that hold all tokens, up to 16 (fp32) or 32 (bf16): the codes are
+  // then read once
+  const int64_t columns = static_cast<int64_t>(p.M) * (sizeof(T) == 4 ? 3 : 1);
+  if (columns <= 8) return launch_cols<T, 1, kGroup, kDirect>(p, stream);
+  if (columns <= 16) return launch_cols<T, 2, kGroup, kDirect>(p, stream);
+  if constexpr (sizeof(T) == 4) {
+    if (columns > 32) return launch_cols<T, 6, kGroup, kDirect>(p, stream);
+  }
+  return launch_cols<T, 4, kGroup, kDirect>(p, stream);
 }
 
-template <typename T>
+template <typename T, bool kDirect>
 cudaError_t launch_group(const W4Params& p, int group, cudaStream_t stream) {
-  return group == 32 ? launch<T, 32>(p, stream) : group == 64 ? launch<T, 64>(p, stream) : launch<T, 128>(p, stream);
+  return group == 32   ? launch<T, 32, kDirect>(p, stream)
+         : group == 64 ? launch<T, 64, kDirect>(p, stream)
+                       : launch<T, 128, kDirect>(p, stream);
+}
+
+// x laid out as columns in the workspace, then the product.
+template <typename T>
+cudaError_t launch_columns(W4Params p, const ssd_w4_matvec_args* a, cudaStream_t stream) {
+  const int row = p.ktiles * 64;
+  const dim3 grid(static_cast<unsigned>(ceil_div(row, kColumnThreads)), static_cast<unsigned>(p.M));
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a->workspace);
+  void (*k)(const T*, int64_t, int, int, __nv_bfloat16*) = columns_kernel;
+  const cudaError_t e =
+      launch_k(k, grid, dim3(kColumnThreads), 0, stream, false, static_cast<const T*>(a->x), a->x_token, p.k, row, out);
+  if (e != cudaSuccess) return e;
+  p.x = out, p.x_token = row, p.k = row;
+  return launch_group<T, false>(p, a->group, stream);
+}
+
+ssd_status check_sizes(const ssd_w4_matvec_args* a) {
+  if (!a || a->size != static_cast<int64_t>(sizeof(*a))) return SSD_ERR_INVALID_ARG;
+  if (a->tokens < 0 || a->n <= 0 || a->k <= 0) return SSD_ERR_INVALID_ARG;
+  if (!known_dtype(a->dtype) || (a->group != 32 && a->group != 64 && a->group != 128) || a->tokens > 65535)
+    return SSD_ERR_UNSUPPORTED;
+  return a->k > (1 << 30) ? SSD_ERR_UNSUPPORTED : SSD_OK;
+}
+
+// Whether x has to be laid out as columns first: 32-bit values, or rows that are not 16-byte vectors.
+bool needs_columns(const ssd_w4_matvec_args* a) {
+  return a->dtype == SSD_F32 || a->k % 8 != 0 || !aligned_to(a->x, 16) || a->x_token % 8 != 0;
 }
 
 }  // namespace
 }  // namespace ssd
 
+extern "C" size_t ssd_w4_matvec_workspace_size(const ssd_w4_matvec_args* a) {
+  using namespace ssd;
+  if (check_sizes(a) != SSD_OK || !needs_columns(a)) return 0;
+  return static_cast<size_t>(a->tokens) * (a->dtype == SSD_F32 ? 3 : 1) * ceil_div(a->k, 64) * 64 * 2;
+}
+
 extern "C" ssd_status ssd_w4_matvec(const ssd_w4_matvec_args* a, ssd_stream_t stream) {
   using namespace ssd;
-  if (!a || a->size != static_cast<int64_t>(sizeof(*a))) return SSD_ERR_INVALID_ARG;
-  if (a->tokens < 0 || a->n <= 0 || a->k <= 0) return SSD_ERR_INVALID_ARG;
-  if (!known_dtype(a->dtype) || (a->group != 32 && a->group != 64 && a->group != 128) || a->tokens > 65535)
-    return SSD_ERR_UNSUPPORTED;
-  if (a->k > (1 << 30)) return SSD_ERR_UNSUPPORTED;
+  const ssd_status st = check_sizes(a);
+  if (st != SSD_OK) return st;
   if (a->tokens == 0) return SSD_OK;
   const size_t es = elem_size(a->dtype);
   if (!a->x || !aligned_to(a->x, es) || !a->y || !aligned_to(a->y, es) || !aligned_to(a->add, es) || !a->packed ||
       !aligned_to(a->packed, 16) || !a->scales || !aligned_to(a->scales, 4))
     return SSD_ERR_INVALID_ARG;
+  const bool columns = needs_columns(a);
+  if (columns) {
+    if (!a->workspace || !aligned_to(a->workspace, 16)) return SSD_ERR_INVALID_ARG;
+    if (a->workspace_bytes < ssd_w4_matvec_workspace_size(a)) return SSD_ERR_WORKSPACE;
+  }
   W4Params p{};
-  p.M = static_cast<int>(a->tokens), p.x_token = a->x_token, p.add_token = a->add_token;
+  p.M = static_cast<int>(a->tokens), p.add_token = a->add_token;
   p.n = a->n, p.k = a->k;
   p.ktiles = static_cast<int>(ceil_div(a->k, 64)), p.ngroups = static_cast<int>(ceil_div(a->k, a->group));
-  p.x = a->x, p.packed = static_cast<const uint4*>(a->packed), p.scales = a->scales, p.add = a->add, p.y = a->y;
-  return launched(a->dtype == SSD_BF16 ? launch_group<__nv_bfloat16>(p, a->group, stream)
-                                       : launch_group<float>(p, a->group, stream));
+  p.packed = static_cast<const uint4*>(a->packed), p.scales = a->scales, p.add = a->add, p.y = a->y;
+  if (a->dtype == SSD_F32) return launched(launch_columns<float>(p, a, stream));
+  if (columns) return launched(launch_columns<__nv_bfloat16>(p, a, stream));
+  p.x = static_cast<const __nv_bfloat16*>(a->x), p.x_token = a->x_token;
+  return launched(launch_group<__nv_bfloat16, true>(p, a->group, stream));
 }

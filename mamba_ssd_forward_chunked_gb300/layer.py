@@ -145,12 +145,14 @@ def w4_quantize(weight: torch.Tensor, group: int = 128) -> Tuple[torch.Tensor, t
 
 
 def ssd_w4_matvec(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, group: int, *,
-                  add: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+                  add: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """y = x W^T (+ add) for a few tokens and a 4-bit W (C: ssd_w4_matvec).
 
     x [M, k] and add [M, n] float32 or bfloat16 (rows may be strided); ``packed``
-    from w4_pack, ``scales`` [n, ceil(k/group)] float32, group 32, 64 or 128."""
-    args = (x, packed, scales, group, add, y)
+    from w4_pack, ``scales`` [n, ceil(k/group)] float32, group 32, 64 or 128.  float32 x, and rows that
+    are not 16-byte vectors, take a workspace of 2 bytes for each of x's (or its three parts') values."""
+    args = (x, packed, scales, group, add, y, workspace)
     return _binding.w4_matvec(*args) if stream is None else _on(stream, _binding.w4_matvec, *args)
 
 

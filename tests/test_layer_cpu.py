@@ -16,7 +16,7 @@ REORDER_MAX = 16
 CONV_ARGS = struct.Struct("@4q8iP2q10P")
 SCAN_ARGS = struct.Struct("@3q6i5P10q8PN")
 STEP_ARGS = struct.Struct("@3q8i3P3q11P")
-W4_ARGS = struct.Struct("@2q4iPq3PqP")
+W4_ARGS = struct.Struct("@2q4iPq3PqPPN")
 SELECT_ARGS = struct.Struct("@2q6iP2q6PN")
 REORDER_ARGS = struct.Struct("@2q4iP%dP%dP%dq" % ((REORDER_MAX,) * 3))
 FAKE = 1 << 20  # an aligned address that no call here reads
@@ -147,7 +147,7 @@ def test_step_refusals(ext, want, kw):
 
 def w4_args(ext, **kw):
     v = dict(size=W4_ARGS.size, tokens=1, n=16, k=64, group=32, dtype=1, x=FAKE, xs=64, packed=FAKE, scales=FAKE,
-             add=0, adds=0, y=FAKE)
+             add=0, adds=0, y=FAKE, ws=0, nbytes=0)
     v.update(kw)
     return W4_ARGS.pack(*v.values())
 
@@ -156,7 +156,9 @@ def w4_args(ext, **kw):
     (1, dict(size=0)), (1, dict(tokens=-1)), (1, dict(n=0)), (1, dict(k=0)), (2, dict(group=16)), (2, dict(group=0)),
     (2, dict(dtype=4)), (2, dict(tokens=65536)), (1, dict(x=0)), (1, dict(x=FAKE + 1)), (1, dict(packed=0)),
     (1, dict(packed=FAKE + 4)), (1, dict(scales=0)), (1, dict(scales=FAKE + 2)), (1, dict(add=FAKE + 1)), (1, dict(y=0)),
-    (0, dict(tokens=0)),
+    (0, dict(tokens=0)), (1, dict(dtype=0)), (1, dict(dtype=0, ws=FAKE + 2, nbytes=384)),
+    (3, dict(dtype=0, ws=FAKE, nbytes=383)), (1, dict(xs=65, tokens=2)), (1, dict(k=63)), (1, dict(x=FAKE + 2)),
+    (3, dict(k=63, ws=FAKE, nbytes=127)),
 ])
 def test_w4_refusals(ext, want, kw):
     assert ext.lib.ssd_w4_matvec(w4_args(ext, **kw), None) == want
