@@ -48,15 +48,15 @@ struct ScanParams {
   float* seg_sum;    // [batch][segments][D]: each segment's sum of steps
 };
 
-// Eight consecutive values as they lie in memory.
+// 16 bytes of consecutive values as they lie in memory.
 template <typename T>
 struct Raw;
 template <>
 struct Raw<__nv_bfloat16> {
+  static constexpr int kE = 8;
   uint4 v;
   __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint4*>(p)); }
-  __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = v; }
   __device__ __forceinline__ void set(int i, __nv_bfloat16 x) {
     const uint32_t bits = __bfloat16_as_ushort(x);
     uint32_t* w = &v.x;
@@ -66,32 +66,38 @@ struct Raw<__nv_bfloat16> {
     const uint32_t w = (&v.x)[i / 2];
     return __uint_as_float(i % 2 ? w & 0xFFFF0000u : w << 16);
   }
+  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&f)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 two = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&two);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
 };
 template <>
 struct Raw<float> {
-  float4 a, b;
-  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ void load(const float* p) {
-    a = __ldg(reinterpret_cast<const float4*>(p));
-    b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  static constexpr int kE = 4;
+  float4 v;
+  __device__ __forceinline__ void zero() { v = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void load(const float* p) { v = __ldg(reinterpret_cast<const float4*>(p)); }
+  __device__ __forceinline__ void set(int i, float x) { (&v.x)[i] = x; }
+  __device__ __forceinline__ float get(int i) const { return (&v.x)[i]; }
+  static __device__ __forceinline__ void store(float* p, const float (&f)[4]) {
+    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
   }
-  __device__ __forceinline__ void store(float* p) const {
-    reinterpret_cast<float4*>(p)[0] = a;
-    reinterpret_cast<float4*>(p)[1] = b;
-  }
-  __device__ __forceinline__ void set(int i, float x) { (i < 4 ? &a.x : &b.x)[i % 4] = x; }
-  __device__ __forceinline__ float get(int i) const { return (i < 4 ? &a.x : &b.x)[i % 4]; }
 };
 
-// Eight values from p, the first n of them there (0 for the rest).  kVec: all or none, 16-byte aligned.
+// A vector from p, its first n values there (0 for the rest).  kVec: all or none, 16-byte aligned.
 template <typename T, bool kVec>
-__device__ __forceinline__ void load8(Raw<T>& r, const T* p, int n) {
+__device__ __forceinline__ void load16(Raw<T>& r, const T* p, int n) {
   r.zero();
   if constexpr (kVec) {
     if (n > 0) r.load(p);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < Raw<T>::kE; ++i)
       if (i < n) r.set(i, p[i]);
   }
 }
@@ -113,17 +119,18 @@ __device__ __forceinline__ void softplus2(float& v0, float& v1) {
   v1 = fmaf(2.f, r1, fmaxf(v1, 0.f));
 }
 
-// Sizes that follow from T, the lanes of a channel (T * kNS states).
-template <int T>
+// Sizes that follow from T, the lanes of a channel (T * kNS states), and the type of the inputs.
+template <typename V, int T>
 struct Shape {
+  static constexpr int kE = Raw<V>::kE;
   static constexpr int kN = T * kNS;
   static constexpr int kChannels = T == 2 ? 32 : 16;       // of a block
   static constexpr int kThreads = kChannels / 2 * T;       // of the recurrence
   static constexpr int kHelp = T == 16 ? 128 : 64;         // of the memory side
-  static constexpr int kCols = kChannels / 8;              // vectors of eight channels in a row
+  static constexpr int kCols = kChannels / kE;             // vectors in a row of channels
   static constexpr int kIO = kTile * kCols;                // and in a tile
   static constexpr int kIOEach = (kIO + kHelp - 1) / kHelp;
-  static constexpr int kBC = kTile * kN / 8;               // vectors of eight in a tile of B (or C)
+  static constexpr int kBC = kTile * kN / kE;              // vectors in a tile of B (or C)
   static constexpr int kBCEach = (2 * kBC + kHelp - 1) / kHelp;
   // rows in floats, padded so that neighbouring rows fall into different banks
   static constexpr int kStepRow = 2 * kChannels + 4, kYRow = kChannels + 8;
@@ -131,8 +138,9 @@ struct Shape {
 
 // kState: only the segment's state from zero and its sum of steps (the first of two launches).
 template <typename V, int T, bool kVec, bool kState>
-__global__ void __launch_bounds__(Shape<T>::kThreads + Shape<T>::kHelp) scan_kernel(ScanParams p) {
-  using S = Shape<T>;
+__global__ void __launch_bounds__(Shape<V, T>::kThreads + Shape<V, T>::kHelp) scan_kernel(ScanParams p) {
+  using S = Shape<V, T>;
+  constexpr int kE = S::kE;
   __shared__ __align__(16) float s_step[2][kTile][S::kStepRow];  // (d, d u) of each channel
   __shared__ __align__(16) float s_B[2][kTile][S::kN], s_C[2][kTile][S::kN];
   __shared__ __align__(16) float s_y[2][kTile][S::kYRow];
@@ -159,10 +167,10 @@ __global__ void __launch_bounds__(Shape<T>::kThreads + Shape<T>::kHelp) scan_ker
     const V* Bm = static_cast<const V*>(p.Bm) + b * p.Bb + static_cast<int64_t>(group) * p.N;
     const V* Cm = static_cast<const V*>(p.Cm) + b * p.Cb + static_cast<int64_t>(group) * p.N;
     // a thread's vectors all lie in the same eight channels (kHelp is a multiple of kCols)
-    const int col0 = tid % S::kCols * 8;
-    float bias[8], skip[8];
+    const int col0 = tid % S::kCols * kE;
+    float bias[kE], skip[kE];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < kE; ++i) {
       bias[i] = p.delta_bias && col0 + i < nc ? p.delta_bias[c0 + col0 + i] : 0.f;
       skip[i] = !kState && p.skip && col0 + i < nc ? p.skip[c0 + col0 + i] : 0.f;
     }
@@ -176,10 +184,10 @@ __global__ void __launch_bounds__(Shape<T>::kThreads + Shape<T>::kHelp) scan_ker
         const int v = tid + i * S::kHelp;
         const int64_t t = t0 + v / S::kCols;
         const int n = v < S::kIO && t < end ? nc - col0 : 0;
-        load8<V, kVec>(r.u[i], u + t * p.ut + col0, n);
-        load8<V, kVec>(r.d[i], delta + t * p.dt + col0, n);
+        load16<V, kVec>(r.u[i], u + t * p.ut + col0, n);
+        load16<V, kVec>(r.d[i], delta + t * p.dt + col0, n);
         if constexpr (!kState) {
-          if (p.z) load8<V, kVec>(r.z[i], z + t * p.zt + col0, n);
+          if (p.z) load16<V, kVec>(r.z[i], z + t * p.zt + col0, n);
         }
       }
 #pragma unroll
@@ -187,10 +195,10 @@ __global__ void __launch_bounds__(Shape<T>::kThreads + Shape<T>::kHelp) scan_ker
         const int v = tid + i * S::kHelp;
         const bool is_c = v >= S::kBC;
         const int at = is_c ? v - S::kBC : v;
-        const int64_t t = t0 + at / (S::kN / 8);
-        const int n = at % (S::kN / 8) * 8;
+        const int64_t t = t0 + at / (S::kN / kE);
+        const int n = at % (S::kN / kE) * kE;
         if (v < (kState ? S::kBC : 2 * S::kBC))
-          load8<V, kVec>(r.bc[i], (is_c ? Cm + t * p.Ct : Bm + t * p.Bt) + n, t < end ? p.N - n : 0);
+          load16<V, kVec>(r.bc[i], (is_c ? Cm + t * p.Ct : Bm + t * p.Bt) + n, t < end ? p.N - n : 0);
       }
     };
     auto stage = [&](int64_t t0, int buf) {  // the tile's steps and rows of B and C
@@ -202,7 +210,7 @@ __global__ void __launch_bounds__(Shape<T>::kThreads + Shape<T>::kHelp) scan_ker
           const bool there = t0 + row < end;
           float4* dst = reinterpret_cast<float4*>(&s_step[buf][row][2 * col0]);
 #pragma unroll
-          for (int i = 0; i < 8; i += 2) {
+          for (int i = 0; i < kE; i += 2) {
             float d0 = r.d[j].get(i) + bias[i], d1 = r.d[j].get(i + 1) + bias[i + 1];
             if (p.softplus) softplus2(d0, d1);
             if (!there) d0 = d1 = 0.f;  // past the end the state stays
@@ -216,9 +224,9 @@ __global__ void __launch_bounds__(Shape<T>::kThreads + Shape<T>::kHelp) scan_ker
         const bool is_c = v >= S::kBC;
         const int at = is_c ? v - S::kBC : v;
         if (v < (kState ? S::kBC : 2 * S::kBC)) {
-          float* dst = (is_c ? s_C : s_B)[buf][at / (S::kN / 8)] + at % (S::kN / 8) * 8;
+          float* dst = (is_c ? s_C : s_B)[buf][at / (S::kN / kE)] + at % (S::kN / kE) * kE;
 #pragma unroll
-          for (int e = 0; e < 8; e += 4)
+          for (int e = 0; e < kE; e += 4)
             *reinterpret_cast<float4*>(dst + e) =
                 make_float4(r.bc[i].get(e), r.bc[i].get(e + 1), r.bc[i].get(e + 2), r.bc[i].get(e + 3));
         }
@@ -231,25 +239,22 @@ __global__ void __launch_bounds__(Shape<T>::kThreads + Shape<T>::kHelp) scan_ker
         const int row = v / S::kCols;
         if (v >= S::kIO || t0 + row >= end || col0 >= nc) continue;
         V* y = static_cast<V*>(p.y) + (b * p.L + t0 + row) * p.D + c0 + col0;
-        float out[8];
+        float out[kE];
 #pragma unroll
-        for (int i = 0; i < 8; i += 4) {
+        for (int i = 0; i < kE; i += 4) {
           const float4 sum = *reinterpret_cast<const float4*>(&s_y[buf][row][col0 + i]);
           out[i] = sum.x, out[i + 1] = sum.y, out[i + 2] = sum.z, out[i + 3] = sum.w;
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < kE; ++i) {
           out[i] = fmaf(skip[i], u2[j].get(i), out[i]);
           if (p.z) out[i] *= silu(z2[j].get(i));
         }
         if constexpr (kVec) {
-          Raw<V> r;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) r.set(i, from_f32<V>(out[i]));
-          r.store(y);
+          Raw<V>::store(y, out);
         } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
+          for (int i = 0; i < kE; ++i)
             if (col0 + i < nc) y[i] = from_f32<V>(out[i]);
         }
       }
@@ -271,7 +276,7 @@ __global__ void __launch_bounds__(Shape<T>::kThreads + Shape<T>::kHelp) scan_ker
       for (int64_t t = (end > begin ? end : begin) + tid / S::kCols; t < stop; t += S::kHelp / S::kCols) {
         V* y = static_cast<V*>(p.y) + (b * p.L + t) * p.D + c0 + col0;  // after the sequence's end
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < kE; ++i)
           if (col0 + i < nc) y[i] = from_f32<V>(0.f);
       }
     }
@@ -542,7 +547,7 @@ cudaError_t launch_token(const ScanParams& p, int64_t batch, cudaStream_t stream
 
 template <typename V, int T, bool kVec>
 cudaError_t launch_lanes(ScanParams p, int64_t batch, cudaStream_t stream) {
-  constexpr int kThreads = Shape<T>::kThreads + Shape<T>::kHelp;
+  constexpr int kThreads = Shape<V, T>::kThreads + Shape<V, T>::kHelp;
   const unsigned blocks = static_cast<unsigned>(p.G * p.tiles);
   if (p.segments > 1) {
     const cudaError_t e = launch_k(scan_kernel<V, T, kVec, true>,
@@ -578,12 +583,12 @@ cudaError_t launch(const ScanParams& p, int64_t batch, cudaStream_t stream) {
       default: return launch_token<T, 16>(p, batch, stream);
     }
   }
-  // 16-byte loads where every row of eight channels (of eight states) starts on 16 bytes and is whole
+  // 16-byte loads where every vector of channels (of states) starts on 16 bytes and is whole
   const int64_t es = sizeof(T);
   auto row16 = [&](const void* t, int64_t s0, int64_t s1) {
     return aligned_to(t, 16) && (batch == 1 || s0 * es % 16 == 0) && s1 * es % 16 == 0;
   };
-  const bool vec = p.per % 8 == 0 && p.N % 8 == 0 && row16(p.u, p.ub, p.ut) && row16(p.delta, p.db, p.dt) &&
+  const bool vec = p.per % Raw<T>::kE == 0 && p.N % Raw<T>::kE == 0 && row16(p.u, p.ub, p.ut) && row16(p.delta, p.db, p.dt) &&
                    row16(p.z, p.zb, p.zt) && row16(p.Bm, p.Bb, p.Bt) && row16(p.Cm, p.Cb, p.Ct) && aligned_to(p.y, 16);
   return vec ? launch_vec<T, true>(p, batch, stream) : launch_vec<T, false>(p, batch, stream);
 }
@@ -595,7 +600,7 @@ ssd_status check_sizes(const ssd_selective_scan_args* a) {
   return SSD_OK;
 }
 
-int channels_of_block(int N) { return lanes_of(N) == 2 ? Shape<2>::kChannels : Shape<4>::kChannels; }
+int channels_of_block(int N) { return lanes_of(N) == 2 ? Shape<float, 2>::kChannels : Shape<float, 4>::kChannels; }
 
 int segments_of(const ssd_selective_scan_args* a) {
   const int64_t blocks = ceil_div(a->channels / a->ngroups, channels_of_block(a->dstate)) * a->ngroups;
