@@ -424,95 +424,91 @@ __global__ void __launch_bounds__(Shape<V, T>::kThreads + Shape<V, T>::kHelp) sc
 }
 
 // One token: every state is read and written once and there is nothing to walk along, so memory
-// bounds it.  A thread takes four states of a channel, T neighbouring lanes share the channel (its
-// step is formed by each of them), and runs over kRows sequences, whose loads are all on their way
-// before the first is used; A and the channel's constants are read once for them.
-constexpr int kTokenThreads = 128, kRows = 2;
+// bounds it.  A thread takes eight states of a channel of one sequence, T neighbouring lanes share the
+// channel (its step is formed by each of them).  64 x 5120, 16 states, bf16, with four states a thread
+// 13.2 us, with eight 9.4, with sixteen 11.3; two sequences a thread 10.8 (fewer warps on the SM).
+constexpr int kTokenThreads = 128, kTokenNS = 8;
 
 template <typename V, int T, bool kVec>
-__global__ void __launch_bounds__(kTokenThreads, 8) scan_token_kernel(ScanParams p, int batch) {
+__global__ void __launch_bounds__(kTokenThreads, 8) scan_token_kernel(ScanParams p) {
   const int64_t id = static_cast<int64_t>(blockIdx.x) * kTokenThreads + threadIdx.x;
-  const int part = static_cast<int>(id % T), n0 = 4 * part;
+  const int part = static_cast<int>(id % T), n0 = kTokenNS * part;
   const bool live = id / T < p.D;
   const int c = live ? static_cast<int>(id / T) : p.D - 1;  // lanes past the end repeat the last channel
   const int g = c / p.per;
-  const int b0 = blockIdx.y * kRows;
+  const int64_t b = blockIdx.y;
 
-  auto load4 = [&](const float* t, float (&v)[4]) {  // four states from t, 0 past N
-    if constexpr (kVec) {
-      float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (n0 < p.N) f = *reinterpret_cast<const float4*>(t);
-      v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
-    } else {
+  auto load_f = [&](const float* t, float (&v)[kTokenNS]) {  // states from t, 0 past N
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = n0 + e < p.N ? t[e] : 0.f;
-    }
-  };
-  auto load_bc = [&](const V* t, float (&v)[4]) {
-    if constexpr (kVec && sizeof(V) == 2) {
-      uint2 w = make_uint2(0, 0);
-      if (n0 < p.N) w = *reinterpret_cast<const uint2*>(t);
-      v[0] = __uint_as_float(w.x << 16), v[1] = __uint_as_float(w.x & 0xFFFF0000u);
-      v[2] = __uint_as_float(w.y << 16), v[3] = __uint_as_float(w.y & 0xFFFF0000u);
-    } else if constexpr (kVec) {
-      load4(reinterpret_cast<const float*>(t), v);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = n0 + e < p.N ? to_f32(t[e]) : 0.f;
-    }
-  };
-
-  float a[4], h[kRows][4], Bv[kRows][4], Cv[kRows][4], u[kRows], d[kRows], z[kRows];
-#pragma unroll
-  for (int r = 0; r < kRows; ++r) {
-    const int64_t b = b0 + r < batch ? b0 + r : batch - 1;
-    const bool on = !p.lengths || p.lengths[b] > 0;
-    u[r] = d[r] = z[r] = 0.f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) h[r][e] = Bv[r][e] = Cv[r][e] = 0.f;
-    if (p.init) load4(p.init + (b * p.D + c) * p.N + n0, h[r]);
-    if (on) {  // a sequence without a token keeps its state, and its inputs are not looked at
-      u[r] = to_f32(static_cast<const V*>(p.u)[b * p.ub + c]);
-      d[r] = to_f32(static_cast<const V*>(p.delta)[b * p.db + c]);
-      if (p.z) z[r] = to_f32(static_cast<const V*>(p.z)[b * p.zb + c]);
-      load_bc(static_cast<const V*>(p.Bm) + b * p.Bb + static_cast<int64_t>(g) * p.N + n0, Bv[r]);
-      load_bc(static_cast<const V*>(p.Cm) + b * p.Cb + static_cast<int64_t>(g) * p.N + n0, Cv[r]);
-    }
-  }
-  load4(p.A + static_cast<int64_t>(c) * p.N + n0, a);
-  const float bias = p.delta_bias ? p.delta_bias[c] : 0.f, skip = p.skip ? p.skip[c] : 0.f;
-#pragma unroll
-  for (int r = 0; r < kRows; ++r) {
-    const int64_t b = b0 + r;
-    if (b >= batch) break;
-    const bool on = !p.lengths || p.lengths[b] > 0;
-    float step = d[r] + bias;
-    if (p.softplus) step = softplus(step);
-    if (!on) step = 0.f;
-    const float du = step * u[r];
-    float sum = 0.f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      h[r][e] = fmaf(exp2_fast(step * (a[e] * kLog2e)), h[r][e], du * Bv[r][e]);
-      sum = fmaf(h[r][e], Cv[r][e], sum);
-    }
-#pragma unroll
-    for (int o = 1; o < T; o *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (!live) continue;
-    if (part == 0) {
-      float y = fmaf(skip, u[r], sum);
-      if (p.z) y *= silu(z[r]);
-      static_cast<V*>(p.y)[b * p.D + c] = from_f32<V>(on ? y : 0.f);
-    }
-    if (p.final_state) {
-      float* out = p.final_state + (b * p.D + c) * p.N + n0;
+    for (int q = 0; q < kTokenNS; q += 4) {
       if constexpr (kVec) {
-        if (n0 < p.N) *reinterpret_cast<float4*>(out) = make_float4(h[r][0], h[r][1], h[r][2], h[r][3]);
+        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (n0 + q < p.N) f = *reinterpret_cast<const float4*>(t + q);
+        v[q] = f.x, v[q + 1] = f.y, v[q + 2] = f.z, v[q + 3] = f.w;
       } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (n0 + e < p.N) out[e] = h[r][e];
+        for (int e = q; e < q + 4; ++e) v[e] = n0 + e < p.N ? t[e] : 0.f;
       }
+    }
+  };
+  auto load_v = [&](const V* t, float (&v)[kTokenNS]) {
+    if constexpr (kVec && sizeof(V) == 2) {
+#pragma unroll
+      for (int q = 0; q < kTokenNS; q += 4) {
+        uint2 w = make_uint2(0, 0);
+        if (n0 + q < p.N) w = *reinterpret_cast<const uint2*>(t + q);
+        v[q] = __uint_as_float(w.x << 16), v[q + 1] = __uint_as_float(w.x & 0xFFFF0000u);
+        v[q + 2] = __uint_as_float(w.y << 16), v[q + 3] = __uint_as_float(w.y & 0xFFFF0000u);
+      }
+    } else if constexpr (kVec) {
+      load_f(reinterpret_cast<const float*>(t), v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < kTokenNS; ++e) v[e] = n0 + e < p.N ? to_f32(t[e]) : 0.f;
+    }
+  };
+
+  const bool on = !p.lengths || p.lengths[b] > 0;
+  float a[kTokenNS], h[kTokenNS] = {}, Bv[kTokenNS] = {}, Cv[kTokenNS] = {}, u = 0.f, step = 0.f, z = 0.f;
+  const int64_t state = (b * p.D + c) * p.N + n0;
+  if (p.init) load_f(p.init + state, h);
+  if (on) {  // a sequence without a token keeps its state, and its inputs are not looked at
+    u = to_f32(static_cast<const V*>(p.u)[b * p.ub + c]);
+    step = to_f32(static_cast<const V*>(p.delta)[b * p.db + c]);
+    if (p.z) z = to_f32(static_cast<const V*>(p.z)[b * p.zb + c]);
+    load_v(static_cast<const V*>(p.Bm) + b * p.Bb + static_cast<int64_t>(g) * p.N + n0, Bv);
+    load_v(static_cast<const V*>(p.Cm) + b * p.Cb + static_cast<int64_t>(g) * p.N + n0, Cv);
+  }
+  load_f(p.A + static_cast<int64_t>(c) * p.N + n0, a);
+  const float skip = p.skip ? p.skip[c] : 0.f;
+  if (p.delta_bias) step += p.delta_bias[c];
+  if (p.softplus) step = softplus(step);
+  if (!on) step = 0.f;
+  const float du = step * u;
+  float sum = 0.f;
+#pragma unroll
+  for (int e = 0; e < kTokenNS; ++e) {
+    h[e] = fmaf(exp2_fast(step * (a[e] * kLog2e)), h[e], du * Bv[e]);
+    sum = fmaf(h[e], Cv[e], sum);
+  }
+#pragma unroll
+  for (int o = 1; o < T; o *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (!live) return;
+  if (part == 0) {
+    float y = fmaf(skip, u, sum);
+    if (p.z) y *= silu(z);
+    static_cast<V*>(p.y)[b * p.D + c] = from_f32<V>(on ? y : 0.f);
+  }
+  if (!p.final_state) return;
+  float* out = p.final_state + state;
+#pragma unroll
+  for (int q = 0; q < kTokenNS; q += 4) {
+    if constexpr (kVec) {
+      if (n0 + q < p.N) *reinterpret_cast<float4*>(out + q) = make_float4(h[q], h[q + 1], h[q + 2], h[q + 3]);
+    } else {
+#pragma unroll
+      for (int e = q; e < q + 4; ++e)
+        if (n0 + e < p.N) out[e] = h[e];
     }
   }
 }
@@ -540,9 +536,9 @@ cudaError_t launch_token(const ScanParams& p, int64_t batch, cudaStream_t stream
                    aligned_to(p.Bm, 4 * es) && aligned_to(p.Cm, 4 * es) &&
                    (batch == 1 || (p.Bb % 4 == 0 && p.Cb % 4 == 0));
   const dim3 grid(static_cast<unsigned>(ceil_div(static_cast<int64_t>(p.D) * T, kTokenThreads)),
-                  static_cast<unsigned>(ceil_div(batch, kRows)));
+                  static_cast<unsigned>(batch));
   return launch_k(vec ? scan_token_kernel<V, T, true> : scan_token_kernel<V, T, false>, grid, dim3(kTokenThreads), 0,
-                  stream, false, p, static_cast<int>(batch));
+                  stream, false, p);
 }
 
 template <typename V, int T, bool kVec>
@@ -576,12 +572,9 @@ cudaError_t launch_vec(const ScanParams& p, int64_t batch, cudaStream_t stream) 
 template <typename T>
 cudaError_t launch(const ScanParams& p, int64_t batch, cudaStream_t stream) {
   if (p.L == 1) {
-    switch (lanes_of(p.N)) {
-      case 2: return launch_token<T, 2>(p, batch, stream);
-      case 4: return launch_token<T, 4>(p, batch, stream);
-      case 8: return launch_token<T, 8>(p, batch, stream);
-      default: return launch_token<T, 16>(p, batch, stream);
-    }
+    if (p.N <= kTokenNS) return launch_token<T, 1>(p, batch, stream);
+    if (p.N <= 2 * kTokenNS) return launch_token<T, 2>(p, batch, stream);
+    return p.N <= 4 * kTokenNS ? launch_token<T, 4>(p, batch, stream) : launch_token<T, 8>(p, batch, stream);
   }
   // 16-byte loads where every vector of channels (of states) starts on 16 bytes and is whole
   const int64_t es = sizeof(T);
