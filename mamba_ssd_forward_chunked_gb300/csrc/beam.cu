@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kThreads) piece_kernel(SelectParams p) {
   __shared__ Key s_group[kMaxGroups], s_bound;
   __shared__ float s_red[2][kThreads / 32];
   __shared__ int s_count;
-  grid_dep_launch();
+  begin_kernel();
   const int piece = blockIdx.x, w = blockIdx.y, tid = threadIdx.x;
   const int64_t b = blockIdx.z, row = b * p.beams + w;
   const int v0 = piece * kThreads * 8 * kEights;
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(kThreads) merge_kernel(SelectParams p, int pie
   __shared__ Key s_keys[kMergeKeys], s_best[kMaxBeams], s_group[kMaxGroups], s_bound;
   __shared__ float s_lse[kMaxBeams], s_score[kMaxBeams];
   __shared__ int s_count;
-  grid_dep_wait();
+  begin_kernel();
   const int64_t b = blockIdx.x;
   const int tid = threadIdx.x, lane = tid % 32;
   const float2* sums = p.sums + b * p.beams * p.pieces;
@@ -413,7 +413,7 @@ cudaError_t launch_pieces(const SelectParams& p, bool vec, int64_t batch, cudaSt
     if (e != cudaSuccess) return e;
   }
   const dim3 grid(static_cast<unsigned>(p.pieces), static_cast<unsigned>(p.beams), static_cast<unsigned>(batch));
-  return launch_k(k, grid, dim3(kThreads), smem, stream, false, p);
+  return launch_k(k, grid, dim3(kThreads), smem, stream, true, p);
 }
 
 template <typename T>
@@ -439,6 +439,7 @@ struct ReorderParams {
 template <typename V, int kK>
 __global__ void __launch_bounds__(kThreads) reorder_kernel(ReorderParams p) {
   __shared__ int s_parent[kK];
+  begin_kernel();
   const int j = blockIdx.z;
   const int64_t b = blockIdx.y;
   const int64_t units = p.row_bytes[j] / static_cast<int64_t>(sizeof(V));
@@ -480,7 +481,7 @@ cudaError_t launch_reorder(const ReorderParams& all, int unit, int64_t batch, cu
                   static_cast<unsigned>(p.count));
   auto k = p.k <= 4 ? reorder_kernel<V, 4> : p.k <= 8 ? reorder_kernel<V, 8> : p.k <= 16 ? reorder_kernel<V, 16>
                                                                                          : reorder_kernel<V, 64>;
-  return launch_k(k, grid, dim3(kThreads), 0, stream, false, p);
+  return launch_k(k, grid, dim3(kThreads), 0, stream, true, p);
 }
 
 ssd_status check_select(const ssd_beam_select_args* a) {

@@ -67,6 +67,7 @@ struct Chans<__nv_bfloat16, 4> {
 template <typename T, int W, int kC>
 __global__ void __launch_bounds__(kThreads) conv_kernel(ConvParams p) {
   using Ch = Chans<T, kC>;
+  begin_kernel();
   const int groups = p.C / kC;
   const int64_t id = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
   const int64_t t0 = id / groups * p.run;
@@ -202,7 +203,7 @@ cudaError_t launch(ConvParams p, int width, int64_t batch, cudaStream_t stream) 
   const dim3 grid(static_cast<unsigned>(ceil_div(groups * runs, kThreads)), static_cast<unsigned>(batch));
   auto k = vec ? (width == 2 ? conv_kernel<T, 2, 4> : width == 3 ? conv_kernel<T, 3, 4> : conv_kernel<T, 4, 4>)
                : (width == 2 ? conv_kernel<T, 2, 1> : width == 3 ? conv_kernel<T, 3, 1> : conv_kernel<T, 4, 1>);
-  return launch_k(k, grid, dim3(kThreads), 0, stream, false, p);
+  return launch_k(k, grid, dim3(kThreads), 0, stream, true, p);
 }
 
 }  // namespace

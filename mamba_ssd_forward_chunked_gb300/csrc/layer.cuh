@@ -77,6 +77,16 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   return r;
 }
 
+// ------------------------------------------------------------------ order of launches
+// Every kernel of these operators is launched as a programmatic dependent of the work before it in the
+// stream and begins with this: it waits until that work has completed and its results are visible
+// (nothing is read or written before), and lets the next such kernel be set up meanwhile.  A decoding
+// loop's launches are a few us long, and this takes the set-up of each out of the chain.
+__device__ __forceinline__ void begin_kernel() {
+  grid_dep_wait();
+  grid_dep_launch();
+}
+
 // ------------------------------------------------------------------ host side
 inline bool aligned_to(const void* p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 inline size_t elem_size(int dtype) { return dtype == SSD_BF16 ? 2 : 4; }

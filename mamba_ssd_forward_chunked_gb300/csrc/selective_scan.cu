@@ -144,6 +144,8 @@ __global__ void __launch_bounds__(Shape<V, T>::kThreads + Shape<V, T>::kHelp) sc
   __shared__ __align__(16) float s_step[2][kTile][S::kStepRow];  // (d, d u) of each channel
   __shared__ __align__(16) float s_B[2][kTile][S::kN], s_C[2][kTile][S::kN];
   __shared__ __align__(16) float s_y[2][kTile][S::kYRow];
+  grid_dep_wait();
+  if constexpr (!kState) grid_dep_launch();  // (the first of two launches: at its end)
 
   const int group = blockIdx.x / p.tiles;
   const int in_group = (blockIdx.x % p.tiles) * S::kChannels;
@@ -310,7 +312,6 @@ __global__ void __launch_bounds__(Shape<V, T>::kThreads + Shape<V, T>::kHelp) sc
     }
   }
   if (!kState && p.segments > 1) {
-    grid_dep_wait();
 #pragma unroll 2
     for (int j = 0; j <= seg; ++j) {  // the state entering this segment
 #pragma unroll
@@ -431,6 +432,7 @@ constexpr int kTokenThreads = 128, kTokenNS = 8;
 
 template <typename V, int T, bool kVec>
 __global__ void __launch_bounds__(kTokenThreads, 8) scan_token_kernel(ScanParams p) {
+  begin_kernel();
   const int64_t id = static_cast<int64_t>(blockIdx.x) * kTokenThreads + threadIdx.x;
   const int part = static_cast<int>(id % T), n0 = kTokenNS * part;
   const bool live = id / T < p.D;
@@ -538,7 +540,7 @@ cudaError_t launch_token(const ScanParams& p, int64_t batch, cudaStream_t stream
   const dim3 grid(static_cast<unsigned>(ceil_div(static_cast<int64_t>(p.D) * T, kTokenThreads)),
                   static_cast<unsigned>(batch));
   return launch_k(vec ? scan_token_kernel<V, T, true> : scan_token_kernel<V, T, false>, grid, dim3(kTokenThreads), 0,
-                  stream, false, p);
+                  stream, true, p);
 }
 
 template <typename V, int T, bool kVec>
@@ -548,12 +550,12 @@ cudaError_t launch_lanes(ScanParams p, int64_t batch, cudaStream_t stream) {
   if (p.segments > 1) {
     const cudaError_t e = launch_k(scan_kernel<V, T, kVec, true>,
                                    dim3(blocks, static_cast<unsigned>(p.segments - 1), static_cast<unsigned>(batch)),
-                                   dim3(kThreads), 0, stream, false, p);
+                                   dim3(kThreads), 0, stream, true, p);
     if (e != cudaSuccess) return e;
   }
   return launch_k(scan_kernel<V, T, kVec, false>,
                   dim3(blocks, static_cast<unsigned>(p.segments), static_cast<unsigned>(batch)), dim3(kThreads),
-                  0, stream, p.segments > 1, p);
+                  0, stream, true, p);
 }
 
 // Lanes a channel's states are spread over.

@@ -43,6 +43,7 @@ __global__ void __launch_bounds__(kThreads) step_kernel(StepParams p) {
   constexpr int kEach = (kChannels + kThreads - 1) / kThreads;
   __shared__ __align__(16) float s_x[kRows], s_B[N], s_C[N];
   __shared__ float s_y[kRows];
+  begin_kernel();
   const int row0 = blockIdx.x % (kP / kRows) * kRows;
   const int h = blockIdx.x / (kP / kRows);
   const int64_t b = blockIdx.y;
@@ -170,7 +171,7 @@ cudaError_t launch(const StepParams& p, int64_t batch, cudaStream_t stream) {
   // a head a block, or quarters of heads while those leave the GPU room
   const bool few = batch * p.H < 2 * static_cast<int64_t>(layer_sm_count());
   const dim3 grid(static_cast<unsigned>(p.H * (few ? 4 : 1)), static_cast<unsigned>(batch));
-  return launch_k(few ? step_kernel<T, N, 16, W> : step_kernel<T, N, 64, W>, grid, dim3(kThreads), 0, stream, false, p);
+  return launch_k(few ? step_kernel<T, N, 16, W> : step_kernel<T, N, 64, W>, grid, dim3(kThreads), 0, stream, true, p);
 }
 
 template <typename T, int N>

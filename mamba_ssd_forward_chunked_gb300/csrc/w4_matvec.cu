@@ -60,14 +60,14 @@ __device__ __forceinline__ float cut(float v) { return __uint_as_float(__float_a
 constexpr int kColumnThreads = 256;
 __global__ void __launch_bounds__(kColumnThreads) columns_kernel(const __nv_bfloat16* x, int64_t x_token, int k, int row,
                                                                  __nv_bfloat16* out) {
-  grid_dep_launch();
+  begin_kernel();  // (the product's launch reads weights before it waits, when all work before this is done)
   const int at = blockIdx.x * kColumnThreads + threadIdx.x;
   const int64_t m = blockIdx.y;
   if (at < row) out[m * row + at] = at < k ? x[m * x_token + at] : __float2bfloat16_rn(0.f);
 }
 __global__ void __launch_bounds__(kColumnThreads) columns_kernel(const float* x, int64_t x_token, int k, int row,
                                                                  __nv_bfloat16* out) {
-  grid_dep_launch();
+  begin_kernel();  // (the product's launch reads weights before it waits, when all work before this is done)
   const int at = blockIdx.x * kColumnThreads + threadIdx.x;
   const int64_t m = blockIdx.y;
   if (at >= row) return;
@@ -92,6 +92,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32) w4_kernel(W4Params p) {
   const int r = lane / 4, c = lane % 4;
   const int m0 = blockIdx.y * kTokens;
   const int row = blockIdx.x * 16 + r;
+  if (kDirect) grid_dep_wait();
+  grid_dep_launch();
 
   const __nv_bfloat16* x[kCols];
 #pragma unroll
@@ -120,7 +122,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) w4_kernel(W4Params p) {
         q[u][h] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);  // zeros past the end
         if (kt < p.ktiles) q[u][h] = __ldg(packed + static_cast<int64_t>(kt) * 32);
       }
-    if (!kDirect && !waited) grid_dep_wait();
+    if (!kDirect && !waited) grid_dep_wait();  // for the launch in front
     waited = true;
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
@@ -201,7 +203,7 @@ cudaError_t launch_cols(const W4Params& p, cudaStream_t stream) {
   if (warps > units) warps = units;
   const size_t smem = static_cast<size_t>(warps) * kCols * 4 * 32 * sizeof(float);
   return launch_k(w4_kernel<T, kCols, kGroup, kDirect>, grid, dim3(static_cast<unsigned>(warps) * 32), smem, stream,
-                  !kDirect, p);
+                  true, p);
 }
 
 template <typename T, int kGroup, bool kDirect>
@@ -232,7 +234,7 @@ cudaError_t launch_columns(W4Params p, const ssd_w4_matvec_args* a, cudaStream_t
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a->workspace);
   void (*k)(const T*, int64_t, int, int, __nv_bfloat16*) = columns_kernel;
   const cudaError_t e =
-      launch_k(k, grid, dim3(kColumnThreads), 0, stream, false, static_cast<const T*>(a->x), a->x_token, p.k, row, out);
+      launch_k(k, grid, dim3(kColumnThreads), 0, stream, true, static_cast<const T*>(a->x), a->x_token, p.k, row, out);
   if (e != cudaSuccess) return e;
   p.x = out, p.x_token = row, p.k = row;
   return launch_group<T, false>(p, a->group, stream);
