@@ -178,6 +178,19 @@ def test_scan_extremes(ssd):
     check_scan(got, ref.scan(**s), F32)
 
 
+@pytest.mark.parametrize("L", [1, 37, 1000])
+def test_scan_steps_of_zero_keep_the_state(ssd, L):
+    g = gen(11)
+    s = scan_inputs(g, 2, L, 48, 16, 1, F32)
+    s["delta"] = torch.zeros_like(s["delta"])
+    init = normal(g, 2, 48, 16)
+    _, h = ssd.ssd_selective_scan(**s, init_state=init)
+    assert torch.equal(h, init)
+    s["delta"], s["u"], s["A"] = s["delta"] + 1.0, torch.zeros_like(s["u"]), torch.zeros_like(s["A"])  # and no decay
+    _, h = ssd.ssd_selective_scan(**s, init_state=init)
+    assert torch.equal(h, init)
+
+
 def test_scan_pieces_and_single_tokens(ssd):
     """A prompt, then tokens one at a time from its state, as the whole at once."""
     g = gen(9)
