@@ -19,14 +19,15 @@
 // has its first codes on their way before it waits for it.  A group's sum is
 // scaled in 32 bits when its columns are done.
 //
-// A block takes 16 rows; its warps take pairs of column tiles in turn and their
+// A block takes 16 or 32 rows; its warps take pairs of column tiles in turn and their
 // sums are joined in shared memory in a fixed order.
 #include "layer.cuh"
 
 namespace ssd {
 namespace {
 
-constexpr int kMaxWarps = 16;  // of a block
+// Warps of a block at most: two row tiles' sums take up to 255 registers a thread.
+constexpr int max_warps(int tiles) { return tiles == 1 ? 16 : 8; }
 
 struct W4Params {
   int64_t x_token, add_token;  // x_token: of the columns
@@ -83,15 +84,15 @@ __global__ void __launch_bounds__(kColumnThreads) columns_kernel(const float* x,
 // kCols: products' columns in blocks of 8.  kGroup: columns of weights a scale holds for.  kDirect: the
 // columns are x itself, read through the read-only cache path (5120 -> 2560, eight tokens: 5.6 us against
 // 7.1 without); columns that the launch in front writes are read by ordinary loads.
-template <typename T, int kCols, int kGroup, bool kDirect>
-__global__ void __launch_bounds__(kMaxWarps * 32) w4_kernel(W4Params p) {
+// kTiles: row tiles of a block, which share what is read of x.
+template <typename T, int kCols, int kTiles, int kGroup, bool kDirect>
+__global__ void __launch_bounds__(max_warps(kTiles) * 32) w4_kernel(W4Params p) {
   constexpr int kParts = sizeof(T) == 4 ? 3 : 1;        // columns of a token
   constexpr int kTokens = kCols * 8 / kParts;           // tokens of a block (fp32: 2 in 8 columns)
-  extern __shared__ float red[];                        // [warps][kCols][4][32]
+  extern __shared__ float red[];                        // [warps][kTiles][kCols][4][32]
   const int warps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int r = lane / 4, c = lane % 4;
   const int m0 = blockIdx.y * kTokens;
-  const int row = blockIdx.x * 16 + r;
   if (kDirect) grid_dep_wait();
   grid_dep_launch();
 
@@ -102,33 +103,42 @@ __global__ void __launch_bounds__(kMaxWarps * 32) w4_kernel(W4Params p) {
     const bool in = col / kParts < kTokens && m0 + col / kParts < p.M;
     x[t] = in ? p.x + (static_cast<int64_t>(m0) * kParts + col) * p.x_token : nullptr;
   }
-  // rows past the matrix hold codes of 8 and any scale will do
-  const float* s0 = p.scales + static_cast<int64_t>(row < p.n ? row : p.n - 1) * p.ngroups;
-  const float* s1 = p.scales + static_cast<int64_t>(row + 8 < p.n ? row + 8 : p.n - 1) * p.ngroups;
-  const uint4* packed = p.packed + static_cast<int64_t>(blockIdx.x) * p.ktiles * 32 + lane;
+  const float *s0[kTiles], *s1[kTiles];
+  const uint4* packed[kTiles];
+#pragma unroll
+  for (int j = 0; j < kTiles; ++j) {
+    // rows past the matrix hold codes of 8 and any scale will do; tiles past it repeat the last
+    const int tiles = (p.n + 15) / 16, tile = blockIdx.x * kTiles + j < tiles ? blockIdx.x * kTiles + j : tiles - 1;
+    const int row = tile * 16 + r;
+    s0[j] = p.scales + static_cast<int64_t>(row < p.n ? row : p.n - 1) * p.ngroups;
+    s1[j] = p.scales + static_cast<int64_t>(row + 8 < p.n ? row + 8 : p.n - 1) * p.ngroups;
+    packed[j] = p.packed + static_cast<int64_t>(tile) * p.ktiles * 32 + lane;
+  }
 
-  float total[kCols][4] = {};
-  // a warp's unit: two tiles, 128 columns; its next kAhead units' codes are on their way together
+  float total[kTiles][kCols][4] = {};
+  // a warp's unit: two column tiles, 128 columns; its next kAhead units' codes are on their way together
   constexpr int kAhead = kCols == 1 ? 4 : 2;
   const int units = (p.ktiles + 1) / 2;
   bool waited = false;
   for (int base = warp; base < units; base += kAhead * warps) {
-    uint4 q[kAhead][2];
+    uint4 q[kAhead][kTiles][2];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int kt = 2 * (base + u * warps) + h;
-        q[u][h] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);  // zeros past the end
-        if (kt < p.ktiles) q[u][h] = __ldg(packed + static_cast<int64_t>(kt) * 32);
-      }
+      for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int kt = 2 * (base + u * warps) + h;
+          q[u][j][h] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);  // zeros past the end
+          if (kt < p.ktiles) q[u][j][h] = __ldg(packed[j] + static_cast<int64_t>(kt) * 32);
+        }
     if (!kDirect && !waited) grid_dep_wait();  // for the launch in front
     waited = true;
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int unit = base + u * warps;
       if (unit >= units) break;
-      float sum[kCols][4] = {};
+      float sum[kTiles][kCols][4] = {};
 #pragma unroll
       for (int part4 = 0; part4 < 4; ++part4) {  // 32 columns: two products
         const int k0 = unit * 128 + part4 * 32 + c * 8;
@@ -142,47 +152,54 @@ __global__ void __launch_bounds__(kMaxWarps * 32) w4_kernel(W4Params p) {
           }
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint4& v = q[u][part4 / 2];
-          const uint32_t w = part4 % 2 ? (i ? v.w : v.z) : (i ? v.y : v.x);
-          const uint32_t a[4] = {codes<0>(w), codes<1>(w), codes<2>(w), codes<3>(w)};
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int t = 0; t < kCols; ++t) mma_bf16(sum[t], a, i ? xw[t].z : xw[t].x, i ? xw[t].w : xw[t].y);
-        }
+          for (int j = 0; j < kTiles; ++j) {
+            const uint4& v = q[u][j][part4 / 2];
+            const uint32_t w = part4 % 2 ? (i ? v.w : v.z) : (i ? v.y : v.x);
+            const uint32_t a[4] = {codes<0>(w), codes<1>(w), codes<2>(w), codes<3>(w)};
+#pragma unroll
+            for (int t = 0; t < kCols; ++t) mma_bf16(sum[j][t], a, i ? xw[t].z : xw[t].x, i ? xw[t].w : xw[t].y);
+          }
         constexpr int kParts32 = kGroup / 32;  // 32-column parts a scale holds for
         if (part4 % kParts32 == kParts32 - 1) {
           const int g = unit * (4 / kParts32) + part4 / kParts32;
-          const float f0 = g < p.ngroups ? __ldg(s0 + g) : 0.f, f1 = g < p.ngroups ? __ldg(s1 + g) : 0.f;
 #pragma unroll
-          for (int t = 0; t < kCols; ++t) {
-            total[t][0] = fmaf(f0, sum[t][0], total[t][0]);
-            total[t][1] = fmaf(f0, sum[t][1], total[t][1]);
-            total[t][2] = fmaf(f1, sum[t][2], total[t][2]);
-            total[t][3] = fmaf(f1, sum[t][3], total[t][3]);
+          for (int j = 0; j < kTiles; ++j) {
+            const float f0 = g < p.ngroups ? __ldg(s0[j] + g) : 0.f, f1 = g < p.ngroups ? __ldg(s1[j] + g) : 0.f;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sum[t][e] = 0.f;
+            for (int t = 0; t < kCols; ++t) {
+              total[j][t][0] = fmaf(f0, sum[j][t][0], total[j][t][0]);
+              total[j][t][1] = fmaf(f0, sum[j][t][1], total[j][t][1]);
+              total[j][t][2] = fmaf(f1, sum[j][t][2], total[j][t][2]);
+              total[j][t][3] = fmaf(f1, sum[j][t][3], total[j][t][3]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) sum[j][t][e] = 0.f;
+            }
           }
         }
       }
     }
   }
 #pragma unroll
-  for (int t = 0; t < kCols; ++t)
+  for (int j = 0; j < kTiles; ++j)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) red[((warp * kCols + t) * 4 + e) * 32 + lane] = total[t][e];
+    for (int t = 0; t < kCols; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) red[(((warp * kTiles + j) * kCols + t) * 4 + e) * 32 + lane] = total[j][t][e];
   __syncthreads();
-  // (row i, token j) of the block: entry e = 2 (i / 8) + col % 2 of lane 4 (i % 8) + col % 8 / 2
-  for (int at = threadIdx.x; at < 16 * kTokens; at += blockDim.x) {
-    const int i = at % 16, j = at / 16;
-    const int n = blockIdx.x * 16 + i, m = m0 + j;
+  // (row i, token m) of the block: entry e = 2 (i % 16 / 8) + col % 2 of lane 4 (i % 8) + col % 8 / 2
+  for (int at = threadIdx.x; at < 16 * kTiles * kTokens; at += blockDim.x) {
+    const int i = at % (16 * kTiles), token = at / (16 * kTiles);
+    const int n = blockIdx.x * 16 * kTiles + i, m = m0 + token;
     if (n >= p.n || m >= p.M) continue;
     float v = 0.f;
 #pragma unroll
     for (int q = 0; q < kParts; ++q) {
-      const int col = j * kParts + q;
-      const int e = 2 * (i / 8) + col % 2, from = 4 * (i % 8) + col % 8 / 2;
+      const int col = token * kParts + q;
+      const int e = 2 * (i % 16 / 8) + col % 2, from = 4 * (i % 8) + col % 8 / 2;
       float part_sum = 0.f;
-      for (int w = 0; w < warps; ++w) part_sum += red[((w * kCols + col / 8) * 4 + e) * 32 + from];
+      for (int w = 0; w < warps; ++w) part_sum += red[(((w * kTiles + i / 16) * kCols + col / 8) * 4 + e) * 32 + from];
       v += part_sum;
     }
     if (p.add) v += to_f32(static_cast<const T*>(p.add)[m * p.add_token + n]);
@@ -190,20 +207,32 @@ __global__ void __launch_bounds__(kMaxWarps * 32) w4_kernel(W4Params p) {
   }
 }
 
-template <typename T, int kCols, int kGroup, bool kDirect>
-cudaError_t launch_cols(const W4Params& p, cudaStream_t stream) {
+template <typename T, int kCols, int kTiles, int kGroup, bool kDirect>
+cudaError_t launch_tiles(const W4Params& p, cudaStream_t stream) {
   constexpr int kTokens = kCols * 8 / (sizeof(T) == 4 ? 3 : 1);
   const int64_t units = ceil_div(p.ktiles, 2);
-  const dim3 grid(static_cast<unsigned>(ceil_div(p.n, 16)), static_cast<unsigned>(ceil_div(p.M, kTokens)));
+  const dim3 grid(static_cast<unsigned>(ceil_div(p.n, 16 * kTiles)), static_cast<unsigned>(ceil_div(p.M, kTokens)));
   // as many warps as give every multiprocessor kWarps, at least 4, and no more than there are units
   // (2560 -> 10576, one token, with 16, 24, 32, 48 and 64: 6.3, 6.3, 6.0, 6.9 and 7.5 us)
   constexpr int64_t kWarps = 32;
   int64_t warps = ceil_div(kWarps * layer_sm_count(), static_cast<int64_t>(grid.x) * grid.y);
-  warps = warps < 4 ? 4 : warps > kMaxWarps ? kMaxWarps : warps;
+  warps = warps < 4 ? 4 : warps > max_warps(kTiles) ? max_warps(kTiles) : warps;
   if (warps > units) warps = units;
-  const size_t smem = static_cast<size_t>(warps) * kCols * 4 * 32 * sizeof(float);
-  return launch_k(w4_kernel<T, kCols, kGroup, kDirect>, grid, dim3(static_cast<unsigned>(warps) * 32), smem, stream,
+  const size_t smem = static_cast<size_t>(warps) * kTiles * kCols * 4 * 32 * sizeof(float);  // at most 48 KB
+  return launch_k(w4_kernel<T, kCols, kTiles, kGroup, kDirect>, grid, dim3(static_cast<unsigned>(warps) * 32), smem, stream,
                   true, p);
+}
+
+// From two blocks of columns on, x is more bytes than the codes for every row tile: two tiles share it
+// where there are rows enough to fill the GPU all the same (8001 -> 16001, 16 fp32 tokens 156 -> 90 us,
+// 16 bf16 tokens 47 -> 44).
+template <typename T, int kCols, int kGroup, bool kDirect>
+cudaError_t launch_cols(const W4Params& p, cudaStream_t stream) {
+  if constexpr (kCols > 1) {
+    if (ceil_div(p.n, 32) >= 2 * static_cast<int64_t>(layer_sm_count()))
+      return launch_tiles<T, kCols, 2, kGroup, kDirect>(p, stream);
+  }
+  return launch_tiles<T, kCols, 1, kGroup, kDirect>(p, stream);
 }
 
 template <typename T, int kGroup, bool kDirect>

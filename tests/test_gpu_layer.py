@@ -320,7 +320,8 @@ def test_step_cache_past_32_bit_offsets(ssd):
 @both_types
 @pytest.mark.parametrize("group", [32, 64, 128])
 @pytest.mark.parametrize("M,n,k", [(1, 16, 64), (1, 1, 1), (2, 50, 200), (3, 33, 129), (8, 48, 320), (9, 20, 65),
-                                   (17, 130, 1000), (1, 700, 2048), (16, 64, 640), (5, 17, 63), (40, 16, 96)])
+                                   (17, 130, 1000), (1, 700, 2048), (16, 64, 640), (5, 17, 63), (40, 16, 96),
+                                   (9, 9731, 257), (16, 9760, 128)])  # two row tiles a block
 def test_w4(ssd, dtype, group, M, n, k):
     g = gen(M * 7 + n + k + group)
     codes = torch.randint(0, 16, (n, k), generator=g)
