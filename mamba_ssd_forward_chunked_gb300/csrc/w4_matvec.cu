@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(kColumnThreads) columns_kernel(const float* x,
 // 7.1 without); columns that the launch in front writes are read by ordinary loads.
 // kTiles: row tiles of a block, which share what is read of x.
 template <typename T, int kCols, int kTiles, int kGroup, bool kDirect>
-__global__ void __launch_bounds__(max_warps(kTiles) * 32) w4_kernel(W4Params p) {
+__global__ void __launch_bounds__(max_warps(kTiles) * 32, kCols == 1 ? 2 : 1) w4_kernel(W4Params p) {
   constexpr int kParts = sizeof(T) == 4 ? 3 : 1;        // columns of a token
   constexpr int kTokens = kCols * 8 / kParts;           // tokens of a block (fp32: 2 in 8 columns)
   extern __shared__ float red[];                        // [warps][kTiles][kCols][4][32]
