@@ -510,6 +510,49 @@ def test_reorder_other_counts_and_bad_parents(ssd):
     assert ssd.ssd_beam_reorder([], par) == []
 
 
+# ------------------------------------------------------------------ offsets past 32 bits
+
+def far_apart(g, rows, C, dtype, L=None):
+    """[rows, L, C] (or [rows, C]) whose rows lie 2^31 + 64 elements apart."""
+    gap = 2 ** 31 + 64
+    shape, stride = ((rows, L, C), (gap, C + 8, 1)) if L else ((rows, C), (gap, 1))
+    t = torch.empty(gap * (rows - 1) + (L or 1) * (C + 8), dtype=dtype, device="cuda").as_strided(shape, stride)
+    return t.copy_(normal(g, *shape, dtype=dtype))
+
+
+def test_inputs_far_apart(ssd):
+    g = gen(41)
+    u = far_apart(g, 2, 40, BF16, L=11)
+    weight = normal(g, 40, 4)
+    y, e, _ = ref.conv(u, weight, None)
+    ref.check("conv", ssd.ssd_conv_fwd(u, weight), y, ref.store(y, e, BF16))
+    s = scan_inputs(g, 2, 11, 40, 16, 1, BF16)
+    s["u"] = u
+    check_scan(ssd.ssd_selective_scan(**s, delta_softplus=True), ref.scan(**s, use_softplus=True), BF16)
+    one = {k: v if k == "A" else v[:, :1] for k, v in s.items()}
+    check_scan(ssd.ssd_selective_scan(**one, delta_softplus=True), ref.scan(**one, use_softplus=True), BF16)
+    del u, s, one
+    x = far_apart(g, 2, 96, BF16)
+    codes = torch.randint(0, 16, (40, 96), generator=g)
+    scales = torch.rand(40, 3, generator=g).cuda()
+    y, e = ref.w4(x, codes, scales, 32)
+    ref.check("w4", ssd.ssd_w4_matvec(x, ssd.w4_pack(codes).cuda(), scales, 32), y, ref.store(y, e, BF16))
+    del x
+    logits = far_apart(g, 2, 300, BF16)[None]
+    scores = normal(g, 1, 2)
+    same_choice(ssd.ssd_beam_select(logits, scores, 5), ref.beam(logits, scores, 5))
+
+
+def test_reorder_of_rows_past_32_bits(ssd):
+    row = 2 ** 31 + 48
+    t = torch.empty(2, row, dtype=torch.uint8, device="cuda")
+    t[0], t[1] = 3, 7
+    t[0, -1], t[1, -1], t[0, 5] = 11, 13, 17
+    ssd.ssd_beam_reorder([t], ints(1, 0).view(1, 2))
+    assert int(t[0, -1]) == 13 and int(t[1, -1]) == 11 and int(t[1, 5]) == 17 and int(t[0, 5]) == 7
+    assert int(t[0, :-1].min()) == 7 == int(t[0, :-1].max())
+
+
 # ------------------------------------------------------------------ streams, repeats, refusals
 
 def test_other_stream_and_repeats(ssd):
