@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kThreads) piece_kernel(SelectParams p) {
   auto at = [&](int g, int i) { return v0 + g * (8 * kThreads) + (kVec ? 8 * tid + i : kThreads * i + tid); };
   const T* src = static_cast<const T*>(p.logits) + b * p.logits_batch + w * p.logits_beam;
   const bool done = p.finished && p.finished[row];
-  const bool plain = kVec && !done && p.vocab - v0 >= kThreads * 8 * kEights;
+  const bool whole = kVec && p.vocab - v0 >= kThreads * 8 * kEights, plain = whole && !done;
   auto read = [&](int g, float (&v)[8]) {
     if (plain) {
       Eight<T> x;
@@ -186,10 +186,12 @@ __global__ void __launch_bounds__(kThreads) piece_kernel(SelectParams p) {
     unpack2(sum2, sum, hi);
     sum += hi;
   };
-  if (plain) {
-    Eight<T> x[kEights];
+  Eight<T> x[kEights];
+  if (whole) {  // (a finished beam's logits too: whether it is finished is not known yet)
 #pragma unroll
     for (int g = 0; g < kEights; ++g) x[g].load(src + at(g, 0));
+  }
+  if (plain) {
 #pragma unroll
     for (int g = 0; g < kEights; ++g) {
       float v[8];

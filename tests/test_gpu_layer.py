@@ -579,6 +579,47 @@ def test_other_stream_and_repeats(ssd):
         assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+def test_decoding_step_in_a_cuda_graph(ssd):
+    """One token's calls captured once and replayed on other inputs give what
+    the calls give outside (states, rings and choices bit for bit)."""
+    g = gen(51)
+    B, W, H, N, V = 2, 3, 4, 64, 500
+    C, rows = H * 64 + 2 * N, B * W
+    u, dt, pos = normal(g, rows, C, dtype=BF16), torch.rand(rows, H, generator=g).cuda(), ints(*range(rows))
+    A, D, weight = -torch.rand(H, generator=g).cuda(), normal(g, H), normal(g, C, 4)
+    state, ring = normal(g, rows, H, 64, N), normal(g, rows, 4, C, dtype=BF16)
+    packed = ssd.w4_pack(torch.randint(0, 16, (V, H * 64), generator=g)).cuda()
+    scales, scores = torch.rand(V, 4, generator=g).cuda() * 0.1, normal(g, B, W)
+
+    def token():
+        y = ssd.ssd_step(u, dt, A, D, weight, None, state, ring, pos)
+        logits = ssd.ssd_w4_matvec(y.view(rows, -1), packed, scales, 64)
+        best, parents, tokens = ssd.ssd_beam_select(logits.view(B, W, V), scores, W)
+        ssd.ssd_beam_reorder([state, ring], parents)
+        return best, parents, tokens
+    keep = [t.clone() for t in (state, ring)]
+    token()
+    for t, k in zip((state, ring), keep):
+        t.copy_(k)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(graph, stream=side):
+            out = token()
+    torch.cuda.current_stream().wait_stream(side)
+    for seed in (1, 2):
+        u.copy_(normal(gen(seed), rows, C, dtype=BF16))
+        for t, k in zip((state, ring), keep):
+            t.copy_(k)
+        want = [t.clone() for t in token()] + [state.clone(), ring.clone()]
+        for t, k in zip((state, ring), keep):
+            t.copy_(k)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip([*out, state, ring], want))
+
+
 def test_refusals(ssd):
     z = lambda *shape, dtype=F32: torch.zeros(*shape, dtype=dtype, device="cuda")  # noqa: E731
     E = ssd.SSDError
