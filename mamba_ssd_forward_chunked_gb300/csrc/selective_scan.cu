@@ -524,18 +524,19 @@ __global__ void __launch_bounds__(kTokenThreads, 8) scan_token_kernel(ScanParams
 }
 
 // Segments a sequence is cut into: enough recurrence warps for kFill on every multiprocessor, but no
-// segment below kLeast tokens.  Measured: 16384 x 2048 fp32 with 8, 12, 16 and 24 warps 362, 370,
-// 364 and 381 us; 2 x 2048 x 5120 whole 171 us, in segments (24 warps) 205.
-constexpr int64_t kFill = 16, kLeast = 128;
+// segment below kLeast tokens and no more than kMost (a segment joins all states before it).  Measured:
+// 16384 x 2048 fp32 in 9, 11, 14, 16, 19 and 23 segments 339, 394, 332, 369, 331 and 349 us (19 taken);
+// 2048 x 2048 bf16 in 4 and 16: 84 and 57 us.  Fewer than five pay more for the first launch than they
+// gain: 513 x 5120 fp32 in four and whole 39 and 36 us, 2 x 2048 x 5120 bf16 in three and whole 205 and
+// 165 us.
+constexpr int64_t kFill = 16, kLeast = 128, kMost = 64;
 
 int segment_count(int64_t batch, int64_t L, int64_t blocks, int warps) {
   const int64_t all = batch * blocks * warps;
-  const int64_t want = kFill * layer_sm_count();
-  if (4 * all > want) return 1;
-  int64_t s = want / all;
-  const int64_t most = L / kLeast;
-  if (s > most) s = most;
-  return s < 3 ? 1 : static_cast<int>(s);  // two segments pay for one in the first launch and gain nothing
+  int64_t s = kFill * layer_sm_count() / all;
+  s = s < L / kLeast ? s : L / kLeast;
+  s = s < kMost ? s : kMost;
+  return s < 5 ? 1 : static_cast<int>(s);
 }
 
 template <typename V, int T>
