@@ -5,7 +5,9 @@
 // is one pass over memory, and HBM bounds it.  A thread takes four channels (8 or
 // 16 bytes) and walks down a run of tokens with the last W - 1 inputs in
 // registers; the next eight tokens are on their way while eight are computed.
-// A run reads the W - 1 tokens before it again (from L2, mostly).
+// A run reads the W - 1 tokens before it again (from L2, mostly).  4 x 4096 x 5376
+// bf16, out of rows of 10576: 63 us, 5.6 TB/s (a contiguous copy of as many bytes
+// 55 us); 3 x 1021 x 2304 fp32 12 us.
 //
 // The ring may be read and updated in place: the thread that owns a channel's
 // first run is the only one that reads the ring, and it writes it too, after

@@ -16,8 +16,9 @@
 //    through softplus once and kept with d u in shared memory, and the outputs
 //    of the tile before (skip term, gate, 16-byte stores).
 // With both sides' work in one warp a block's latency, not its work, set the
-// pace (2 x 2048 x 5120, 16 states, bf16: 304 us); one warp for the memory side
-// 194, two 171.
+// pace (2 x 2048 x 5120, 16 states, bf16: 304 us); with one warp for the memory
+// side 194, with two 165.  A multiprocessor takes about 30 cycles a token of a
+// block, of which its instructions fill 24 (at two issue slots for an f32x2).
 //
 // Segments.  With few channels a sequence is cut into segments that run side by
 // side: a first launch computes every segment's state from zero and its sum of
@@ -175,7 +176,7 @@ __global__ void __launch_bounds__(Shape<V, T>::kThreads + Shape<V, T>::kHelp) sc
     const V* z = static_cast<const V*>(p.z) + b * p.zb + c0;
     const V* Bm = static_cast<const V*>(p.Bm) + b * p.Bb + static_cast<int64_t>(group) * p.N;
     const V* Cm = static_cast<const V*>(p.Cm) + b * p.Cb + static_cast<int64_t>(group) * p.N;
-    // a thread's vectors all lie in the same eight channels (kHelp is a multiple of kCols)
+    // a thread's vectors all lie in the same channels (kHelp is a multiple of kCols)
     const int col0 = tid % S::kCols * kE;
     float bias[kE], skip[kE];
 #pragma unroll

@@ -7,11 +7,13 @@
 // its rows where there are few heads in the batch.  The convolution's inputs and
 // then the block's states (16 bytes a load, up to 16 loads a thread) are all on
 // their way before it forms the head's x and its group's B and C by itself, so
-// that the whole layer step is one launch: B
-// and C are formed again by every head of a group, a few hundred multiplications
-// against the head's 2 x 32 KB of state.  The ring has one slot more than the
-// taps reach back, so the slot that takes the new token is read by nobody in
-// this launch, and B's and C's are written by one block of the group alone.
+// that the whole layer step is one launch: B and C are formed again by every
+// head of a group, a few hundred multiplications against the head's 2 x 32 KB of
+// state.  The ring has one slot more than the taps reach back, so the slot that
+// takes the new token is read by nobody in this launch, and B's and C's are
+// written by one block of the group alone.  80 heads of 64 x 128 states: 256
+// sequences 202 us, 6.7 TB/s (states asked for before the convolution's inputs:
+// 292 us); one sequence 3.3 us.
 #include "layer.cuh"
 
 namespace ssd {

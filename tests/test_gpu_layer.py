@@ -129,6 +129,7 @@ def check_scan(got, want, dtype):
 @pytest.mark.parametrize("B,L,C,N,G", [
     (1, 1, 8, 16, 1), (3, 1, 130, 16, 1), (2, 5, 33, 1, 1), (1, 70, 96, 16, 3), (2, 129, 40, 13, 1), (1, 64, 64, 8, 2),
     (1, 33, 24, 32, 1), (1, 40, 17, 64, 1), (1, 700, 48, 16, 1), (2, 517, 8, 5, 1), (1, 260, 36, 33, 2),
+    (1, 9001, 16, 16, 1), (1, 1300, 8, 40, 1),  # in 64 segments, the last of them empty; in ten
 ])
 def test_scan(ssd, dtype, B, L, C, N, G):
     g = gen(B + 10 * L + C + N)
