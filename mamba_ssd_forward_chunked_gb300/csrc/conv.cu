@@ -6,8 +6,8 @@
 // 16 bytes) and walks down a run of tokens with the last W - 1 inputs in
 // registers; the next eight tokens are on their way while eight are computed.
 // A run reads the W - 1 tokens before it again (from L2, mostly).  4 x 4096 x 5376
-// bf16, out of rows of 10576: 63 us, 5.6 TB/s (a contiguous copy of as many bytes
-// 55 us); 3 x 1021 x 2304 fp32 12 us.
+// bf16, out of rows of 10576: 59 us, 6.0 TB/s (a contiguous copy of as many bytes
+// 55 us); 3 x 1021 x 2304 fp32 10 us.
 //
 // The ring may be read and updated in place: the thread that owns a channel's
 // first run is the only one that reads the ring, and it writes it too, after
@@ -196,11 +196,16 @@ cudaError_t launch(ConvParams p, int width, int64_t batch, cudaStream_t stream) 
              aligned_to(p.ring, bytes) && aligned_to(p.new_ring, bytes);
   for (int i = 0; i < 3; ++i) vec = vec && p.begin[i] % 4 == 0 && aligned_to(p.out[i], bytes);
   const int64_t groups = vec ? p.C / 4 : p.C;
-  // Long runs re-read least, and the longest that still gives 1024 threads a multiprocessor is taken,
-  // or runs of 8.  4 x 4096 x 5376 bf16 with runs of 16, 32, 64 and 128: 84, 69, 65 and 63 us.
+  // The shortest runs whose blocks are all resident at once (five a multiprocessor in bf16, four in
+  // fp32, by their registers): every thread starts at once and none waits for a second wave.  Up to
+  // kMost tokens; above that blocks come in waves.  Runs of 8, 16, 24 and 32 for 3 x 1021 x 2304 fp32
+  // (24 fit): 12.2, 11.4, 9.6 and 10.9 us; 4 x 4096 x 5376 bf16 with runs of 64, 128 and 240 (which fit):
+  // 65, 63 and 59 us; 2 x 8191 x 4352 fp32 with 128 and 472: 87 and 92 us.
+  constexpr bool kHalf = sizeof(T) == 2;
+  constexpr int kMost = kHalf ? 1024 : 128;
+  const int64_t resident = (kHalf ? 5 : 4) * static_cast<int64_t>(layer_sm_count());
   p.run = kStep;
-  for (int run : {32, 64, 128})
-    if (batch * groups * ceil_div(p.L, run) >= 1024 * static_cast<int64_t>(layer_sm_count())) p.run = run;
+  while (p.run < kMost && ceil_div(groups * ceil_div(p.L, p.run), kThreads) * batch > resident) p.run += kStep;
   const int64_t runs = p.L > 0 ? ceil_div(p.L, p.run) : 1;
   const dim3 grid(static_cast<unsigned>(ceil_div(groups * runs, kThreads)), static_cast<unsigned>(batch));
   auto k = vec ? (width == 2 ? conv_kernel<T, 2, 4> : width == 3 ? conv_kernel<T, 3, 4> : conv_kernel<T, 4, 4>)
