@@ -25,8 +25,6 @@
 // Reordering moves bytes: a thread owns 16 bytes' position in all rows of a
 // request, reads them all, then writes, so that it may work in place.  256 rows
 // of 268 KB: 14 us.
-#include <cfloat>
-
 #include "layer.cuh"
 
 namespace ssd {
