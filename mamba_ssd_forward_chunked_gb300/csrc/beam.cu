@@ -289,6 +289,15 @@ __global__ void __launch_bounds__(kThreads) merge_kernel(SelectParams p, int pie
   const int64_t b = blockIdx.x;
   const int tid = threadIdx.x, lane = tid % 32;
   const float2* sums = p.sums + b * p.beams * p.pieces;
+  const int per = p.pieces * p.keep, all = p.beams * per;
+  const Key* keys = p.keys + b * all;
+  // As a rule a thread's candidates fit registers: they are on their way before the sums are joined,
+  // and read once.
+  constexpr int kOwn = 4;
+  const bool few = all <= kOwn * kThreads;
+  Key own[kOwn];
+#pragma unroll
+  for (int q = 0; q < kOwn; ++q) own[q] = few && tid + q * kThreads < all ? keys[tid + q * kThreads] : 0;
   for (int w = tid / 32; w < p.beams; w += kThreads / 32) {  // a warp a beam
     float top = -INFINITY, sum = 0.f;
     for (int i = lane; i < p.pieces; i += 32) top = fmaxf(top, sums[w * p.pieces + i].x);
@@ -308,27 +317,32 @@ __global__ void __launch_bounds__(kThreads) merge_kernel(SelectParams p, int pie
   if (tid == 0) s_count = 0;
   __syncthreads();
 
-  const int per = p.pieces * p.keep, all = p.beams * per;
-  const Key* keys = p.keys + b * all;
-  auto candidate = [&](int i) -> Key {
-    const Key key = keys[i];
+  // of a piece's key (logit, index in the row): the candidate's (score, index in the request)
+  auto candidate = [&](int i, Key key) -> Key {
     if (!key) return 0;
     const int w = i / per;
     return key_of(score_of(s_score[w], key_value(key), s_lse[w]), static_cast<uint32_t>(w) * p.vocab + key_index(key));
   };
-  Key mine = 0;
-  for (int i = tid; i < all; i += kThreads) {
-    const Key key = candidate(i);
+  Key mine = 0, scored[kOwn];
+#pragma unroll
+  for (int q = 0; q < kOwn; ++q) {
+    scored[q] = candidate(tid + q * kThreads, own[q]);
+    mine = scored[q] > mine ? scored[q] : mine;
+  }
+  for (int i = tid; !few && i < all; i += kThreads) {
+    const Key key = candidate(i, keys[i]);
     mine = key > mine ? key : mine;
   }
   const Key bound = bound_of(mine, p.k, s_group, s_bound);
-  for (int i = tid; i < all; i += kThreads) {
-    const Key key = candidate(i);
+  auto collect = [&](Key key) {
     if (key && key >= bound) {
       const int n = atomicAdd(&s_count, 1);
       if (n < kMergeKeys) s_keys[n] = key;
     }
-  }
+  };
+#pragma unroll
+  for (int q = 0; q < kOwn; ++q) collect(scored[q]);
+  for (int i = tid; !few && i < all; i += kThreads) collect(candidate(i, keys[i]));
   __syncthreads();
   if (s_count <= kMergeKeys) {
     rank_keys(s_keys, s_count, p.k, s_best);
@@ -339,7 +353,7 @@ __global__ void __launch_bounds__(kThreads) merge_kernel(SelectParams p, int pie
     for (int i = 0; i < p.k; ++i) {
       mine = 0;
       for (int j = tid; j < all; j += kThreads) {
-        const Key key = candidate(j);
+        const Key key = candidate(j, keys[j]);
         if (key < last && key > mine) mine = key;
       }
       last = bound_of(mine, 1, s_group, s_bound);
@@ -351,14 +365,17 @@ __global__ void __launch_bounds__(kThreads) merge_kernel(SelectParams p, int pie
   // equal scores below a piece's list
   const uint32_t worst = static_cast<uint32_t>(s_best[p.k - 1] >> 32);
   bool hidden = false;
-  for (int i = tid; i < p.beams * p.pieces; i += kThreads) {
-    const Key key = keys[static_cast<int64_t>(i) * p.keep + p.k];
-    const int w = i / p.pieces;
+  auto hides = [&](int w, Key key) {  // a piece's last key: whether candidates at the k-th score may lie behind it
     // (behind a last key of -infinity there is nothing but -infinity at higher indexes)
-    if (key && key_value(key) > -INFINITY &&
-        order_of(score_of(s_score[w], key_value(key), s_lse[w])) == worst)
-      hidden = true;
+    return key && key_value(key) > -INFINITY && order_of(score_of(s_score[w], key_value(key), s_lse[w])) == worst;
+  };
+#pragma unroll
+  for (int q = 0; q < kOwn; ++q) {
+    const int i = tid + q * kThreads;
+    if (own[q] && i % p.keep == p.k && hides(i / per, own[q])) hidden = true;
   }
+  for (int i = tid; !few && i < p.beams * p.pieces; i += kThreads)
+    if (hides(i / p.pieces, keys[static_cast<int64_t>(i) * p.keep + p.k])) hidden = true;
   if (__syncthreads_or(hidden)) {
     int found = 0;  // the candidates above the k-th score stay; those at it are gathered by rising index
     while (static_cast<uint32_t>(s_best[found] >> 32) != worst) ++found;
