@@ -17,8 +17,14 @@
 //    of the tile before (skip term, gate, 16-byte stores).
 // With both sides' work in one warp a block's latency, not its work, set the
 // pace (2 x 2048 x 5120, 16 states, bf16: 304 us); with one warp for the memory
-// side 194, with two 165.  A multiprocessor takes about 30 cycles a token of a
-// block, of which its instructions fill 24 (at two issue slots for an f32x2).
+// side 194, with two 165.  Four blocks on a multiprocessor take about 31 cycles
+// a token each, of which their instructions fill 24 (at two issue slots for an
+// f32x2); their recurrence warps lie on its four schedulers then.  With a fifth
+// two share one (2 x 2048 tokens, 16 states, bf16, 1, 2, 3, 4 and 5 blocks of 16
+// channels a multiprocessor: 88, 101, 115, 124 and 166 us), and a grid that
+// starts while the one in front still runs is spread as unevenly as that.  So
+// it starts alone, and numbers of blocks that do not divide evenly are cut in
+// runs that do (scan_slots_kernel; 2 x 2048 x 5120: 166 -> 142 us).
 //
 // Segments.  With few channels a sequence is cut into segments that run side by
 // side: a first launch computes every segment's state from zero and its sum of
@@ -47,6 +53,9 @@ struct ScanParams {
   int64_t segment;   // tokens a segment, a multiple of kTile
   float* seg_state;  // [batch][segments][D][N]: init_state, then each segment's state from zero
   float* seg_sum;    // [batch][segments][D]: each segment's sum of steps
+  int64_t quota;     // slots: tiles of tokens a block takes, no fewer than a sequence has
+  uint64_t* handed;  // slots: states at a cut, [batch][G * tiles][states of a lane, two each][lane]
+  int* ready;        // slots: [batch][G * tiles], 0, then kReady or kTaken
 };
 
 // 16 bytes of consecutive values as they lie in memory.
@@ -135,6 +144,9 @@ struct Shape {
   static constexpr int kChannels = T == 2 ? 32 : 16;       // of a block
   static constexpr int kThreads = kChannels / 2 * T;       // of the recurrence
   static constexpr int kHelp = T == 16 ? 128 : 64;         // of the memory side
+  // blocks that a multiprocessor's registers have to hold: of the outputs' launch, of the states'
+  static constexpr int kBlocks[2] = {T == 2 ? (kE == 4 ? 2 : 4) : T == 4 ? (kE == 4 ? 4 : 5) : T == 8 ? (kE == 4 ? 3 : 4) : 2,
+                                     T == 2 ? 7 : T == 4 ? 8 : T == 8 ? 6 : 3};
   static constexpr int kCols = kChannels / kE;             // vectors in a row of channels
   static constexpr int kIO = kTile * kCols;                // and in a tile
   static constexpr int kIOEach = (kIO + kHelp - 1) / kHelp;
@@ -144,28 +156,32 @@ struct Shape {
   static constexpr int kStepRow = 2 * kChannels + 4, kYRow = kChannels + 8;
 };
 
+// What a block walks along: tokens [begin, stop) of a sequence.
+struct Walk {
+  int64_t begin, stop;
+  int seg;               // the segment, 0 of 1 elsewhere
+  bool last;             // the sequence's last tokens: the state is the final one
+  const uint64_t* from;  // a state left by another block to start from, or null
+  uint64_t* to;          // where the state is left for another block, or null
+};
+
 // kState: only the segment's state from zero and its sum of steps (the first of two launches).
 template <typename V, int T, bool kVec, bool kState>
-__global__ void __launch_bounds__(Shape<V, T>::kThreads + Shape<V, T>::kHelp) scan_kernel(ScanParams p) {
+__device__ __forceinline__ void walk(const ScanParams& p, int block, int64_t b, const Walk& w) {
   using S = Shape<V, T>;
   constexpr int kE = S::kE;
   __shared__ __align__(16) float s_step[2][kTile][S::kStepRow];  // (d, d u) of each channel
   __shared__ __align__(16) float s_B[2][kTile][S::kN], s_C[2][kTile][S::kN];
   __shared__ __align__(16) float s_y[2][kTile][S::kYRow];
-  grid_dep_wait();
-  if constexpr (!kState) grid_dep_launch();  // (the first of two launches: at its end)
-
-  const int group = blockIdx.x / p.tiles;
-  const int in_group = (blockIdx.x % p.tiles) * S::kChannels;
+  const int group = block / p.tiles;
+  const int in_group = (block % p.tiles) * S::kChannels;
   const int c0 = group * p.per + in_group;
   const int nc = p.per - in_group < S::kChannels ? p.per - in_group : S::kChannels;
-  const int64_t b = blockIdx.z;
-  const int seg = blockIdx.y;
+  const int seg = w.seg;
   int64_t len = p.L;
   if (p.lengths) len = p.lengths[b] < 0 ? 0 : p.lengths[b] < p.L ? p.lengths[b] : p.L;
-  const int64_t begin = seg * p.segment;
-  const int64_t stop = seg + 1 < p.segments && begin + p.segment < p.L ? begin + p.segment : p.L;  // of the outputs
-  const int64_t end = len < stop ? len : stop;                                 // of the recurrence
+  const int64_t begin = w.begin, stop = w.stop;  // of the outputs
+  const int64_t end = len < stop ? len : stop;   // of the recurrence
   const int tiles = end > begin ? static_cast<int>((end - begin + kTile - 1) / kTile) : 0;
 
   if (threadIdx.x >= S::kThreads) {
@@ -278,7 +294,7 @@ __global__ void __launch_bounds__(Shape<V, T>::kThreads + Shape<V, T>::kHelp) sc
 #pragma unroll
         for (int j = 0; j < S::kIOEach; ++j) u2[j] = u1[j], z2[j] = z1[j], u1[j] = r.u[j], z1[j] = r.z[j];
       }
-      if (i + 1 < tiles) fetch(t0 + kTile);
+      fetch(t0 + kTile);  // (past the end: no loads)
       __syncthreads();
     }
     if constexpr (!kState) {
@@ -290,7 +306,7 @@ __global__ void __launch_bounds__(Shape<V, T>::kThreads + Shape<V, T>::kHelp) sc
           if (col0 + i < nc) y[i] = from_f32<V>(0.f);
       }
     }
-    return;
+    return;  // (of this walk)
   }
 
   // ---- the recurrence: two channels a lane, a share of their states ----
@@ -309,14 +325,14 @@ __global__ void __launch_bounds__(Shape<V, T>::kThreads + Shape<V, T>::kHelp) sc
         const int n = n0 + 2 * i + e;
         const bool in = ch + k < nc && n < p.N;
         a[e] = in ? p.A[static_cast<int64_t>(c0 + ch + k) * p.N + n] * kLog2e : 0.f;
-        h[e] = in && p.init && p.segments == 1 ? p.init[state_row + n] : 0.f;
+        h[e] = in && p.init && p.segments == 1 && !w.from ? p.init[state_row + n] : 0.f;
         // final_state may be init_state, and the last segment's block may end before another reads
         // its state: in segments all read a copy
         if (kState && seg == 0 && in)
           p.seg_state[(b * p.segments * p.D + c0 + ch + k) * p.N + n] = p.init ? p.init[state_row + n] : 0.f;
       }
       a2[k][i] = pack2(a[0], a[1]);
-      h2[k][i] = pack2(h[0], h[1]);
+      h2[k][i] = w.from ? __ldcg(w.from + (k * kNS / 2 + i) * S::kThreads + tid) : pack2(h[0], h[1]);
     }
   }
   if (!kState && p.segments > 1) {
@@ -417,7 +433,12 @@ __global__ void __launch_bounds__(Shape<V, T>::kThreads + Shape<V, T>::kHelp) sc
         if (n0 + 2 * i + 1 < p.N) p.seg_state[at * p.N + n0 + 2 * i + 1] = hi;
       }
     }
-  } else if (p.final_state && seg + 1 == p.segments) {
+  } else if (w.to) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int i = 0; i < kNS / 2; ++i) w.to[(k * kNS / 2 + i) * S::kThreads + tid] = h2[k][i];
+  } else if (p.final_state && w.last) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       if (ch + k >= nc) continue;
@@ -431,6 +452,85 @@ __global__ void __launch_bounds__(Shape<V, T>::kThreads + Shape<V, T>::kHelp) sc
       }
     }
   }
+}
+
+// A grid of (blocks, segments, batch): every block takes a segment, the whole sequence if there is one.
+template <typename V, int T, bool kVec, bool kState>
+__global__ void __launch_bounds__(Shape<V, T>::kThreads + Shape<V, T>::kHelp, Shape<V, T>::kBlocks[kState]) scan_kernel(ScanParams p) {
+  grid_dep_wait();
+  if constexpr (!kState) grid_dep_launch();  // (the first of two launches: at its end)
+  const int seg = blockIdx.y;
+  const int64_t begin = seg * p.segment;
+  const bool last = seg + 1 == p.segments;
+  const int64_t stop = !last && begin + p.segment < p.L ? begin + p.segment : p.L;
+  walk<V, T, kVec, kState>(p, blockIdx.x, blockIdx.z, {begin, stop, seg, last, nullptr, nullptr});
+}
+
+// Slots.  All sequences' tiles of tokens, one (sequence, block of channels) after the other, are cut into
+// equal runs, one a block of the grid, and all blocks are resident at once.  A run is as long as a sequence or
+// longer, below two, so a sequence is cut at most once.  A block walks its run's last part first: the earlier
+// tokens of a cut sequence are a block's first work and the later ones the next block's last, and by the time
+// that these begin the state at the cut has been there for (quota - tiles of a sequence) tiles.
+// 2 x 2048 tokens, 16 states, bf16, 5120, 5504, 6080 and 7296 channels: 141, 152, 166 and 204 us, whole sequences
+// 166, 166, 166 and 219.  The loop over walks costs some 8 % of the rate (one walk alone 124 us, in the loop 134: the
+// memory side waits for loads it holds across it); the walks written out one after the other cost more where the
+// blocks of a multiprocessor are in different ones (5504: 182).
+constexpr int kSlots = 4;  // blocks on a multiprocessor
+constexpr int kReady = 1, kTaken = 2, kPolls = 1 << 20;
+
+template <typename V, int T, bool kVec>
+__global__ void __launch_bounds__(Shape<V, T>::kThreads + Shape<V, T>::kHelp, kSlots)
+scan_slots_kernel(ScanParams p, int64_t batch) {
+  constexpr int kStates = kNS * Shape<V, T>::kThreads;
+  __shared__ int s_flag;
+  begin_kernel();
+  const int64_t length = (p.L + kTile - 1) / kTile, blocks = static_cast<int64_t>(p.G) * p.tiles;
+  const int64_t lo = blockIdx.x * p.quota, total = batch * blocks * length;
+  const int64_t hi = lo + p.quota < total ? lo + p.quota : total;
+  for (int64_t top = hi; top > lo;) {
+    const int64_t q = (top - 1) / length;  // the sequence and block of channels
+    int64_t begin = lo > q * length ? (lo - q * length) * kTile : 0;
+    const bool last = top == (q + 1) * length;
+    const int64_t stop = last ? p.L : (top - q * length) * kTile;
+    uint64_t* state = p.handed + q * kStates;
+    top = lo > q * length ? lo : q * length;
+    bool mine = true;
+    if (begin > 0) {
+      // The state comes from the block before.  Should it not come (the hardware starts blocks in their order, but
+      // does not promise it), this block takes the sequence over from its first token.
+      if (threadIdx.x == 0) {
+        int flag = 0;
+        for (int i = 0; i < kPolls && flag != kReady; ++i) {
+          asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(flag) : "l"(p.ready + q) : "memory");
+          if (flag != kReady) __nanosleep(200);
+        }
+        s_flag = flag == kReady ? flag : atomicCAS(p.ready + q, 0, kTaken);
+      }
+      __syncthreads();
+      if (s_flag != kReady) begin = 0;
+    } else if (!last && p.init && p.init == p.final_state) {
+      // in place, a block that took the sequence over may have overwritten the state to start from
+      if (threadIdx.x == 0) s_flag = atomicAdd(p.ready + q, 0);
+      __syncthreads();
+      mine = s_flag != kTaken;
+    }
+    if (mine)
+      walk<V, T, kVec, false>(p, static_cast<int>(q % blocks), q / blocks,
+                              {begin, stop, 0, last, begin > 0 ? state : nullptr, last ? nullptr : state});
+    __syncthreads();
+    if (!last && mine && threadIdx.x == 0) {
+      __threadfence();
+      atomicCAS(p.ready + q, 0, kReady);
+    }
+  }
+}
+
+// In front of it; it starts when this has ended, on a GPU that holds nothing else, so that the hardware
+// gives every multiprocessor the same number of blocks.
+__global__ void __launch_bounds__(256) clear_kernel(int* ready, int64_t n) {
+  grid_dep_wait();
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i < n) ready[i] = 0;
 }
 
 // One token: every state is read and written once and there is nothing to walk along, so memory
@@ -529,12 +629,14 @@ __global__ void __launch_bounds__(kTokenThreads, 8) scan_token_kernel(ScanParams
 // 16384 x 2048 fp32 in 9, 11, 14, 16, 19 and 23 segments 339, 394, 332, 369, 331 and 349 us (19 taken);
 // 2048 x 2048 bf16 in 4 and 16: 84 and 57 us.  Fewer than five pay more for the first launch than they
 // gain: 513 x 5120 fp32 in four and whole 39 and 36 us, 2 x 2048 x 5120 bf16 in three and whole 205 and
-// 165 us.
-constexpr int64_t kFill = 16, kLeast = 128, kMost = 64;
+// 165 us.  Nor does it pay where whole sequences fill the multiprocessors nearly as well: 2 x 2048 x 3648 in five and
+// whole 143 and 118 us, 2 x 2048 x 2432 in eight and whole 104 and 101; so seven at least by the first rule (kWorth).
+constexpr int64_t kFill = 16, kLeast = 128, kMost = 64, kWorth = 7;
 
 int segment_count(int64_t batch, int64_t L, int64_t blocks, int warps) {
   const int64_t all = batch * blocks * warps;
   int64_t s = kFill * layer_sm_count() / all;
+  if (s < kWorth) return 1;
   s = s < L / kLeast ? s : L / kLeast;
   s = s < kMost ? s : kMost;
   return s < 5 ? 1 : static_cast<int>(s);
@@ -557,15 +659,30 @@ template <typename V, int T, bool kVec>
 cudaError_t launch_lanes(ScanParams p, int64_t batch, cudaStream_t stream) {
   constexpr int kThreads = Shape<V, T>::kThreads + Shape<V, T>::kHelp;
   const unsigned blocks = static_cast<unsigned>(p.G * p.tiles);
+  const int64_t all = batch * blocks;
+  if constexpr (T == 4) {
+    if (p.quota > 0) {
+      const cudaError_t e = launch_k(clear_kernel, dim3(static_cast<unsigned>(ceil_div(all, 256))), dim3(256), 0,
+                                     stream, true, p.ready, all);
+      if (e != cudaSuccess) return e;
+      return launch_k(scan_slots_kernel<V, T, kVec>,
+                      dim3(static_cast<unsigned>(ceil_div(all * ceil_div(p.L, kTile), p.quota))), dim3(kThreads), 0,
+                      stream, true, p, batch);
+    }
+  }
   if (p.segments > 1) {
     const cudaError_t e = launch_k(scan_kernel<V, T, kVec, true>,
                                    dim3(blocks, static_cast<unsigned>(p.segments - 1), static_cast<unsigned>(batch)),
                                    dim3(kThreads), 0, stream, true, p);
     if (e != cudaSuccess) return e;
   }
+  // Blocks that start while the kernel in front still holds multiprocessors are spread unevenly, and where a
+  // multiprocessor gets several, the one with most sets the time (2 x 2048 x 4864, 16 states, bf16: 160 us, started
+  // after that kernel's end 123; 3 x 501 x 2056: 40 and 32).
+  const bool overlap = p.segments > 1 || all <= layer_sm_count();
   return launch_k(scan_kernel<V, T, kVec, false>,
                   dim3(blocks, static_cast<unsigned>(p.segments), static_cast<unsigned>(batch)), dim3(kThreads),
-                  0, stream, true, p);
+                  0, stream, overlap, p);
 }
 
 // Lanes a channel's states are spread over.
@@ -607,9 +724,29 @@ ssd_status check_sizes(const ssd_selective_scan_args* a) {
 
 int channels_of_block(int N) { return lanes_of(N) == 2 ? Shape<float, 2>::kChannels : Shape<float, 4>::kChannels; }
 
+int64_t blocks_of(const ssd_selective_scan_args* a) {
+  return ceil_div(a->channels / a->ngroups, channels_of_block(a->dstate)) * a->ngroups;
+}
+
 int segments_of(const ssd_selective_scan_args* a) {
-  const int64_t blocks = ceil_div(a->channels / a->ngroups, channels_of_block(a->dstate)) * a->ngroups;
+  const int64_t blocks = blocks_of(a);
   return segment_count(a->batch, a->seqlen, blocks, lanes_of(a->dstate) < 4 ? 1 : lanes_of(a->dstate) / 4);
+}
+
+// Slots are taken where whole sequences would leave some multiprocessors with a block more than others, and no more
+// than seven on each: with more, blocks that end early make room for others (eight: 256 us in slots, 245 whole).
+int64_t quota_of(const ssd_selective_scan_args* a) {
+  if (segments_of(a) > 1 || a->seqlen <= kTile || lanes_of(a->dstate) != 4) return 0;
+  const int64_t all = a->batch * blocks_of(a), sm = layer_sm_count();
+  if (all <= kSlots * sm || all > 7 * sm) return 0;
+  const int64_t length = ceil_div(a->seqlen, kTile), quota = ceil_div(all * length, kSlots * sm);
+  return quota < 2 * length ? quota : 0;
+}
+
+// Bytes of the states at the cuts; the flags follow.
+size_t handed_bytes(const ssd_selective_scan_args* a) {
+  const int lanes = channels_of_block(a->dstate) / 2 * lanes_of(a->dstate);
+  return static_cast<size_t>(a->batch) * blocks_of(a) * kNS * lanes * sizeof(uint64_t);
 }
 
 }  // namespace
@@ -618,6 +755,7 @@ int segments_of(const ssd_selective_scan_args* a) {
 extern "C" size_t ssd_selective_scan_workspace_size(const ssd_selective_scan_args* a) {
   using namespace ssd;
   if (check_sizes(a) != SSD_OK || a->batch == 0) return 0;
+  if (quota_of(a) > 0) return handed_bytes(a) + static_cast<size_t>(a->batch) * blocks_of(a) * sizeof(int);
   const int s = segments_of(a);
   return s == 1 ? 0 : static_cast<size_t>(s) * a->batch * a->channels * (a->dstate + 1) * sizeof(float);
 }
@@ -642,13 +780,18 @@ extern "C" ssd_status ssd_selective_scan(const ssd_selective_scan_args* a, ssd_s
   }
   ScanParams p{};
   p.segments = segments_of(a);
-  if (p.segments > 1) {
+  p.quota = quota_of(a);
+  if (p.segments > 1 || p.quota > 0) {
     if (!a->workspace || !aligned_to(a->workspace, 16)) return SSD_ERR_INVALID_ARG;
     if (a->workspace_bytes < ssd_selective_scan_workspace_size(a)) return SSD_ERR_WORKSPACE;
   }
   p.segment = ceil_div(ceil_div(a->seqlen, p.segments), kTile) * kTile;
   p.seg_state = static_cast<float*>(a->workspace);
   if (p.segments > 1) p.seg_sum = p.seg_state + static_cast<int64_t>(p.segments) * a->batch * a->channels * a->dstate;
+  if (p.quota > 0) {
+    p.handed = static_cast<uint64_t*>(a->workspace);
+    p.ready = reinterpret_cast<int*>(static_cast<char*>(a->workspace) + handed_bytes(a));
+  }
   p.L = a->seqlen;
   p.D = a->channels;
   p.N = a->dstate;

@@ -166,6 +166,40 @@ def test_scan_lengths_and_in_place(ssd, dtype, L, C, N):
     assert torch.equal(state[0], init[0])
 
 
+@both_types
+@pytest.mark.parametrize("B,L,C,N,G", [(2, 70, 5120, 16, 1), (1, 100, 10001, 11, 1), (3, 65, 3400, 13, 2), (1, 33, 9800, 16, 1)])
+def test_scan_blocks_share_sequences(ssd, dtype, B, L, C, N, G):
+    """More blocks of channels than the GPU holds in even numbers: blocks take
+    equal runs of tokens, and hand over the states where a run ends inside a
+    sequence.  Again with the same workspace, whatever it holds."""
+    g = gen(B + L + C)
+    s = scan_inputs(g, B, L, C, N, G, dtype)
+    more = dict(D=normal(g, C), z=sliced(g, B, L, C, dtype), delta_bias=normal(g, C) - 2, init_state=normal(g, B, C, N))
+    want = ref.scan(**s, **{k: v for k, v in more.items() if k != "init_state"}, use_softplus=True, init=more["init_state"])
+    got = ssd.ssd_selective_scan(**s, **more, delta_softplus=True)
+    check_scan(got, want, dtype)
+    workspace = torch.full((ssd.ssd_selective_scan_workspace_size(B, L, C, N, G),), 1, dtype=torch.uint8, device="cuda")
+    assert workspace.numel() > 0
+    for _ in range(2):
+        again = ssd.ssd_selective_scan(**s, **more, delta_softplus=True, workspace=workspace)
+        assert all(torch.equal(x, y) for x, y in zip(again, got))
+
+
+@both_types
+def test_scan_blocks_share_sequences_in_place(ssd, dtype):
+    g = gen(8)
+    B, L, C, N = 6, 100, 1700, 16
+    s = scan_inputs(g, B, L, C, N, 1, dtype)
+    lengths = ints(0, 1, L, L - 1, L // 2, 2)
+    state = normal(g, B, C, N)
+    init = state.clone()
+    y, h = ssd.ssd_selective_scan(**s, delta_softplus=True, init_state=state, final_state=state, lengths=lengths)
+    check_scan((y, h), ref.scan(**s, use_softplus=True, init=init, lengths=lengths), dtype)
+    for b in range(B):
+        assert (y[b, int(lengths[b]):] == 0).all()
+    assert torch.equal(state[0], init[0])
+
+
 def test_scan_extremes(ssd):
     """Steps of zero, decays that vanish and states that never fade."""
     g = gen(8)
