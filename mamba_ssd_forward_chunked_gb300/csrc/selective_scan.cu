@@ -24,7 +24,7 @@
 // channels a multiprocessor: 88, 101, 115, 124 and 166 us), and a grid that
 // starts while the one in front still runs is spread as unevenly as that.  So
 // it starts alone, and numbers of blocks that do not divide evenly are cut in
-// runs that do (scan_slots_kernel; 2 x 2048 x 5120: 166 -> 142 us).
+// runs that do (scan_slots_kernel; 2 x 2048 x 5120: 166 -> 141 us).
 //
 // Segments.  With few channels a sequence is cut into segments that run side by
 // side: a first launch computes every segment's state from zero and its sum of
