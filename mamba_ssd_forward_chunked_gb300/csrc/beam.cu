@@ -19,8 +19,9 @@
 // Rounding can give different logits of a beam one score, and then the lower
 // index goes first although its logit is smaller.  Such a candidate may be
 // missing from its piece's list, but only if the piece's (k + 1)-th still has
-// the k-th best score; then the second launch looks through the pieces that
-// reach this score once more, in the order of indexes.
+// the k-th best score (or, where that is -infinity, lists finite logits with
+// this score); then the second launch looks through the pieces that reach this
+// score once more, in the order of indexes.
 //
 // Reordering moves bytes: a thread owns 16 bytes' position in all rows of a
 // request, reads them all, then writes, so that it may work in place.  256 rows
@@ -365,17 +366,23 @@ __global__ void __launch_bounds__(kThreads) merge_kernel(SelectParams p, int pie
   // equal scores below a piece's list
   const uint32_t worst = static_cast<uint32_t>(s_best[p.k - 1] >> 32);
   bool hidden = false;
-  auto hides = [&](int w, Key key) {  // a piece's last key: whether candidates at the k-th score may lie behind it
-    // (behind a last key of -infinity there is nothing but -infinity at higher indexes)
-    return key && key_value(key) > -INFINITY && order_of(score_of(s_score[w], key_value(key), s_lse[w])) == worst;
+  auto at_worst = [&](int w, Key key) { return order_of(score_of(s_score[w], key_value(key), s_lse[w])) == worst; };
+  auto hides = [&](int i, int w, Key key) {  // a piece's last key, the i-th of all: whether candidates at the k-th
+    if (!key || !at_worst(w, key)) return false;  // score, at lower indexes than some of the piece's, lie behind it
+    if (key_value(key) > -INFINITY) return true;
+    // Behind a last key of -infinity there are logits of -infinity alone, at higher indexes than the listed ones.
+    // The lowest logit above -infinity that is listed may lie higher still: in a lost beam its score is the same.
+    for (int j = 1; j <= p.k; ++j)
+      if (key_value(keys[i - j]) > -INFINITY) return at_worst(w, keys[i - j]);
+    return false;
   };
 #pragma unroll
   for (int q = 0; q < kOwn; ++q) {
     const int i = tid + q * kThreads;
-    if (own[q] && i % p.keep == p.k && hides(i / per, own[q])) hidden = true;
+    if (own[q] && i % p.keep == p.k && hides(i, i / per, own[q])) hidden = true;
   }
-  for (int i = tid; !few && i < p.beams * p.pieces; i += kThreads)
-    if (hides(i / p.pieces, keys[static_cast<int64_t>(i) * p.keep + p.k])) hidden = true;
+  for (int i = p.k + tid * p.keep; !few && i < all; i += kThreads * p.keep)
+    if (hides(i, i / per, keys[i])) hidden = true;
   if (__syncthreads_or(hidden)) {
     int found = 0;  // the candidates above the k-th score stay; those at it are gathered by rising index
     while (static_cast<uint32_t>(s_best[found] >> 32) != worst) ++found;
