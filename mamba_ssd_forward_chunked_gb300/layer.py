@@ -32,8 +32,8 @@ _binding.set_error(SSDError)
 def _on(stream, fn, *args):
     """fn(*args) with ``stream`` as the current stream, so that the outputs it
     allocates belong to it."""
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream))
+    if not hasattr(stream, "cuda_stream"):  # 0, the default stream, is not one for ExternalStream: it would be a new one
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
     with torch.cuda.stream(stream):
         return fn(*args)
 
