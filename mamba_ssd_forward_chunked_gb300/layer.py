@@ -9,10 +9,10 @@ per channel and state, ``ssd_selective_scan``); every further token through
 As in the rest of the package nothing is computed here: tensors are checked,
 outputs that are not given are allocated, and the C entry point of the same
 name runs on the current stream (or on ``stream``, which may be a
-torch.cuda.Stream or a raw handle; the caller orders it against the work that
-made the inputs).  Errors raise SSDError before anything is enqueued.  The
-checks are compiled (csrc/binding.cpp), because a decoding loop makes these
-calls for every layer and token.
+torch.cuda.Stream or a raw handle, of the tensors' device; the caller orders it
+against the work that made the inputs).  Errors raise SSDError before anything
+is enqueued.  The checks are compiled (csrc/binding.cpp), because a decoding
+loop makes these calls for every layer and token.
 """
 from __future__ import annotations
 
@@ -30,10 +30,16 @@ _binding.set_error(SSDError)
 
 
 def _on(stream, fn, *args):
-    """fn(*args) with ``stream`` as the current stream, so that the outputs it
-    allocates belong to it."""
+    """fn(*args) with ``stream`` as the current stream of the tensors' device, so
+    that the work runs there and the outputs it allocates belong to it."""
+    device = next((t.device for t in args if isinstance(t, torch.Tensor)), None)
+    if device is None or device.type != "cuda":
+        return fn(*args)  # refused there
     if not hasattr(stream, "cuda_stream"):  # 0, the default stream, is not one for ExternalStream: it would be a new one
-        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+        handle = int(stream)
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+    if stream.device != device:
+        raise SSDError(1, f"the stream is on {stream.device}, the tensors on {device}")
     with torch.cuda.stream(stream):
         return fn(*args)
 
