@@ -26,7 +26,7 @@ class Stream:
 
 @pytest.fixture
 def fake(monkeypatch):
-    """tensors(index): two of that device; the stream that is current is appended to `seen`."""
+    """tensors(): two of the first device; the stream that is current is appended to `seen`."""
     if FakeTensorMode is None:
         pytest.skip("no tensors without memory")
     seen = []
@@ -39,25 +39,25 @@ def fake(monkeypatch):
     monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: Stream(torch.device(device).index, handle))
     monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: Stream(torch.device(device).index, 0))
 
-    def tensors(index):
+    def tensors():
         with FakeTensorMode():
-            return torch.empty(4, 3, device=f"cuda:{index}"), torch.empty(2, 2, device=f"cuda:{index}")
+            return torch.empty(4, 3, device="cuda:0"), torch.empty(2, 2, device="cuda:0")
     return tensors, seen
 
 
 def test_a_stream_of_another_device_is_refused(ext, fake):
     tensors, seen = fake
     ran = []
-    with pytest.raises(ext.SSDError, match="cuda:0.*cuda:1"):
-        ext.layer._on(Stream(0), lambda *a: ran.append(a), None, *tensors(1))
+    with pytest.raises(ext.SSDError, match="cuda:1.*cuda:0"):
+        ext.layer._on(Stream(1), lambda *a: ran.append(a), None, *tensors())
     assert not ran and not seen
-    with pytest.raises(ext.SSDError, match="cuda:0"):  # the states in a list, the parents beside it
-        ext.layer._on(Stream(0), lambda *a: ran.append(a), [tensors(1)[0]], tensors(1)[1], None)
+    with pytest.raises(ext.SSDError, match="cuda:1"):  # the states in a list, the parents beside it
+        ext.layer._on(Stream(1), lambda *a: ran.append(a), [tensors()[0]], tensors()[1], None)
     assert not ran
 
 
 def test_streams_are_those_of_the_tensors_device(ext, fake):
     tensors, seen = fake
-    for stream in (Stream(1), 96, 0):
-        assert ext.layer._on(stream, lambda *a: len(a), *tensors(1), None) == 3
-    assert seen == [(1, 64), (1, 96), (1, 0)]
+    for stream in (Stream(0), 96, 0):
+        assert ext.layer._on(stream, lambda *a: len(a), *tensors(), None) == 3
+    assert seen == [(0, 64), (0, 96), (0, 0)]
