@@ -368,6 +368,13 @@ typedef struct {
 size_t ssd_selective_scan_workspace_size(const ssd_selective_scan_args* args);
 ssd_status ssd_selective_scan(const ssd_selective_scan_args* args, ssd_stream_t stream);
 
+/* Test hook: ssd_selective_scan, but where a sequence is shared by two blocks
+ * the state that one hands to the other does not arrive (`taken` not 0: the
+ * first is also told that the second has taken the sequence over).  After a
+ * bounded wait the second computes the sequence alone: the results are
+ * ssd_selective_scan's, bit for bit. */
+ssd_status ssd_debug_scan_handover(const ssd_selective_scan_args* args, int32_t taken, ssd_stream_t stream);
+
 /* One token of a Mamba-2 layer's convolution and recurrence, for every
  * sequence of a batch: x, Bm, Cm = silu(convolution of u and the ring), the
  * ring takes u, and with d = dt + dt_bias (through softplus where set)

@@ -27,7 +27,8 @@ EXPORTS = ("ssd_status_string", "ssd_validate_shape", "ssd_fwd_workspace_layout"
            "ssd_fwd", "ssd_fwd_check", "ssd_chunk_cumsum", "ssd_chunk_state", "ssd_state_passing",
            "ssd_compute_out", "ssd_debug_timeout_probe", "ssd_fwd_kernel_count", "ssd_fwd_static_scratch",
            "ssd_fwd_fused", "ssd_fused_pass", "ssd_fwd_range", "ssd_causal_cb",
-           "ssd_conv_fwd", "ssd_selective_scan", "ssd_selective_scan_workspace_size", "ssd_step", "ssd_w4_matvec",
+           "ssd_conv_fwd", "ssd_selective_scan", "ssd_selective_scan_workspace_size", "ssd_debug_scan_handover",
+           "ssd_step", "ssd_w4_matvec",
            "ssd_w4_matvec_workspace_size", "ssd_beam_select", "ssd_beam_select_workspace_size", "ssd_beam_reorder")
 
 # Size of the library's own workspace array used by ssd_fwd_static_scratch.
@@ -104,6 +105,8 @@ def _load() -> ctypes.CDLL:
                  "ssd_beam_reorder"):  # (argument struct, stream)
         getattr(lib, name).restype = c_int
         getattr(lib, name).argtypes = [vp, vp]
+    lib.ssd_debug_scan_handover.restype = c_int
+    lib.ssd_debug_scan_handover.argtypes = [vp, ctypes.c_int32, vp]
     for name in ("ssd_selective_scan_workspace_size", "ssd_w4_matvec_workspace_size", "ssd_beam_select_workspace_size"):
         getattr(lib, name).restype = sz
         getattr(lib, name).argtypes = [vp]

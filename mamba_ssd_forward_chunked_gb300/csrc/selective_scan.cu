@@ -55,7 +55,8 @@ struct ScanParams {
   float* seg_sum;    // [batch][segments][D]: each segment's sum of steps
   int64_t quota;     // slots: tiles of tokens a block takes, no fewer than a sequence has
   uint64_t* handed;  // slots: states at a cut, [batch][G * tiles][states of a lane, two each][lane]
-  int* ready;        // slots: [batch][G * tiles], 0, then kReady or kTaken
+  int* ready;        // slots: [batch][G * tiles], `at_first`, then kReady or kTaken
+  int at_first, polls;  // slots: 0, and how often a block looks for a state before it gives up
 };
 
 // 16 bytes of consecutive values as they lie in memory.
@@ -476,7 +477,25 @@ __global__ void __launch_bounds__(Shape<V, T>::kThreads + Shape<V, T>::kHelp, Sh
 // memory side waits for loads it holds across it); the walks written out one after the other cost more where the
 // blocks of a multiprocessor are in different ones (5504: 182).
 constexpr int kSlots = 4;  // blocks on a multiprocessor
-constexpr int kReady = 1, kTaken = 2, kPolls = 1 << 20;
+constexpr int kReady = 1, kTaken = 2, kLost = 3, kPolls = 1 << 20;  // (kLost: never ready, for tests)
+
+// The states a block of channels starts from, as one block hands them to another.
+template <typename V, int T>
+__device__ __forceinline__ void copy_init(const ScanParams& p, int block, int64_t b, uint64_t* to) {
+  using S = Shape<V, T>;
+  const int tid = threadIdx.x;
+  if (tid >= S::kThreads) return;
+  const int in_group = block % p.tiles * S::kChannels + tid / T * 2;
+  for (int k = 0; k < 2; ++k) {
+    const int64_t row = (b * p.D + block / p.tiles * p.per + in_group + k) * p.N;
+    for (int i = 0; i < kNS / 2; ++i) {
+      const int n = tid % T * kNS + 2 * i;
+      const bool in = in_group + k < p.per;
+      to[(k * kNS / 2 + i) * S::kThreads + tid] =
+          pack2(in && n < p.N ? p.init[row + n] : 0.f, in && n + 1 < p.N ? p.init[row + n + 1] : 0.f);
+    }
+  }
+}
 
 template <typename V, int T, bool kVec>
 __global__ void __launch_bounds__(Shape<V, T>::kThreads + Shape<V, T>::kHelp, kSlots)
@@ -494,29 +513,35 @@ scan_slots_kernel(ScanParams p, int64_t batch) {
     const int64_t stop = last ? p.L : (top - q * length) * kTile;
     uint64_t* state = p.handed + q * kStates;
     top = lo > q * length ? lo : q * length;
-    bool mine = true;
+    bool mine = true, copied = false;
     if (begin > 0) {
       // The state comes from the block before.  Should it not come (the hardware starts blocks in their order, but
       // does not promise it), this block takes the sequence over from its first token.
       if (threadIdx.x == 0) {
         int flag = 0;
-        for (int i = 0; i < kPolls && flag != kReady; ++i) {
+        for (int i = 0; i < p.polls && flag != kReady; ++i) {
           asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(flag) : "l"(p.ready + q) : "memory");
           if (flag != kReady) __nanosleep(200);
         }
         s_flag = flag == kReady ? flag : atomicCAS(p.ready + q, 0, kTaken);
+        __threadfence();  // what the block writes comes after its claim
       }
       __syncthreads();
       if (s_flag != kReady) begin = 0;
     } else if (!last && p.init && p.init == p.final_state) {
-      // in place, a block that took the sequence over may have overwritten the state to start from
+      // In place, a block that took the sequence over may have overwritten the state to start from, or do so at any
+      // time: this one starts from a copy, which is whole if the sequence was not yet taken over after it was made.
+      copy_init<V, T>(p, static_cast<int>(q % blocks), q / blocks, state);
+      copied = true;
+      __threadfence();
+      __syncthreads();
       if (threadIdx.x == 0) s_flag = atomicAdd(p.ready + q, 0);
       __syncthreads();
       mine = s_flag != kTaken;
     }
     if (mine)
       walk<V, T, kVec, false>(p, static_cast<int>(q % blocks), q / blocks,
-                              {begin, stop, 0, last, begin > 0 ? state : nullptr, last ? nullptr : state});
+                              {begin, stop, 0, last, begin > 0 || copied ? state : nullptr, last ? nullptr : state});
     __syncthreads();
     if (!last && mine && threadIdx.x == 0) {
       __threadfence();
@@ -527,10 +552,10 @@ scan_slots_kernel(ScanParams p, int64_t batch) {
 
 // In front of it; it starts when this has ended, on a GPU that holds nothing else, so that the hardware
 // gives every multiprocessor the same number of blocks.
-__global__ void __launch_bounds__(256) clear_kernel(int* ready, int64_t n) {
+__global__ void __launch_bounds__(256) clear_kernel(int* ready, int64_t n, int at_first) {
   grid_dep_wait();
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i < n) ready[i] = 0;
+  if (i < n) ready[i] = at_first;
 }
 
 // One token: every state is read and written once and there is nothing to walk along, so memory
@@ -663,7 +688,7 @@ cudaError_t launch_lanes(ScanParams p, int64_t batch, cudaStream_t stream) {
   if constexpr (T == 4) {
     if (p.quota > 0) {
       const cudaError_t e = launch_k(clear_kernel, dim3(static_cast<unsigned>(ceil_div(all, 256))), dim3(256), 0,
-                                     stream, true, p.ready, all);
+                                     stream, true, p.ready, all, p.at_first);
       if (e != cudaSuccess) return e;
       return launch_k(scan_slots_kernel<V, T, kVec>,
                       dim3(static_cast<unsigned>(ceil_div(all * ceil_div(p.L, kTile), p.quota))), dim3(kThreads), 0,
@@ -760,7 +785,8 @@ extern "C" size_t ssd_selective_scan_workspace_size(const ssd_selective_scan_arg
   return s == 1 ? 0 : static_cast<size_t>(s) * a->batch * a->channels * (a->dstate + 1) * sizeof(float);
 }
 
-extern "C" ssd_status ssd_selective_scan(const ssd_selective_scan_args* a, ssd_stream_t stream) {
+// at_first, polls: ScanParams.
+static ssd_status scan(const ssd_selective_scan_args* a, int at_first, int polls, ssd_stream_t stream) {
   using namespace ssd;
   ssd_status st = check_sizes(a);
   if (st != SSD_OK) return st;
@@ -792,6 +818,7 @@ extern "C" ssd_status ssd_selective_scan(const ssd_selective_scan_args* a, ssd_s
     p.handed = static_cast<uint64_t*>(a->workspace);
     p.ready = reinterpret_cast<int*>(static_cast<char*>(a->workspace) + handed_bytes(a));
   }
+  p.at_first = at_first, p.polls = polls;
   p.L = a->seqlen;
   p.D = a->channels;
   p.N = a->dstate;
@@ -808,4 +835,12 @@ extern "C" ssd_status ssd_selective_scan(const ssd_selective_scan_args* a, ssd_s
   p.lengths = a->lengths;
   return launched(a->dtype == SSD_BF16 ? launch<__nv_bfloat16>(p, a->batch, stream)
                                        : launch<float>(p, a->batch, stream));
+}
+
+extern "C" ssd_status ssd_selective_scan(const ssd_selective_scan_args* a, ssd_stream_t stream) {
+  return scan(a, 0, ssd::kPolls, stream);
+}
+
+extern "C" ssd_status ssd_debug_scan_handover(const ssd_selective_scan_args* a, int32_t taken, ssd_stream_t stream) {
+  return scan(a, taken ? ssd::kTaken : ssd::kLost, 1000, stream);
 }
