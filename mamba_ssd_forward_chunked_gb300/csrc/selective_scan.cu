@@ -67,7 +67,7 @@ struct Raw<__nv_bfloat16> {
   static constexpr int kE = 8;
   uint4 v;
   __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ void set(int i, __nv_bfloat16 x) {
     const uint32_t bits = __bfloat16_as_ushort(x);
     uint32_t* w = &v.x;
@@ -92,7 +92,7 @@ struct Raw<float> {
   static constexpr int kE = 4;
   float4 v;
   __device__ __forceinline__ void zero() { v = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ void load(const float* p) { v = __ldg(reinterpret_cast<const float4*>(p)); }
+  __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float4*>(p); }
   __device__ __forceinline__ void set(int i, float x) { (&v.x)[i] = x; }
   __device__ __forceinline__ float get(int i) const { return (&v.x)[i]; }
   static __device__ __forceinline__ void store(float* p, const float (&f)[4]) {

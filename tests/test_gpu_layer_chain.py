@@ -1,0 +1,45 @@
+"""Calls that read what the call in front of them writes, again and again into
+the same buffers: a launch is set up while the one in front still runs, and must
+see what that one writes, not what lay there before."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+both_types = pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+
+
+@pytest.fixture(scope="module")
+def ssd():
+    import mamba_ssd_forward_chunked_gb300 as m
+    return m
+
+
+def alternate(chain, inputs, rounds=40):
+    """chain(input) for inputs in turn, with nothing in between, against each one waited for."""
+    want = []
+    for x in inputs:
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in chain(x)])
+        torch.cuda.synchronize()
+    got = [[t.clone() for t in chain(inputs[i % len(inputs)])] for i in range(rounds)]
+    torch.cuda.synchronize()
+    for i, outs in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(outs, want[i % len(inputs)])), i
+
+
+@both_types
+@pytest.mark.parametrize("B,L,C,N", [(1, 200, 64, 16), (2, 70, 5120, 16), (1, 2000, 48, 16), (3, 1, 512, 16)],
+                         ids=["few", "shared", "segments", "token"])
+def test_scan_after_its_convolution(ssd, dtype, B, L, C, N):
+    g = torch.Generator().manual_seed(L)
+    rand = lambda *s: torch.randn(*s, generator=g).cuda()  # noqa: E731
+    weight, A = rand(C + 2 * N, 4), -torch.rand(C, N, generator=g).cuda() * N
+    out = [torch.empty(B, L, n, dtype=dtype, device="cuda") for n in (C, N, N)]
+    y, h = torch.empty(B, L, C, dtype=dtype, device="cuda"), torch.empty(B, C, N, device="cuda")
+
+    def chain(u):
+        ssd.ssd_conv_fwd(u, weight, split=(C, N, N), out=out)
+        x, Bm, Cm = out
+        return ssd.ssd_selective_scan(x, x, A, Bm.unsqueeze(2), Cm.unsqueeze(2), z=x, delta_softplus=True, y=y, final_state=h)
+    alternate(chain, [rand(B, L, C + 2 * N).to(dtype) for _ in range(2)])
