@@ -83,10 +83,12 @@ __global__ void __launch_bounds__(kColumnThreads) columns_kernel(const float* x,
   out[2 * row] = __float2bfloat16_rn(lo);
 }
 
-// kCols: products' columns in blocks of 8.  kGroup: columns of weights a scale holds for.  kDirect: the
-// columns are x itself, read through the read-only cache path (5120 -> 2560, eight tokens: 5.6 us against
-// 7.1 without); columns that the launch in front writes are read by ordinary loads.
-// kTiles: row tiles of a block, which share what is read of x.
+// kCols: products' columns in blocks of 8.  kGroup: columns of weights a scale holds for.  kTiles: row tiles of a
+// block, which share what is read of x.  kDirect: the columns are x itself; the launch in front may be writing x, the
+// codes or the scales while this one is set up, so all is read after the wait.  Else that launch is columns_kernel,
+// which lets this one start only when it has waited for all work before it: the codes may be read before the wait.
+// Ordinary loads everywhere (the read-only path is not for what may be written meanwhile, and gains nothing: 6.2 and
+// 5.7 us for the layer's two projections, 6.3 and 5.6 through it).
 template <typename T, int kCols, int kTiles, int kGroup, bool kDirect>
 __global__ void __launch_bounds__(max_warps(kTiles) * 32, kCols == 1 ? 2 : 1) w4_kernel(W4Params p) {
   constexpr int kParts = sizeof(T) == 4 ? 3 : 1;        // columns of a token
@@ -132,7 +134,7 @@ __global__ void __launch_bounds__(max_warps(kTiles) * 32, kCols == 1 ? 2 : 1) w4
         for (int h = 0; h < 2; ++h) {
           const int kt = 2 * (base + u * warps) + h;
           q[u][j][h] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);  // zeros past the end
-          if (kt < p.ktiles) q[u][j][h] = __ldg(packed[j] + static_cast<int64_t>(kt) * 32);
+          if (kt < p.ktiles) q[u][j][h] = packed[j][static_cast<int64_t>(kt) * 32];
         }
     if (!kDirect && !waited) grid_dep_wait();  // for the launch in front
     waited = true;
@@ -148,10 +150,7 @@ __global__ void __launch_bounds__(max_warps(kTiles) * 32, kCols == 1 ? 2 : 1) w4
 #pragma unroll
         for (int t = 0; t < kCols; ++t) {
           xw[t] = make_uint4(0, 0, 0, 0);
-          if (x[t] && k0 < p.k) {
-            const uint4* from = reinterpret_cast<const uint4*>(x[t] + k0);
-            xw[t] = kDirect ? __ldg(from) : *from;
-          }
+          if (x[t] && k0 < p.k) xw[t] = *reinterpret_cast<const uint4*>(x[t] + k0);
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -168,7 +167,7 @@ __global__ void __launch_bounds__(max_warps(kTiles) * 32, kCols == 1 ? 2 : 1) w4
           const int g = unit * (4 / kParts32) + part4 / kParts32;
 #pragma unroll
           for (int j = 0; j < kTiles; ++j) {
-            const float f0 = g < p.ngroups ? __ldg(s0[j] + g) : 0.f, f1 = g < p.ngroups ? __ldg(s1[j] + g) : 0.f;
+            const float f0 = g < p.ngroups ? s0[j][g] : 0.f, f1 = g < p.ngroups ? s1[j][g] : 0.f;
 #pragma unroll
             for (int t = 0; t < kCols; ++t) {
               total[j][t][0] = fmaf(f0, sum[j][t][0], total[j][t][0]);

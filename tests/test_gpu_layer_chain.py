@@ -43,3 +43,24 @@ def test_scan_after_its_convolution(ssd, dtype, B, L, C, N):
         x, Bm, Cm = out
         return ssd.ssd_selective_scan(x, x, A, Bm.unsqueeze(2), Cm.unsqueeze(2), z=x, delta_softplus=True, y=y, final_state=h)
     alternate(chain, [rand(B, L, C + 2 * N).to(dtype) for _ in range(2)])
+
+
+@both_types
+@pytest.mark.parametrize("M", [1, 8, 16])
+@pytest.mark.parametrize("width", [512, 509], ids=["vectors", "odd"])
+def test_products_after_each_other(ssd, dtype, M, width):
+    g = torch.Generator().manual_seed(M)
+    layers = []
+    for _ in range(4):
+        w = torch.randn(width, width, generator=g).cuda() / width ** 0.5
+        layers.append(ssd.w4_quantize(w, 64))
+    space = torch.empty(1 << 16, dtype=torch.uint8, device="cuda")
+    x, y = (torch.empty(M, width, dtype=dtype, device="cuda") for _ in range(2))
+
+    def chain(first):
+        ssd.ssd_w4_matvec(first, *layers[0], 64, y=x, workspace=space)
+        ssd.ssd_w4_matvec(x, *layers[1], 64, y=y, workspace=space)
+        ssd.ssd_w4_matvec(y, *layers[2], 64, y=x, workspace=space)
+        ssd.ssd_w4_matvec(x, *layers[3], 64, y=y, add=x, workspace=space)
+        return x, y
+    alternate(chain, [torch.randn(M, width, generator=g).to(dtype).cuda() for _ in range(2)])
