@@ -431,12 +431,24 @@ int eights_of(int64_t batch, int beams, int vocab) {
   return batch * beams * ceil_div(vocab, 64 * kThreads) >= 4 * static_cast<int64_t>(layer_sm_count()) ? 8 : 1;
 }
 
+// Bytes of a piece's list of keys.
+constexpr size_t list_bytes(int keep, int eights) {
+  return static_cast<size_t>(keep) * share_of(keep) * 8 * eights * sizeof(Key);
+}
+// The most that any k takes: four threads share a group up to the largest `keep` but one.
+constexpr size_t most_list_bytes(int eights) {
+  static_assert(share_of(kMaxBeams) == 4 && share_of(kMaxBeams + 1) == 2, "keep is at most kMaxBeams + 1");
+  return list_bytes(kMaxBeams, eights);
+}
+
 template <typename T, int kEights>
 cudaError_t launch_pieces(const SelectParams& p, bool vec, int64_t batch, cudaStream_t stream) {
-  const size_t smem = static_cast<size_t>(p.keep) * share_of(p.keep) * 8 * kEights * sizeof(Key);
+  const size_t smem = list_bytes(p.keep, kEights);
   auto k = vec ? piece_kernel<T, kEights, true> : piece_kernel<T, kEights, false>;
   if (smem > 40 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    // one limit whatever k is: it belongs to the kernel, and other threads' launches go by it too
+    const cudaError_t e =
+        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most_list_bytes(kEights)));
     if (e != cudaSuccess) return e;
   }
   const dim3 grid(static_cast<unsigned>(p.pieces), static_cast<unsigned>(p.beams), static_cast<unsigned>(batch));
