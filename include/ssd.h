@@ -363,8 +363,8 @@ typedef struct {
   size_t workspace_bytes;
 } ssd_selective_scan_args;
 
-/* Bytes of workspace (0 where none is needed or the sizes are refused); only
- * batch, seqlen, channels, dstate and ngroups are read. */
+/* Bytes of workspace on the current device (0 where none is needed or the sizes
+ * are refused); only batch, seqlen, channels, dstate and ngroups are read. */
 size_t ssd_selective_scan_workspace_size(const ssd_selective_scan_args* args);
 ssd_status ssd_selective_scan(const ssd_selective_scan_args* args, ssd_stream_t stream);
 
@@ -452,7 +452,7 @@ typedef struct {
   size_t workspace_bytes;
 } ssd_beam_select_args;
 
-/* Only batch, beams, vocab, k are read. */
+/* Bytes of workspace on the current device; only batch, beams, vocab, k are read. */
 size_t ssd_beam_select_workspace_size(const ssd_beam_select_args* args);
 ssd_status ssd_beam_select(const ssd_beam_select_args* args, ssd_stream_t stream);
 

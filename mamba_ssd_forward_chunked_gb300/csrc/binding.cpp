@@ -125,10 +125,16 @@ struct Items {
   ~Items() { Py_XDECREF(seq); }
 };
 
+// The tensors' device is the current one while this lives: workspaces are sized for it, and the call runs on it.
+struct On {
+  c10::cuda::OptionalCUDAGuard guard;
+  explicit On(int dev) {
+    if (c10::cuda::current_device() != dev) guard.set_index(static_cast<c10::DeviceIndex>(dev));
+  }
+};
+
 template <typename Args>
 void call(ssd_status (*fn)(const Args*, ssd_stream_t), const char* name, Args& a, int dev) {
-  c10::cuda::OptionalCUDAGuard guard;
-  if (c10::cuda::current_device() != dev) guard.set_index(static_cast<c10::DeviceIndex>(dev));
   a.size = sizeof(Args);
   const ssd_status st = fn(&a, c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream());
   if (st != SSD_OK) throw Refused{st, name};
@@ -158,6 +164,7 @@ PyObject* wrap_all(std::initializer_list<at::Tensor> ts) {
 // u, weight, bias, activation, split, ring, positions, lengths, slots, new_ring, out
 PyObject* conv_fwd(PyObject* const* p) {
   const First u = first(p[0], "u", 3);
+  const On device(u.dev);
   const int64_t B = u.t.size(0), L = u.t.size(1), C = u.t.size(2);
   ssd_conv_args a{};
   a.batch = B, a.seqlen = L, a.channels = small(C, "channels"), a.dtype = u.dtype;
@@ -221,6 +228,7 @@ PyObject* conv_fwd(PyObject* const* p) {
 // u, delta, A, Bm, Cm, D, z, delta_bias, delta_softplus, init_state, lengths, y, final_state, workspace, want_final_state
 PyObject* selective_scan(PyObject* const* p) {
   const First u = first(p[0], "u", 3);
+  const On device(u.dev);
   const int64_t B = u.t.size(0), L = u.t.size(1), C = u.t.size(2);
   if (!THPVariable_Check(p[3]) || THPVariable_Unpack(p[3]).dim() != 4) throw Refused{1, "Bm must be a 4-D tensor"};
   const int64_t G = THPVariable_Unpack(p[3]).size(2), N = THPVariable_Unpack(p[3]).size(3);
@@ -280,6 +288,7 @@ PyObject* selective_scan(PyObject* const* p) {
 // u, dt, A, D, weight, bias, state, ring, positions, ngroups, z, dt_bias, dt_softplus, slots, new_state, y
 PyObject* step(PyObject* const* p) {
   const First u = first(p[0], "u", 2);
+  const On device(u.dev);
   if (!THPVariable_Check(p[6]) || THPVariable_Unpack(p[6]).dim() != 4) throw Refused{1, "state must be a 4-D tensor"};
   const at::Tensor& state = THPVariable_Unpack(p[6]);
   const int64_t B = u.t.size(0), C = u.t.size(1), S = state.size(0), H = state.size(1), P = state.size(2), N = state.size(3);
@@ -324,6 +333,7 @@ PyObject* step(PyObject* const* p) {
 // x, packed, scales, group, add, y, workspace
 PyObject* w4_matvec(PyObject* const* p) {
   const First x = first(p[0], "x", 2);
+  const On device(x.dev);
   const int64_t M = x.t.size(0), K = x.t.size(1), group = whole(p[3], "group");
   if (!THPVariable_Check(p[2]) || THPVariable_Unpack(p[2]).dim() != 2) throw Refused{1, "scales must be a 2-D tensor"};
   if (group != 32 && group != 64 && group != 128)
@@ -360,6 +370,7 @@ PyObject* w4_matvec(PyObject* const* p) {
 // logits, scores, k, finished, eos, workspace
 PyObject* beam_select(PyObject* const* p) {
   const First x = first(p[0], "logits", 3);
+  const On device(x.dev);
   const int64_t B = x.t.size(0), W = x.t.size(1), V = x.t.size(2), k = whole(p[2], "k");
   if (k < 1 || k > 64) throw Refused{k < 1 ? 1 : 2, "k is " + std::to_string(k) + ", expected 1 to 64"};
   ssd_beam_select_args a{};
@@ -395,6 +406,7 @@ PyObject* beam_reorder(PyObject* const* p) {
   const at::Tensor& parents = THPVariable_Unpack(p[1]);
   if (!parents.is_cuda()) throw Refused{1, "parents must be a CUDA tensor (got " + parents.device().str() + ")"};
   const int dev = parents.get_device();
+  const On device(dev);
   const int64_t B = parents.size(0), k = parents.size(1);
   const int32_t* pp = dense<const int32_t>(p[1], "parents", dev, at::kInt, {B, k});
   Items states(p[0], "states");

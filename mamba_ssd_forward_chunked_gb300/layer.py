@@ -71,7 +71,8 @@ def ssd_conv_fwd(u: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Ten
 # ------------------------------------------------------------------ selective scan
 
 def ssd_selective_scan_workspace_size(batch: int, seqlen: int, channels: int, dstate: int, ngroups: int) -> int:
-    """Bytes of workspace ssd_selective_scan needs for these sizes (0: none)."""
+    """Bytes of workspace ssd_selective_scan needs for these sizes on the current
+    device (0: none)."""
     return _binding.scan_workspace(batch, seqlen, channels, dstate, ngroups)
 
 
@@ -165,7 +166,7 @@ def ssd_w4_matvec(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, g
 # ------------------------------------------------------------------ beam search
 
 def ssd_beam_select_workspace_size(batch: int, beams: int, vocab: int, k: int) -> int:
-    """Bytes of workspace ssd_beam_select needs for these sizes."""
+    """Bytes of workspace ssd_beam_select needs for these sizes on the current device."""
     return _binding.select_workspace(batch, beams, vocab, k)
 
 
