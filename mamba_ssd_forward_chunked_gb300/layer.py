@@ -16,17 +16,35 @@ loop makes these calls for every layer and token.
 """
 from __future__ import annotations
 
+import importlib
 from typing import List, Optional, Sequence, Tuple, Union
 
 import torch
 
 from . import SSDError
-from . import _layer_binding as _binding
+
+
+class _NoBinding:
+    """In the compiled binding's place where it cannot be loaded: the rest of the
+    package needs none of it, and the layer's calls have no other path."""
+
+    def __init__(self, why: ImportError):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"the layer operators need _layer_binding.so, which cannot be loaded ({self._why}): build it "
+                          "with `python mamba_ssd_forward_chunked_gb300/build_ext.py`") from self._why
+
+
+try:
+    _binding = importlib.import_module("._layer_binding", __package__)
+except ImportError as why:
+    _binding = _NoBinding(why)
+else:
+    _binding.set_error(SSDError)
 
 __all__ = ["ssd_conv_fwd", "ssd_selective_scan", "ssd_step", "ssd_w4_matvec", "ssd_beam_select", "ssd_beam_reorder",
            "ssd_selective_scan_workspace_size", "ssd_beam_select_workspace_size", "w4_pack", "w4_quantize"]
-
-_binding.set_error(SSDError)
 
 
 def _on(stream, fn, *args):
