@@ -61,6 +61,21 @@ def _binding_link(obj: str, out: str):
             "-Wl,-rpath,$ORIGIN", "-L", lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
 
 
+def _binding_made_for(cmds) -> str:
+    """What the binding depends on beside its sources: the commands, this Python
+    and the installed torch, whose files may be older than what was built."""
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    with open(os.path.join(torch, "version.py")) as f:
+        return "\n".join([sys.version, f.read(), *(" ".join(cmd) for cmd in cmds)])
+
+
+def _read(path: str):
+    if not os.path.exists(path):
+        return None
+    with open(path) as f:
+        return f.read()
+
+
 def _run(cmd, what: str) -> None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
@@ -90,8 +105,11 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
             jobs.append([nvcc, *ARCH, *flags, "-I", INCLUDE, "-I", CSRC, "-c", src, "-o", obj])
     binding_src = os.path.join(CSRC, "binding.cpp")
     binding_obj = os.path.join(BUILD, "binding.o")
-    if force or _stale(binding_obj, [binding_src, os.path.join(INCLUDE, "ssd.h")]):
-        jobs.append(_binding_compile(binding_src, binding_obj))
+    binding = [_binding_compile(binding_src, binding_obj), _binding_link(binding_obj, BINDING + ".tmp")]
+    made_for, note = _binding_made_for(binding), os.path.join(BUILD, "binding.txt")
+    other = _read(note) != made_for
+    if force or other or _stale(binding_obj, [binding_src, os.path.join(INCLUDE, "ssd.h")]):
+        jobs.append(binding[0])
     if jobs:
         with cf.ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
             results = list(ex.map(lambda c: subprocess.run(c, capture_output=True, text=True), jobs))
@@ -103,9 +121,11 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
     if force or jobs or _stale(OUT, objs):
         _run([nvcc, *ARCH, "-shared", "-cudart", "static", "-o", OUT + ".tmp", *objs], "link")
         os.replace(OUT + ".tmp", OUT)
-    if force or _stale(BINDING, [binding_obj, OUT]):
-        _run(_binding_link(binding_obj, BINDING + ".tmp"), "link of the binding")
+    if force or other or _stale(BINDING, [binding_obj, OUT]):
+        _run(binding[1], "link of the binding")
         os.replace(BINDING + ".tmp", BINDING)
+        with open(note, "w") as f:
+            f.write(made_for)
     return OUT
 
 
