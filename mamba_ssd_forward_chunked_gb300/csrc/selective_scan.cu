@@ -126,10 +126,10 @@ __device__ __forceinline__ void softplus2(float& v0, float& v1) {
   const uint64_t s = pack2(e0 * rcp_fast(2.f + e0), e1 * rcp_fast(2.f + e1));
   const uint64_t q = mul2(s, s);
   auto both = [](float c) { return pack2(c, c); };
-  uint64_t r = fma2(q, both(1.f / 11.f), both(1.f / 9.f));
-  r = fma2(q, r, both(1.f / 7.f));
-  r = fma2(q, r, both(1.f / 5.f));
-  r = fma2(q, r, both(1.f / 3.f));
+  uint64_t r = fma2(q, both(kAtanh4), both(kAtanh3));
+  r = fma2(q, r, both(kAtanh2));
+  r = fma2(q, r, both(kAtanh1));
+  r = fma2(q, r, both(kAtanh0));
   r = fma2(mul2(q, s), r, s);
   float r0, r1;
   unpack2(r, r0, r1);

@@ -1,0 +1,41 @@
+"""Values and arguments of the layer operators that the wider tests' bounds are
+too wide, or too few, to see."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ssd():
+    import mamba_ssd_forward_chunked_gb300 as m
+    return m
+
+
+@pytest.mark.parametrize("how", ["step", "token", "prompt"])
+def test_softplus_has_no_bias(ssd, how):
+    """Steps are added up over a whole prompt, so their softplus must not lean to
+    one side: half a unit of a 32-bit number in [1/2, 1), 3e-8, which is 4.3e-8 of
+    log 2, and a tenth more."""
+    C = 4096
+    v = torch.linspace(-0.05, 0.05, C)
+    one = torch.ones(1, 1, C, device="cuda")
+    if how == "step":  # y = softplus(dt) x.b c: x = b = c = 1, one state of 64 counts
+        H, N = C, 64
+        channels = H * 64 + 2 * N
+        u = torch.zeros(1, channels, device="cuda")
+        u[:, :H * 64], u[:, H * 64], u[:, H * 64 + N] = 1.0, 1.0, 1.0
+        weight = torch.zeros(channels, 2, device="cuda")
+        state, ring = torch.zeros(1, H, 64, N, device="cuda"), torch.zeros(1, 2, channels, device="cuda")
+        weight[:, 1] = 20.0  # silu(20) = 20 - 4e-8
+        ssd.ssd_step(u, v.view(1, C).cuda(), torch.zeros(H, device="cuda"), torch.zeros(H, device="cuda"), weight, None,
+                     state, ring, torch.zeros(1, dtype=torch.int32, device="cuda"), dt_softplus=True)
+        got = state[0, :, 0, 0].double().cpu() / 400.0
+    else:  # the state is the last step's d u b: in the prompt nothing is left of the first
+        L = 1 if how == "token" else 2
+        x, b = one.expand(1, L, C).contiguous(), torch.ones(1, L, 1, 1, device="cuda")
+        delta = v.cuda().view(1, 1, C).expand(1, L, C).contiguous()
+        _, h = ssd.ssd_selective_scan(x, delta, torch.full((C, 1), -1000.0, device="cuda"), b, b, delta_softplus=True)
+        got = h[0, :, 0].double().cpu()
+    want = torch.log1p(torch.exp(v.double()))
+    assert abs(float(((got - want) / want).mean())) < 4.7e-8
