@@ -101,6 +101,12 @@ int64_t whole(PyObject* o, const char* name) {
   return v;
 }
 
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw PythonError{};  // as of a tensor of several values
+  return v == 1;
+}
+
 int small(int64_t v, const char* name) {
   if (v > INT32_MAX || v < INT32_MIN) throw Refused{2, std::string(name) + " is " + std::to_string(v)};
   return static_cast<int>(v);
@@ -234,7 +240,7 @@ PyObject* selective_scan(PyObject* const* p) {
   const int64_t G = THPVariable_Unpack(p[3]).size(2), N = THPVariable_Unpack(p[3]).size(3);
   ssd_selective_scan_args a{};
   a.batch = B, a.seqlen = L, a.channels = small(C, "channels"), a.dstate = small(N, "dstate");
-  a.ngroups = small(G, "ngroups"), a.dtype = u.dtype, a.softplus = PyObject_IsTrue(p[8]) == 1;
+  a.ngroups = small(G, "ngroups"), a.dtype = u.dtype, a.softplus = truth(p[8]);
   a.u = rows(p[0], "u", u.dev, u.type, {B, L, C});
   a.u_batch = u.t.stride(0), a.u_token = u.t.stride(1);
   a.delta = rows(p[1], "delta", u.dev, u.type, {B, L, C});
@@ -262,7 +268,7 @@ PyObject* selective_scan(PyObject* const* p) {
   at::Tensor final_state;
   if (p[12] != Py_None) {
     final_state = tensor(p[12], "final_state");
-  } else if (PyObject_IsTrue(p[14]) == 1) {
+  } else if (truth(p[14])) {
     final_state = empty({B, C, N}, at::kFloat, u.t);
     a.final_state = static_cast<float*>(final_state.data_ptr());
   }
@@ -300,7 +306,7 @@ PyObject* step(PyObject* const* p) {
   a.ngroups = small(G, "ngroups"), a.dstate = small(N, "dstate"), a.dtype = u.dtype;
   const int64_t W = THPVariable_Check(p[4]) && THPVariable_Unpack(p[4]).dim() == 2 ? THPVariable_Unpack(p[4]).size(1) : 0;
   a.width = small(W, "width");
-  a.softplus = PyObject_IsTrue(p[12]) == 1;
+  a.softplus = truth(p[12]);
   a.u = rows(p[0], "u", u.dev, u.type, {B, C});
   a.u_batch = u.t.stride(0);
   if (p[10] != Py_None) {

@@ -39,3 +39,16 @@ def test_softplus_has_no_bias(ssd, how):
         got = h[0, :, 0].double().cpu()
     want = torch.log1p(torch.exp(v.double()))
     assert abs(float(((got - want) / want).mean())) < 4.7e-8
+
+
+def test_flags_that_are_neither(ssd):
+    """What has no truth value is an error of its own, not a lost one."""
+    z = lambda *s: torch.zeros(*s, device="cuda")  # noqa: E731
+    two = z(2)
+    step = (z(2, 384), z(2, 4), z(4), z(4), z(384, 4), None, z(2, 4, 64, 64), z(2, 4, 384), z(2).to(torch.int32))
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        ssd.ssd_step(*step, dt_softplus=two)
+    scan = (z(2, 1, 12), z(2, 1, 12), z(12, 16), z(2, 1, 1, 16), z(2, 1, 1, 16))
+    for flag in ("delta_softplus", "want_final_state"):
+        with pytest.raises(RuntimeError, match="ambiguous"):
+            ssd.ssd_selective_scan(*scan, **{flag: two})
