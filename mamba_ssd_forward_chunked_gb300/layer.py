@@ -137,7 +137,7 @@ def ssd_step(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, D: torch.Tensor
 # ------------------------------------------------------------------ 4-bit weights
 
 def w4_pack(codes: torch.Tensor) -> torch.Tensor:
-    """4-bit codes [n, k] (values 0 to 15; a weight is (code - 8) * scale) in the
+    """4-bit codes [n, k] (values 0 to 15, others are refused; a weight is (code - 8) * scale) in the
     order ssd_w4_matvec reads, int32 [ceil(n/16), ceil(k/64), 32, 4].  Done once
     per weight, on any device."""
     if not isinstance(codes, torch.Tensor) or codes.dim() != 2 or codes.is_floating_point():
@@ -146,6 +146,8 @@ def w4_pack(codes: torch.Tensor) -> torch.Tensor:
     rows, cols = -(-n // 16), -(-k // 64)
     full = codes.new_full((rows * 16, cols * 64), 8, dtype=torch.int64)
     full[:n, :k] = codes
+    if codes.numel() and not 0 <= int(full.min()) <= int(full.max()) <= 15:  # (others would change their neighbours)
+        raise SSDError(1, f"codes from {int(full.min())} to {int(full.max())}, expected 0 to 15")
     # [row tile, a, r, column tile, h, c, i, e, p] -> [row tile, column tile, r, c, h, i, e, a, p]
     v = full.view(rows, 2, 8, cols, 2, 4, 2, 2, 2).permute(0, 3, 2, 5, 4, 6, 7, 1, 8)
     e, a, p = torch.meshgrid(*[torch.arange(2, device=codes.device)] * 3, indexing="ij")
