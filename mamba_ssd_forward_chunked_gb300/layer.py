@@ -158,15 +158,20 @@ def w4_pack(codes: torch.Tensor) -> torch.Tensor:
 
 def w4_quantize(weight: torch.Tensor, group: int = 128) -> Tuple[torch.Tensor, torch.Tensor]:
     """(packed codes, scales) of a weight [n, k] for ssd_w4_matvec: per row and
-    group of columns the scale that puts the largest magnitude at 7."""
+    group of columns the scale that puts the largest magnitude at 7.  Weights that
+    are not finite are refused."""
     if group not in (32, 64, 128):
         raise SSDError(2, f"group {group}, expected 32, 64 or 128")
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise SSDError(1, "weight must be a 2-D tensor")
     n, k = weight.shape
     groups = -(-k // group)
     w = weight.new_zeros((n, groups * group), dtype=torch.float32)
     w[:, :k] = weight
     w = w.view(n, groups, group)
     scales = w.abs().amax(-1) / 7.0
+    if not bool(torch.isfinite(scales).all()):
+        raise SSDError(1, "weight must be finite")
     codes = torch.round(w / torch.where(scales > 0, scales, 1.0)[..., None]).clamp_(-7, 7) + 8
     return w4_pack(codes.view(n, groups * group)[:, :k].to(torch.int64)), scales
 

@@ -14,5 +14,19 @@ def test_codes_outside_four_bits_are_refused(ext, code):  # noqa: F811
         ext.w4_pack(codes)
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_weights_that_are_not_finite_are_refused(ext, bad):  # noqa: F811
+    weight = torch.randn(5, 100)
+    weight[2, 70] = bad
+    with pytest.raises(ext.SSDError, match="finite"):
+        ext.w4_quantize(weight, 32)
+
+
+@pytest.mark.parametrize("weight", [torch.zeros(4), torch.zeros(2, 3, 4)])
+def test_weights_that_are_no_matrix_are_refused(ext, weight):  # noqa: F811
+    with pytest.raises(ext.SSDError, match="2-D"):
+        ext.w4_quantize(weight, 32)
+
+
 def test_packing_nothing(ext):  # noqa: F811
     assert ext.w4_pack(torch.zeros(0, 5, dtype=torch.uint8)).shape == (0, 1, 32, 4)
