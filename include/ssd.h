@@ -412,8 +412,8 @@ ssd_status ssd_step(const ssd_step_args* args, ssd_stream_t stream);
  * enters exactly, fp32 x as the exact sum of three bf16 parts. */
 typedef struct {
   int64_t size;
-  int64_t tokens; /* >= 0 */
-  int32_t n, k, group, dtype; /* group 32, 64 or 128; dtype of x, add and y */
+  int64_t tokens; /* 0..65535 */
+  int32_t n, k, group, dtype; /* n, k <= 2^30; group 32, 64 or 128; dtype of x, add and y */
   const void* x;  /* rows [tokens][k] */
   int64_t x_token;
   const void* packed; /* 16-byte aligned */

@@ -275,7 +275,7 @@ ssd_status check_sizes(const ssd_w4_matvec_args* a) {
   if (a->tokens < 0 || a->n <= 0 || a->k <= 0) return SSD_ERR_INVALID_ARG;
   if (!known_dtype(a->dtype) || (a->group != 32 && a->group != 64 && a->group != 128) || a->tokens > 65535)
     return SSD_ERR_UNSUPPORTED;
-  return a->k > (1 << 30) ? SSD_ERR_UNSUPPORTED : SSD_OK;
+  return a->k > (1 << 30) || a->n > (1 << 30) ? SSD_ERR_UNSUPPORTED : SSD_OK;
 }
 
 // Whether x has to be laid out as columns first: 32-bit values, or rows that are not 16-byte vectors.

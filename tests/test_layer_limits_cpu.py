@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from test_layer_cpu import ext  # noqa: F401  (fixture)
+from test_layer_cpu import ext, step_args, w4_args  # noqa: F401  (ext: fixture)
 
 
 @pytest.mark.parametrize("code", [-1, 16, 255])
@@ -30,3 +30,9 @@ def test_weights_that_are_no_matrix_are_refused(ext, weight):  # noqa: F811
 
 def test_packing_nothing(ext):  # noqa: F811
     assert ext.w4_pack(torch.zeros(0, 5, dtype=torch.uint8)).shape == (0, 1, 32, 4)
+
+
+@pytest.mark.parametrize("big", [dict(n=2 ** 31 - 1), dict(n=2 ** 30 + 1), dict(k=2 ** 30 + 1)])
+def test_products_of_sizes_past_32_bits_are_refused(ext, big):  # noqa: F811
+    """Row tiles and rows are counted in 32 bits.  (Refused before anything is looked at.)"""
+    assert ext.lib.ssd_w4_matvec(w4_args(ext, **big, x=0, y=0, packed=0), None) == 2
