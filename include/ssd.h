@@ -393,7 +393,7 @@ typedef struct {
   const float* A;       /* [nheads] */
   const float* D;       /* [nheads] */
   const float* dt_bias; /* [nheads] or NULL */
-  void* ring;           /* [nslots][width][...], updated in place */
+  void* ring;           /* [nslots][width][...], updated in place; a row has fewer than 2^31 elements */
   const float* state;   /* [nslots][nheads][headdim][dstate], 16-byte aligned */
   float* new_state;     /* the state after the token; NULL: updated in place */
   const int32_t* positions; /* [batch] tokens before this one */

@@ -199,6 +199,9 @@ extern "C" ssd_status ssd_step(const ssd_step_args* a, ssd_stream_t stream) {
   if (!known_dtype(a->dtype) || (a->dt_dtype != a->dtype && a->dt_dtype != SSD_F32)) return SSD_ERR_UNSUPPORTED;
   if (a->headdim != kP || (a->dstate != 64 && a->dstate != 128 && a->dstate != 256)) return SSD_ERR_UNSUPPORTED;
   if (a->nheads % a->ngroups != 0 || a->width < 2 || a->width > 4 || a->batch > 65535) return SSD_ERR_UNSUPPORTED;
+  // offsets within a row of the ring are 32 bits
+  const int64_t channels = int64_t(a->nheads) * a->headdim + 2 * int64_t(a->ngroups) * a->dstate;
+  if (channels * a->width >= int64_t(1) << 31) return SSD_ERR_UNSUPPORTED;
   if (a->batch == 0) return SSD_OK;
   const size_t es = elem_size(a->dtype);
   for (const void* t : {a->u, (const void*)a->ring, (const void*)a->y})

@@ -36,3 +36,13 @@ def test_packing_nothing(ext):  # noqa: F811
 def test_products_of_sizes_past_32_bits_are_refused(ext, big):  # noqa: F811
     """Row tiles and rows are counted in 32 bits.  (Refused before anything is looked at.)"""
     assert ext.lib.ssd_w4_matvec(w4_args(ext, **big, x=0, y=0, packed=0), None) == 2
+
+
+@pytest.mark.parametrize("width,groups", [(4, 2 ** 20), (3, 3 * 2 ** 19), (2, 2 ** 21)])
+def test_step_rings_past_32_bits_are_refused(ext, width, groups):  # noqa: F811
+    """Offsets within a ring's row of width * channels are 32 bits: 576 channels a head here."""
+    args = dict(nheads=groups, ngroups=groups, dstate=256, width=width)
+    assert width * groups * 576 >= 2 ** 31
+    assert ext.lib.ssd_step(step_args(ext, **args, u=0, ring=0, state=0), None) == 2
+    most = (2 ** 31 - 1) // (width * 576)
+    assert ext.lib.ssd_step(step_args(ext, **{**args, "nheads": most, "ngroups": most}, u=0, ring=0, state=0), None) == 1
