@@ -140,8 +140,8 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(ConvParams p) {
     if (p.new_ring && len < W) {  // slots that no token of this call takes
 #pragma unroll
       for (int q = 0; q < W; ++q) {
-        v.load(ring + q * p.C);
-        v.store(keep + q * p.C);
+        v.load(ring + static_cast<int64_t>(q) * p.C);
+        v.store(keep + static_cast<int64_t>(q) * p.C);
       }
     }
     for (int64_t t = len > W ? len - W : 0; t < len; ++t) {

@@ -52,3 +52,15 @@ def test_flags_that_are_neither(ssd):
     for flag in ("delta_softplus", "want_final_state"):
         with pytest.raises(RuntimeError, match="ambiguous"):
             ssd.ssd_selective_scan(*scan, **{flag: two})
+
+
+def test_conv_ring_of_more_channels_than_32_bit_offsets_reach(ssd):
+    """The last of a ring's slots begins beyond 2^31 elements of its row."""
+    C, W = 720_000_016, 4
+    ring = torch.zeros(1, W, C, dtype=torch.bfloat16, device="cuda")
+    for q in range(W):
+        ring[0, q, ::4096], ring[0, q, -1] = 1.0 + q, 5.0 + q
+    new = torch.full_like(ring, 9.0)
+    ssd.ssd_conv_fwd(torch.empty(1, 0, C, dtype=torch.bfloat16, device="cuda"), torch.zeros(C, W, device="cuda"),
+                     ring=ring, new_ring=new)
+    assert torch.equal(ring, new)
