@@ -81,6 +81,22 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   return r;
 }
 
+// Loads past the L1, or of what is read once, that stay behind the waits in front of them (griddepcontrol.wait, the
+// acquire of a flag): volatile, with a clobber, where a plain hint is an expression that the compiler may move.
+__device__ __forceinline__ float4 load_once(const float* p) {
+  float4 v;
+  asm volatile("ld.global.cs.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "l"(__cvta_generic_to_global(p))
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint64_t load_l2(const uint64_t* p) {
+  uint64_t v;
+  asm volatile("ld.global.cg.b64 %0, [%1];" : "=l"(v) : "l"(__cvta_generic_to_global(p)) : "memory");
+  return v;
+}
+
 // ------------------------------------------------------------------ order of launches
 // Every kernel of these operators is launched as a programmatic dependent of the work before it in the
 // stream and begins with this: it waits until that work has completed and its results are visible

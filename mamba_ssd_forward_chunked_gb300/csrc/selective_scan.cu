@@ -333,7 +333,7 @@ __device__ __forceinline__ void walk(const ScanParams& p, int block, int64_t b, 
           p.seg_state[(b * p.segments * p.D + c0 + ch + k) * p.N + n] = p.init ? p.init[state_row + n] : 0.f;
       }
       a2[k][i] = pack2(a[0], a[1]);
-      h2[k][i] = w.from ? __ldcg(w.from + (k * kNS / 2 + i) * S::kThreads + tid) : pack2(h[0], h[1]);
+      h2[k][i] = w.from ? load_l2(w.from + (k * kNS / 2 + i) * S::kThreads + tid) : pack2(h[0], h[1]);
     }
   }
   if (!kState && p.segments > 1) {

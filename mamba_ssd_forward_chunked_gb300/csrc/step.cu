@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(kThreads) step_kernel(StepParams p) {
   for (int i = 0; i < kPasses; ++i)
 #pragma unroll
     for (int v = 0; v < kVecs; ++v)
-      st[i][v] = __ldcs(reinterpret_cast<const float4*>(from + i * kPerPass * N + v * 4 * kLanes));
+      st[i][v] = load_once(from + i * kPerPass * N + v * 4 * kLanes);
 
 #pragma unroll
   for (int e = 0; e < kEach; ++e) {

@@ -64,3 +64,26 @@ def test_products_after_each_other(ssd, dtype, M, width):
         ssd.ssd_w4_matvec(x, *layers[3], 64, y=y, add=x, workspace=space)
         return x, y
     alternate(chain, [torch.randn(M, width, generator=g).to(dtype).cuda() for _ in range(2)])
+
+
+@both_types
+@pytest.mark.parametrize("B,H,slots", [(1, 8, False), (24, 16, False), (24, 16, True)], ids=["one", "batch", "slots"])
+def test_steps_in_place(ssd, dtype, B, H, slots):
+    """Token after token on the same state and ring, which each launch finds as the one in front left them."""
+    g = torch.Generator().manual_seed(B)
+    rand = lambda *s: torch.randn(*s, generator=g).cuda()  # noqa: E731
+    N = 128
+    C = H * 64 + 2 * N
+    A, D, weight = -torch.rand(H, generator=g).cuda(), rand(H), rand(C, 4) * 0.5
+    state, ring = torch.empty(B, H, 64, N, device="cuda"), torch.empty(B, 4, C, dtype=dtype, device="cuda")
+    rows = torch.arange(B, dtype=torch.int32, device="cuda") if slots else None
+    positions = [torch.full((B,), t, dtype=torch.int32, device="cuda") for t in range(6)]
+    y = [torch.empty(B, H, 64, dtype=dtype, device="cuda") for _ in range(6)]
+
+    def chain(x):
+        u, dt = x
+        state.zero_()
+        for t in range(6):
+            ssd.ssd_step(u[t], dt[t], A, D, weight, None, state, ring, positions[t], dt_softplus=True, slots=rows, y=y[t])
+        return [state, ring, *y]
+    alternate(chain, [(rand(6, B, C).to(dtype), rand(6, B, H).to(dtype)) for _ in range(2)])
