@@ -327,7 +327,8 @@ typedef struct {
   const float* weight;       /* [channels][width] */
   const float* bias;         /* [channels] or NULL */
   const void* ring;          /* or NULL: nothing came before, nothing is kept */
-  void* new_ring;            /* the ring after the call; NULL: `ring` is updated in place */
+  void* new_ring;            /* the ring after the call, written in the rows of this call's sequences alone;
+                              * NULL: `ring` is updated in place */
   const int32_t* positions;  /* [batch] tokens before this call; NULL: 0 */
   const int32_t* lengths;    /* [batch] tokens of this call, taken into [0, seqlen]; NULL: seqlen */
   const int32_t* slots;      /* [batch] or NULL */

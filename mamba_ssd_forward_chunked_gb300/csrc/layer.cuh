@@ -98,10 +98,18 @@ __device__ __forceinline__ uint64_t load_l2(const uint64_t* p) {
 }
 
 // ------------------------------------------------------------------ order of launches
-// Every kernel of these operators is launched as a programmatic dependent of the work before it in the
-// stream and begins with this: it waits until that work has completed and its results are visible
-// (nothing is read or written before), and lets the next such kernel be set up meanwhile.  A decoding
-// loop's launches are a few us long, and this takes the set-up of each out of the chain.
+// These kernels are launched as programmatic dependents of the work before them in the stream and begin
+// with this: a wait until that work has completed and its results are visible (nothing is read or
+// written before), and the signal that lets the next such kernel be set up meanwhile.  A decoding loop's
+// launches are a few us long, and this takes the set-up of each out of the chain.  What differs:
+//  - whole-sequence scans of more than one block a multiprocessor start when the work before has ended
+//    (launch_lanes), and clear_kernel, in front of scan_slots_kernel, never signals, for the same reason;
+//  - scan_kernel's states' launch signals at its end, w4_kernel before its wait.  A signal only allows the
+//    next kernel to be set up; that kernel's own wait is for this one's completion all the same;
+//  - w4_kernel behind columns_kernel reads its codes before it waits: columns_kernel signals after its own
+//    wait, so by then nobody writes them.
+// What the kernel in front may write is read by ordinary or volatile loads, never through the read-only
+// path, which wants data that stay unchanged for as long as the kernel is resident.
 __device__ __forceinline__ void begin_kernel() {
   grid_dep_wait();
   grid_dep_launch();

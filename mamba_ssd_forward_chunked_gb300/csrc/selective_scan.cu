@@ -4,8 +4,9 @@
 //   y_t[c] = (sum_n h_t[c][n] C_t[n] + D[c] u_t[c]) silu(z_t[c]).
 //
 // Work and split.  Per token and state one exponential and three multiply-adds:
-// at 16 states the issue slots and the filling of registers from shared memory
-// bound it, not memory.  A block of 16 channels (32 for up to 8 states) walks
+// at 16 states latency bounds it, not memory and no unit (2 x 2048 x 5120 bf16:
+// issue slots 54 %, shared memory 63 %, special-function unit 31 %): the
+// registers leave each scheduler one warp of the recurrence.  A block of 16 channels (32 for up to 8 states) walks
 // down the tokens in tiles of 32, and has two sides that meet once a tile:
 //  - the recurrence: a lane keeps four states of two channels in registers (so
 //    a token's B and C are read once for both), T lanes share a channel,
@@ -18,13 +19,13 @@
 // With both sides' work in one warp a block's latency, not its work, set the
 // pace (2 x 2048 x 5120, 16 states, bf16: 304 us); with one warp for the memory
 // side 194, with two 165.  Four blocks on a multiprocessor take about 31 cycles
-// a token each, of which their instructions fill 24 (at two issue slots for an
-// f32x2); their recurrence warps lie on its four schedulers then.  With a fifth
-// two share one (2 x 2048 tokens, 16 states, bf16, 1, 2, 3, 4 and 5 blocks of 16
-// channels a multiprocessor: 88, 101, 115, 124 and 166 us), and a grid that
-// starts while the one in front still runs is spread as unevenly as that.  So
-// it starts alone, and numbers of blocks that do not divide evenly are cut in
-// runs that do (scan_slots_kernel; 2 x 2048 x 5120: 166 -> 141 us).
+// a token each, and issue in 54 % of them; their recurrence warps lie on its four
+// schedulers then.  With a fifth two share one (whole sequences of 2 x 2048
+// tokens, 16 states, bf16, 1, 2, 3, 4 and 5 blocks of 16 channels a
+// multiprocessor: 88, 101, 115, 124 and 166 us), and a grid that starts while the
+// one in front still runs is spread as unevenly as that.  So it starts alone, and
+// numbers of blocks that do not divide evenly are cut in runs that do
+// (scan_slots_kernel; 2 x 2048 x 5120: 166 -> 142 us).
 //
 // Segments.  With few channels a sequence is cut into segments that run side by
 // side: a first launch computes every segment's state from zero and its sum of
@@ -472,7 +473,7 @@ __global__ void __launch_bounds__(Shape<V, T>::kThreads + Shape<V, T>::kHelp, Sh
 // longer, below two, so a sequence is cut at most once.  A block walks its run's last part first: the earlier
 // tokens of a cut sequence are a block's first work and the later ones the next block's last, and by the time
 // that these begin the state at the cut has been there for (quota - tiles of a sequence) tiles.
-// 2 x 2048 tokens, 16 states, bf16, 5120, 5504, 6080 and 7296 channels: 141, 152, 166 and 204 us, whole sequences
+// 2 x 2048 tokens, 16 states, bf16, 5120, 5504, 6080 and 7296 channels: 142, 154, 169 and 206 us, whole sequences
 // 166, 166, 166 and 219.  The loop over walks costs some 8 % of the rate (one walk alone 124 us, in the loop 134: the
 // memory side waits for loads it holds across it); the walks written out one after the other cost more where the
 // blocks of a multiprocessor are in different ones (5504: 182).

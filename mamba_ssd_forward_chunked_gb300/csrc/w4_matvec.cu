@@ -21,8 +21,9 @@
 //
 // A block takes 16 or 32 rows; its warps take pairs of column tiles in turn and
 // their sums are joined in shared memory in a fixed order.  2560 -> 10576, one
-// bf16 token: 6.1 us (2.4 TB/s, one wave of loads and a join: latency); 5120 ->
-// 2560, eight: 5.6 us; 8001 -> 16001, 16 fp32 tokens: 90 us.
+// bf16 token: 6.2 us (2.3 TB/s; codes, then x and scales, then a join: latency, in
+// 661 blocks of which 608 are resident); 5120 -> 2560, eight: 5.7 us; 8001 ->
+// 16001, 16 fp32 tokens: 96 us.
 #include "layer.cuh"
 
 namespace ssd {
@@ -225,7 +226,7 @@ cudaError_t launch_tiles(const W4Params& p, cudaStream_t stream) {
 }
 
 // From two blocks of columns on, x is more bytes than the codes for every row tile: two tiles share it
-// where there are rows enough to fill the GPU all the same (8001 -> 16001, 16 fp32 tokens 156 -> 90 us,
+// where there are rows enough to fill the GPU all the same (8001 -> 16001, 16 fp32 tokens 156 -> 96 us,
 // 16 bf16 tokens 47 -> 44).
 template <typename T, int kCols, int kGroup, bool kDirect>
 cudaError_t launch_cols(const W4Params& p, cudaStream_t stream) {

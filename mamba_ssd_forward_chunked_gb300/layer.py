@@ -78,10 +78,10 @@ def ssd_conv_fwd(u: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Ten
     ``split`` gives the channels of two or three outputs, e.g. (H*64, G*N, G*N)
     for x, Bm and Cm as ssd_fwd takes them; without it there is one output.
     ``ring`` [slots, W, C] is the cache: the inputs of the last tokens, updated
-    in place or written to ``new_ring``.  ``positions`` [B] int32 are the tokens
-    before this call (0), ``lengths`` [B] int32 this call's tokens (L; outputs
-    after them are 0), ``slots`` [B] int32 the cache rows (the first B; a
-    sequence whose row does not exist is idle)."""
+    in place or written to ``new_ring`` (only the rows of this call's sequences).
+    ``positions`` [B] int32 are the tokens before this call (0), ``lengths`` [B]
+    int32 this call's tokens (L; outputs after them are 0), ``slots`` [B] int32
+    the cache rows (the first B; a sequence whose row does not exist is idle)."""
     args = (u, weight, bias, activation, split, ring, positions, lengths, slots, new_ring, out)
     return _binding.conv_fwd(*args) if stream is None else _on(stream, _binding.conv_fwd, *args)
 
