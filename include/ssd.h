@@ -284,8 +284,9 @@ ssd_status ssd_fwd_static_scratch(const ssd_shape* shape, const void* x, const f
 /* ===========================================================================
  * The layer around ssd_fwd, for serving: the short causal convolution in front
  * of it, the selective scan (a decay per channel and state instead of one per
- * head), the single-token form of both recurrences, products of a few tokens
- * with 4-bit weights, and beam search's selection and reordering of states.
+ * head), the single-token form of both recurrences, the gated delta rule,
+ * products of a few tokens with 4-bit weights, beam search's selection and
+ * reordering of states, and the verification of drafted tokens.
  * The pages describe none of these; the formulas are stated with each call.
  *
  * Each call takes one argument struct.  Its first field is the struct's own
@@ -473,6 +474,82 @@ typedef struct {
 } ssd_beam_reorder_args;
 
 ssd_status ssd_beam_reorder(const ssd_beam_reorder_args* args, ssd_stream_t stream);
+
+/* The gated delta rule: the recurrence of ssd_fwd, but what the state already
+ * returns for the key b_t = Bm_t is taken off the value before it is written:
+ *     h' = exp(dt_t * A_h) * h_{t-1}
+ *     h_t = h' + beta_t * (x_t - h' b_t) b_t^T,      y_t = scale * h_t c_t
+ * for t < lengths[b]; y is 0 after that and the state stays.  Head h reads group
+ * h / (nheads/ngroups) of Bm and Cm.  dt is dt + dt_bias, through softplus where
+ * set; beta goes through a sigmoid where set; with norm_eps >= 0 every row v of
+ * Bm and Cm counts as v / sqrt(|v|^2 + norm_eps) (a row of zeros as zeros).
+ * State, decay and sums are 32 bits.  Any seqlen: whole prompts, a few drafted
+ * tokens, single tokens.  Sequence b's state is row slots[b] (as for the caches
+ * above) of init_state and final_state, which may be one tensor, updated in
+ * place, and must not overlap otherwise; a sequence at position 0 starts from 0
+ * whatever its row holds.  Rows of final_state that no sequence of the call has
+ * stay as they are. */
+typedef struct {
+  int64_t size;
+  int64_t batch, seqlen;    /* batch <= 65535, seqlen <= 2^30 */
+  int64_t nslots;           /* rows of the states; >= batch where slots is NULL */
+  int32_t nheads, headdim, ngroups, dstate; /* headdim a multiple of 16, <= 1024; dstate 64, 128 or 256 */
+  int32_t dtype, gate_dtype; /* of x, Bm, Cm, y; of dt and beta (dtype or SSD_F32) */
+  int32_t dt_softplus, beta_sigmoid;
+  float scale, norm_eps;    /* finite; norm_eps < 0: Bm and Cm as they are */
+  const void *x, *Bm, *Cm;  /* [batch][seqlen][nheads][headdim], [..][ngroups][dstate], the last two dimensions contiguous */
+  int64_t x_batch, x_token, B_batch, B_token, C_batch, C_token;
+  const void *dt, *beta;    /* rows [batch][seqlen][nheads] */
+  int64_t dt_batch, dt_token, beta_batch, beta_token;
+  const float* A;           /* [nheads] */
+  const float* dt_bias;     /* [nheads] or NULL (0) */
+  const float* init_state;  /* [nslots][nheads][headdim][dstate] or NULL (0), 16-byte aligned */
+  float* final_state;       /* the same shape, or NULL, 16-byte aligned */
+  const int32_t* slots;     /* [batch] or NULL */
+  const int32_t* positions; /* [batch] tokens before this call; NULL: every sequence has a state */
+  const int32_t* lengths;   /* [batch] tokens of this call, taken into [0, seqlen]; NULL: seqlen */
+  void* y;                  /* [batch][seqlen][nheads][headdim] */
+} ssd_delta_args;
+
+ssd_status ssd_delta_fwd(const ssd_delta_args* args, ssd_stream_t stream);
+
+/* Verification of drafted tokens (speculative decoding).  With p_i and q_i the
+ * softmax of scale[b] * logits[b][i] and scale[b] * draft_logits[b][i] (without
+ * draft_logits, all of q_i is at the drafted token: a draft that was looked up),
+ * draft i is accepted while uniforms[b][i] * q_i(draft_i) < p_i(draft_i).  Let n
+ * be the first that is not, or lengths[b].  Then one token is drawn from
+ * max(p_n - q_n, 0) (from p_n where n is lengths[b], or where nothing is left of
+ * the difference): the first v whose sum up to v is above uniforms[b][drafts]
+ * times the sum of all.  tokens[b] = the n accepted drafts, that token, then -1;
+ * accepted[b] = n; logprobs = log p of each token, 0 beside a -1.  n + 1 is the
+ * number of tokens to commit where the model has run on the last token and the
+ * drafts: the `lengths` of ssd_conv_fwd, ssd_selective_scan and ssd_delta_fwd.
+ * A NaN logit counts as -infinity; a row with +infinity is shared by its
+ * infinities.  A drafted token outside the vocabulary is not accepted, and
+ * nothing is taken off p for it.  Where the target's row allows no token, or
+ * scale[b] is not positive and finite (then n is 0), -1 is drawn. */
+typedef struct {
+  int64_t size;
+  int64_t batch; /* <= 65535 */
+  int32_t drafts, vocab, dtype, reserved; /* drafts 0..64; vocab <= 2^24; dtype of both logits */
+  const void* logits;       /* rows [batch][drafts + 1][vocab] */
+  int64_t logits_batch, logits_row;
+  const void* draft_logits; /* rows [batch][drafts][vocab] or NULL */
+  int64_t draft_logits_batch, draft_logits_row;
+  const int32_t* draft;     /* [batch][drafts] */
+  const float* uniforms;    /* [batch][drafts + 1], in [0, 1) */
+  const float* scale;       /* [batch] or NULL (1): the inverse of the temperature */
+  const int32_t* lengths;   /* [batch] drafts of each sequence, taken into [0, drafts]; NULL: drafts */
+  int32_t* tokens;          /* [batch][drafts + 1] */
+  int32_t* accepted;        /* [batch] */
+  float* logprobs;          /* [batch][drafts + 1] */
+  void* workspace;          /* 16-byte aligned */
+  size_t workspace_bytes;
+} ssd_draft_verify_args;
+
+/* Bytes of workspace on the current device; batch, drafts, vocab, dtype and whether draft_logits is NULL are read. */
+size_t ssd_draft_verify_workspace_size(const ssd_draft_verify_args* args);
+ssd_status ssd_draft_verify(const ssd_draft_verify_args* args, ssd_stream_t stream);
 
 #ifdef __cplusplus
 }

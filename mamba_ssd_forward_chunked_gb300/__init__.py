@@ -29,7 +29,8 @@ EXPORTS = ("ssd_status_string", "ssd_validate_shape", "ssd_fwd_workspace_layout"
            "ssd_fwd_fused", "ssd_fused_pass", "ssd_fwd_range", "ssd_causal_cb",
            "ssd_conv_fwd", "ssd_selective_scan", "ssd_selective_scan_workspace_size", "ssd_debug_scan_handover",
            "ssd_step", "ssd_w4_matvec",
-           "ssd_w4_matvec_workspace_size", "ssd_beam_select", "ssd_beam_select_workspace_size", "ssd_beam_reorder")
+           "ssd_w4_matvec_workspace_size", "ssd_beam_select", "ssd_beam_select_workspace_size", "ssd_beam_reorder",
+           "ssd_delta_fwd", "ssd_draft_verify", "ssd_draft_verify_workspace_size")
 
 # Size of the library's own workspace array used by ssd_fwd_static_scratch.
 SSD_STATIC_SCRATCH_BYTES = 32 << 20
@@ -102,12 +103,13 @@ def _load() -> ctypes.CDLL:
     lib.ssd_fwd_static_scratch.restype = c_int
     lib.ssd_fwd_static_scratch.argtypes = [sp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
     for name in ("ssd_conv_fwd", "ssd_selective_scan", "ssd_step", "ssd_w4_matvec", "ssd_beam_select",
-                 "ssd_beam_reorder"):  # (argument struct, stream)
+                 "ssd_beam_reorder", "ssd_delta_fwd", "ssd_draft_verify"):  # (argument struct, stream)
         getattr(lib, name).restype = c_int
         getattr(lib, name).argtypes = [vp, vp]
     lib.ssd_debug_scan_handover.restype = c_int
     lib.ssd_debug_scan_handover.argtypes = [vp, ctypes.c_int32, vp]
-    for name in ("ssd_selective_scan_workspace_size", "ssd_w4_matvec_workspace_size", "ssd_beam_select_workspace_size"):
+    for name in ("ssd_selective_scan_workspace_size", "ssd_w4_matvec_workspace_size", "ssd_beam_select_workspace_size",
+                 "ssd_draft_verify_workspace_size"):
         getattr(lib, name).restype = sz
         getattr(lib, name).argtypes = [vp]
     return lib
@@ -507,5 +509,5 @@ def ssd_fwd_static_scratch(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B
 
 # The layer around ssd_fwd (convolution, selective scan, single tokens, 4-bit products, beam search).
 from .layer import (ssd_beam_reorder, ssd_beam_select, ssd_beam_select_workspace_size, ssd_conv_fwd,  # noqa: E402
-                    ssd_selective_scan, ssd_selective_scan_workspace_size, ssd_step, ssd_w4_matvec, w4_pack,
-                    w4_quantize)
+                    ssd_delta_fwd, ssd_draft_verify, ssd_draft_verify_workspace_size, ssd_selective_scan,
+                    ssd_selective_scan_workspace_size, ssd_step, ssd_w4_matvec, w4_pack, w4_quantize)

@@ -15,6 +15,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <initializer_list>
 #include <string>
 #include <vector>
@@ -86,6 +87,14 @@ const void* rows(PyObject* o, const char* name, int dev, at::ScalarType type, at
     throw Refused{1, std::string(name) + " must be contiguous in its last dimension"};
   return t.data_ptr();
 }
+// The address of a tensor [batch][seqlen][...] whose last two dimensions are contiguous.
+const void* inner(PyObject* o, const char* name, int dev, at::ScalarType type, at::IntArrayRef shape) {
+  const void* at = rows(o, name, dev, type, shape);
+  const at::Tensor& t = THPVariable_Unpack(o);
+  if (shape[2] > 1 && t.stride(2) != shape[3])
+    throw Refused{1, std::string(name) + " must be contiguous in its last two dimensions"};
+  return at;
+}
 int64_t stride(PyObject* o, int d) { return THPVariable_Unpack(o).stride(d); }
 
 at::Tensor empty(at::IntArrayRef shape, at::ScalarType type, const at::Tensor& like) {
@@ -99,6 +108,15 @@ int64_t whole(PyObject* o, const char* name) {
     throw Refused{1, std::string(name) + " must be a whole number"};
   }
   return v;
+}
+
+float real(PyObject* o, const char* name) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) {
+    PyErr_Clear();
+    throw Refused{1, std::string(name) + " must be a number"};
+  }
+  return static_cast<float>(v);
 }
 
 bool truth(PyObject* o) {
@@ -447,6 +465,106 @@ PyObject* beam_reorder(PyObject* const* p) {
   return r;
 }
 
+// x, dt, A, Bm, Cm, beta, scale, dt_bias, dt_softplus, beta_sigmoid, norm_eps, init_state, slots, positions, lengths, y,
+// final_state, want_final_state
+PyObject* delta_fwd(PyObject* const* p) {
+  const First x = first(p[0], "x", 4);
+  const On device(x.dev);
+  const int64_t B = x.t.size(0), L = x.t.size(1), H = x.t.size(2), P = x.t.size(3);
+  if (!THPVariable_Check(p[3]) || THPVariable_Unpack(p[3]).dim() != 4) throw Refused{1, "Bm must be a 4-D tensor"};
+  const int64_t G = THPVariable_Unpack(p[3]).size(2), N = THPVariable_Unpack(p[3]).size(3);
+  ssd_delta_args a{};
+  a.batch = B, a.seqlen = L, a.nheads = small(H, "nheads"), a.headdim = small(P, "headdim");
+  a.ngroups = small(G, "ngroups"), a.dstate = small(N, "dstate"), a.dtype = x.dtype;
+  a.scale = p[6] == Py_None ? static_cast<float>(1.0 / std::sqrt(static_cast<double>(N))) : real(p[6], "scale");
+  a.norm_eps = p[10] == Py_None ? -1.f : real(p[10], "norm_eps");
+  if (p[10] != Py_None && !(a.norm_eps >= 0.f)) throw Refused{1, "norm_eps must not be negative"};
+  a.dt_softplus = truth(p[8]), a.beta_sigmoid = truth(p[9]);
+  a.x = inner(p[0], "x", x.dev, x.type, {B, L, H, P});
+  a.x_batch = x.t.stride(0), a.x_token = x.t.stride(1);
+  a.Bm = inner(p[3], "Bm", x.dev, x.type, {B, L, G, N});
+  a.B_batch = stride(p[3], 0), a.B_token = stride(p[3], 1);
+  a.Cm = inner(p[4], "Cm", x.dev, x.type, {B, L, G, N});
+  a.C_batch = stride(p[4], 0), a.C_token = stride(p[4], 1);
+  const bool gates32 = THPVariable_Check(p[1]) && THPVariable_Unpack(p[1]).scalar_type() == at::kFloat;
+  a.gate_dtype = gates32 ? static_cast<int>(SSD_F32) : x.dtype;
+  const at::ScalarType gates = gates32 ? at::kFloat : x.type;
+  a.dt = rows(p[1], "dt", x.dev, gates, {B, L, H});
+  a.dt_batch = stride(p[1], 0), a.dt_token = stride(p[1], 1);
+  a.beta = rows(p[5], "beta", x.dev, gates, {B, L, H});
+  a.beta_batch = stride(p[5], 0), a.beta_token = stride(p[5], 1);
+  if (p[2] == Py_None) throw Refused{1, "A must be a torch.Tensor"};
+  a.A = dense<const float>(p[2], "A", x.dev, at::kFloat, {H});
+  a.dt_bias = dense<const float>(p[7], "dt_bias", x.dev, at::kFloat, {H});
+  const bool want = truth(p[17]);
+  a.nslots = B;
+  for (int i : {11, 16})
+    if (p[i] != Py_None) a.nslots = tensor(p[i], i == 11 ? "init_state" : "final_state").dim() == 4 ? THPVariable_Unpack(p[i]).size(0) : 0;
+  a.init_state = dense<const float>(p[11], "init_state", x.dev, at::kFloat, {a.nslots, H, P, N});
+  a.final_state = dense<float>(p[16], "final_state", x.dev, at::kFloat, {a.nslots, H, P, N});
+  a.slots = dense<const int32_t>(p[12], "slots", x.dev, at::kInt, {B});
+  a.positions = dense<const int32_t>(p[13], "positions", x.dev, at::kInt, {B});
+  a.lengths = dense<const int32_t>(p[14], "lengths", x.dev, at::kInt, {B});
+  if (p[12] != Py_None && p[11] == Py_None && p[16] == Py_None) throw Refused{1, "slots belong to states"};
+  dense<void>(p[15], "y", x.dev, x.type, {B, L, H, P});
+  const at::Tensor y = p[15] != Py_None ? tensor(p[15], "y") : empty({B, L, H, P}, x.type, x.t);
+  a.y = y.data_ptr();
+  at::Tensor final_state;
+  if (p[16] != Py_None) {
+    final_state = tensor(p[16], "final_state");
+  } else if (want) {
+    if (p[12] != Py_None) throw Refused{1, "with slots, final_state must be given"};
+    final_state = empty({a.nslots, H, P, N}, at::kFloat, x.t);
+    a.final_state = static_cast<float*>(final_state.data_ptr());
+  }
+  call(ssd_delta_fwd, "ssd_delta_fwd", a, x.dev);
+  if (final_state.defined()) return wrap_all({y, final_state});
+  PyObject* r = PyTuple_New(2);
+  if (!r) throw PythonError{};
+  PyTuple_SET_ITEM(r, 1, Py_NewRef(Py_None));
+  PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(y));
+  return r;
+}
+
+// logits, draft, uniforms, draft_logits, scale, lengths, workspace
+PyObject* draft_verify(PyObject* const* p) {
+  const First x = first(p[0], "logits", 3);
+  const On device(x.dev);
+  const int64_t B = x.t.size(0), T = x.t.size(1) - 1, V = x.t.size(2);
+  if (T < 0) throw Refused{1, "logits must have a row for every draft and one more"};
+  ssd_draft_verify_args a{};
+  a.batch = B, a.drafts = small(T, "drafts"), a.vocab = small(V, "vocab"), a.dtype = x.dtype;
+  a.logits = rows(p[0], "logits", x.dev, x.type, {B, T + 1, V});
+  a.logits_batch = x.t.stride(0), a.logits_row = x.t.stride(1);
+  for (int i : {1, 2})
+    if (p[i] == Py_None) throw Refused{1, "draft and uniforms must be tensors"};
+  a.draft = dense<const int32_t>(p[1], "draft", x.dev, at::kInt, {B, T});
+  a.uniforms = dense<const float>(p[2], "uniforms", x.dev, at::kFloat, {B, T + 1});
+  if (p[3] != Py_None && T > 0) {
+    a.draft_logits = rows(p[3], "draft_logits", x.dev, x.type, {B, T, V});
+    a.draft_logits_batch = stride(p[3], 0), a.draft_logits_row = stride(p[3], 1);
+  }
+  a.scale = dense<const float>(p[4], "scale", x.dev, at::kFloat, {B});
+  a.lengths = dense<const int32_t>(p[5], "lengths", x.dev, at::kInt, {B});
+  a.size = sizeof(a);
+  at::Tensor space;
+  if (p[6] != Py_None) {
+    const int64_t bytes = tensor(p[6], "workspace").numel();
+    a.workspace = dense<void>(p[6], "workspace", x.dev, at::kByte, {bytes});
+    a.workspace_bytes = static_cast<size_t>(bytes);
+  } else {
+    a.workspace_bytes = ssd_draft_verify_workspace_size(&a);
+    space = empty({static_cast<int64_t>(a.workspace_bytes)}, at::kByte, x.t);
+    a.workspace = space.data_ptr();
+  }
+  const at::Tensor tokens = empty({B, T + 1}, at::kInt, x.t), accepted = empty({B}, at::kInt, x.t),
+                   logprobs = empty({B, T + 1}, at::kFloat, x.t);
+  a.tokens = static_cast<int32_t*>(tokens.data_ptr()), a.accepted = static_cast<int32_t*>(accepted.data_ptr());
+  a.logprobs = static_cast<float*>(logprobs.data_ptr());
+  call(ssd_draft_verify, "ssd_draft_verify", a, x.dev);
+  return wrap_all({tokens, accepted, logprobs});
+}
+
 // batch, seqlen, channels, dstate, ngroups
 PyObject* scan_workspace(PyObject* const* p) {
   ssd_selective_scan_args a{};
@@ -463,6 +581,16 @@ PyObject* select_workspace(PyObject* const* p) {
   a.batch = whole(p[0], "batch"), a.beams = small(whole(p[1], "beams"), "beams");
   a.vocab = small(whole(p[2], "vocab"), "vocab"), a.k = small(whole(p[3], "k"), "k");
   return PyLong_FromSize_t(ssd_beam_select_workspace_size(&a));
+}
+
+// batch, drafts, vocab, bf16, draft_logits
+PyObject* verify_workspace(PyObject* const* p) {
+  ssd_draft_verify_args a{};
+  a.size = sizeof(a);
+  a.batch = whole(p[0], "batch"), a.drafts = small(whole(p[1], "drafts"), "drafts");
+  a.vocab = small(whole(p[2], "vocab"), "vocab"), a.dtype = truth(p[3]) ? SSD_BF16 : SSD_F32;
+  a.draft_logits = truth(p[4]) && a.drafts > 0 ? &a : nullptr;  // whether there are any is all that is read
+  return PyLong_FromSize_t(ssd_draft_verify_workspace_size(&a));
 }
 
 // No C++ exception leaves the module.
@@ -508,8 +636,11 @@ PyMODINIT_FUNC PyInit__layer_binding() {
       method<w4_matvec, 7>("w4_matvec"),
       method<beam_select, 6>("beam_select"),
       method<beam_reorder, 3>("beam_reorder"),
+      method<delta_fwd, 18>("delta_fwd"),
+      method<draft_verify, 7>("draft_verify"),
       method<scan_workspace, 5>("scan_workspace"),
       method<select_workspace, 4>("select_workspace"),
+      method<verify_workspace, 5>("verify_workspace"),
       {nullptr, nullptr, 0, nullptr},
   };
   static PyModuleDef def = {PyModuleDef_HEAD_INIT, "_layer_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

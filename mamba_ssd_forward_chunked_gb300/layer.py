@@ -2,9 +2,12 @@
 ``include/ssd.h`` describes under "The layer around ssd_fwd".
 
 A prompt runs through ``ssd_conv_fwd`` and then ``ssd_fwd`` (or, with a decay
-per channel and state, ``ssd_selective_scan``); every further token through
-``ssd_w4_matvec`` (the projections), ``ssd_step`` and, for beam search,
-``ssd_beam_select`` and ``ssd_beam_reorder``.
+per channel and state, ``ssd_selective_scan``; or, with the delta rule,
+``ssd_delta_fwd``); every further token through ``ssd_w4_matvec`` (the
+projections), ``ssd_step`` (or the same calls as the prompt) and, for beam
+search, ``ssd_beam_select`` and ``ssd_beam_reorder``.  With drafted tokens the
+model runs on several at a time, ``ssd_draft_verify`` says how many hold, and
+their number is the ``lengths`` with which the states are committed.
 
 As in the rest of the package nothing is computed here: tensors are checked,
 outputs that are not given are allocated, and the C entry point of the same
@@ -44,7 +47,8 @@ else:
     _binding.set_error(SSDError)
 
 __all__ = ["ssd_conv_fwd", "ssd_selective_scan", "ssd_step", "ssd_w4_matvec", "ssd_beam_select", "ssd_beam_reorder",
-           "ssd_selective_scan_workspace_size", "ssd_beam_select_workspace_size", "w4_pack", "w4_quantize"]
+           "ssd_selective_scan_workspace_size", "ssd_beam_select_workspace_size", "w4_pack", "w4_quantize",
+           "ssd_delta_fwd", "ssd_draft_verify", "ssd_draft_verify_workspace_size"]
 
 
 def _on(stream, fn, *args):
@@ -134,6 +138,33 @@ def ssd_step(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, D: torch.Tensor
     return _binding.step(*args) if stream is None else _on(stream, _binding.step, *args)
 
 
+# ------------------------------------------------------------------ delta rule
+
+def ssd_delta_fwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, Bm: torch.Tensor, Cm: torch.Tensor,
+                  beta: torch.Tensor, *, scale: Optional[float] = None, dt_bias: Optional[torch.Tensor] = None,
+                  dt_softplus: bool = False, beta_sigmoid: bool = False, norm_eps: Optional[float] = None,
+                  init_state: Optional[torch.Tensor] = None, slots: Optional[torch.Tensor] = None,
+                  positions: Optional[torch.Tensor] = None, lengths: Optional[torch.Tensor] = None,
+                  y: Optional[torch.Tensor] = None, final_state: Optional[torch.Tensor] = None,
+                  want_final_state: bool = True, stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """The gated delta rule (C: ssd_delta_fwd), for prompts, a few drafted tokens
+    and single tokens.  Returns (y, final_state).
+
+    x [B, L, H, P] (P a multiple of 16), Bm and Cm [B, L, G, N] (N 64, 128 or
+    256) share float32 or bfloat16 and may be slices of wider rows; dt and beta
+    [B, L, H] have that type or float32.  A, dt_bias [H] and the states
+    [slots, H, P, N] are float32.  ``scale`` is 1/sqrt(N) unless given;
+    ``norm_eps`` normalises the rows of Bm and Cm.  ``slots`` [B] int32 are the
+    rows of the states (the first B; a sequence whose row does not exist is
+    idle), ``positions`` [B] int32 the tokens before this call (a sequence at 0
+    starts from a state of 0), ``lengths`` [B] int32 this call's tokens (L;
+    outputs after them are 0).  final_state may be init_state; with ``slots`` it
+    has to be given (or ``want_final_state=False``)."""
+    args = (x, dt, A, Bm, Cm, beta, scale, dt_bias, dt_softplus, beta_sigmoid, norm_eps, init_state, slots, positions,
+            lengths, y, final_state, want_final_state)
+    return _binding.delta_fwd(*args) if stream is None else _on(stream, _binding.delta_fwd, *args)
+
+
 # ------------------------------------------------------------------ 4-bit weights
 
 def w4_pack(codes: torch.Tensor) -> torch.Tensor:
@@ -217,3 +248,29 @@ def ssd_beam_reorder(states: Sequence[torch.Tensor], parents: torch.Tensor, *,
     reordered tensors."""
     args = (states, parents, out)
     return _binding.beam_reorder(*args) if stream is None else _on(stream, _binding.beam_reorder, *args)
+
+
+# ------------------------------------------------------------------ drafted tokens
+
+def ssd_draft_verify_workspace_size(batch: int, drafts: int, vocab: int, dtype: torch.dtype, draft_logits: bool) -> int:
+    """Bytes of workspace ssd_draft_verify needs for these sizes on the current device."""
+    return _binding.verify_workspace(batch, drafts, vocab, dtype == torch.bfloat16, draft_logits)
+
+
+def ssd_draft_verify(logits: torch.Tensor, draft: torch.Tensor, uniforms: torch.Tensor, *,
+                     draft_logits: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+                     lengths: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                     stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """How many drafted tokens the target's probabilities accept, and the token
+    after them (C: ssd_draft_verify).  Returns (tokens [B, T+1] int32: the
+    accepted drafts, the drawn token, then -1; accepted [B] int32; log-probabilities
+    [B, T+1] float32 of the tokens).
+
+    logits [B, T+1, V] and ``draft_logits`` [B, T, V] float32 or bfloat16 (rows
+    may be strided) are the target's and the draft model's; without the latter
+    the drafts count as certain.  draft [B, T] int32, uniforms [B, T+1] float32 in
+    [0, 1) (one for every draft, the last for the drawn token), ``scale`` [B]
+    float32 the inverse temperatures (1), ``lengths`` [B] int32 the drafts of each
+    sequence (T)."""
+    args = (logits, draft, uniforms, draft_logits, scale, lengths, workspace)
+    return _binding.draft_verify(*args) if stream is None else _on(stream, _binding.draft_verify, *args)

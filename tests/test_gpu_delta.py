@@ -1,0 +1,145 @@
+"""The gated delta rule against its recurrence in 64 bits."""
+import pytest
+import torch
+
+import delta_ref as ref
+from layer_ref import check, store
+
+pytestmark = pytest.mark.gpu
+
+NORM = 1e-6
+
+
+@pytest.fixture(scope="module")
+def ssd():
+    import mamba_ssd_forward_chunked_gb300 as m
+    return m
+
+
+def inputs(B, L, H, G, P, N, dtype=torch.float32, cached=False, seed=0, gates=None):
+    g = torch.Generator().manual_seed(seed)
+    rand = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    gates = gates or dtype
+    a = dict(x=rand(B, L, H, P).to(dtype), dt=(rand(B, L, H) * 0.5).to(gates), A=-torch.exp(torch.rand(H, generator=g) * 2.7),
+             Bm=rand(B, L, G, N).to(dtype), Cm=rand(B, L, G, N).to(dtype), beta=rand(B, L, H).to(gates))
+    o = dict(dt_bias=torch.linspace(-5.0, -2.0, H), dt_softplus=True, beta_sigmoid=True, norm_eps=NORM)
+    if cached:
+        S = B + 2
+        o["init_state"] = rand(S, H, P, N) * 0.3
+        o["slots"] = torch.randperm(S, generator=g)[:B].to(torch.int32)
+        o["final_state"] = torch.full((S, H, P, N), 7.0)
+    return a, o
+
+
+def to(d, dev="cuda"):
+    return {k: v.to(dev) if isinstance(v, torch.Tensor) else v for k, v in d.items()}
+
+
+def run(ssd, a, o, spread=1.0, **more):
+    y, final = ssd.ssd_delta_fwd(**to(a), **to({**o, **more}))
+    torch.cuda.synchronize()
+    ry, by, rf, bf = ref.delta(**a, **{k: v for k, v in {**o, **more}.items() if k not in ("want_final_state", "y")}, spread=spread)
+    check("y", y, ry, store(ry, by, a["x"].dtype))
+    if final is not None:
+        check("final", final, rf, bf)
+    return y, final
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("B,L,H,G,P,N", [
+    (1, 1, 1, 1, 128, 128), (2, 1, 3, 1, 64, 64), (3, 5, 4, 2, 128, 128), (2, 16, 2, 2, 16, 128), (1, 17, 6, 3, 48, 64),
+    (2, 33, 4, 1, 80, 256), (1, 31, 2, 1, 272, 128), (5, 2, 2, 2, 128, 256), (1, 1, 2, 1, 1024, 64)])
+def test_tokens(ssd, B, L, H, G, P, N, dtype):
+    a, o = inputs(B, L, H, G, P, N, dtype, seed=L + P)
+    run(ssd, a, o)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("L", [1, 4, 19, 40])
+def test_cache_rows_lengths_and_positions(ssd, L, dtype):
+    a, o = inputs(5, L, 4, 2, 128, 128, dtype, cached=True, seed=3)
+    o["lengths"] = torch.tensor([L, 0, L - 1, -3, L + 9], dtype=torch.int32)
+    o["positions"] = torch.tensor([4, 2, 0, 0, 1], dtype=torch.int32)
+    run(ssd, a, o)
+    o["slots"][0], o["slots"][4] = 7, -1  # idle
+    y, final = run(ssd, a, o)
+    assert not y[0].any() and not y[4].any()
+
+
+def test_rows_of_nobody_stay(ssd):
+    a, o = inputs(2, 3, 2, 1, 64, 64, cached=True)
+    o["slots"] = torch.tensor([3, 1], dtype=torch.int32)
+    _, final = run(ssd, a, o)
+    assert (final[[0, 2]] == 7.0).all()
+
+
+def test_in_place_and_without_a_state(ssd):
+    a, o = inputs(3, 9, 4, 2, 128, 128, torch.bfloat16, cached=True, seed=5)
+    y, final = run(ssd, a, o)
+    state = o["init_state"].cuda()
+    y2, same = ssd.ssd_delta_fwd(**to(a), **to({**o, "init_state": state, "final_state": state}))
+    assert same.data_ptr() == state.data_ptr() and torch.equal(y, y2)
+    rows = o["slots"].long().cuda()
+    assert torch.equal(state[rows], final[rows])
+    others = [i for i in range(5) if i not in o["slots"].tolist()]
+    assert torch.equal(state[others].cpu(), o["init_state"][others])
+    y3, none = ssd.ssd_delta_fwd(**to(a), **to({**o, "final_state": None, "want_final_state": False}))
+    assert none is None and torch.equal(y, y3)
+
+
+def test_plain_arguments(ssd):
+    """No norms, no activations, a scale of its own, 32-bit gates beside bf16."""
+    a, o = inputs(2, 11, 2, 2, 64, 64, torch.bfloat16, gates=torch.float32, seed=9)
+    a["Bm"], a["Cm"] = a["Bm"] * 0.125, a["Cm"] * 0.5
+    a["dt"], a["beta"] = a["dt"].abs() * 0.1, torch.rand(2, 11, 2) * 2
+    run(ssd, a, dict(scale=-0.75))
+
+
+def test_strides(ssd):
+    B, L, H, G, P, N = 2, 21, 4, 2, 64, 128
+    a, o = inputs(B, L, H, G, P, N, torch.bfloat16, seed=2)
+    for pad in (0, 8, 3):  # 16-byte rows and others
+        wide = torch.zeros(B, L, H * P + 2 * G * N + 2 * H + pad, dtype=torch.bfloat16)
+        parts = [H * P, G * N, G * N, H, H]
+        views = [v.unflatten(2, s) if s else v for v, s in zip(wide[:, :, pad:].split(parts, 2), [(H, P), (G, N), (G, N), None, None])]
+        for v, k in zip(views, ("x", "Bm", "Cm", "dt", "beta")):
+            v.copy_(a[k])
+        dev = wide.cuda()
+        views = [v.unflatten(2, s) if s else v for v, s in zip(dev[:, :, pad:].split(parts, 2), [(H, P), (G, N), (G, N), None, None])]
+        y, _ = ssd.ssd_delta_fwd(views[0], views[3], a["A"].cuda(), views[1], views[2], views[4], **to(o))
+        assert torch.equal(y, ssd.ssd_delta_fwd(**to(a), **to(o))[0])
+    t = a["x"].transpose(0, 1).contiguous().cuda().transpose(0, 1)  # the batch inside
+    y2, _ = ssd.ssd_delta_fwd(**to({**a, "x": t}), **to(o))
+    assert torch.equal(y, y2)
+
+
+def test_values_at_the_edge(ssd):
+    """Zero rows with and without an epsilon, a gate that forgets everything, beta 0 and 1."""
+    a, o = inputs(1, 6, 2, 1, 64, 64, seed=4)
+    a["Bm"][0, 1] = 0
+    a["Cm"][0, 2] = 0
+    a["dt"][0, 3] = 200.0
+    a["beta"][0, 4] = -200.0
+    a["beta"][0, 5] = 200.0
+    run(ssd, a, o)
+    run(ssd, a, {**o, "norm_eps": 0.0})
+
+
+def test_masked_tokens_may_hold_anything(ssd):
+    a, o = inputs(2, 40, 2, 1, 128, 128, torch.bfloat16, cached=True, seed=6)
+    o["lengths"] = torch.tensor([23, 7], dtype=torch.int32)
+    y, final = ssd.ssd_delta_fwd(**to(a), **to(o))
+    for b, n in enumerate((23, 7)):
+        for k in ("x", "Bm", "Cm", "dt", "beta"):
+            a[k][b, n:] = float("nan")
+    y2, final2 = ssd.ssd_delta_fwd(**to(a), **to({**o, "final_state": o["final_state"].clone()}))
+    assert torch.equal(y, y2) and torch.equal(final, final2)
+
+
+def test_empty(ssd):
+    a, o = inputs(2, 0, 2, 1, 64, 64, cached=True)
+    y, final = ssd.ssd_delta_fwd(**to(a), **to(o))
+    rows = o["slots"].long()
+    assert y.shape == (2, 0, 2, 64) and torch.equal(final.cpu()[rows], o["init_state"][rows])
+    a, o = inputs(0, 3, 2, 1, 64, 64)
+    assert ssd.ssd_delta_fwd(**to(a), **to(o))[0].shape == (0, 3, 2, 64)
