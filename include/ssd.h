@@ -527,11 +527,11 @@ ssd_status ssd_delta_fwd(const ssd_delta_args* args, ssd_stream_t stream);
  * A NaN logit counts as -infinity; a row with +infinity is shared by its
  * infinities.  A drafted token outside the vocabulary is not accepted, and
  * nothing is taken off p for it.  Where the target's row allows no token, or
- * scale[b] is not positive and finite (then n is 0), -1 is drawn. */
+ * scale[b] is not above 0 and at most 1e37 (then n is 0), -1 is drawn. */
 typedef struct {
   int64_t size;
   int64_t batch; /* <= 65535 */
-  int32_t drafts, vocab, dtype, reserved; /* drafts 0..64; vocab <= 2^24; dtype of both logits */
+  int32_t drafts, vocab, dtype, reserved; /* drafts 0..64; vocab <= 2^19; dtype of both logits */
   const void* logits;       /* rows [batch][drafts + 1][vocab] */
   int64_t logits_batch, logits_row;
   const void* draft_logits; /* rows [batch][drafts][vocab] or NULL */

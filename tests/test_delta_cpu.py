@@ -73,7 +73,7 @@ def verify(**change):
 @pytest.mark.parametrize("change,status", [
     (dict(batch=0), OK), (dict(size=8), INVALID), (dict(batch=-1), INVALID), (dict(drafts=-1), INVALID), (dict(vocab=0), INVALID),
     (dict(dtype=2), UNSUPPORTED), (dict(batch=65536), UNSUPPORTED), (dict(drafts=65), UNSUPPORTED),
-    (dict(vocab=(1 << 24) + 1), UNSUPPORTED), (dict(workspace_bytes=8), WORKSPACE), (dict(workspace=4104), INVALID),
+    (dict(vocab=(1 << 19) + 1), UNSUPPORTED), (dict(workspace_bytes=8), WORKSPACE), (dict(workspace=4104), INVALID),
     *[({n: None}, INVALID) for n in ("logits", "draft", "uniforms", "tokens", "accepted", "logprobs", "workspace")],
     *[({n: 4098}, INVALID) for n in ("logits", "draft_logits", "draft", "uniforms", "scale", "lengths", "tokens", "accepted", "logprobs")]])
 def test_verify_arguments(change, status):

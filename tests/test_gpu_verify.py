@@ -135,11 +135,12 @@ def test_nothing_left_of_the_difference(ssd):
 
 
 @pytest.mark.parametrize("V", [50001, 131072])
-def test_drawn_tokens_are_those_of_64_bits(ssd, V):
-    """Many numbers over flat distributions, where a token has 1e-5 of them."""
+@pytest.mark.parametrize("width", [1.0, 3.0, 6.0])
+def test_drawn_tokens_are_those_of_64_bits(ssd, V, width):
+    """Many numbers over flat and over steep distributions, where most tokens have less than 1e-5 of them."""
     g = torch.Generator().manual_seed(11)
-    logits = torch.randn(1, 1, V, generator=g).expand(256, 1, V)
-    u = torch.rand(256, 1, generator=g)
-    got = ssd.ssd_draft_verify(logits.cuda(), torch.zeros(256, 0, dtype=torch.int32).cuda(), u.cuda())[0].cpu()
+    logits = (width * torch.randn(1, 1, V, generator=g)).expand(2048, 1, V)
+    u = torch.rand(2048, 1, generator=g)
+    got = ssd.ssd_draft_verify(logits.cuda(), torch.zeros(2048, 0, dtype=torch.int32).cuda(), u.cuda())[0].cpu()
     c = torch.softmax(logits[0, 0].double(), 0).cumsum(0)
     assert torch.equal(got[:, 0].long(), torch.searchsorted(c, u[:, 0].double() * c[-1], right=True))
