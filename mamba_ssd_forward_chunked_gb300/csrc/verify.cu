@@ -30,7 +30,7 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 
 constexpr int kThreads = 256;
 constexpr int kMaxDrafts = 64;
-constexpr int kCluster = 8;
+constexpr int kMaxCluster = 8;
 constexpr int kDrawThreads = 512;
 constexpr int kDrawWarps = kDrawThreads / 32;
 constexpr int kMaxVocab = 1 << 19;  // sums of weights stay below 2^63
@@ -349,13 +349,13 @@ __device__ __forceinline__ uint64_t rest_of(const uint64_t (&run)[kSums], bool p
 }
 
 template <typename T>
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(VerifyParams p) {
+__global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(VerifyParams p) {
   constexpr bool kExact = sizeof(T) == 4;
-  constexpr int kRuns = kCluster * kDrawWarps;
+  constexpr int kMaxRuns = kMaxCluster * kDrawWarps;
   __shared__ float2 s_row[2 * kMaxDrafts + 1];  // maximum and sum of every row
   __shared__ float2 s_powers[kPowers];
   __shared__ uint64_t s_mine[kDrawWarps][kSums];  // of the block's runs
-  __shared__ uint64_t s_run[kRuns][kSums];        // of all
+  __shared__ uint64_t s_run[kMaxRuns][kSums];     // of all
   __shared__ Share s_share[2];
   __shared__ uint64_t s_upto[2][kDrawWarps];
   __shared__ uint32_t s_taken[kMaxDrafts / 32];
@@ -364,7 +364,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kDrawThreads,
   begin_kernel();
   cg::cluster_group cluster = cg::this_cluster();
   const int64_t b = blockIdx.y;
-  const int part = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int part = blockIdx.x, runs = gridDim.x * kDrawWarps;  // a cluster is a row of the grid
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const float scale = scale_of(p, b);
   int32_t* tokens = p.tokens + b * (p.T + 1);
   float* logprobs = p.logprobs + b * (p.T + 1);
@@ -463,7 +464,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kDrawThreads,
   const bool vec = (reinterpret_cast<uintptr_t>(row) & 15) == 0, vec_q = (reinterpret_cast<uintptr_t>(row_q) & 15) == 0;
 
   // the sums of every warp's run of the vocabulary
-  const int run = (p.V + kRuns * 256 - 1) / (kRuns * 256) * 256;
+  const int run = (p.V + runs * 256 - 1) / (runs * 256) * 256;
   {
     const int first = (part * kDrawWarps + warp) * run;  // (below 2^20)
     const int end = first >= p.V ? first : p.V - first < run ? p.V : first + run;
@@ -506,7 +507,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kDrawThreads,
     }
   }
   cluster_arrive(), cluster_wait();
-  for (int i = tid; i < kRuns * kSums; i += kDrawThreads)
+  for (int i = tid; i < runs * kSums; i += kDrawThreads)
     (&s_run[0][0])[i] = cluster.map_shared_rank(&s_mine[0][0], i / (kDrawWarps * kSums))[i % (kDrawWarps * kSums)];
   cluster_arrive();  // (waited for at the end: nobody leaves while the others read its sums)
   __syncthreads();
@@ -516,7 +517,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kDrawThreads,
     uint64_t sum[kSums];
     for (int i = 0; i < kSums; ++i) {
       sum[i] = 0;
-      for (int r = lane; r < kRuns; r += 32) sum[i] += s_run[r][i];
+      for (int r = lane; r < runs; r += 32) sum[i] += s_run[r][i];
       sum[i] = warp_sum(sum[i]);
     }
     const Share share = share_of(lane == 0 ? sum[kAllP] : sum[kAllQ]);
@@ -525,22 +526,21 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kDrawThreads,
     const Share share_p = s_share[0], share_q = s_share[1];
     // p itself where (next to) nothing is left of p - q: 2^-49, which the runs' roundings cannot use up
     const bool plain = d.minus == 0 || share_p(sum[kMoreP]) <= share_q(sum[kMoreQ]) + 4096;
-    // runs of four to a lane
+    const int each = (runs + 31) / 32, first = lane * each;  // a lane's runs
     uint64_t part_sum = 0;
-    constexpr int kEach = kRuns / 32;
-    for (int r = 0; r < kEach; ++r) part_sum += rest_of(s_run[lane * kEach + r], plain, share_p, share_q);
+    for (int r = first; r < first + each && r < runs; ++r) part_sum += rest_of(s_run[r], plain, share_p, share_q);
     const uint64_t upto = warp_scan(part_sum, lane);
     const uint64_t total = __shfl_sync(0xffffffffu, upto, 31);
     const uint64_t goal = goal_of(u[p.T], total);
     uint64_t below = upto - part_sum;
     if (goal >= below && goal < upto) {  // one lane's
-      int r = 0;
-      for (; r + 1 < kEach; ++r) {
-        const uint64_t more = rest_of(s_run[lane * kEach + r], plain, share_p, share_q);
+      int r = first;
+      for (; r + 1 < first + each; ++r) {
+        const uint64_t more = rest_of(s_run[r], plain, share_p, share_q);
         if (goal - below < more) break;
         below += more;
       }
-      s_which = lane * kEach + r, s_below = goal - below, s_plain = plain;
+      s_which = r, s_below = goal - below, s_plain = plain;
     }
   }
   if (tid == 0) s_found = INT_MAX;
@@ -609,7 +609,22 @@ cudaError_t launch_verify(const VerifyParams& p, int64_t batch, cudaStream_t str
   const cudaError_t e = vecs >= 4 ? launch_sums<T, 4>(p, batch, stream) : vecs == 2 ? launch_sums<T, 2>(p, batch, stream)
                                                                                     : launch_sums<T, 1>(p, batch, stream);
   if (e != cudaSuccess) return e;
-  return launch_k(verify_draw_kernel<T>, dim3(kCluster, static_cast<unsigned>(batch)), dim3(kDrawThreads), 0, stream, true, p);
+  // as large a cluster a sequence as leaves all of them resident at once, two blocks a multiprocessor
+  // (64 sequences of 50001 tokens: 8 blocks each 30 us, 4 26)
+  int cluster = kMaxCluster;
+  while (cluster > 1 && cluster * batch > 2 * layer_sm_count()) cluster /= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(cluster), static_cast<unsigned>(batch));
+  cfg.blockDim = dim3(kDrawThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster), attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, verify_draw_kernel<T>, p);
 }
 
 ssd_status check_verify(const ssd_draft_verify_args* a) {
