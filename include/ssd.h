@@ -509,8 +509,13 @@ typedef struct {
   const int32_t* positions; /* [batch] tokens before this call; NULL: every sequence has a state */
   const int32_t* lengths;   /* [batch] tokens of this call, taken into [0, seqlen]; NULL: seqlen */
   void* y;                  /* [batch][seqlen][nheads][headdim] */
+  void* workspace;          /* 16-byte aligned */
+  size_t workspace_bytes;
 } ssd_delta_args;
 
+/* Bytes of workspace on the current device: for bf16 prompts (0 otherwise, or
+ * where the sizes are refused); the sizes and dtype are read, no tensor. */
+size_t ssd_delta_workspace_size(const ssd_delta_args* args);
 ssd_status ssd_delta_fwd(const ssd_delta_args* args, ssd_stream_t stream);
 
 /* Verification of drafted tokens (speculative decoding).  With p_i and q_i the

@@ -30,7 +30,7 @@ EXPORTS = ("ssd_status_string", "ssd_validate_shape", "ssd_fwd_workspace_layout"
            "ssd_conv_fwd", "ssd_selective_scan", "ssd_selective_scan_workspace_size", "ssd_debug_scan_handover",
            "ssd_step", "ssd_w4_matvec",
            "ssd_w4_matvec_workspace_size", "ssd_beam_select", "ssd_beam_select_workspace_size", "ssd_beam_reorder",
-           "ssd_delta_fwd", "ssd_draft_verify", "ssd_draft_verify_workspace_size")
+           "ssd_delta_fwd", "ssd_delta_workspace_size", "ssd_draft_verify", "ssd_draft_verify_workspace_size")
 
 # Size of the library's own workspace array used by ssd_fwd_static_scratch.
 SSD_STATIC_SCRATCH_BYTES = 32 << 20
@@ -109,7 +109,7 @@ def _load() -> ctypes.CDLL:
     lib.ssd_debug_scan_handover.restype = c_int
     lib.ssd_debug_scan_handover.argtypes = [vp, ctypes.c_int32, vp]
     for name in ("ssd_selective_scan_workspace_size", "ssd_w4_matvec_workspace_size", "ssd_beam_select_workspace_size",
-                 "ssd_draft_verify_workspace_size"):
+                 "ssd_delta_workspace_size", "ssd_draft_verify_workspace_size"):
         getattr(lib, name).restype = sz
         getattr(lib, name).argtypes = [vp]
     return lib
@@ -509,5 +509,6 @@ def ssd_fwd_static_scratch(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B
 
 # The layer around ssd_fwd (convolution, selective scan, single tokens, 4-bit products, beam search).
 from .layer import (ssd_beam_reorder, ssd_beam_select, ssd_beam_select_workspace_size, ssd_conv_fwd,  # noqa: E402
-                    ssd_delta_fwd, ssd_draft_verify, ssd_draft_verify_workspace_size, ssd_selective_scan,
-                    ssd_selective_scan_workspace_size, ssd_step, ssd_w4_matvec, w4_pack, w4_quantize)
+                    ssd_delta_fwd, ssd_delta_workspace_size, ssd_draft_verify,
+                    ssd_draft_verify_workspace_size, ssd_selective_scan, ssd_selective_scan_workspace_size,
+                    ssd_step, ssd_w4_matvec, w4_pack, w4_quantize)

@@ -466,7 +466,7 @@ PyObject* beam_reorder(PyObject* const* p) {
 }
 
 // x, dt, A, Bm, Cm, beta, scale, dt_bias, dt_softplus, beta_sigmoid, norm_eps, init_state, slots, positions, lengths, y,
-// final_state, want_final_state
+// final_state, workspace, want_final_state
 PyObject* delta_fwd(PyObject* const* p) {
   const First x = first(p[0], "x", 4);
   const On device(x.dev);
@@ -496,7 +496,7 @@ PyObject* delta_fwd(PyObject* const* p) {
   if (p[2] == Py_None) throw Refused{1, "A must be a torch.Tensor"};
   a.A = dense<const float>(p[2], "A", x.dev, at::kFloat, {H});
   a.dt_bias = dense<const float>(p[7], "dt_bias", x.dev, at::kFloat, {H});
-  const bool want = truth(p[17]);
+  const bool want = truth(p[18]);
   a.nslots = B;
   for (int i : {11, 16})
     if (p[i] != Py_None) a.nslots = tensor(p[i], i == 11 ? "init_state" : "final_state").dim() == 4 ? THPVariable_Unpack(p[i]).size(0) : 0;
@@ -516,6 +516,16 @@ PyObject* delta_fwd(PyObject* const* p) {
     if (p[12] != Py_None) throw Refused{1, "with slots, final_state must be given"};
     final_state = empty({a.nslots, H, P, N}, at::kFloat, x.t);
     a.final_state = static_cast<float*>(final_state.data_ptr());
+  }
+  a.size = sizeof(a);
+  at::Tensor space;
+  if (p[17] != Py_None) {
+    const int64_t bytes = tensor(p[17], "workspace").numel();
+    a.workspace = dense<void>(p[17], "workspace", x.dev, at::kByte, {bytes});
+    a.workspace_bytes = static_cast<size_t>(bytes);
+  } else if (const size_t need = ssd_delta_workspace_size(&a)) {
+    space = empty({static_cast<int64_t>(need)}, at::kByte, x.t);
+    a.workspace = space.data_ptr(), a.workspace_bytes = need;
   }
   call(ssd_delta_fwd, "ssd_delta_fwd", a, x.dev);
   if (final_state.defined()) return wrap_all({y, final_state});
@@ -583,6 +593,17 @@ PyObject* select_workspace(PyObject* const* p) {
   return PyLong_FromSize_t(ssd_beam_select_workspace_size(&a));
 }
 
+// batch, seqlen, nheads, headdim, dstate, bf16
+PyObject* delta_workspace(PyObject* const* p) {
+  ssd_delta_args a{};
+  a.size = sizeof(a);
+  a.batch = whole(p[0], "batch"), a.seqlen = whole(p[1], "seqlen"), a.nslots = a.batch;
+  a.nheads = small(whole(p[2], "nheads"), "nheads"), a.headdim = small(whole(p[3], "headdim"), "headdim");
+  a.ngroups = 1, a.dstate = small(whole(p[4], "dstate"), "dstate");
+  a.dtype = a.gate_dtype = truth(p[5]) ? SSD_BF16 : SSD_F32;
+  return PyLong_FromSize_t(ssd_delta_workspace_size(&a));
+}
+
 // batch, drafts, vocab, bf16, draft_logits
 PyObject* verify_workspace(PyObject* const* p) {
   ssd_draft_verify_args a{};
@@ -636,10 +657,11 @@ PyMODINIT_FUNC PyInit__layer_binding() {
       method<w4_matvec, 7>("w4_matvec"),
       method<beam_select, 6>("beam_select"),
       method<beam_reorder, 3>("beam_reorder"),
-      method<delta_fwd, 18>("delta_fwd"),
+      method<delta_fwd, 19>("delta_fwd"),
       method<draft_verify, 7>("draft_verify"),
       method<scan_workspace, 5>("scan_workspace"),
       method<select_workspace, 4>("select_workspace"),
+      method<delta_workspace, 6>("delta_workspace"),
       method<verify_workspace, 5>("verify_workspace"),
       {nullptr, nullptr, 0, nullptr},
   };

@@ -7,6 +7,7 @@
 // are joined by shuffles.  Tokens are laid out in shared memory, a tile at a
 // time: k and q with their norms, x, the gates.
 #include "delta.cuh"
+#include "delta_chunk.cuh"
 
 namespace ssd {
 namespace {
@@ -179,11 +180,7 @@ cudaError_t launch_delta(const DeltaParams& p, cudaStream_t stream) {
                                                                       : launch_scan<T, 256, 4, 4>(p, stream);
 }
 
-}  // namespace
-}  // namespace ssd
-
-extern "C" ssd_status ssd_delta_fwd(const ssd_delta_args* a, ssd_stream_t stream) {
-  using namespace ssd;
+ssd_status check_delta(const ssd_delta_args* a) {
   if (!a || a->size != static_cast<int64_t>(sizeof(*a))) return SSD_ERR_INVALID_ARG;
   if (a->batch < 0 || a->seqlen < 0 || a->nslots < 0 || a->nheads <= 0 || a->headdim <= 0 || a->ngroups <= 0 || a->dstate <= 0)
     return SSD_ERR_INVALID_ARG;
@@ -192,19 +189,10 @@ extern "C" ssd_status ssd_delta_fwd(const ssd_delta_args* a, ssd_stream_t stream
   if (a->nheads % a->ngroups != 0 || a->nheads > 65535 || a->batch > 65535 || a->seqlen > int64_t(1) << 30) return SSD_ERR_UNSUPPORTED;
   // (written so that NaN is refused)
   if (!(a->scale >= -3.4e38f && a->scale <= 3.4e38f) || !(a->norm_eps >= -3.4e38f && a->norm_eps <= 3.4e38f)) return SSD_ERR_INVALID_ARG;
-  if (a->batch == 0) return SSD_OK;
-  const size_t es = elem_size(a->dtype), gs = elem_size(a->gate_dtype);
-  if (a->seqlen > 0) {
-    for (const void* t : {a->x, a->Bm, a->Cm, (const void*)a->y})
-      if (!t || !aligned_to(t, es)) return SSD_ERR_INVALID_ARG;
-    for (const void* t : {a->dt, a->beta})
-      if (!t || !aligned_to(t, gs)) return SSD_ERR_INVALID_ARG;
-    if (!a->A) return SSD_ERR_INVALID_ARG;
-  }
-  for (const void* t : {(const void*)a->A, (const void*)a->dt_bias, (const void*)a->slots, (const void*)a->positions, (const void*)a->lengths})
-    if (!aligned_to(t, 4)) return SSD_ERR_INVALID_ARG;
-  if (!aligned_to(a->init_state, 16) || !aligned_to(a->final_state, 16)) return SSD_ERR_INVALID_ARG;
-  if (!a->slots && a->nslots < a->batch) return SSD_ERR_INVALID_ARG;
+  return SSD_OK;
+}
+
+DeltaParams params_of(const ssd_delta_args* a) {
   DeltaParams p{};
   p.batch = a->batch, p.seqlen = a->seqlen, p.nslots = a->nslots;
   p.x_batch = a->x_batch, p.x_token = a->x_token;
@@ -218,5 +206,41 @@ extern "C" ssd_status ssd_delta_fwd(const ssd_delta_args* a, ssd_stream_t stream
   p.init_state = a->init_state, p.final_state = a->final_state;
   p.slots = a->slots, p.positions = a->positions, p.lengths = a->lengths;
   p.y = a->y;
+  return p;
+}
+
+}  // namespace
+}  // namespace ssd
+
+extern "C" size_t ssd_delta_workspace_size(const ssd_delta_args* a) {
+  using namespace ssd;
+  if (check_delta(a) != SSD_OK || a->batch == 0 || !delta_chunked(a->dtype, a->seqlen, a->dstate)) return 0;
+  return delta_chunks_workspace(params_of(a));
+}
+
+
+extern "C" ssd_status ssd_delta_fwd(const ssd_delta_args* a, ssd_stream_t stream) {
+  using namespace ssd;
+  const ssd_status st = check_delta(a);
+  if (st != SSD_OK) return st;
+  if (a->batch == 0) return SSD_OK;
+  const size_t es = elem_size(a->dtype), gs = elem_size(a->gate_dtype);
+  if (a->seqlen > 0) {
+    for (const void* t : {a->x, a->Bm, a->Cm, (const void*)a->y})
+      if (!t || !aligned_to(t, es)) return SSD_ERR_INVALID_ARG;
+    for (const void* t : {a->dt, a->beta})
+      if (!t || !aligned_to(t, gs)) return SSD_ERR_INVALID_ARG;
+    if (!a->A) return SSD_ERR_INVALID_ARG;
+  }
+  for (const void* t : {(const void*)a->A, (const void*)a->dt_bias, (const void*)a->slots, (const void*)a->positions, (const void*)a->lengths})
+    if (!aligned_to(t, 4)) return SSD_ERR_INVALID_ARG;
+  if (!aligned_to(a->init_state, 16) || !aligned_to(a->final_state, 16)) return SSD_ERR_INVALID_ARG;
+  if (!a->slots && a->nslots < a->batch) return SSD_ERR_INVALID_ARG;
+  const DeltaParams p = params_of(a);
+  if (const size_t need = ssd_delta_workspace_size(a)) {
+    if (!a->workspace || !aligned_to(a->workspace, 16)) return SSD_ERR_INVALID_ARG;
+    if (a->workspace_bytes < need) return SSD_ERR_WORKSPACE;
+    if (delta_chunks_aligned(p)) return launch_delta_chunks(p, a->workspace, stream);
+  }
   return launched(a->dtype == SSD_BF16 ? launch_delta<__nv_bfloat16>(p, stream) : launch_delta<float>(p, stream));
 }

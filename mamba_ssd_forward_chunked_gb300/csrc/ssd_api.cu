@@ -11,10 +11,6 @@
 #include "ssd_internal.cuh"
 
 namespace ssd {
-namespace {
-
-constexpr size_t kAlign = 1024;
-inline size_t align_up(size_t v) { return (v + kAlign - 1) & ~(kAlign - 1); }
 
 uint64_t spin_limit_ns() {
   static uint64_t v = [] {
@@ -29,6 +25,11 @@ uint64_t spin_limit_ns() {
   }();
   return v;
 }
+
+namespace {
+
+constexpr size_t kAlign = 1024;
+inline size_t align_up(size_t v) { return (v + kAlign - 1) & ~(kAlign - 1); }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
@@ -282,6 +283,11 @@ bool build_onepass_maps(const ssd_shape& s, const void* x, const void* Bm, const
 }
 
 }  // namespace
+
+bool encode_bf16_map(CUtensorMap* m, int rank, const void* base, const uint64_t* dims, const uint64_t* strides_bytes,
+                     const uint32_t* box) {
+  return encode(m, true, rank, base, dims, strides_bytes, box);
+}
 }  // namespace ssd
 
 using namespace ssd;

@@ -48,7 +48,7 @@ else:
 
 __all__ = ["ssd_conv_fwd", "ssd_selective_scan", "ssd_step", "ssd_w4_matvec", "ssd_beam_select", "ssd_beam_reorder",
            "ssd_selective_scan_workspace_size", "ssd_beam_select_workspace_size", "w4_pack", "w4_quantize",
-           "ssd_delta_fwd", "ssd_draft_verify", "ssd_draft_verify_workspace_size"]
+           "ssd_delta_fwd", "ssd_delta_workspace_size", "ssd_draft_verify", "ssd_draft_verify_workspace_size"]
 
 
 def _on(stream, fn, *args):
@@ -140,13 +140,20 @@ def ssd_step(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, D: torch.Tensor
 
 # ------------------------------------------------------------------ delta rule
 
+def ssd_delta_workspace_size(batch: int, seqlen: int, nheads: int, headdim: int, dstate: int, dtype: torch.dtype) -> int:
+    """Bytes of workspace ssd_delta_fwd needs for these sizes on the current
+    device (0: none)."""
+    return _binding.delta_workspace(batch, seqlen, nheads, headdim, dstate, dtype == torch.bfloat16)
+
+
 def ssd_delta_fwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, Bm: torch.Tensor, Cm: torch.Tensor,
                   beta: torch.Tensor, *, scale: Optional[float] = None, dt_bias: Optional[torch.Tensor] = None,
                   dt_softplus: bool = False, beta_sigmoid: bool = False, norm_eps: Optional[float] = None,
                   init_state: Optional[torch.Tensor] = None, slots: Optional[torch.Tensor] = None,
                   positions: Optional[torch.Tensor] = None, lengths: Optional[torch.Tensor] = None,
                   y: Optional[torch.Tensor] = None, final_state: Optional[torch.Tensor] = None,
-                  want_final_state: bool = True, stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+                  workspace: Optional[torch.Tensor] = None, want_final_state: bool = True,
+                  stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """The gated delta rule (C: ssd_delta_fwd), for prompts, a few drafted tokens
     and single tokens.  Returns (y, final_state).
 
@@ -161,7 +168,7 @@ def ssd_delta_fwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, Bm: torch.
     outputs after them are 0).  final_state may be init_state; with ``slots`` it
     has to be given (or ``want_final_state=False``)."""
     args = (x, dt, A, Bm, Cm, beta, scale, dt_bias, dt_softplus, beta_sigmoid, norm_eps, init_state, slots, positions,
-            lengths, y, final_state, want_final_state)
+            lengths, y, final_state, workspace, want_final_state)
     return _binding.delta_fwd(*args) if stream is None else _on(stream, _binding.delta_fwd, *args)
 
 

@@ -17,7 +17,7 @@ class Delta(ctypes.Structure):
                 + [("scale", f32), ("norm_eps", f32)] + [(n, ptr) for n in ("x", "Bm", "Cm")]
                 + [(n, i64) for n in ("x_batch", "x_token", "B_batch", "B_token", "C_batch", "C_token")]
                 + [("dt", ptr), ("beta", ptr)] + [(n, i64) for n in ("dt_batch", "dt_token", "beta_batch", "beta_token")]
-                + [(n, ptr) for n in ("A", "dt_bias", "init_state", "final_state", "slots", "positions", "lengths", "y")])
+                + [(n, ptr) for n in ("A", "dt_bias", "init_state", "final_state", "slots", "positions", "lengths", "y", "workspace")] + [("workspace_bytes", ctypes.c_size_t)])
 
 
 class Verify(ctypes.Structure):
