@@ -514,7 +514,9 @@ typedef struct {
 } ssd_delta_args;
 
 /* Bytes of workspace on the current device: for bf16 prompts (0 otherwise, or
- * where the sizes are refused); the sizes and dtype are read, no tensor. */
+ * where the sizes are refused); the sizes and dtype are read, no tensor.  A
+ * wait in these prompts' kernels that runs out (see above) leaves NaN in the
+ * outputs of its head. */
 size_t ssd_delta_workspace_size(const ssd_delta_args* args);
 ssd_status ssd_delta_fwd(const ssd_delta_args* args, ssd_stream_t stream);
 

@@ -240,7 +240,7 @@ extern "C" ssd_status ssd_delta_fwd(const ssd_delta_args* a, ssd_stream_t stream
   if (const size_t need = ssd_delta_workspace_size(a)) {
     if (!a->workspace || !aligned_to(a->workspace, 16)) return SSD_ERR_INVALID_ARG;
     if (a->workspace_bytes < need) return SSD_ERR_WORKSPACE;
-    if (delta_chunks_aligned(p)) return launch_delta_chunks(p, a->workspace, stream);
+    return launch_delta_chunks(p, a->workspace, stream);
   }
   return launched(a->dtype == SSD_BF16 ? launch_delta<__nv_bfloat16>(p, stream) : launch_delta<float>(p, stream));
 }

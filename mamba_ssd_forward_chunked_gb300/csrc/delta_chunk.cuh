@@ -7,17 +7,17 @@ namespace ssd {
 // The chunks of a pair of launches.
 struct DeltaChunks {
   int first, count, last;  // chunks of 64 tokens from `first` on; last: the sequences end with them
+  int vectors;             // x, Bm, Cm and y are rows of 16-byte vectors
   uint8_t* records;        // [batch][nheads][count]: what the first launch leaves for the second
+  uint8_t* rows;           // [batch][ngroups][count]: and K and Q of the group
   float* carry;            // [batch][nheads][headdim][dstate]: states between pairs of launches
   uint64_t limit_ns;       // of a wait
 };
 
-// Whether these sizes take the chunked form, given tensors that TMA can read.
+// Whether these sizes take the chunked form.
 bool delta_chunked(int dtype, int64_t seqlen, int dstate);
 // Bytes of its workspace.
 size_t delta_chunks_workspace(const DeltaParams& p);
-// False where a tensor's address or strides are none for TMA.
-bool delta_chunks_aligned(const DeltaParams& p);
 ssd_status launch_delta_chunks(const DeltaParams& p, void* workspace, cudaStream_t stream);
 
 }  // namespace ssd

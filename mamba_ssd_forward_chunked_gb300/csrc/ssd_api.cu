@@ -283,11 +283,6 @@ bool build_onepass_maps(const ssd_shape& s, const void* x, const void* Bm, const
 }
 
 }  // namespace
-
-bool encode_bf16_map(CUtensorMap* m, int rank, const void* base, const uint64_t* dims, const uint64_t* strides_bytes,
-                     const uint32_t* box) {
-  return encode(m, true, rank, base, dims, strides_bytes, box);
-}
 }  // namespace ssd
 
 using namespace ssd;

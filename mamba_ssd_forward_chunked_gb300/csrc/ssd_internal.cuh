@@ -55,10 +55,6 @@ struct OnePassMaps {
   CUtensorMap y;   // y [B][L][H*P], box {64 p, 128 tokens, 1} (TMA stores)
 };
 
-// Tiled map of a bf16 tensor, 128-byte swizzle, zero fill outside (rank, base, dims innermost first,
-// strides in bytes of all but the innermost, box).
-bool encode_bf16_map(CUtensorMap* m, int rank, const void* base, const uint64_t* dims, const uint64_t* strides_bytes,
-                     const uint32_t* box);
 // Limit of the bounded waits.
 uint64_t spin_limit_ns();
 

@@ -163,11 +163,7 @@ def test_strides(ssd, L):
         views = [v.unflatten(2, s) if s else v for v, s in zip(dev[:, :, pad:].split(parts, 2), [(H, P), (G, N), (G, N), None, None])]
         y, final = ssd.ssd_delta_fwd(views[0], views[3], a["A"].cuda(), views[1], views[2], views[4], **to(o))
         want, wantf = ssd.ssd_delta_fwd(**to(a), **to(o))
-        if L < 64 or pad != 3:
-            assert torch.equal(y, want) and torch.equal(final, wantf)
-        else:  # rows that TMA cannot read go token by token
-            near("final", final, wantf.double().cpu(), 2.0 ** -18)
-            near("y", y, want.double().cpu(), 2.0 ** -7)
+        assert torch.equal(y, want) and torch.equal(final, wantf)
     t = a["x"].transpose(0, 1).contiguous().cuda().transpose(0, 1)  # the batch inside
     y2, _ = ssd.ssd_delta_fwd(**to({**a, "x": t}), **to(o))
     assert torch.equal(want, y2)
