@@ -3,19 +3,19 @@
 // With G the sum of dt A from the chunk's start to a token (that one included), k and q the normalised
 // rows and h the state that enters the chunk, the values that the rule writes, v_i, solve
 //     v_i + sum_{j<i} beta_i e^{G_i-G_j} (k_i.k_j) v_j = r_i,     r_i = beta_i (x_i - e^{G_i} h k_i),
-// so with A that strictly lower triangular matrix and T = (I + A)^-1
+// so with A that strictly lower triangular matrix, T = (I + A)^-1 and P the products of q and k
 //     v = T r,   y_i = scale (e^{G_i} h q_i + sum_{j<=i} e^{G_i-G_j} (q_i.k_j) v_j) = .. + (P T r)_i,
-//     h <- e^{G_64} h + sum_j e^{G_64-G_j} v_j k_j^T.
-// T, P T and the tokens' factors need no state: a first launch forms them for all chunks at once.  The
-// second has a block for some columns of a head's state and walks the chunks: three products each, [K; Q] h,
-// [T; P T] r and K^T v, with tokens or state rows in the 128 lanes of tensor memory.
+//     h <- e^{G_64} h + sum_j e^{G_64-G_j} v_j k_j^T = .. + (W r)^T,   W = sum_i e^{G_64-G_i} k_i T_i.
+// W, P T and the tokens' factors need no state: a first launch forms them for all chunks at once.  The
+// second has a block for some columns of a head's state and walks the chunks: r from [K; Q] h, then the new
+// state from W r (and y from P T r beside it), with tokens or state rows in the 128 lanes of tensor memory.
+// Nobody forms v: that would be a third product in the chain, and its way through the threads.
 //
-// The state stays in registers, in 32 bits, and enters its product as two fp16 parts, as r and v do theirs:
-// 11 bits each, and with a power of two that brings a tile's largest value to 2^14 the second part's last
-// place is at most 2^-22 of a value or 2^-38 of the largest.  (Three bf16 parts need no scale, but half as
-// much again of shared memory, stores and products: one block a multiprocessor instead of two, and 5500
-// instead of TODO cycles a chunk.)  K and Q are bf16, so rows of them times a power of two are fp16.  Parts
-// lie side by side along the product's columns, and the threads add up what comes out.
+// The state stays in registers, in 32 bits, and enters its product as two fp16 parts, as r does: 11 bits
+// each, and with a power of two that brings a tile's largest value to 2^14 the second part's last place is
+// at most 2^-22 of a value or 2^-38 of the largest.  (Three bf16 parts need no scale, but half as much again
+// of shared memory, stores and products.)  K and Q are bf16, so rows of them times a power of two are fp16.
+// Parts lie side by side along the product's columns, and the threads add up what comes out.
 #include <cuda_fp16.h>
 
 #include "delta_chunk.cuh"
@@ -27,15 +27,16 @@ constexpr int kC = 64;  // tokens of a chunk
 constexpr int64_t kMinTokens = 64;
 
 // What the first launch leaves, as shared memory holds it (rows of 128 bytes in the 128-byte swizzle).  Of a
-// chunk of a head: the parts of [T; P T], and the tokens' factors.  Of a chunk of a group, for every 64 of N:
-// 64 rows of K, then of Q.
-constexpr uint32_t kPartBytes = 16384, kTileBytes = 2 * kPartBytes;
-enum { kBeta, kFromState, kToState, kOutState, kOutRest, kDecay, kFactors };  // (of kDecay one number)
-constexpr uint32_t kRecord = kTileBytes + kFactors * kC * 4;
+// chunk of a head: two parts of W (N rows), two of P T (64 rows), and the tokens' factors.  Of a chunk of a
+// group, for every 64 of N: 64 rows of K, then of Q.
 constexpr uint32_t kSlab = 8192;  // 64 rows of 128 bytes
+enum { kBeta, kFromState, kOutState, kOutRest, kScalars, kFactors };
+enum { kDecay, kUpdate };  // the scalars: e^{G_64}, and what undoes the scale of W
+__host__ __device__ constexpr uint32_t tile_bytes(int N) { return 2 * (N / 64 + 1) * kSlab; }
+__host__ __device__ constexpr uint32_t record_bytes(int N) { return tile_bytes(N) + kFactors * kC * 4; }
 __host__ __device__ constexpr uint32_t rows_bytes(int N) { return N / 64 * 2 * kSlab; }
 
-constexpr float kTScale = 16.f;  // of T and P T: T's diagonal is 1, its other entries' last places 2^-29
+constexpr float kTScale = 16.f;  // of T and P T: T's diagonal is 1, so second parts' last places are 2^-29 of that
 
 // The power of two that brings numbers up to `largest` (its bits) below 2^15, and its inverse.
 struct Scale {
@@ -65,6 +66,12 @@ __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t at) {
                : "r"(at)
                : "memory");
 }
+__device__ __forceinline__ void ldmatrix4_t(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -79,20 +86,23 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], 
 template <int N>
 struct PrepSmem {
   static constexpr uint32_t kRow = N * 2 + 16;  // bytes of a row of K or Q, eight rows in different banks
-  static constexpr uint32_t kRows = 128 * kRow, kMats = kC * (kStrideA + kStrideT) * 4;
-  static constexpr uint32_t kVec = kRows > kMats ? kRows : kMats;  // A and T take the rows' place
-  static constexpr uint32_t kTotal = kVec + 5 * kC * 4 + 16;
+  // K; Q, whose place A takes; T
+  static constexpr uint32_t kA = kC * kRow, kSize = kRow > kStrideA * 4 ? kRow : kStrideA * 4, kT = kA + kC * kSize;
+  static constexpr uint32_t kVec = kT + kC * kStrideT * 4;
+  static constexpr uint32_t kTotal = kVec + 6 * kC * 4 + 32;
 };
 
 template <int N>
-__global__ void __launch_bounds__(kPrepThreads, 5) delta_prepare_kernel(DeltaParams p, DeltaChunks s) {
+__global__ void __launch_bounds__(kPrepThreads, 4) delta_prepare_kernel(DeltaParams p, DeltaChunks s) {
   using M = PrepSmem<N>;
   extern __shared__ __align__(16) uint8_t smem[];
-  float* s_A = reinterpret_cast<float*>(smem);
-  float* s_T = s_A + kC * kStrideA;
+  float* s_A = reinterpret_cast<float*>(smem + M::kA);
+  float* s_T = reinterpret_cast<float*>(smem + M::kT);
   float* s_hi = reinterpret_cast<float*>(smem + M::kVec);
-  float *s_lo = s_hi + kC, *s_beta = s_lo + kC, *s_kn = s_beta + kC, *s_qn = s_kn + kC;
-  int64_t* s_half = reinterpret_cast<int64_t*>(s_qn + kC);
+  float *s_lo = s_hi + kC, *s_beta = s_lo + kC, *s_kn = s_beta + kC, *s_qn = s_kn + kC, *s_to = s_qn + kC;
+  int64_t* s_half = reinterpret_cast<int64_t*>(s_to + kC);
+  uint32_t* s_largest = reinterpret_cast<uint32_t*>(s_half + 1);  // of every warp
+  float* s_most = reinterpret_cast<float*>(s_largest + 4);
   begin_kernel();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t b = blockIdx.z;
@@ -200,7 +210,7 @@ __global__ void __launch_bounds__(kPrepThreads, 5) delta_prepare_kernel(DeltaPar
       }
     }
   }
-  __syncthreads();  // the rows have been read
+  __syncthreads();  // Q's rows have been read
   // A; P, whose rows' norms, powers of two and scale wait for the end, stays in registers
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
@@ -229,6 +239,20 @@ __global__ void __launch_bounds__(kPrepThreads, 5) delta_prepare_kernel(DeltaPar
     }
   }
   __syncthreads();
+
+  // the factors of T's rows in W, e^{G_64-G_i} k's norm, over the largest of them
+  if (warp == 3) {
+    float v[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int i = lane + 32 * e;
+      v[e] = i < n ? s_kn[i] * exp2f((s_hi[kC - 1] - s_hi[i]) + (s_lo[kC - 1] - s_lo[i])) : 0.f;
+    }
+    const float most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(v[0], v[1]))));
+    const float f = most > 0.f ? kTScale / most : 0.f;
+    s_to[lane] = v[0] * f, s_to[lane + 32] = v[1] * f;
+    if (lane == 0) *s_most = most;
+  }
 
   // T: the diagonal blocks of 16 by substitution, the others below from those above them,
   // T_ij = -T_ii sum_{j <= k < i} A_ik T_kj
@@ -338,36 +362,99 @@ __global__ void __launch_bounds__(kPrepThreads, 5) delta_prepare_kernel(DeltaPar
   }
   __syncthreads();
 
-  uint8_t* out = s.records + ((b * p.H + h) * s.count + blockIdx.x) * static_cast<int64_t>(kRecord);
+  uint8_t* out = s.records + ((b * p.H + h) * s.count + blockIdx.x) * static_cast<int64_t>(record_bytes(N));
+  {
+    uint8_t* pt = out + 2 * (N / 64) * kSlab;
 #pragma unroll 2
-  for (int i = 0; i < 8; ++i) {
-    const int item = tid + kPrepThreads * i, row = item >> 3, q = item & 7, t = row & 63;
-    uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
-    if (8 * q <= t) {
-      const float4* src = reinterpret_cast<const float4*>(row < kC ? &s_T[t * kStrideT + 8 * q] : &s_A[t * kStrideA + 8 * q]);
-      const float4 a = src[0], c4 = src[1];
-      const float v[8] = {a.x, a.y, a.z, a.w, c4.x, c4.y, c4.z, c4.w};
+    for (int i = 0; i < 4; ++i) {
+      const int item = tid + kPrepThreads * i, row = item >> 3, q = item & 7;
+      uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
+      if (8 * q <= row) {
+        const float4* src = reinterpret_cast<const float4*>(&s_A[row * kStrideA + 8 * q]);
+        const float4 a = src[0], c4 = src[1];
+        const float v[8] = {a.x, a.y, a.z, a.w, c4.x, c4.y, c4.z, c4.w};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int col = 8 * q + 2 * e;
-        split(col <= t ? v[2 * e] * kTScale : 0.f, col + 1 <= t ? v[2 * e + 1] * kTScale : 0.f, (&hi.x)[e], (&lo.x)[e]);
+        for (int e = 0; e < 4; ++e) {
+          const int col = 8 * q + 2 * e;
+          split(col <= row ? v[2 * e] * kTScale : 0.f, col + 1 <= row ? v[2 * e + 1] * kTScale : 0.f, (&hi.x)[e], (&lo.x)[e]);
+        }
+      }
+      uint8_t* to = pt + row * 128 + ((q ^ (row & 7)) << 4);
+      *reinterpret_cast<uint4*>(to) = hi;
+      *reinterpret_cast<uint4*>(to + kSlab) = lo;
+    }
+  }
+
+  // W = K^T T', T's rows times their factors in two fp16 parts (K is one): 8 columns at a time, a warp has two
+  // such, those with fewest rows of T beside those with most
+  constexpr int kTiles = N / 16;
+  float w[2][kTiles][4];
+  uint32_t bh[2][4][2], bl[2][4][2];
+  const int nt[2] = {warp, 7 - warp};
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+#pragma unroll
+    for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[u][m][e] = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k < nt[u] >> 1) continue;  // above the diagonal
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int i = 16 * k + 8 * e + (lane & 3) * 2;
+        const float* t = &s_T[i * kStrideT + 8 * nt[u] + (lane >> 2)];
+        split(t[0] * s_to[i], t[kStrideT] * s_to[i + 1], bh[u][k][e], bl[u][k][e]);
       }
     }
-    uint8_t* to = out + row * 128 + ((q ^ (row & 7)) << 4);
-    *reinterpret_cast<uint4*>(to) = hi;
-    *reinterpret_cast<uint4*>(to + kPartBytes) = lo;
   }
+  const uint32_t kt = rows + ((lane & 7) + (lane >> 4) * 8) * M::kRow + ((lane >> 3) & 1) * 16;
+#pragma unroll
+  for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k < nt[0] >> 1) continue;
+      uint32_t a[4];
+      ldmatrix4_t(a, kt + k * 16 * M::kRow + m * 32);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (k < nt[u] >> 1) continue;
+        mma_f16(w[u][m], a, bl[u][k][0], bl[u][k][1]);
+        mma_f16(w[u][m], a, bh[u][k][0], bh[u][k][1]);
+      }
+    }
+  float top = 0.f;
+#pragma unroll
+  for (int u = 0; u < 2; ++u)
+#pragma unroll
+    for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(w[u][m][e]));
+  const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+  if (lane == 0) s_largest[warp] = bits;
+  __syncthreads();
+  const Scale scale = scale_for(max(max(s_largest[0], s_largest[1]), max(s_largest[2], s_largest[3])));
+#pragma unroll
+  for (int u = 0; u < 2; ++u)
+#pragma unroll
+    for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int row = 16 * m + (lane >> 2) + 8 * e;
+        uint32_t hi, lo;
+        split(w[u][m][2 * e] * scale.up, w[u][m][2 * e + 1] * scale.up, hi, lo);
+        uint8_t* to = out + row * 128 + ((nt[u] ^ (row & 7)) << 4) + (lane & 3) * 4;
+        *reinterpret_cast<uint32_t*>(to) = hi;
+        *reinterpret_cast<uint32_t*>(to + N / 64 * kSlab) = lo;
+      }
   if (tid < kC) {
-    float* factors = reinterpret_cast<float*>(out + kTileBytes);
-    const float since = exp2f(s_hi[tid] + s_lo[tid]);
-    const float until = exp2f((s_hi[kC - 1] - s_hi[tid]) + (s_lo[kC - 1] - s_lo[tid]));
-    const float qn = p.scale * s_qn[tid];
+    float* factors = reinterpret_cast<float*>(out + tile_bytes(N));
+    const float since = exp2f(s_hi[tid] + s_lo[tid]), qn = p.scale * s_qn[tid];
     factors[kBeta * kC + tid] = s_beta[tid];
     factors[kFromState * kC + tid] = s_beta[tid] * s_kn[tid] * since;
-    factors[kToState * kC + tid] = s_kn[tid] * until / kTScale;
     factors[kOutState * kC + tid] = qn * since;
     factors[kOutRest * kC + tid] = qn * (0x1p14f / kTScale);
-    if (tid == kC - 1) factors[kDecay * kC] = since;
+    if (tid == kC - 1) factors[kScalars * kC + kDecay] = since, factors[kScalars * kC + kUpdate] = scale.down * *s_most / kTScale;
   }
 }
 
@@ -382,14 +469,14 @@ struct Walk {
   static constexpr int kCols = kPT / kGroups;              // of a thread
   static constexpr int kSlabs = 2 * kPT / 64;              // 64 columns each of the two parts side by side
   static constexpr uint32_t kSlabS = N * 128;
-  static constexpr uint32_t kRows = 0, kTile = kRows + kStages * rows_bytes(N), kS = kTile + kStages * kTileBytes;
-  static constexpr uint32_t kEnd = kS + kSlabs * (N < kC ? kC : N) * 128;  // r and v take the state's place
-  static constexpr uint32_t kTotal = kEnd + 16 * 8 + 8 * 4;
+  static constexpr uint32_t kRows = 0, kTile = kRows + kStages * rows_bytes(N), kS = kTile + kStages * tile_bytes(N);
+  static constexpr uint32_t kEnd = kS + kSlabs * N * 128;  // r takes the state's place
+  static constexpr uint32_t kTotal = kEnd + 16 * 8 + 4 * 4 + 4 * kWorkers * 4;
   static constexpr uint32_t kTmem = 4 * kPT;               // columns of tensor memory
 };
 
 enum { kRowsFull, kRowsFull1, kRowsEmpty, kRowsEmpty1, kTileFull, kTileFull1, kTileEmpty, kTileEmpty1, kStateReady, kFromStateDone,
-       kRestReady, kValuesDone, kValuesReady, kUpdateDone, kDrained, kBarriers };
+       kRestReady, kUpdateDone, kRestDone, kDrained, kBarriers };
 
 // cp.async.bulk: bytes from global to shared memory, counted by the barrier.
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -408,21 +495,20 @@ template <int N, int kPT, int kGroups, int kStages, int kBlocks>
 __global__ void __launch_bounds__(Walk<N, kPT, kGroups, kStages>::kThreads, kBlocks) delta_walk_kernel(DeltaParams p, DeltaChunks s) {
   using M = Walk<N, kPT, kGroups, kStages>;
   constexpr int kCols = M::kCols, kWorkers = M::kWorkers;
-  constexpr uint32_t kColD1 = 0, kColD3 = 2 * kPT;  // K^T v goes where [K; Q] h was
+  constexpr uint32_t kColD1 = 0, kColD3 = 2 * kPT;  // W r goes where [K; Q] h was
   extern __shared__ __align__(1024) uint8_t walk_smem[];
   uint8_t* smem = walk_smem;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + M::kEnd);
   uint32_t* holder = reinterpret_cast<uint32_t*>(bars + kBarriers);
   volatile int* failed = reinterpret_cast<volatile int*>(holder + 1);
-  uint32_t* s_largest = holder + 2;  // [state, rest, values][chunk mod 2]: bits of a tile's largest magnitude
+  uint32_t* s_largest = holder + 4;  // [state, rest][chunk mod 2][warp]: bits of the largest magnitude
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t b = blockIdx.z;
   const int h = blockIdx.y, p0 = blockIdx.x * kPT;
   if (tid == 0) {
-    for (int i = 0; i < kBarriers; ++i) mbar_init(&bars[i], i == kStateReady || i == kRestReady || i == kValuesReady ? kWorkers : 1);
+    for (int i = 0; i < kBarriers; ++i) mbar_init(&bars[i], i == kStateReady || i == kRestReady ? kWorkers : 1);
     fence_mbar_init();
     *failed = 0;
-    for (int i = 0; i < 6; ++i) s_largest[i] = 0;
   }
   if (warp == kWorkers) {
     tmem_alloc(holder, M::kTmem);
@@ -440,7 +526,7 @@ __global__ void __launch_bounds__(Walk<N, kPT, kGroups, kStages>::kThreads, kBlo
   const int64_t length = seq.row < 0 || seq.length < begin ? begin : seq.length < end ? seq.length : end;
   const int chunks = static_cast<int>((length - begin + kC - 1) / kC);
   const int g = h / (p.H / p.G);
-  const uint8_t* records = s.records + (b * p.H + h) * s.count * static_cast<int64_t>(kRecord);
+  const uint8_t* records = s.records + (b * p.H + h) * s.count * static_cast<int64_t>(record_bytes(N));
   const uint8_t* rows = s.rows + (b * p.G + g) * s.count * static_cast<int64_t>(rows_bytes(N));
   auto wait = [&](int bar, int phase) {
     if (mbar_try_wait_short(&bars[bar], phase & 1)) return true;
@@ -459,24 +545,19 @@ __global__ void __launch_bounds__(Walk<N, kPT, kGroups, kStages>::kThreads, kBlo
     // loads
     if (lane == 0) {
       int c = 0, t = 0;  // chunks whose rows, and whose tiles, are on their way
-      auto load_rows = [&] {
-        const int st = c % kStages, turn = c / kStages;
-        if (turn > 0 && !wait(kRowsEmpty + st, turn - 1)) return false;
+      bool ok = true;
+      while (t < chunks) {
+        const int st = t % kStages, turn = t / kStages;
+        ok = turn == 0 || wait(kRowsEmpty + st, turn - 1);
+        if (!ok) break;
         mbar_arrive_expect_tx(&bars[kRowsFull + st], rows_bytes(N));
         bulk_load(smem + M::kRows + st * rows_bytes(N), rows + c * static_cast<int64_t>(rows_bytes(N)), rows_bytes(N), &bars[kRowsFull + st]);
         ++c;
-        return true;
-      };
-      bool ok = true;
-      while (ok && t < chunks) {
-        if (c < kStages) load_rows();  // (nobody has to be waited for)
-        const int st = t % kStages, turn = t / kStages;
-        ok = turn == 0 || wait(kTileEmpty + st, turn - 1);  // a tile's buffer is free before the rows' of its chunk
+        ok = turn == 0 || wait(kTileEmpty + st, turn - 1);
         if (!ok) break;
-        mbar_arrive_expect_tx(&bars[kTileFull + st], kTileBytes);
-        bulk_load(smem + M::kTile + st * kTileBytes, records + t * static_cast<int64_t>(kRecord), kTileBytes, &bars[kTileFull + st]);
+        mbar_arrive_expect_tx(&bars[kTileFull + st], tile_bytes(N));
+        bulk_load(smem + M::kTile + st * tile_bytes(N), records + t * static_cast<int64_t>(record_bytes(N)), tile_bytes(N), &bars[kTileFull + st]);
         ++t;
-        if (c < t) ok = load_rows();
       }
       if (!ok) {  // nothing is in flight when the block ends
         for (int i = c > kStages ? c - kStages : 0; i < c; ++i) mbar_wait(&bars[kRowsFull + i % kStages], (i / kStages) & 1, s.limit_ns);
@@ -486,8 +567,7 @@ __global__ void __launch_bounds__(Walk<N, kPT, kGroups, kStages>::kThreads, kBlo
   } else if (warp == kWorkers + 1) {
     // products
     if (lane == 0) {
-      constexpr uint32_t id_two = idesc_f32acc(0, 128, 2 * kPT, 0, 1), id_one = idesc_f32acc(0, 128, kPT, 0, 1),
-                         id_update = idesc_f32acc(0, 128, 2 * kPT, 1, 1);
+      constexpr uint32_t id_two = idesc_f32acc(0, 128, 2 * kPT, 0, 1), id_one = idesc_f32acc(0, 128, kPT, 0, 1);
       const uint32_t base = smem_u32(smem);
       const uint64_t dS = sdesc_sw128(base + M::kS, M::kSlabS, 1024), dR = sdesc_sw128(base + M::kS, kSlab, 1024);
       for (int c = 0; c < chunks; ++c) {
@@ -500,24 +580,25 @@ __global__ void __launch_bounds__(Walk<N, kPT, kGroups, kStages>::kThreads, kBlo
         for (int k = 0; k < N / 16; ++k)
           mma_ss<false>(tmem + kColD1, kq_rows + (((k >> 2) * 2 * kSlab + (k & 3) * 32) >> 4), dS + (k * 2048 >> 4), id_two, k != 0);
         mma_commit(&bars[kFromStateDone]);
+        mma_commit(&bars[kRowsEmpty + st]);
         if (!wait(kTileFull + st, turn) || !wait(kRestReady, c)) break;
         tc_fence_after();
-        const uint64_t tile = sdesc_sw128(base + M::kTile + st * kTileBytes, 16, 1024);
+        // both first parts, and the second of either with the first of the other
+        const uint32_t tile = base + M::kTile + st * tile_bytes(N);
+        auto product = [&](uint32_t column, uint32_t first_part, uint32_t part) {
+          const uint64_t a = sdesc_sw128(first_part, 16, 1024);
 #pragma unroll
-        for (int k = 0; k < kC / 16; ++k) {  // both first parts, and the second of either with the first of the other
-          mma_ss<false>(tmem + kColD3, tile + (k * 32 >> 4), dR + (k * 2048 >> 4), id_two, k != 0);
-          mma_ss<false>(tmem + kColD3, tile + ((kPartBytes + k * 32) >> 4), dR + (k * 2048 >> 4), id_one, 1);
-        }
-        mma_commit(&bars[kValuesDone]);
-        mma_commit(&bars[kTileEmpty + st]);
-        if (!wait(kValuesReady, c)) break;
-        tc_fence_after();
-        const uint64_t k_cols = sdesc_sw128(kq, 2 * kSlab, 1024);  // (64 of N: the upper lanes' product is nobody's)
-#pragma unroll
-        for (int k = 0; k < kC / 16; ++k)
-          mma_ss<false>(tmem + kColD1, k_cols + (k * 2048 >> 4), dR + (k * 2048 >> 4), id_update, k != 0);
+          for (int k = 0; k < kC / 16; ++k) {
+            mma_ss<false>(tmem + column, a + (k * 32 >> 4), dR + (k * 2048 >> 4), id_two, k != 0);
+            mma_ss<false>(tmem + column, a + ((part + k * 32) >> 4), dR + (k * 2048 >> 4), id_one, 1);
+          }
+        };
+        product(kColD1, tile, N / 64 * kSlab);  // (N 64: the upper lanes' product is nobody's)
         mma_commit(&bars[kUpdateDone]);
-        mma_commit(&bars[kRowsEmpty + st]);
+        // P T's 64 rows go to the lanes of Q: they are the second half of 128 that begin in what lies before them
+        product(kColD3, tile + (2 * (N / 64) - 1) * kSlab, kSlab);
+        mma_commit(&bars[kRestDone]);
+        mma_commit(&bars[kTileEmpty + st]);
       }
       mma_commit(&bars[kDrained]);
       mbar_wait(&bars[kDrained], 0, s.limit_ns);
@@ -575,18 +656,27 @@ __global__ void __launch_bounds__(Walk<N, kPT, kGroups, kStages>::kThreads, kBlo
       if (lane == 0) mbar_arrive(&bars[bar]);
     };
     auto all_wait = [&](int bar, int phase) { return __all_sync(0xffffffffu, wait(bar, phase)) != 0; };
-    // The scale of what `threads` threads hold of a tile, in chunk c; false for all of them where one says
-    // that it is not ok, so that none is left waiting for it.
-    auto agree = [&](bool ok, int which, int c, const float (&v)[kCols], uint32_t threads, Scale& scale) {
+    // The scale of what `warps` warps hold of a tile, in chunk c; false for all of them where one says that it
+    // is not ok, so that none is left waiting for it.
+    auto largest_of = [&](int which, int c, int warps) {
+      const uint4* at = reinterpret_cast<const uint4*>(s_largest + (2 * which + (c & 1)) * kWorkers);
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < kWorkers / 4; ++i) {
+        if (4 * i >= warps) break;
+        const uint4 v = at[i];
+        top = max(max(top, max(v.x, v.y)), max(v.z, v.w));
+      }
+      return scale_for(top);
+    };
+    auto agree = [&](bool ok, int which, int c, const float (&v)[kCols], int place, int warps, Scale& scale) {
       float top = 0.f;
 #pragma unroll
       for (int i = 0; i < kCols; ++i) top = fmaxf(top, fabsf(v[i]));
       const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
-      uint32_t* at = s_largest + 2 * which;
-      if (lane == 0) atomicMax(&at[c & 1], bits);
-      if (named_bar_or(1 + which, threads, !ok)) return false;
-      scale = scale_for(*reinterpret_cast<volatile uint32_t*>(&at[c & 1]));
-      if (tid == 0) at[(c + 1) & 1] = 0;  // (read by everybody before this barrier)
+      if (lane == 0) s_largest[(2 * which + (c & 1)) * kWorkers + place] = bits;
+      if (named_bar_or(1 + which, 32 * warps, !ok)) return false;
+      scale = largest_of(which, c, warps);
       return true;
     };
 
@@ -598,124 +688,97 @@ __global__ void __launch_bounds__(Walk<N, kPT, kGroups, kStages>::kThreads, kBlo
       for (int i = 0; i < kCols; ++i)
         S[i] = from && has_state && col0 + i < p.P ? from[(static_cast<int64_t>(h) * p.P + col0 + i) * N + row] : 0.f;
     }
-    // what comes from global memory is asked for a chunk ahead
-    uint4 next_x[kCols / 8];
-    float next_a = 0.f, next_b = 0.f, next_c = 0.f, next_decay = 0.f;
-    auto ask = [&](int c) {
-      if (c >= chunks) return;
-      const float* f = reinterpret_cast<const float*>(records + c * static_cast<int64_t>(kRecord) + kTileBytes);
-      const int64_t t = begin + static_cast<int64_t>(c) * kC + token;
-      next_decay = f[kDecay * kC];
-      if (is_token) {
-        next_a = f[kBeta * kC + token], next_b = f[kFromState * kC + token], next_c = f[kToState * kC + token];
-#pragma unroll
-        for (int i = 0; i < kCols / 8; ++i) {
-          next_x[i] = make_uint4(0, 0, 0, 0);
-          if (t >= length || col0 + 8 * i >= p.P) continue;
-          if (s.vectors) {
-            next_x[i] = *reinterpret_cast<const uint4*>(x + t * p.x_token + 8 * i);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) reinterpret_cast<__nv_bfloat16*>(&next_x[i])[e] = x[t * p.x_token + 8 * i + e];
-          }
-        }
-      } else {
-        next_a = f[kOutState * kC + token], next_b = f[kOutRest * kC + token];
-      }
-    };
-    ask(0);
     Scale state{1.f, 1.f};
-    bool ok = chunks == 0 || agree(true, 0, 0, S, 32 * kWorkers, state);
+    bool ok = true;
     if (chunks > 0) {
+      ok = agree(true, 0, 0, S, warp, kWorkers, state);
       if (has_state) put(M::kSlabS, row, S, state.up);
       arrive(kStateReady);
     }
     for (int c = 0; c < chunks; ++c) {
       const int64_t t = begin + static_cast<int64_t>(c) * kC + token;
       const bool live = t < length;
-      const float fa = next_a, fb = next_b, fc = next_c, decay = next_decay;
+      // what comes from global memory: factors and x, in L2 by now; the next chunk's x is sent for
+      const float* f = reinterpret_cast<const float*>(records + c * static_cast<int64_t>(record_bytes(N)) + tile_bytes(N));
+      const float fa = f[(is_token ? kBeta : kOutState) * kC + token], fb = f[(is_token ? kFromState : kOutRest) * kC + token];
+      const float decay = f[kScalars * kC + kDecay], update = f[kScalars * kC + kUpdate];
       uint4 xs[kCols / 8];
+      if (is_token) {
 #pragma unroll
-      for (int i = 0; i < kCols / 8; ++i) xs[i] = next_x[i];
-      ask(c + 1);
+        for (int i = 0; i < kCols / 8; ++i) {
+          xs[i] = make_uint4(0, 0, 0, 0);
+          if (!live || col0 + 8 * i >= p.P) continue;
+          if (s.vectors) {
+            xs[i] = *reinterpret_cast<const uint4*>(x + t * p.x_token + 8 * i);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) reinterpret_cast<__nv_bfloat16*>(&xs[i])[e] = x[t * p.x_token + 8 * i + e];
+          }
+        }
+        if (t + kC < length && col0 < p.P) asm volatile("prefetch.global.L2 [%0];" ::"l"(x + (t + kC) * p.x_token));
+      }
       float v[kCols];
       ok = all_wait(kFromStateDone, c);
       tc_fence_after();
       if (ok) take(kColD1, v);
+      Scale scale{1.f, 1.f};
+      float out[kCols];
       if (is_token) {
         // r = beta x - beta e^G h k
-        Scale scale{1.f, 1.f};
         const float from_state = fb * state.down;
 #pragma unroll
         for (int i = 0; i < kCols; ++i) {
           const uint32_t w = (&xs[i / 8].x)[i / 2 % 4];
           v[i] = live ? fmaf(fa, i & 1 ? bf16_hi(w) : bf16_lo(w), -from_state * v[i]) : 0.f;
         }
-        ok = agree(ok, 1, c, v, 16 * kWorkers, scale);
-        if (ok) {
-          put(kSlab, token, v, scale.up);
-          arrive(kRestReady);
-          ok = all_wait(kValuesDone, c);
-        }
-        // v = T r, as the state takes it
-        tc_fence_after();
-        if (ok) take(kColD3, v);
-        const float to_state = fc * scale.down;
-#pragma unroll
-        for (int i = 0; i < kCols; ++i) v[i] = live ? to_state * v[i] : 0.f;
-        ok = agree(ok, 2, c, v, 16 * kWorkers, scale);
-        if (ok) {
-          put(kSlab, token, v, scale.up);
-          arrive(kValuesReady);
-        }
-      } else if (ok) {
-        // y: the state's part, and P T r
-        arrive(kRestReady);
-        float out[kCols];
+        ok = agree(ok, 1, c, v, 2 * group + quarter, kWorkers / 2, scale);
+        if (ok) put(kSlab, token, v, scale.up);
+      } else {
         const float from_state = fa * state.down;
 #pragma unroll
         for (int i = 0; i < kCols; ++i) out[i] = from_state * v[i];
-        ok = all_wait(kValuesDone, c);
-        tc_fence_after();
-        if (ok) {
-          take(kColD3, v);
-          arrive(kValuesReady);
-        }
-        // (the scale of r is known by now)
-        const float from_rest = fb * scale_for(*reinterpret_cast<volatile uint32_t*>(&s_largest[2 + (c & 1)])).down;
-        if (ok && live) {
-#pragma unroll
-          for (int i = 0; i < kCols / 8; ++i) {
-            if (col0 + 8 * i >= p.P) break;
-            uint4 w;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int at = 8 * i + 2 * e;
-              (&w.x)[e] = pack_bf16x2(fmaf(from_rest, v[at], out[at]), fmaf(from_rest, v[at + 1], out[at + 1]));
-            }
-            if (s.vectors) {
-              *reinterpret_cast<uint4*>(y + t * y_token + 8 * i) = w;
-            } else {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) y[t * y_token + 8 * i + e] = reinterpret_cast<const __nv_bfloat16*>(&w)[e];
-            }
-          }
-        }
       }
+      if (ok) arrive(kRestReady);
       // the state
       ok = ok && all_wait(kUpdateDone, c);
       tc_fence_after();
       if (ok) take(kColD1, v);
+      if (!is_token) scale = largest_of(1, c, kWorkers / 2);  // (known by now)
       if (has_state) {
-        const float back = scale_for(*reinterpret_cast<volatile uint32_t*>(&s_largest[4 + (c & 1)])).down;
+        const float back = update * scale.down;
 #pragma unroll
         for (int i = 0; i < kCols; ++i) S[i] = fmaf(decay, S[i], back * v[i]);
       }
       if (c + 1 < chunks) {
-        ok = agree(ok, 0, c + 1, S, 32 * kWorkers, state);
+        ok = agree(ok, 0, c + 1, S, warp, kWorkers, state);
         if (!ok) break;
-        if (has_state) put(M::kSlabS, row, S, state.up);
-        arrive(kStateReady);
+      }
+      // P T has read r, whose place the state takes
+      const bool done = ok && all_wait(kRestDone, c);
+      tc_fence_after();
+      if (c + 1 < chunks && has_state && done) put(M::kSlabS, row, S, state.up);
+      if (!is_token && done) take(kColD3, v);
+      if (c + 1 < chunks && done) arrive(kStateReady);
+      ok = done;
+      if (!is_token && live && done) {
+        // y: the state's part, and P T r
+        const float from_rest = fb * scale.down;
+#pragma unroll
+        for (int i = 0; i < kCols / 8; ++i) {
+          if (col0 + 8 * i >= p.P) break;
+          uint4 w;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int at = 8 * i + 2 * e;
+            (&w.x)[e] = pack_bf16x2(fmaf(from_rest, v[at], out[at]), fmaf(from_rest, v[at + 1], out[at + 1]));
+          }
+          if (s.vectors) {
+            *reinterpret_cast<uint4*>(y + t * y_token + 8 * i) = w;
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[t * y_token + 8 * i + e] = reinterpret_cast<const __nv_bfloat16*>(&w)[e];
+          }
+        }
       }
     }
     if (!ok) {
@@ -775,7 +838,7 @@ constexpr int64_t kRecordBytes = int64_t(1) << 40;
 
 // Chunks of a pair of launches: as many as keep what the first leaves within half the L2.
 int64_t chunks_at_once(const DeltaParams& p) {
-  const int64_t all = ceil_div(p.seqlen, kC), fit = kRecordBytes / (p.batch * (kRecord * p.H + rows_bytes(p.N) * p.G));
+  const int64_t all = ceil_div(p.seqlen, kC), fit = kRecordBytes / (p.batch * (record_bytes(p.N) * p.H + rows_bytes(p.N) * p.G));
   return fit < 8 ? (all < 8 ? all : 8) : fit < all ? fit : all;
 }
 
@@ -787,7 +850,7 @@ bool delta_chunked(int dtype, int64_t seqlen, int dstate) {
 
 size_t delta_chunks_workspace(const DeltaParams& p) {
   const int64_t count = chunks_at_once(p);
-  return static_cast<size_t>(p.batch) * count * (kRecord * p.H + rows_bytes(p.N) * p.G) +
+  return static_cast<size_t>(p.batch) * count * (record_bytes(p.N) * p.H + rows_bytes(p.N) * p.G) +
          (count * kC < p.seqlen ? static_cast<size_t>(p.batch) * p.H * p.P * p.N * sizeof(float) : 0);
 }
 
@@ -795,7 +858,7 @@ ssd_status launch_delta_chunks(const DeltaParams& p, void* workspace, cudaStream
   const int64_t all = ceil_div(p.seqlen, kC), most = chunks_at_once(p);
   DeltaChunks s{};
   s.records = static_cast<uint8_t*>(workspace);
-  s.rows = s.records + p.batch * p.H * most * kRecord;
+  s.rows = s.records + p.batch * p.H * most * record_bytes(p.N);
   s.carry = reinterpret_cast<float*>(s.rows + p.batch * p.G * most * rows_bytes(p.N));
   s.limit_ns = spin_limit_ns();
   s.vectors = 1;
