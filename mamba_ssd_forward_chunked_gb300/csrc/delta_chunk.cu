@@ -27,12 +27,12 @@ constexpr int kC = 64;  // tokens of a chunk
 constexpr int64_t kMinTokens = 64;
 
 // What the first launch leaves, as shared memory holds it (rows of 128 bytes in the 128-byte swizzle).  Of a
-// chunk of a head: two parts of W (N rows), two of P T (64 rows), and the tokens' factors.  Of a chunk of a
-// group, for every 64 of N: 64 rows of K, then of Q.
+// chunk of a head: two parts of W (N rows), one of P T (64 rows; it goes into y alone, which has 8 bits), and
+// the tokens' factors.  Of a chunk of a group, for every 64 of N: 64 rows of K, then of Q.
 constexpr uint32_t kSlab = 8192;  // 64 rows of 128 bytes
 enum { kBeta, kFromState, kOutState, kOutRest, kScalars, kFactors };
-enum { kDecay, kUpdate };  // the scalars: e^{G_64}, and what undoes the scale of W
-__host__ __device__ constexpr uint32_t tile_bytes(int N) { return 2 * (N / 64 + 1) * kSlab; }
+enum { kDecay, kUpdate, kReach, kSpread };  // the scalars: e^{G_64}; what undoes W's scale; see the bounds of delta_walk_kernel
+__host__ __device__ constexpr uint32_t tile_bytes(int N) { return (2 * (N / 64) + 1) * kSlab; }
 __host__ __device__ constexpr uint32_t record_bytes(int N) { return tile_bytes(N) + kFactors * kC * 4; }
 __host__ __device__ constexpr uint32_t rows_bytes(int N) { return N / 64 * 2 * kSlab; }
 
@@ -72,6 +72,13 @@ __device__ __forceinline__ void ldmatrix4_t(uint32_t (&r)[4], uint32_t at) {
                : "r"(at)
                : "memory");
 }
+__device__ __forceinline__ void stmatrix4(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+// cp.async.bulk: bytes from shared to global memory, of the thread's bulk group.
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(__cvta_generic_to_global(dst)), "r"(src), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -89,7 +96,7 @@ struct PrepSmem {
   // K; Q, whose place A takes; T
   static constexpr uint32_t kA = kC * kRow, kSize = kRow > kStrideA * 4 ? kRow : kStrideA * 4, kT = kA + kC * kSize;
   static constexpr uint32_t kVec = kT + kC * kStrideT * 4;
-  static constexpr uint32_t kTotal = kVec + 6 * kC * 4 + 32;
+  static constexpr uint32_t kTotal = kVec + 7 * kC * 4 + 48;
 };
 
 template <int N>
@@ -99,10 +106,10 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prepare_kernel(DeltaPar
   float* s_A = reinterpret_cast<float*>(smem + M::kA);
   float* s_T = reinterpret_cast<float*>(smem + M::kT);
   float* s_hi = reinterpret_cast<float*>(smem + M::kVec);
-  float *s_lo = s_hi + kC, *s_beta = s_lo + kC, *s_kn = s_beta + kC, *s_qn = s_kn + kC, *s_to = s_qn + kC;
-  int64_t* s_half = reinterpret_cast<int64_t*>(s_to + kC);
+  float *s_lo = s_hi + kC, *s_beta = s_lo + kC, *s_kn = s_beta + kC, *s_qn = s_kn + kC, *s_to = s_qn + kC, *s_len = s_to + kC;
+  int64_t* s_half = reinterpret_cast<int64_t*>(s_len + kC);
   uint32_t* s_largest = reinterpret_cast<uint32_t*>(s_half + 1);  // of every warp
-  float* s_most = reinterpret_cast<float*>(s_largest + 4);
+  float *s_most = reinterpret_cast<float*>(s_largest + 4), *s_reach = s_most + 1;
   begin_kernel();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t b = blockIdx.z;
@@ -180,7 +187,11 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prepare_kernel(DeltaPar
     *reinterpret_cast<uint4*>(smem + r * M::kRow + col * 16) = half;
     if (rows_out)
       *reinterpret_cast<uint4*>(rows_out + (col >> 3) * 2 * kSlab + r * 128 + (((col & 7) ^ (r & 7)) << 4)) = half;
-    if (col == 0) (r < kC ? s_kn : s_qn)[r & 63] = delta_norm(p, squares) * scale.down;
+    if (col == 0) {
+      const float norm = delta_norm(p, squares);
+      (r < kC ? s_kn : s_qn)[r & 63] = norm * scale.down;
+      if (r < kC) s_len[r] = norm * sqrtf(squares);
+    }
   }
   __syncthreads();
 
@@ -242,16 +253,18 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prepare_kernel(DeltaPar
 
   // the factors of T's rows in W, e^{G_64-G_i} k's norm, over the largest of them
   if (warp == 3) {
-    float v[2];
+    float v[2], reach = 0.f;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int i = lane + 32 * e;
+      reach = fmaxf(reach, fabsf(s_beta[i]) * exp2f(s_hi[i] + s_lo[i]) * s_len[i]);
       v[e] = i < n ? s_kn[i] * exp2f((s_hi[kC - 1] - s_hi[i]) + (s_lo[kC - 1] - s_lo[i])) : 0.f;
     }
     const float most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(v[0], v[1]))));
     const float f = most > 0.f ? kTScale / most : 0.f;
     s_to[lane] = v[0] * f, s_to[lane + 32] = v[1] * f;
-    if (lane == 0) *s_most = most;
+    reach = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(reach)));
+    if (lane == 0) *s_most = most, *s_reach = reach;
   }
 
   // T: the diagonal blocks of 16 by substitution, the others below from those above them,
@@ -352,36 +365,18 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prepare_kernel(DeltaPar
         mma_tf32(o[j], ah, th[0], th[1]);
       }
     }
-    float* to = &s_A[(16 * mt[1] + (lane >> 2)) * kStrideA + (lane & 3) * 2];
+    // as the second launch reads it, where A was; blocks above the diagonal are 0
+    const int at_row = 16 * mt[1] + (lane >> 3 & 1) * 8 + (lane & 7);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (j > 2 * mt[1] + 1) break;
-      *reinterpret_cast<float2*>(to + 8 * j) = make_float2(o[j][0], o[j][1]);
-      *reinterpret_cast<float2*>(to + 8 * kStrideA + 8 * j) = make_float2(o[j][2], o[j][3]);
-    }
-  }
-  __syncthreads();
-
-  uint8_t* out = s.records + ((b * p.H + h) * s.count + blockIdx.x) * static_cast<int64_t>(record_bytes(N));
-  {
-    uint8_t* pt = out + 2 * (N / 64) * kSlab;
-#pragma unroll 2
-    for (int i = 0; i < 4; ++i) {
-      const int item = tid + kPrepThreads * i, row = item >> 3, q = item & 7;
-      uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
-      if (8 * q <= row) {
-        const float4* src = reinterpret_cast<const float4*>(&s_A[row * kStrideA + 8 * q]);
-        const float4 a = src[0], c4 = src[1];
-        const float v[8] = {a.x, a.y, a.z, a.w, c4.x, c4.y, c4.z, c4.w};
+    for (int j = 0; j < 8; j += 2) {
+      uint32_t v[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int col = 8 * q + 2 * e;
-          split(col <= row ? v[2 * e] * kTScale : 0.f, col + 1 <= row ? v[2 * e + 1] * kTScale : 0.f, (&hi.x)[e], (&lo.x)[e]);
-        }
+      for (int e = 0; e < 4; ++e) {
+        const float* from = &o[j + (e >> 1)][e & 1 ? 2 : 0];
+        const __half2 pair = __floats2half2_rn(from[0] * kTScale, from[1] * kTScale);
+        v[e] = *reinterpret_cast<const uint32_t*>(&pair);
       }
-      uint8_t* to = pt + row * 128 + ((q ^ (row & 7)) << 4);
-      *reinterpret_cast<uint4*>(to) = hi;
-      *reinterpret_cast<uint4*>(to + kSlab) = lo;
+      stmatrix4(rows + M::kA + at_row * 128 + (((j + (lane >> 4)) ^ (at_row & 7)) << 4), v[0], v[1], v[2], v[3]);
     }
   }
 
@@ -434,19 +429,20 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prepare_kernel(DeltaPar
   if (lane == 0) s_largest[warp] = bits;
   __syncthreads();
   const Scale scale = scale_for(max(max(s_largest[0], s_largest[1]), max(s_largest[2], s_largest[3])));
+  // the parts where K and T were, and all into global memory
 #pragma unroll
   for (int u = 0; u < 2; ++u)
 #pragma unroll
-    for (int m = 0; m < kTiles; ++m)
+    for (int m = 0; m < kTiles; ++m) {
+      const int at_row = 16 * m + (lane >> 3 & 1) * 8 + (lane & 7);
+      uint32_t hi[2], lo[2];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int row = 16 * m + (lane >> 2) + 8 * e;
-        uint32_t hi, lo;
-        split(w[u][m][2 * e] * scale.up, w[u][m][2 * e + 1] * scale.up, hi, lo);
-        uint8_t* to = out + row * 128 + ((nt[u] ^ (row & 7)) << 4) + (lane & 3) * 4;
-        *reinterpret_cast<uint32_t*>(to) = hi;
-        *reinterpret_cast<uint32_t*>(to + N / 64 * kSlab) = lo;
-      }
+      for (int e = 0; e < 2; ++e) split(w[u][m][2 * e] * scale.up, w[u][m][2 * e + 1] * scale.up, hi[e], lo[e]);
+      stmatrix4(rows + (lane < 16 ? 0 : M::kT) + at_row * 128 + ((nt[u] ^ (at_row & 7)) << 4), hi[0], hi[1], lo[0], lo[1]);
+    }
+  fence_proxy_async_smem();
+  __syncthreads();
+  uint8_t* out = s.records + ((b * p.H + h) * s.count + blockIdx.x) * static_cast<int64_t>(record_bytes(N));
   if (tid < kC) {
     float* factors = reinterpret_cast<float*>(out + tile_bytes(N));
     const float since = exp2f(s_hi[tid] + s_lo[tid]), qn = p.scale * s_qn[tid];
@@ -454,7 +450,19 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prepare_kernel(DeltaPar
     factors[kFromState * kC + tid] = s_beta[tid] * s_kn[tid] * since;
     factors[kOutState * kC + tid] = qn * since;
     factors[kOutRest * kC + tid] = qn * (0x1p14f / kTScale);
-    if (tid == kC - 1) factors[kScalars * kC + kDecay] = since, factors[kScalars * kC + kUpdate] = scale.down * *s_most / kTScale;
+    if (tid == kC - 1) {
+      float* scalars = factors + kScalars * kC;
+      scalars[kDecay] = since, scalars[kUpdate] = scale.down * *s_most / kTScale;
+      scalars[kReach] = *s_reach * (N == 64 ? 8.f : 11.5f);  // (a row's sum of magnitudes is sqrt(N) of its length at most)
+      scalars[kSpread] = kC * 32768.f * scalars[kUpdate];    // (W's largest is below 2^15 of its unit)
+    }
+  }
+  if (tid == kC) {
+    bulk_store(out, rows, N * 128);
+    bulk_store(out + N * 128, rows + M::kT, N * 128);
+    bulk_store(out + 2 * N * 128, rows + M::kA, kSlab);
+    tma_store_commit();
+    tma_store_wait_all();
   }
 }
 
@@ -471,7 +479,8 @@ struct Walk {
   static constexpr uint32_t kSlabS = N * 128;
   static constexpr uint32_t kRows = 0, kTile = kRows + kStages * rows_bytes(N), kS = kTile + kStages * tile_bytes(N);
   static constexpr uint32_t kEnd = kS + kSlabs * N * 128;  // r takes the state's place
-  static constexpr uint32_t kTotal = kEnd + 16 * 8 + 4 * 4 + 4 * kWorkers * 4;
+  static constexpr uint32_t kX = kEnd + 16 * 8 + 4 * 4 + 4 * kWorkers * 4;  // a chunk's x, every thread's where it put it
+  static constexpr uint32_t kTotal = kX + kC * kPT * 2;
   static constexpr uint32_t kTmem = 4 * kPT;               // columns of tensor memory
 };
 
@@ -583,20 +592,18 @@ __global__ void __launch_bounds__(Walk<N, kPT, kGroups, kStages>::kThreads, kBlo
         mma_commit(&bars[kRowsEmpty + st]);
         if (!wait(kTileFull + st, turn) || !wait(kRestReady, c)) break;
         tc_fence_after();
-        // both first parts, and the second of either with the first of the other
         const uint32_t tile = base + M::kTile + st * tile_bytes(N);
-        auto product = [&](uint32_t column, uint32_t first_part, uint32_t part) {
-          const uint64_t a = sdesc_sw128(first_part, 16, 1024);
+        const uint64_t w = sdesc_sw128(tile, 16, 1024);
 #pragma unroll
-          for (int k = 0; k < kC / 16; ++k) {
-            mma_ss<false>(tmem + column, a + (k * 32 >> 4), dR + (k * 2048 >> 4), id_two, k != 0);
-            mma_ss<false>(tmem + column, a + ((part + k * 32) >> 4), dR + (k * 2048 >> 4), id_one, 1);
-          }
-        };
-        product(kColD1, tile, N / 64 * kSlab);  // (N 64: the upper lanes' product is nobody's)
+        for (int k = 0; k < kC / 16; ++k) {  // both first parts, and the second of either with the first of the other
+          mma_ss<false>(tmem + kColD1, w + (k * 32 >> 4), dR + (k * 2048 >> 4), id_two, k != 0);
+          mma_ss<false>(tmem + kColD1, w + ((N / 64 * kSlab + k * 32) >> 4), dR + (k * 2048 >> 4), id_one, 1);
+        }  // (N 64: the upper lanes' product is nobody's)
         mma_commit(&bars[kUpdateDone]);
         // P T's 64 rows go to the lanes of Q: they are the second half of 128 that begin in what lies before them
-        product(kColD3, tile + (2 * (N / 64) - 1) * kSlab, kSlab);
+        const uint64_t pt = sdesc_sw128(tile + (2 * (N / 64) - 1) * kSlab, 16, 1024);
+#pragma unroll
+        for (int k = 0; k < kC / 16; ++k) mma_ss<false>(tmem + kColD3, pt + (k * 32 >> 4), dR + (k * 2048 >> 4), id_two, k != 0);
         mma_commit(&bars[kRestDone]);
         mma_commit(&bars[kTileEmpty + st]);
       }
@@ -656,8 +663,11 @@ __global__ void __launch_bounds__(Walk<N, kPT, kGroups, kStages>::kThreads, kBlo
       if (lane == 0) mbar_arrive(&bars[bar]);
     };
     auto all_wait = [&](int bar, int phase) { return __all_sync(0xffffffffu, wait(bar, phase)) != 0; };
-    // The scale of what `warps` warps hold of a tile, in chunk c; false for all of them where one says that it
-    // is not ok, so that none is left waiting for it.
+    // Largest magnitudes that the warps have left, [state, beta x][chunk mod 2][warp].
+    auto leave = [&](int which, int c, float v, int place) {
+      const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(v));
+      if (lane == 0) s_largest[(2 * which + (c & 1)) * kWorkers + place] = bits;
+    };
     auto largest_of = [&](int which, int c, int warps) {
       const uint4* at = reinterpret_cast<const uint4*>(s_largest + (2 * which + (c & 1)) * kWorkers);
       uint32_t top = 0;
@@ -667,17 +677,13 @@ __global__ void __launch_bounds__(Walk<N, kPT, kGroups, kStages>::kThreads, kBlo
         const uint4 v = at[i];
         top = max(max(top, max(v.x, v.y)), max(v.z, v.w));
       }
-      return scale_for(top);
+      return __uint_as_float(top);
     };
-    auto agree = [&](bool ok, int which, int c, const float (&v)[kCols], int place, int warps, Scale& scale) {
+    auto magnitude = [&](const float (&v)[kCols]) {
       float top = 0.f;
 #pragma unroll
       for (int i = 0; i < kCols; ++i) top = fmaxf(top, fabsf(v[i]));
-      const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
-      if (lane == 0) s_largest[(2 * which + (c & 1)) * kWorkers + place] = bits;
-      if (named_bar_or(1 + which, 32 * warps, !ok)) return false;
-      scale = largest_of(which, c, warps);
-      return true;
+      return top;
     };
 
     float S[kCols];
@@ -688,81 +694,110 @@ __global__ void __launch_bounds__(Walk<N, kPT, kGroups, kStages>::kThreads, kBlo
       for (int i = 0; i < kCols; ++i)
         S[i] = from && has_state && col0 + i < p.P ? from[(static_cast<int64_t>(h) * p.P + col0 + i) * N + row] : 0.f;
     }
+    // What comes from global memory is asked for a chunk ahead: factors into registers, x into shared memory.
+    uint4* s_x = reinterpret_cast<uint4*>(smem + M::kX) + (2 * group + quarter) * 32 + lane;  // (of tokens)
+    constexpr int kStrideX = 16 * kWorkers;
+    float next_a = 0.f, next_b = 0.f;
+    float4 next_scalars = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto ask = [&](int c) {
+      if (c >= chunks) return;
+      const float* f = reinterpret_cast<const float*>(records + c * static_cast<int64_t>(record_bytes(N)) + tile_bytes(N));
+      next_scalars = *reinterpret_cast<const float4*>(f + kScalars * kC);
+      next_a = f[(is_token ? kBeta : kOutState) * kC + token], next_b = f[(is_token ? kFromState : kOutRest) * kC + token];
+      const int64_t t = begin + static_cast<int64_t>(c) * kC + token;
+      if (!is_token) return;
+#pragma unroll
+      for (int i = 0; i < kCols / 8; ++i) {
+        uint4* to = s_x + i * kStrideX;
+        const __nv_bfloat16* from = x + t * p.x_token + 8 * i;
+        if (t >= length || col0 + 8 * i >= p.P) {
+          *to = make_uint4(0, 0, 0, 0);
+        } else if (s.vectors) {
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(__cvta_generic_to_global(from)) : "memory");
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) reinterpret_cast<__nv_bfloat16*>(to)[e] = from[e];
+        }
+      }
+    };
+    ask(0);
+
+    // Scales go by bounds that are known while the products run, not by what comes out of them, so that nobody
+    // waits for the others in the chain: with s the largest of the state
+    //     |r| <= max |beta x| + s max_j beta e^{G_j} |k_j|_1,    |state after| <= e^{G_64} s + 64 max |W| max |r|.
+    // They can be a thousand times too large (the sums' signs); two parts have 2^17 to spare.
     Scale state{1.f, 1.f};
     bool ok = true;
     if (chunks > 0) {
-      ok = agree(true, 0, 0, S, warp, kWorkers, state);
+      leave(0, 1, magnitude(S), warp);
+      named_bar_sync(1, 32 * kWorkers);
+      state = scale_for(__float_as_uint(largest_of(0, 1, kWorkers)));
       if (has_state) put(M::kSlabS, row, S, state.up);
       arrive(kStateReady);
     }
     for (int c = 0; c < chunks; ++c) {
       const int64_t t = begin + static_cast<int64_t>(c) * kC + token;
       const bool live = t < length;
-      // what comes from global memory: factors and x, in L2 by now; the next chunk's x is sent for
-      const float* f = reinterpret_cast<const float*>(records + c * static_cast<int64_t>(record_bytes(N)) + tile_bytes(N));
-      const float fa = f[(is_token ? kBeta : kOutState) * kC + token], fb = f[(is_token ? kFromState : kOutRest) * kC + token];
-      const float decay = f[kScalars * kC + kDecay], update = f[kScalars * kC + kUpdate];
-      uint4 xs[kCols / 8];
+      const float fa = next_a, fb = next_b;
+      const float4 scalars = next_scalars;
+      const float decay = scalars.x, update = scalars.y;
+      float bx[kCols];
       if (is_token) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll
         for (int i = 0; i < kCols / 8; ++i) {
-          xs[i] = make_uint4(0, 0, 0, 0);
-          if (!live || col0 + 8 * i >= p.P) continue;
-          if (s.vectors) {
-            xs[i] = *reinterpret_cast<const uint4*>(x + t * p.x_token + 8 * i);
-          } else {
+          const uint4 xs = s_x[i * kStrideX];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) reinterpret_cast<__nv_bfloat16*>(&xs[i])[e] = x[t * p.x_token + 8 * i + e];
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t w = (&xs.x)[e];
+            bx[8 * i + 2 * e] = fa * bf16_lo(w), bx[8 * i + 2 * e + 1] = fa * bf16_hi(w);
           }
         }
-        if (t + kC < length && col0 < p.P) asm volatile("prefetch.global.L2 [%0];" ::"l"(x + (t + kC) * p.x_token));
+        leave(1, c, magnitude(bx), 2 * group + quarter);
       }
+      ask(c + 1);
+      leave(0, c, magnitude(S), warp);
+      ok = !named_bar_or(1, 32 * kWorkers, !ok);  // (whoever has given up takes the others along)
+      if (!ok) break;
+      const float largest = largest_of(0, c, kWorkers);
+      const float rest_bound = largest_of(1, c, kWorkers / 2) + scalars.z * largest;
+      const Scale rest = scale_for(__float_as_uint(rest_bound));
+      const Scale next = scale_for(__float_as_uint(fmaf(decay, largest, scalars.w * rest_bound)));
       float v[kCols];
       ok = all_wait(kFromStateDone, c);
       tc_fence_after();
       if (ok) take(kColD1, v);
-      Scale scale{1.f, 1.f};
-      float out[kCols];
       if (is_token) {
         // r = beta x - beta e^G h k
         const float from_state = fb * state.down;
 #pragma unroll
-        for (int i = 0; i < kCols; ++i) {
-          const uint32_t w = (&xs[i / 8].x)[i / 2 % 4];
-          v[i] = live ? fmaf(fa, i & 1 ? bf16_hi(w) : bf16_lo(w), -from_state * v[i]) : 0.f;
-        }
-        ok = agree(ok, 1, c, v, 2 * group + quarter, kWorkers / 2, scale);
-        if (ok) put(kSlab, token, v, scale.up);
+        for (int i = 0; i < kCols; ++i) v[i] = live ? fmaf(-from_state, v[i], bx[i]) : 0.f;
+        if (ok) put(kSlab, token, v, rest.up);
       } else {
         const float from_state = fa * state.down;
 #pragma unroll
-        for (int i = 0; i < kCols; ++i) out[i] = from_state * v[i];
+        for (int i = 0; i < kCols; ++i) bx[i] = from_state * v[i];  // the state's part of y
       }
       if (ok) arrive(kRestReady);
       // the state
       ok = ok && all_wait(kUpdateDone, c);
       tc_fence_after();
       if (ok) take(kColD1, v);
-      if (!is_token) scale = largest_of(1, c, kWorkers / 2);  // (known by now)
       if (has_state) {
-        const float back = update * scale.down;
+        const float back = update * rest.down;
 #pragma unroll
         for (int i = 0; i < kCols; ++i) S[i] = fmaf(decay, S[i], back * v[i]);
       }
-      if (c + 1 < chunks) {
-        ok = agree(ok, 0, c + 1, S, warp, kWorkers, state);
-        if (!ok) break;
-      }
+      state = next;
       // P T has read r, whose place the state takes
-      const bool done = ok && all_wait(kRestDone, c);
+      ok = ok && all_wait(kRestDone, c);
       tc_fence_after();
-      if (c + 1 < chunks && has_state && done) put(M::kSlabS, row, S, state.up);
-      if (!is_token && done) take(kColD3, v);
-      if (c + 1 < chunks && done) arrive(kStateReady);
-      ok = done;
-      if (!is_token && live && done) {
+      if (c + 1 < chunks && has_state && ok) put(M::kSlabS, row, S, state.up);
+      if (!is_token && ok) take(kColD3, v);
+      if (c + 1 < chunks && ok) arrive(kStateReady);
+      if (!is_token && live && ok) {
         // y: the state's part, and P T r
-        const float from_rest = fb * scale.down;
+        const float from_rest = fb * rest.down;
 #pragma unroll
         for (int i = 0; i < kCols / 8; ++i) {
           if (col0 + 8 * i >= p.P) break;
@@ -770,7 +805,7 @@ __global__ void __launch_bounds__(Walk<N, kPT, kGroups, kStages>::kThreads, kBlo
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int at = 8 * i + 2 * e;
-            (&w.x)[e] = pack_bf16x2(fmaf(from_rest, v[at], out[at]), fmaf(from_rest, v[at + 1], out[at + 1]));
+            (&w.x)[e] = pack_bf16x2(fmaf(from_rest, v[at], bx[at]), fmaf(from_rest, v[at + 1], bx[at + 1]));
           }
           if (s.vectors) {
             *reinterpret_cast<uint4*>(y + t * y_token + 8 * i) = w;

@@ -12,7 +12,9 @@ units of 2^-24, the gates and the norms of k by a few more, EPS (layer_ref) bein
 system whose inverse has entries of at most m^C beta |k|^2: an error of one
 token's value reaches the C - 1 after it, each by that much, so `spread` is 1 + C
 there.  An output is off by |scale| |q| times the state's error and EPS of the
-state's norm."""
+state's norm; in chunks, where it is the entering state's part plus
+sum_j (P T)_tj r_j, also by P T's rounding to 11 bits, 2^-12 |(P T)_tj| |r_j|.
+(P T)_tj is scale q_t.z_j, z_j being k_j carried through the tokens after j."""
 import torch
 
 from layer_ref import EPS, HALF_BF16, d64, softplus
@@ -47,6 +49,7 @@ def delta(x, dt, A, Bm, Cm, beta, scale=None, dt_bias=None, dt_softplus=False, b
         if init_state is not None and (positions is None or int(positions[b]) > 0):
             h = d64(init_state)[row].clone()
         e = torch.zeros(H, P, dtype=torch.float64)
+        carried, rests, entering = [], [], h
         n = L if lengths is None else min(max(int(lengths[b]), 0), L)
         for t in range(n):
             k, q = Bm[b, t].repeat_interleave(H // G, 0), Cm[b, t].repeat_interleave(H // G, 0)
@@ -56,10 +59,18 @@ def delta(x, dt, A, Bm, Cm, beta, scale=None, dt_bias=None, dt_softplus=False, b
             own = eps * (size + (w.abs() * kn)[:, None] * (x[b, t].abs() + 2 * size * kn[:, None]))
             m = torch.maximum((1 - w * kn * kn).abs(), torch.ones_like(w))
             e = (m * a)[:, None] * e + spread * own
+            if spread > 1:
+                if t % 64 == 0:
+                    carried, rests, entering = [], [], h
+                entering = entering * a[:, None, None]
+                rests.append(w[:, None] * (x[b, t] - (entering * k[:, None]).sum(-1)))
+                carried = [a[:, None] * (z - (w * (z * k).sum(-1))[:, None] * k) for z in carried] + [k]
             h = h * a[:, None, None]
             h = h + (w[:, None] * (x[b, t] - (h * k[:, None]).sum(-1)))[..., None] * k[:, None]
             y[b, t] = scale * (h * q[:, None]).sum(-1)
-            ybound[b, t] = abs(scale) * q.norm(dim=-1)[:, None] * (e + eps * h.norm(dim=-1))
+            for z, r in zip(carried, rests):
+                ybound[b, t] += 2.0 ** -12 * abs(scale) * (q * z).sum(-1).abs()[:, None] * r.abs()
+            ybound[b, t] += abs(scale) * q.norm(dim=-1)[:, None] * (e + eps * h.norm(dim=-1))
         out[row], err[row] = h, e[..., None].expand(H, P, N)
     return y, ybound, out, err + 2.0 ** -23 * out.abs() + 1e-30
 
