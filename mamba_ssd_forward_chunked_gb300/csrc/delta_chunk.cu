@@ -30,7 +30,8 @@ constexpr int64_t kMinTokens = 64;
 // chunk of a head: two parts of W (N rows), one of P T (64 rows; it goes into y alone, which has 8 bits), and
 // the tokens' factors.  Of a chunk of a group, for every 64 of N: 64 rows of K, then of Q.
 constexpr uint32_t kSlab = 8192;  // 64 rows of 128 bytes
-enum { kBeta, kFromState, kOutState, kOutRest, kScalars, kFactors };
+enum { kBeta, kFromState, kScalars, kOutState, kOutRest, kFactors };
+constexpr uint32_t kFactorBytes = 2 * kC * 4 + 16;  // those that the second launch keeps in shared memory: up to the scalars
 enum { kDecay, kUpdate, kReach, kSpread };  // the scalars: e^{G_64}; what undoes W's scale; see the bounds of delta_walk_kernel
 __host__ __device__ constexpr uint32_t tile_bytes(int N) { return (2 * (N / 64) + 1) * kSlab; }
 __host__ __device__ constexpr uint32_t record_bytes(int N) { return tile_bytes(N) + kFactors * kC * 4; }
@@ -47,11 +48,10 @@ __device__ __forceinline__ Scale scale_for(uint32_t largest) {
   return {__uint_as_float((268 - e) << 23), __uint_as_float((e - 14) << 23)};
 }
 
-// Two neighbouring values as two fp16 parts.
+// Two neighbouring values as two fp16 parts: the first 11 bits, and what is left of them.
 __device__ __forceinline__ void split(float a, float b, uint32_t& hi, uint32_t& lo) {
-  const __half2 h = __floats2half2_rn(a, b);
-  const float2 f = __half22float2(h);
-  const __half2 l = __floats2half2_rn(a - f.x, b - f.y);
+  const float ah = __uint_as_float(__float_as_uint(a) & 0xFFFFE000u), bh = __uint_as_float(__float_as_uint(b) & 0xFFFFE000u);
+  const __half2 h = __floats2half2_rn(ah, bh), l = __floats2half2_rn(a - ah, b - bh);
   hi = *reinterpret_cast<const uint32_t*>(&h), lo = *reinterpret_cast<const uint32_t*>(&l);
 }
 
@@ -478,8 +478,12 @@ struct Walk {
   static constexpr int kSlabs = 2 * kPT / 64;              // 64 columns each of the two parts side by side
   static constexpr uint32_t kSlabS = N * 128;
   static constexpr uint32_t kRows = 0, kTile = kRows + kStages * rows_bytes(N), kS = kTile + kStages * tile_bytes(N);
-  static constexpr uint32_t kEnd = kS + kSlabs * N * 128;  // r takes the state's place
-  static constexpr uint32_t kX = kEnd + 16 * 8 + 4 * 4 + 4 * kWorkers * 4;  // a chunk's x, every thread's where it put it
+  static constexpr bool kOwnR = kStages > 1;               // r has a place of its own, or the state's
+  static constexpr uint32_t kR = kS + (kOwnR ? kSlabs * kSlabS : 0);
+  static constexpr uint32_t kEnd = kS + kSlabs * kSlabS + (kOwnR ? kSlabs * kSlab : 0);
+  static constexpr int kFactorSlots = kStages == 1 ? 1 : kStages + 1;
+  static constexpr uint32_t kLargest = kEnd + 16 * 8 + 4 * 4, kF = kLargest + 4 * kWorkers * 4;
+  static constexpr uint32_t kX = kF + kFactorSlots * kFactorBytes;  // a chunk's x, every thread's where it put it
   static constexpr uint32_t kTotal = kX + kC * kPT * 2;
   static constexpr uint32_t kTmem = 4 * kPT;               // columns of tensor memory
 };
@@ -510,7 +514,7 @@ __global__ void __launch_bounds__(Walk<N, kPT, kGroups, kStages>::kThreads, kBlo
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + M::kEnd);
   uint32_t* holder = reinterpret_cast<uint32_t*>(bars + kBarriers);
   volatile int* failed = reinterpret_cast<volatile int*>(holder + 1);
-  uint32_t* s_largest = holder + 4;  // [state, rest][chunk mod 2][warp]: bits of the largest magnitude
+  uint32_t* s_largest = reinterpret_cast<uint32_t*>(smem + M::kLargest);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t b = blockIdx.z;
   const int h = blockIdx.y, p0 = blockIdx.x * kPT;
@@ -549,6 +553,12 @@ __global__ void __launch_bounds__(Walk<N, kPT, kGroups, kStages>::kThreads, kBlo
       }
     }
   };
+  // The same without suspending the thread between tests: the products' thread is in the chain.
+  auto spin = [&](int bar, int phase) {
+    for (int i = 0; i < 4096; ++i)
+      if (mbar_test_wait(&bars[bar], phase & 1)) return true;
+    return wait(bar, phase);
+  };
 
   if (warp == kWorkers) {
     // loads
@@ -558,9 +568,14 @@ __global__ void __launch_bounds__(Walk<N, kPT, kGroups, kStages>::kThreads, kBlo
       while (t < chunks) {
         const int st = t % kStages, turn = t / kStages;
         ok = turn == 0 || wait(kRowsEmpty + st, turn - 1);
+        // the factors' place: with one for every stage and one more, its readers are a chunk further; with one in
+        // all they have read it when they have formed r
+        if (kStages == 1 && c > 0) ok = ok && wait(kRestReady, c - 1);
         if (!ok) break;
-        mbar_arrive_expect_tx(&bars[kRowsFull + st], rows_bytes(N));
+        mbar_arrive_expect_tx(&bars[kRowsFull + st], rows_bytes(N) + kFactorBytes);
         bulk_load(smem + M::kRows + st * rows_bytes(N), rows + c * static_cast<int64_t>(rows_bytes(N)), rows_bytes(N), &bars[kRowsFull + st]);
+        bulk_load(smem + M::kF + c % M::kFactorSlots * kFactorBytes, records + c * static_cast<int64_t>(record_bytes(N)) + tile_bytes(N), kFactorBytes,
+                  &bars[kRowsFull + st]);
         ++c;
         ok = turn == 0 || wait(kTileEmpty + st, turn - 1);
         if (!ok) break;
@@ -578,11 +593,11 @@ __global__ void __launch_bounds__(Walk<N, kPT, kGroups, kStages>::kThreads, kBlo
     if (lane == 0) {
       constexpr uint32_t id_two = idesc_f32acc(0, 128, 2 * kPT, 0, 1), id_one = idesc_f32acc(0, 128, kPT, 0, 1);
       const uint32_t base = smem_u32(smem);
-      const uint64_t dS = sdesc_sw128(base + M::kS, M::kSlabS, 1024), dR = sdesc_sw128(base + M::kS, kSlab, 1024);
+      const uint64_t dS = sdesc_sw128(base + M::kS, M::kSlabS, 1024), dR = sdesc_sw128(base + M::kR, kSlab, 1024);
       for (int c = 0; c < chunks; ++c) {
         const int st = c % kStages, turn = c / kStages;
         const uint32_t kq = base + M::kRows + st * rows_bytes(N);
-        if (!wait(kRowsFull + st, turn) || !wait(kStateReady, c)) break;
+        if (!wait(kRowsFull + st, turn) || !spin(kStateReady, c)) break;
         tc_fence_after();
         const uint64_t kq_rows = sdesc_sw128(kq, 16, 1024);
 #pragma unroll
@@ -590,7 +605,7 @@ __global__ void __launch_bounds__(Walk<N, kPT, kGroups, kStages>::kThreads, kBlo
           mma_ss<false>(tmem + kColD1, kq_rows + (((k >> 2) * 2 * kSlab + (k & 3) * 32) >> 4), dS + (k * 2048 >> 4), id_two, k != 0);
         mma_commit(&bars[kFromStateDone]);
         mma_commit(&bars[kRowsEmpty + st]);
-        if (!wait(kTileFull + st, turn) || !wait(kRestReady, c)) break;
+        if (!wait(kTileFull + st, turn) || !spin(kRestReady, c)) break;
         tc_fence_after();
         const uint32_t tile = base + M::kTile + st * tile_bytes(N);
         const uint64_t w = sdesc_sw128(tile, 16, 1024);
@@ -623,14 +638,14 @@ __global__ void __launch_bounds__(Walk<N, kPT, kGroups, kStages>::kThreads, kBlo
     const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x) + b * p.x_batch + static_cast<int64_t>(h) * p.P + col0;
 
     // kCols values of a row, scaled, as two parts side by side: rows of 128 bytes in slabs of 64 columns
-    auto put = [&](uint32_t slab, int at_row, const float (&v)[kCols], float up) {
+    auto put = [&](uint32_t tile, uint32_t slab, int at_row, const float (&v)[kCols], float up) {
 #pragma unroll
       for (int i = 0; i < kCols / 8; ++i) {
         uint4 hi, lo;
 #pragma unroll
         for (int e = 0; e < 4; ++e) split(v[8 * i + 2 * e] * up, v[8 * i + 2 * e + 1] * up, (&hi.x)[e], (&lo.x)[e]);
         const int c0 = group * kCols + 8 * i, c1 = kPT + c0;
-        uint8_t* to = smem + M::kS + at_row * 128;
+        uint8_t* to = smem + tile + at_row * 128;
         *reinterpret_cast<uint4*>(to + (c0 >> 6) * slab + ((((c0 & 63) >> 3) ^ (at_row & 7)) << 4)) = hi;
         *reinterpret_cast<uint4*>(to + (c1 >> 6) * slab + ((((c1 & 63) >> 3) ^ (at_row & 7)) << 4)) = lo;
       }
@@ -694,18 +709,11 @@ __global__ void __launch_bounds__(Walk<N, kPT, kGroups, kStages>::kThreads, kBlo
       for (int i = 0; i < kCols; ++i)
         S[i] = from && has_state && col0 + i < p.P ? from[(static_cast<int64_t>(h) * p.P + col0 + i) * N + row] : 0.f;
     }
-    // What comes from global memory is asked for a chunk ahead: factors into registers, x into shared memory.
+    // x is asked for a chunk ahead, into shared memory
     uint4* s_x = reinterpret_cast<uint4*>(smem + M::kX) + (2 * group + quarter) * 32 + lane;  // (of tokens)
     constexpr int kStrideX = 16 * kWorkers;
-    float next_a = 0.f, next_b = 0.f;
-    float4 next_scalars = make_float4(0.f, 0.f, 0.f, 0.f);
     auto ask = [&](int c) {
-      if (c >= chunks) return;
-      const float* f = reinterpret_cast<const float*>(records + c * static_cast<int64_t>(record_bytes(N)) + tile_bytes(N));
-      next_scalars = *reinterpret_cast<const float4*>(f + kScalars * kC);
-      next_a = f[(is_token ? kBeta : kOutState) * kC + token], next_b = f[(is_token ? kFromState : kOutRest) * kC + token];
       const int64_t t = begin + static_cast<int64_t>(c) * kC + token;
-      if (!is_token) return;
 #pragma unroll
       for (int i = 0; i < kCols / 8; ++i) {
         uint4* to = s_x + i * kStrideX;
@@ -720,7 +728,7 @@ __global__ void __launch_bounds__(Walk<N, kPT, kGroups, kStages>::kThreads, kBlo
         }
       }
     };
-    ask(0);
+    if (is_token) ask(0);
 
     // Scales go by bounds that are known while the products run, not by what comes out of them, so that nobody
     // waits for the others in the chain: with s the largest of the state
@@ -732,17 +740,22 @@ __global__ void __launch_bounds__(Walk<N, kPT, kGroups, kStages>::kThreads, kBlo
       leave(0, 1, magnitude(S), warp);
       named_bar_sync(1, 32 * kWorkers);
       state = scale_for(__float_as_uint(largest_of(0, 1, kWorkers)));
-      if (has_state) put(M::kSlabS, row, S, state.up);
+      if (has_state) put(M::kS, M::kSlabS, row, S, state.up);
       arrive(kStateReady);
     }
     for (int c = 0; c < chunks; ++c) {
       const int64_t t = begin + static_cast<int64_t>(c) * kC + token;
       const bool live = t < length;
-      const float fa = next_a, fb = next_b;
-      const float4 scalars = next_scalars;
+      const float* out_factors = reinterpret_cast<const float*>(records + c * static_cast<int64_t>(record_bytes(N)) + tile_bytes(N));
+      float fa, fb;
+      if (!is_token) fa = out_factors[kOutState * kC + token], fb = out_factors[kOutRest * kC + token];
+      ok = ok && all_wait(kRowsFull + c % kStages, c / kStages);
+      const float* factors = reinterpret_cast<const float*>(smem + M::kF + c % M::kFactorSlots * kFactorBytes);
+      const float4 scalars = *reinterpret_cast<const float4*>(factors + kScalars * kC);
       const float decay = scalars.x, update = scalars.y;
       float bx[kCols];
       if (is_token) {
+        fa = factors[kBeta * kC + token], fb = factors[kFromState * kC + token];
         asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll
         for (int i = 0; i < kCols / 8; ++i) {
@@ -753,9 +766,9 @@ __global__ void __launch_bounds__(Walk<N, kPT, kGroups, kStages>::kThreads, kBlo
             bx[8 * i + 2 * e] = fa * bf16_lo(w), bx[8 * i + 2 * e + 1] = fa * bf16_hi(w);
           }
         }
+        if (c + 1 < chunks) ask(c + 1);
         leave(1, c, magnitude(bx), 2 * group + quarter);
       }
-      ask(c + 1);
       leave(0, c, magnitude(S), warp);
       ok = !named_bar_or(1, 32 * kWorkers, !ok);  // (whoever has given up takes the others along)
       if (!ok) break;
@@ -772,7 +785,7 @@ __global__ void __launch_bounds__(Walk<N, kPT, kGroups, kStages>::kThreads, kBlo
         const float from_state = fb * state.down;
 #pragma unroll
         for (int i = 0; i < kCols; ++i) v[i] = live ? fmaf(-from_state, v[i], bx[i]) : 0.f;
-        if (ok) put(kSlab, token, v, rest.up);
+        if (ok) put(M::kR, kSlab, token, v, rest.up);
       } else {
         const float from_state = fa * state.down;
 #pragma unroll
@@ -789,12 +802,17 @@ __global__ void __launch_bounds__(Walk<N, kPT, kGroups, kStages>::kThreads, kBlo
         for (int i = 0; i < kCols; ++i) S[i] = fmaf(decay, S[i], back * v[i]);
       }
       state = next;
-      // P T has read r, whose place the state takes
-      ok = ok && all_wait(kRestDone, c);
+      const bool more = c + 1 < chunks;
+      if constexpr (M::kOwnR) {
+        if (more && has_state && ok) put(M::kS, M::kSlabS, row, S, state.up);
+        if (!is_token) ok = ok && all_wait(kRestDone, c);
+      } else {
+        ok = ok && all_wait(kRestDone, c);  // P T has read r, whose place the state takes
+        if (more && has_state && ok) put(M::kS, M::kSlabS, row, S, state.up);
+      }
       tc_fence_after();
-      if (c + 1 < chunks && has_state && ok) put(M::kSlabS, row, S, state.up);
       if (!is_token && ok) take(kColD3, v);
-      if (c + 1 < chunks && ok) arrive(kStateReady);
+      if (more && ok) arrive(kStateReady);
       if (!is_token && live && ok) {
         // y: the state's part, and P T r
         const float from_rest = fb * rest.down;

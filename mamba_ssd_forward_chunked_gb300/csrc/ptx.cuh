@@ -75,6 +75,18 @@ __device__ __forceinline__ bool mbar_try_wait_short(uint64_t* bar, uint32_t pari
       : "memory");
   return ok != 0;
 }
+// One test of a phase parity that does not suspend the thread.
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ bool mbar_wait_short(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
   if (mbar_try_wait_short(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
