@@ -110,6 +110,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prepare_kernel(DeltaPar
   int64_t* s_half = reinterpret_cast<int64_t*>(s_len + kC);
   uint32_t* s_largest = reinterpret_cast<uint32_t*>(s_half + 1);  // of every warp
   float *s_most = reinterpret_cast<float*>(s_largest + 4), *s_reach = s_most + 1;
+  float2* s_squares = reinterpret_cast<float2*>(smem + M::kT);  // of a row, and what undoes its scale (T comes later)
   begin_kernel();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t b = blockIdx.z;
@@ -158,7 +159,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prepare_kernel(DeltaPar
     s_lo[tid] = static_cast<float>(static_cast<int>(G & 0xFFFFFF)) * 0x1p-32f;
     s_beta[tid] = beta;
   }
-  // in fp16, times a power of two; s_kn and s_qn undo it and normalise
+  // in fp16, times a power of two
   uint8_t* rows_out = h == g * per ? s.rows + ((b * p.G + g) * s.count + blockIdx.x) * static_cast<int64_t>(rows_bytes(N)) : nullptr;
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
@@ -187,13 +188,15 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prepare_kernel(DeltaPar
     *reinterpret_cast<uint4*>(smem + r * M::kRow + col * 16) = half;
     if (rows_out)
       *reinterpret_cast<uint4*>(rows_out + (col >> 3) * 2 * kSlab + r * 128 + (((col & 7) ^ (r & 7)) << 4)) = half;
-    if (col == 0) {
-      const float norm = delta_norm(p, squares);
-      (r < kC ? s_kn : s_qn)[r & 63] = norm * scale.down;
-      if (r < kC) s_len[r] = norm * sqrtf(squares);
-    }
+    if (col == 0) s_squares[r] = make_float2(squares, scale.down);
   }
   __syncthreads();
+  {
+    const float2 v = s_squares[tid];
+    const float norm = delta_norm(p, v.x);
+    (tid < kC ? s_kn : s_qn)[tid & 63] = norm * v.y;  // undoes the power of two and normalises
+    if (tid < kC) s_len[tid] = norm * sqrtf(v.x);
+  }
 
   // K K^T and Q K^T, 16 rows a warp of each (those with fewest columns beside those with most)
   float acc[2][8][4];
@@ -475,7 +478,7 @@ struct Walk {
   static constexpr int kWorkers = 4 * kGroups;             // warps with the state
   static constexpr int kThreads = 32 * (kWorkers + 2);     // and one that loads, one that issues the products
   static constexpr int kCols = kPT / kGroups;              // of a thread
-  static constexpr int kSlabs = 2 * kPT / 64;              // 64 columns each of the two parts side by side
+  static constexpr int kSlabs = (2 * kPT + 63) / 64;       // 64 columns each of the two parts side by side
   static constexpr uint32_t kSlabS = N * 128;
   static constexpr uint32_t kRows = 0, kTile = kRows + kStages * rows_bytes(N), kS = kTile + kStages * tile_bytes(N);
   static constexpr bool kOwnR = kStages > 1;               // r has a place of its own, or the state's
@@ -522,6 +525,7 @@ __global__ void __launch_bounds__(Walk<N, kPT, kGroups, kStages>::kThreads, kBlo
     for (int i = 0; i < kBarriers; ++i) mbar_init(&bars[i], i == kStateReady || i == kRestReady ? kWorkers : 1);
     fence_mbar_init();
     *failed = 0;
+    for (int i = 0; i < 4 * kWorkers; ++i) s_largest[i] = 0;
   }
   if (warp == kWorkers) {
     tmem_alloc(holder, M::kTmem);
@@ -883,8 +887,13 @@ cudaError_t launch_chunks(const DeltaParams& p, const DeltaChunks& s, cudaStream
     e = launch_k(delta_prepare_kernel<N>, dim3(static_cast<unsigned>(s.count), static_cast<unsigned>(p.H), static_cast<unsigned>(p.batch)),
                  dim3(kPrepThreads), bytes, stream, true, p, s);
   if (e != cudaSuccess) return e;
-  const bool narrow = p.batch * p.H * ceil_div(p.P, 32) <= layer_sm_count();
-  return narrow ? launch_walk<N, 32, 4, 2, 1>(p, s, stream) : launch_walk<N, 64, 2, 1, 2>(p, s, stream);
+  // Columns of a block: as few as leave every block a multiprocessor of its own (the chain is the shorter, and what is
+  // loaded for it the same), 32 where there are more, two blocks on each.  16 heads of 128 x 128, 16384 tokens:
+  // 16 columns 379 us, 32 482; 128 heads, 4096 tokens: 32 columns 479 and, two blocks each, 360, 16 491.
+  const int64_t heads = p.batch * p.H, sms = layer_sm_count();
+  return heads * ceil_div(p.P, 16) <= sms ? launch_walk<N, 16, 2, 2, 1>(p, s, stream)
+         : heads * ceil_div(p.P, 32) <= sms ? launch_walk<N, 32, 2, 2, 1>(p, s, stream)
+                                            : launch_walk<N, 32, 2, 1, 2>(p, s, stream);
 }
 
 constexpr int64_t kRecordBytes = int64_t(1) << 40;
