@@ -57,8 +57,8 @@ __device__ __forceinline__ void split(float a, float b, uint32_t& hi, uint32_t& 
 
 // ------------------------------------------------------------------ first launch
 
-constexpr int kPrepThreads = 128;
-constexpr int kStrideA = 68, kStrideT = 72;  // (floats) rows that the fragments' and vectors' loads find in different banks
+constexpr int kPrepThreads = 256;
+constexpr int kStride = 68;  // (floats) of A and T: what a fragment's load takes lies in 32 banks
 
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t at) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -90,13 +90,27 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// A product in TF32, each factor as two parts (2^-22 of it is left out).  A thread gives rows g and g + 8 of the
+// first factor in columns 2 c and 2 c + 1 (a[0], a[1] and a[2], a[3]; g = lane / 4, c = lane % 4), as an earlier
+// product leaves them, where the instruction wants c and c + 4: so it gives those rows of the second factor, at
+// column g.
+__device__ __forceinline__ void mma_tf32_parts(float (&o)[4], const float (&a)[4], float b0, float b1) {
+  uint32_t ah[4], al[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) ah[e] = __float_as_uint(a[e]) & 0xFFFFE000u, al[e] = __float_as_uint(a[e] - __uint_as_float(ah[e]));
+  const uint32_t h0 = __float_as_uint(b0) & 0xFFFFE000u, h1 = __float_as_uint(b1) & 0xFFFFE000u;
+  mma_tf32(o, al, h0, h1);
+  mma_tf32(o, ah, __float_as_uint(b0 - __uint_as_float(h0)), __float_as_uint(b1 - __uint_as_float(h1)));
+  mma_tf32(o, ah, h0, h1);
+}
+
 template <int N>
 struct PrepSmem {
   static constexpr uint32_t kRow = N * 2 + 16;  // bytes of a row of K or Q, eight rows in different banks
   // K; Q, whose place A takes; T
-  static constexpr uint32_t kA = kC * kRow, kSize = kRow > kStrideA * 4 ? kRow : kStrideA * 4, kT = kA + kC * kSize;
-  static constexpr uint32_t kVec = kT + kC * kStrideT * 4;
-  static constexpr uint32_t kTotal = kVec + 7 * kC * 4 + 48;
+  static constexpr uint32_t kA = kC * kRow, kSize = kRow > kStride * 4 ? kRow : kStride * 4, kT = kA + kC * kSize;
+  static constexpr uint32_t kVec = kT + kC * kStride * 4;
+  static constexpr uint32_t kTotal = kVec + 7 * kC * 4 + 64;
 };
 
 template <int N>
@@ -109,26 +123,35 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prepare_kernel(DeltaPar
   float *s_lo = s_hi + kC, *s_beta = s_lo + kC, *s_kn = s_beta + kC, *s_qn = s_kn + kC, *s_to = s_qn + kC, *s_len = s_to + kC;
   int64_t* s_half = reinterpret_cast<int64_t*>(s_len + kC);
   uint32_t* s_largest = reinterpret_cast<uint32_t*>(s_half + 1);  // of every warp
-  float *s_most = reinterpret_cast<float*>(s_largest + 4), *s_reach = s_most + 1;
+  float *s_most = reinterpret_cast<float*>(s_largest + 8), *s_reach = s_most + 1;
   float2* s_squares = reinterpret_cast<float2*>(smem + M::kT);  // of a row, and what undoes its scale (T comes later)
-  begin_kernel();
+  // A pair of launches before this one may still walk its chunks, from the other buffer: only the end of this
+  // launch waits for it, in one block, so that the next walk finds both complete (see launch_delta_chunks).
+  if (s.first == 0)
+    begin_kernel();
+  else
+    grid_dep_launch();
+  const bool holds_on = s.first > 0 && blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1 && blockIdx.z == gridDim.z - 1;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t b = blockIdx.z;
   const int h = blockIdx.y, chunk = s.first + blockIdx.x;
   const DeltaSeq seq = delta_sequence(p, b);
   const int64_t t0 = static_cast<int64_t>(chunk) * kC;
-  if (seq.row < 0 || t0 >= seq.length) return;
+  if (seq.row < 0 || t0 >= seq.length) {
+    if (holds_on) grid_dep_wait();
+    return;
+  }
   const int n = seq.length - t0 < kC ? static_cast<int>(seq.length - t0) : kC;
   const int per = p.H / p.G, g = h / per;
 
   // rows of K, then of Q; rows behind the sequence are 0
-  constexpr int kRowLanes = N / 8, kPer = 32 / kRowLanes, kLoads = 32 / kPer;
+  constexpr int kRowLanes = N / 8, kPer = 32 / kRowLanes, kLoads = 16 / kPer;
   const __nv_bfloat16* from[2] = {static_cast<const __nv_bfloat16*>(p.Bm) + b * p.B_batch + t0 * p.B_token + static_cast<int64_t>(g) * N,
                                   static_cast<const __nv_bfloat16*>(p.Cm) + b * p.C_batch + t0 * p.C_token + static_cast<int64_t>(g) * N};
   uint4 raw[kLoads];
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
-    const int r = warp * 32 + i * kPer + lane / kRowLanes, t = r & 63;
+    const int r = warp * 16 + i * kPer + lane / kRowLanes, t = r & 63;
     raw[i] = make_uint4(0, 0, 0, 0);
     if (t < n) {
       const __nv_bfloat16* row = (r < kC ? from[0] + t * p.B_token : from[1] + t * p.C_token) + lane % kRowLanes * 8;
@@ -163,7 +186,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prepare_kernel(DeltaPar
   uint8_t* rows_out = h == g * per ? s.rows + ((b * p.G + g) * s.count + blockIdx.x) * static_cast<int64_t>(rows_bytes(N)) : nullptr;
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
-    const int r = warp * 32 + i * kPer + lane / kRowLanes;
+    const int r = warp * 16 + i * kPer + lane / kRowLanes;
     const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
     float squares = 0.f;
     uint32_t largest = 0;
@@ -191,24 +214,24 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prepare_kernel(DeltaPar
     if (col == 0) s_squares[r] = make_float2(squares, scale.down);
   }
   __syncthreads();
-  {
+  if (tid < 2 * kC) {
     const float2 v = s_squares[tid];
     const float norm = delta_norm(p, v.x);
     (tid < kC ? s_kn : s_qn)[tid & 63] = norm * v.y;  // undoes the power of two and normalises
     if (tid < kC) s_len[tid] = norm * sqrtf(v.x);
   }
 
-  // K K^T and Q K^T, 16 rows a warp of each (those with fewest columns beside those with most)
-  float acc[2][8][4];
-  const int mt[2] = {warp, 3 - warp};
+  // K K^T (four warps, 16 rows each) and Q K^T (four more)
+  const bool is_q = warp >= 4;
+  const int mt = is_q ? 7 - warp : warp;  // (beside a warp of few columns one of many)
   const uint32_t rows = smem_u32(smem);
+  float acc[8][4];
 #pragma unroll
-  for (int m = 0; m < 2; ++m) {
+  for (int i = 0; i < 8; ++i)
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[m][i][e] = 0.f;
-    const uint32_t at = rows + (64 * m + 16 * mt[m] + (lane & 15)) * M::kRow + (lane >> 4) * 16;
+    for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
+  {
+    const uint32_t at = rows + ((is_q ? kC : 0) + 16 * mt + (lane & 15)) * M::kRow + (lane >> 4) * 16;
     const uint32_t bt = rows + ((lane & 7) + (lane >> 4) * 8) * M::kRow + ((lane >> 3) & 1) * 16;
 #pragma unroll
     for (int k = 0; k < N / 16; ++k) {
@@ -216,39 +239,38 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prepare_kernel(DeltaPar
       ldmatrix4(a, at + k * 32);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        if (j > mt[m]) break;
+        if (j > mt) break;
         uint32_t v[4];
         ldmatrix4(v, bt + j * 16 * M::kRow + k * 32);
-        mma_f16(acc[m][2 * j], a, v[0], v[1]);
-        mma_f16(acc[m][2 * j + 1], a, v[2], v[3]);
+        mma_f16(acc[2 * j], a, v[0], v[1]);
+        mma_f16(acc[2 * j + 1], a, v[2], v[3]);
       }
     }
   }
   __syncthreads();  // Q's rows have been read
   // A; P, whose rows' norms, powers of two and scale wait for the end, stays in registers
-#pragma unroll
-  for (int m = 0; m < 2; ++m) {
-    const int row = 16 * mt[m] + (lane >> 2);
+  {
+    const int row = 16 * mt + (lane >> 2);
     const float hi0 = s_hi[row], hi8 = s_hi[row + 8], lo0 = s_lo[row], lo8 = s_lo[row + 8];
-    const float f0 = m == 0 ? s_kn[row] * s_beta[row] : 0x1p-14f, f8 = m == 0 ? s_kn[row + 8] * s_beta[row + 8] : 0x1p-14f;
+    const float f0 = is_q ? 0x1p-14f : s_kn[row] * s_beta[row], f8 = is_q ? 0x1p-14f : s_kn[row + 8] * s_beta[row + 8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      if (j > 2 * mt[m] + 1) break;
+      if (j > 2 * mt + 1) break;
       const int col = 8 * j + (lane & 3) * 2;
       const float2 hi = *reinterpret_cast<const float2*>(&s_hi[col]), lo = *reinterpret_cast<const float2*>(&s_lo[col]),
                    kn = *reinterpret_cast<const float2*>(&s_kn[col]);
-      float(&v)[4] = acc[m][j];
+      float(&v)[4] = acc[j];
       v[0] *= exp2_fast((hi0 - hi.x) + (lo0 - lo.x)) * (kn.x * f0);
       v[1] *= exp2_fast((hi0 - hi.y) + (lo0 - lo.y)) * (kn.y * f0);
       v[2] *= exp2_fast((hi8 - hi.x) + (lo8 - lo.x)) * (kn.x * f8);
       v[3] *= exp2_fast((hi8 - hi.y) + (lo8 - lo.y)) * (kn.y * f8);
       // below the diagonal (P: and on it); a factor above it may be infinite
-      const int below = col + (m == 0 ? 0 : -1);
+      const int below = col - (is_q ? 1 : 0);
       v[0] = below < row ? v[0] : 0.f, v[1] = below + 1 < row ? v[1] : 0.f;
       v[2] = below < row + 8 ? v[2] : 0.f, v[3] = below + 1 < row + 8 ? v[3] : 0.f;
-      if (m == 0) {
-        *reinterpret_cast<float2*>(&s_A[row * kStrideA + col]) = make_float2(v[0], v[1]);
-        *reinterpret_cast<float2*>(&s_A[(row + 8) * kStrideA + col]) = make_float2(v[2], v[3]);
+      if (!is_q) {
+        *reinterpret_cast<float2*>(&s_A[row * kStride + col]) = make_float2(v[0], v[1]);
+        *reinterpret_cast<float2*>(&s_A[(row + 8) * kStride + col]) = make_float2(v[2], v[3]);
       }
     }
   }
@@ -280,96 +302,84 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prepare_kernel(DeltaPar
       float sum = r == c ? 1.f : 0.f;
 #pragma unroll
       for (int k4 = 0; k4 < r; k4 += 4) {
-        const float4 a = *reinterpret_cast<const float4*>(&s_A[(d0 + r) * kStrideA + d0 + k4]);
+        const float4 a = *reinterpret_cast<const float4*>(&s_A[(d0 + r) * kStride + d0 + k4]);
         sum = fmaf(-a.x, v[k4], sum);
         if (k4 + 1 < r) sum = fmaf(-a.y, v[k4 + 1], sum);
         if (k4 + 2 < r) sum = fmaf(-a.z, v[k4 + 2], sum);
         if (k4 + 3 < r) sum = fmaf(-a.w, v[k4 + 3], sum);
       }
       v[r] = sum;
-      s_T[(d0 + r) * kStrideT + d0 + c] = sum;
+      s_T[(d0 + r) * kStride + d0 + c] = sum;
     }
   }
   __syncthreads();
-  const int c = tid & 15, r = tid >> 4 << 1;  // a thread's column and two rows of every block
+  // (two warps a row of blocks, 8 columns each; the products T_ii A_ik need nothing but the diagonal)
+  {
+    const int i = 1 + (warp >> 1), half = warp & 1;
+    const int gr = lane >> 2, gc = (lane & 3) * 2;
+    float f[3][2][4];
+    if (i < 4) {
+      float t[2][4];
 #pragma unroll
-  for (int d = 1; d < 4; ++d) {
-    float w[3][2];
-#pragma unroll
-    for (int j = 0; j + d < 4; ++j) {
-      const int i = j + d;
-      float s0 = 0.f, s1 = 0.f;
-#pragma unroll 4
-      for (int k = 16 * j; k < 16 * i; k += 4) {
-        const float4 a0 = *reinterpret_cast<const float4*>(&s_A[(16 * i + r) * kStrideA + k]);
-        const float4 a1 = *reinterpret_cast<const float4*>(&s_A[(16 * i + r + 1) * kStrideA + k]);
-        const float* t = &s_T[k * kStrideT + 16 * j + c];
-        s0 = fmaf(a0.x, t[0], s0), s1 = fmaf(a1.x, t[0], s1);
-        s0 = fmaf(a0.y, t[kStrideT], s0), s1 = fmaf(a1.y, t[kStrideT], s1);
-        s0 = fmaf(a0.z, t[2 * kStrideT], s0), s1 = fmaf(a1.z, t[2 * kStrideT], s1);
-        s0 = fmaf(a0.w, t[3 * kStrideT], s0), s1 = fmaf(a1.w, t[3 * kStrideT], s1);
+      for (int k = 0; k < 2; ++k) {
+        const float* at = &s_T[(16 * i + gr) * kStride + 16 * i + 8 * k + gc];
+        const float2 a = *reinterpret_cast<const float2*>(at), b8 = *reinterpret_cast<const float2*>(at + 8 * kStride);
+        t[k][0] = a.x, t[k][1] = b8.x, t[k][2] = a.y, t[k][3] = b8.y;
       }
-      s_T[(16 * i + r) * kStrideT + 16 * j + c] = s0;
-      s_T[(16 * i + r + 1) * kStrideT + 16 * j + c] = s1;
-    }
-    __syncthreads();
 #pragma unroll
-    for (int j = 0; j + d < 4; ++j) {
-      const int i = j + d;
-      float s0 = 0.f, s1 = 0.f;
+      for (int k = 0; k < 3; ++k) {
+        if (k >= i) break;
 #pragma unroll
-      for (int k = 0; k < 16; k += 4) {
-        const float4 a0 = *reinterpret_cast<const float4*>(&s_T[(16 * i + r) * kStrideT + 16 * i + k]);
-        const float4 a1 = *reinterpret_cast<const float4*>(&s_T[(16 * i + r + 1) * kStrideT + 16 * i + k]);
-        const float* t = &s_T[(16 * i + k) * kStrideT + 16 * j + c];
-        s0 = fmaf(a0.x, t[0], s0), s1 = fmaf(a1.x, t[0], s1);
-        s0 = fmaf(a0.y, t[kStrideT], s0), s1 = fmaf(a1.y, t[kStrideT], s1);
-        s0 = fmaf(a0.z, t[2 * kStrideT], s0), s1 = fmaf(a1.z, t[2 * kStrideT], s1);
-        s0 = fmaf(a0.w, t[3 * kStrideT], s0), s1 = fmaf(a1.w, t[3 * kStrideT], s1);
+        for (int u = 0; u < 2; ++u) {
+          float o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float* at = &s_A[(16 * i + 8 * e + gc) * kStride + 16 * k + 8 * u + gr];
+            mma_tf32_parts(o, t[e], at[0], at[kStride]);
+          }
+          f[k][u][0] = o[0], f[k][u][1] = o[2], f[k][u][2] = o[1], f[k][u][3] = o[3];
+        }
       }
-      w[j][0] = -s0, w[j][1] = -s1;
     }
-    __syncthreads();
 #pragma unroll
-    for (int j = 0; j + d < 4; ++j) {
-      s_T[(16 * (j + d) + r) * kStrideT + 16 * j + c] = w[j][0];
-      s_T[(16 * (j + d) + r + 1) * kStrideT + 16 * j + c] = w[j][1];
+    for (int d = 1; d < 4; ++d) {
+      const int j = i - d;
+      if (i < 4 && j >= 0) {
+        float o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          if (k < j || k >= i) continue;
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const float* at = &s_T[(16 * k + 8 * u + gc) * kStride + 16 * j + 8 * half + gr];
+            mma_tf32_parts(o, f[k][u], at[0], at[kStride]);
+          }
+        }
+        float* to = &s_T[(16 * i + gr) * kStride + 16 * j + 8 * half + gc];
+        *reinterpret_cast<float2*>(to) = make_float2(-o[0], -o[1]);
+        *reinterpret_cast<float2*>(to + 8 * kStride) = make_float2(-o[2], -o[3]);
+      }
+      __syncthreads();
     }
-    __syncthreads();
   }
 
-  // P T in place of A: TF32 products, each factor as two parts (2^-22 of it is left out).  A thread has
-  // columns 2 c and 2 c + 1 of P where the product wants c and c + 4: so T's rows are taken in that order.
-  {
+  // P T, whose rows a warp has in registers as the products of above have theirs
+  if (is_q) {
     float o[8][4];
 #pragma unroll
     for (int j = 0; j < 8; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
-    const float* t = s_T + (lane & 3) * 2 * kStrideT + (lane >> 2);
+    const float* t = s_T + (lane & 3) * 2 * kStride + (lane >> 2);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      if (k > 2 * mt[1] + 1) break;
-      uint32_t ah[4], al[4];
-      const int order[4] = {0, 2, 1, 3};
+      if (k > 2 * mt + 1) break;
+      const float a[4] = {acc[k][0], acc[k][2], acc[k][1], acc[k][3]};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float v = acc[1][k][order[e]];
-        ah[e] = __float_as_uint(round_tf32(v)), al[e] = __float_as_uint(v - __uint_as_float(ah[e]));
-      }
-#pragma unroll
-      for (int j = 0; j <= k; ++j) {
-        const float v[2] = {t[8 * k * kStrideT + 8 * j], t[(8 * k + 1) * kStrideT + 8 * j]};
-        uint32_t th[2], tl[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) th[e] = __float_as_uint(round_tf32(v[e])), tl[e] = __float_as_uint(v[e] - __uint_as_float(th[e]));
-        mma_tf32(o[j], al, th[0], th[1]);
-        mma_tf32(o[j], ah, tl[0], tl[1]);
-        mma_tf32(o[j], ah, th[0], th[1]);
-      }
+      for (int j = 0; j <= k; ++j) mma_tf32_parts(o[j], a, t[8 * k * kStride + 8 * j], t[(8 * k + 1) * kStride + 8 * j]);
     }
     // as the second launch reads it, where A was; blocks above the diagonal are 0
-    const int at_row = 16 * mt[1] + (lane >> 3 & 1) * 8 + (lane & 7);
+    const int at_row = 16 * mt + (lane >> 3 & 1) * 8 + (lane & 7);
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
       uint32_t v[4];
@@ -383,66 +393,57 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prepare_kernel(DeltaPar
     }
   }
 
-  // W = K^T T', T's rows times their factors in two fp16 parts (K is one): 8 columns at a time, a warp has two
-  // such, those with fewest rows of T beside those with most
+  // W = K^T T', T's rows times their factors in two fp16 parts (K is one): 8 columns a warp
   constexpr int kTiles = N / 16;
-  float w[2][kTiles][4];
-  uint32_t bh[2][4][2], bl[2][4][2];
-  const int nt[2] = {warp, 7 - warp};
+  float w[kTiles][4];
+  uint32_t bh[4][2], bl[4][2];
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
+  for (int m = 0; m < kTiles; ++m)
 #pragma unroll
-    for (int m = 0; m < kTiles; ++m)
+    for (int e = 0; e < 4; ++e) w[m][e] = 0.f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) w[u][m][e] = 0.f;
+  for (int k = 0; k < 4; ++k) {
+    if (k < warp >> 1) continue;  // above the diagonal
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (k < nt[u] >> 1) continue;  // above the diagonal
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int i = 16 * k + 8 * e + (lane & 3) * 2;
-        const float* t = &s_T[i * kStrideT + 8 * nt[u] + (lane >> 2)];
-        split(t[0] * s_to[i], t[kStrideT] * s_to[i + 1], bh[u][k][e], bl[u][k][e]);
-      }
+    for (int e = 0; e < 2; ++e) {
+      const int i = 16 * k + 8 * e + (lane & 3) * 2;
+      const float* t = &s_T[i * kStride + 8 * warp + (lane >> 2)];
+      split(t[0] * s_to[i], t[kStride] * s_to[i + 1], bh[k][e], bl[k][e]);
     }
   }
   const uint32_t kt = rows + ((lane & 7) + (lane >> 4) * 8) * M::kRow + ((lane >> 3) & 1) * 16;
 #pragma unroll
-  for (int m = 0; m < kTiles; ++m)
+  for (int k = 0; k < 4; ++k) {
+    if (k < warp >> 1) continue;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (k < nt[0] >> 1) continue;
+    for (int m = 0; m < kTiles; ++m) {
       uint32_t a[4];
       ldmatrix4_t(a, kt + k * 16 * M::kRow + m * 32);
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        if (k < nt[u] >> 1) continue;
-        mma_f16(w[u][m], a, bl[u][k][0], bl[u][k][1]);
-        mma_f16(w[u][m], a, bh[u][k][0], bh[u][k][1]);
-      }
+      mma_f16(w[m], a, bl[k][0], bl[k][1]);
+      mma_f16(w[m], a, bh[k][0], bh[k][1]);
     }
+  }
   float top = 0.f;
 #pragma unroll
-  for (int u = 0; u < 2; ++u)
+  for (int m = 0; m < kTiles; ++m)
 #pragma unroll
-    for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(w[u][m][e]));
+    for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(w[m][e]));
   const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
   if (lane == 0) s_largest[warp] = bits;
   __syncthreads();
-  const Scale scale = scale_for(max(max(s_largest[0], s_largest[1]), max(s_largest[2], s_largest[3])));
+  uint32_t most_bits = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) most_bits = max(most_bits, s_largest[i]);
+  const Scale scale = scale_for(most_bits);
   // the parts where K and T were, and all into global memory
 #pragma unroll
-  for (int u = 0; u < 2; ++u)
+  for (int m = 0; m < kTiles; ++m) {
+    const int at_row = 16 * m + (lane >> 3 & 1) * 8 + (lane & 7);
+    uint32_t hi[2], lo[2];
 #pragma unroll
-    for (int m = 0; m < kTiles; ++m) {
-      const int at_row = 16 * m + (lane >> 3 & 1) * 8 + (lane & 7);
-      uint32_t hi[2], lo[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) split(w[u][m][2 * e] * scale.up, w[u][m][2 * e + 1] * scale.up, hi[e], lo[e]);
-      stmatrix4(rows + (lane < 16 ? 0 : M::kT) + at_row * 128 + ((nt[u] ^ (at_row & 7)) << 4), hi[0], hi[1], lo[0], lo[1]);
-    }
+    for (int e = 0; e < 2; ++e) split(w[m][2 * e] * scale.up, w[m][2 * e + 1] * scale.up, hi[e], lo[e]);
+    stmatrix4(rows + (lane < 16 ? 0 : M::kT) + at_row * 128 + ((warp ^ (at_row & 7)) << 4), hi[0], hi[1], lo[0], lo[1]);
+  }
   fence_proxy_async_smem();
   __syncthreads();
   uint8_t* out = s.records + ((b * p.H + h) * s.count + blockIdx.x) * static_cast<int64_t>(record_bytes(N));
@@ -467,6 +468,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prepare_kernel(DeltaPar
     tma_store_commit();
     tma_store_wait_all();
   }
+  if (holds_on) grid_dep_wait();
 }
 
 // ------------------------------------------------------------------ second launch
@@ -484,14 +486,13 @@ struct Walk {
   static constexpr bool kOwnR = kStages > 1;               // r has a place of its own, or the state's
   static constexpr uint32_t kR = kS + (kOwnR ? kSlabs * kSlabS : 0);
   static constexpr uint32_t kEnd = kS + kSlabs * kSlabS + (kOwnR ? kSlabs * kSlab : 0);
-  static constexpr int kFactorSlots = kStages == 1 ? 1 : kStages + 1;
-  static constexpr uint32_t kLargest = kEnd + 16 * 8 + 4 * 4, kF = kLargest + 4 * kWorkers * 4;
-  static constexpr uint32_t kX = kF + kFactorSlots * kFactorBytes;  // a chunk's x, every thread's where it put it
+  static constexpr uint32_t kLargest = kEnd + 18 * 8 + 4 * 4, kF = kLargest + 4 * kWorkers * 4;
+  static constexpr uint32_t kX = kF + kStages * kFactorBytes;  // a chunk's x, every thread's where it put it
   static constexpr uint32_t kTotal = kX + kC * kPT * 2;
   static constexpr uint32_t kTmem = 4 * kPT;               // columns of tensor memory
 };
 
-enum { kRowsFull, kRowsFull1, kRowsEmpty, kRowsEmpty1, kTileFull, kTileFull1, kTileEmpty, kTileEmpty1, kStateReady, kFromStateDone,
+enum { kRowsFull, kRowsFull1, kRowsEmpty, kRowsEmpty1, kFactorsRead, kFactorsRead1, kTileFull, kTileFull1, kTileEmpty, kTileEmpty1, kStateReady, kFromStateDone,
        kRestReady, kUpdateDone, kRestDone, kDrained, kBarriers };
 
 // cp.async.bulk: bytes from global to shared memory, counted by the barrier.
@@ -522,7 +523,7 @@ __global__ void __launch_bounds__(Walk<N, kPT, kGroups, kStages>::kThreads, kBlo
   const int64_t b = blockIdx.z;
   const int h = blockIdx.y, p0 = blockIdx.x * kPT;
   if (tid == 0) {
-    for (int i = 0; i < kBarriers; ++i) mbar_init(&bars[i], i == kStateReady || i == kRestReady ? kWorkers : 1);
+    for (int i = 0; i < kBarriers; ++i) mbar_init(&bars[i], i == kStateReady || i == kRestReady || i == kFactorsRead || i == kFactorsRead1 ? kWorkers : 1);
     fence_mbar_init();
     *failed = 0;
     for (int i = 0; i < 4 * kWorkers; ++i) s_largest[i] = 0;
@@ -572,13 +573,13 @@ __global__ void __launch_bounds__(Walk<N, kPT, kGroups, kStages>::kThreads, kBlo
       while (t < chunks) {
         const int st = t % kStages, turn = t / kStages;
         ok = turn == 0 || wait(kRowsEmpty + st, turn - 1);
-        // the factors' place: with one for every stage and one more, its readers are a chunk further; with one in
-        // all they have read it when they have formed r
-        if (kStages == 1 && c > 0) ok = ok && wait(kRestReady, c - 1);
+        // (the rows' product does not wait for those who read the factors, nor would they notice that the stage
+        // has been filled twice)
+        ok = ok && (turn == 0 || wait(kFactorsRead + st, turn - 1));
         if (!ok) break;
         mbar_arrive_expect_tx(&bars[kRowsFull + st], rows_bytes(N) + kFactorBytes);
         bulk_load(smem + M::kRows + st * rows_bytes(N), rows + c * static_cast<int64_t>(rows_bytes(N)), rows_bytes(N), &bars[kRowsFull + st]);
-        bulk_load(smem + M::kF + c % M::kFactorSlots * kFactorBytes, records + c * static_cast<int64_t>(record_bytes(N)) + tile_bytes(N), kFactorBytes,
+        bulk_load(smem + M::kF + c % kStages * kFactorBytes, records + c * static_cast<int64_t>(record_bytes(N)) + tile_bytes(N), kFactorBytes,
                   &bars[kRowsFull + st]);
         ++c;
         ok = turn == 0 || wait(kTileEmpty + st, turn - 1);
@@ -754,7 +755,7 @@ __global__ void __launch_bounds__(Walk<N, kPT, kGroups, kStages>::kThreads, kBlo
       float fa, fb;
       if (!is_token) fa = out_factors[kOutState * kC + token], fb = out_factors[kOutRest * kC + token];
       ok = ok && all_wait(kRowsFull + c % kStages, c / kStages);
-      const float* factors = reinterpret_cast<const float*>(smem + M::kF + c % M::kFactorSlots * kFactorBytes);
+      const float* factors = reinterpret_cast<const float*>(smem + M::kF + c % kStages * kFactorBytes);
       const float4 scalars = *reinterpret_cast<const float4*>(factors + kScalars * kC);
       const float decay = scalars.x, update = scalars.y;
       float bx[kCols];
@@ -773,6 +774,8 @@ __global__ void __launch_bounds__(Walk<N, kPT, kGroups, kStages>::kThreads, kBlo
         if (c + 1 < chunks) ask(c + 1);
         leave(1, c, magnitude(bx), 2 * group + quarter);
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[kFactorsRead + c % kStages]);
       leave(0, c, magnitude(S), warp);
       ok = !named_bar_or(1, 32 * kWorkers, !ok);  // (whoever has given up takes the others along)
       if (!ok) break;
@@ -896,12 +899,16 @@ cudaError_t launch_chunks(const DeltaParams& p, const DeltaChunks& s, cudaStream
                                             : launch_walk<N, 32, 2, 1, 2>(p, s, stream);
 }
 
-constexpr int64_t kRecordBytes = int64_t(1) << 40;
+// Chunks of a pair of launches.  Pairs overlap, the first launch of one with the walk of the one before, and what
+// the one leaves for the other stays in the L2; but every walk begins and ends once more.  Where the walk leaves
+// no room (more blocks than multiprocessors) pairs only limit the workspace.  16 heads, 16384 tokens: 48 MB 538 us,
+// 24 MB 549, one pair 568; 128 heads, 4096 tokens: one pair 651, 48 MB 675.
+constexpr int64_t kPairBytes = int64_t(48) << 20, kPairBytesFull = int64_t(512) << 20;
 
-// Chunks of a pair of launches: as many as keep what the first leaves within half the L2.
+int64_t bytes_of_chunk(const DeltaParams& p) { return p.batch * (int64_t(record_bytes(p.N)) * p.H + int64_t(rows_bytes(p.N)) * p.G); }
 int64_t chunks_at_once(const DeltaParams& p) {
-  const int64_t all = ceil_div(p.seqlen, kC), fit = kRecordBytes / (p.batch * (record_bytes(p.N) * p.H + rows_bytes(p.N) * p.G));
-  return fit < 8 ? (all < 8 ? all : 8) : fit < all ? fit : all;
+  const int64_t all = ceil_div(p.seqlen, kC), fit = (p.batch * p.H * ceil_div(p.P, 16) <= layer_sm_count() ? kPairBytes : kPairBytesFull) / bytes_of_chunk(p);
+  return ceil_div(all, ceil_div(all, fit < 16 ? 16 : fit));
 }
 
 }  // namespace
@@ -912,21 +919,25 @@ bool delta_chunked(int dtype, int64_t seqlen, int dstate) {
 
 size_t delta_chunks_workspace(const DeltaParams& p) {
   const int64_t count = chunks_at_once(p);
-  return static_cast<size_t>(p.batch) * count * (record_bytes(p.N) * p.H + rows_bytes(p.N) * p.G) +
-         (count * kC < p.seqlen ? static_cast<size_t>(p.batch) * p.H * p.P * p.N * sizeof(float) : 0);
+  const size_t pair = static_cast<size_t>(count * bytes_of_chunk(p));
+  return count * kC >= p.seqlen ? pair : 2 * pair + static_cast<size_t>(p.batch) * p.H * p.P * p.N * sizeof(float);
 }
 
 ssd_status launch_delta_chunks(const DeltaParams& p, void* workspace, cudaStream_t stream) {
   const int64_t all = ceil_div(p.seqlen, kC), most = chunks_at_once(p);
   DeltaChunks s{};
-  s.records = static_cast<uint8_t*>(workspace);
-  s.rows = s.records + p.batch * p.H * most * record_bytes(p.N);
-  s.carry = reinterpret_cast<float*>(s.rows + p.batch * p.G * most * rows_bytes(p.N));
+  uint8_t* pairs = static_cast<uint8_t*>(workspace);  // two, used in turn
+  s.carry = reinterpret_cast<float*>(pairs + 2 * most * bytes_of_chunk(p));
   s.limit_ns = spin_limit_ns();
   s.vectors = 1;
   for (const void* t : {p.x, p.Bm, p.Cm, (const void*)p.y}) s.vectors &= aligned_to(t, 16);
   for (int64_t stride : {p.x_batch, p.x_token, p.B_batch, p.B_token, p.C_batch, p.C_token}) s.vectors &= stride % 8 == 0;
-  for (int64_t first = 0; first < all; first += most) {
+  // Each launch is a dependent of the one before it in the stream and may begin beside it.  A walk waits for the
+  // first launch of its pair, which ends after the walk before; a first launch writes a buffer whose last walk
+  // ended before the present one began.
+  for (int64_t first = 0, pair = 0; first < all; first += most, ++pair) {
+    s.records = pairs + (pair & 1) * most * bytes_of_chunk(p);
+    s.rows = s.records + p.batch * p.H * most * record_bytes(p.N);
     s.first = static_cast<int>(first), s.count = static_cast<int>(all - first < most ? all - first : most);
     s.last = first + most >= all;
     const cudaError_t e = p.N == 64 ? launch_chunks<64>(p, s, stream) : launch_chunks<128>(p, s, stream);
