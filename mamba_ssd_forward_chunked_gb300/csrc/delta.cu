@@ -199,6 +199,7 @@ DeltaParams params_of(const ssd_delta_args* a) {
   p.B_batch = a->B_batch, p.B_token = a->B_token, p.C_batch = a->C_batch, p.C_token = a->C_token;
   p.dt_batch = a->dt_batch, p.dt_token = a->dt_token, p.beta_batch = a->beta_batch, p.beta_token = a->beta_token;
   p.H = a->nheads, p.G = a->ngroups, p.P = a->headdim, p.N = a->dstate;
+  p.parts = a->dtype == SSD_BF16 ? 1 : 2;
   p.gate_f32 = a->gate_dtype == SSD_F32, p.softplus = a->dt_softplus != 0, p.sigmoid = a->beta_sigmoid != 0;
   p.scale = a->scale, p.norm_eps = a->norm_eps;
   p.x = a->x, p.Bm = a->Bm, p.Cm = a->Cm, p.dt = a->dt, p.beta = a->beta;

@@ -8,6 +8,7 @@ struct DeltaParams {
   int64_t batch, seqlen, nslots;
   int64_t x_batch, x_token, B_batch, B_token, C_batch, C_token, dt_batch, dt_token, beta_batch, beta_token;
   int H, G, P, N;
+  int parts;  // 16-bit numbers a value of x, Bm, Cm and y takes: 1 or 2
   int gate_f32, softplus, sigmoid;
   float scale, norm_eps;  // norm_eps below 0: rows as they are
   const void *x, *Bm, *Cm, *dt, *beta;

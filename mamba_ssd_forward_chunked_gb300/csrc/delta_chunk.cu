@@ -1,4 +1,4 @@
-// The gated delta rule for whole bf16 prompts, in chunks of 64 tokens on the tensor cores.
+// The gated delta rule for whole prompts, in chunks of 64 tokens on the tensor cores.
 //
 // With G the sum of dt A from the chunk's start to a token (that one included), k and q the normalised
 // rows and h the state that enters the chunk, the values that the rule writes, v_i, solve
@@ -14,8 +14,8 @@
 // The state stays in registers, in 32 bits, and enters its product as two fp16 parts, as r does: 11 bits
 // each, and with a power of two that brings a tile's largest value to 2^14 the second part's last place is
 // at most 2^-22 of a value or 2^-38 of the largest.  (Three bf16 parts need no scale, but half as much again
-// of shared memory, stores and products.)  K and Q are bf16, so rows of them times a power of two are fp16.
-// Parts lie side by side along the product's columns, and the threads add up what comes out.
+// of shared memory, stores and products.)  A row of bf16 K or Q times a power of two is fp16; 32-bit ones have
+// two parts as well, and so has P T then.  Parts lie side by side along the product's columns, and the threads add up what comes out.
 #include <cuda_fp16.h>
 
 #include "delta_chunk.cuh"
@@ -27,15 +27,17 @@ constexpr int kC = 64;  // tokens of a chunk
 constexpr int64_t kMinTokens = 64;
 
 // What the first launch leaves, as shared memory holds it (rows of 128 bytes in the 128-byte swizzle).  Of a
-// chunk of a head: two parts of W (N rows), one of P T (64 rows; it goes into y alone, which has 8 bits), and
-// the tokens' factors.  Of a chunk of a group, for every 64 of N: 64 rows of K, then of Q.
+// chunk of a head: two parts of W (N rows), P T (64 rows; for bf16 one part, as it goes into y alone, which has
+// 8 bits), and the tokens' factors.  Of a chunk of a group, for every part and 64 of N: 64 rows of K, then of Q.
 constexpr uint32_t kSlab = 8192;  // 64 rows of 128 bytes
 enum { kBeta, kFromState, kScalars, kOutState, kOutRest, kFactors };
 constexpr uint32_t kFactorBytes = 2 * kC * 4 + 16;  // those that the second launch keeps in shared memory: up to the scalars
 enum { kDecay, kUpdate, kReach, kSpread };  // the scalars: e^{G_64}; what undoes W's scale; see the bounds of delta_walk_kernel
-__host__ __device__ constexpr uint32_t tile_bytes(int N) { return (2 * (N / 64) + 1) * kSlab; }
-__host__ __device__ constexpr uint32_t record_bytes(int N) { return tile_bytes(N) + kFactors * kC * 4; }
-__host__ __device__ constexpr uint32_t rows_bytes(int N) { return N / 64 * 2 * kSlab; }
+template <typename T>
+constexpr int kParts = sizeof(T) == 2 ? 1 : 2;  // of K, Q and P T
+__host__ __device__ constexpr uint32_t tile_bytes(int N, int parts) { return (2 * (N / 64) + parts) * kSlab; }
+__host__ __device__ constexpr uint32_t record_bytes(int N, int parts) { return tile_bytes(N, parts) + kFactors * kC * 4; }
+__host__ __device__ constexpr uint32_t rows_bytes(int N, int parts) { return N / 64 * 2 * kSlab * parts; }
 
 constexpr float kTScale = 16.f;  // of T and P T: T's diagonal is 1, so second parts' last places are 2^-29 of that
 
@@ -104,18 +106,20 @@ __device__ __forceinline__ void mma_tf32_parts(float (&o)[4], const float (&a)[4
   mma_tf32(o, ah, h0, h1);
 }
 
-template <int N>
+template <typename T, int N>
 struct PrepSmem {
   static constexpr uint32_t kRow = N * 2 + 16;  // bytes of a row of K or Q, eight rows in different banks
-  // K; Q, whose place A takes; T
+  // K; Q, whose place A takes; T; second parts of K and Q
   static constexpr uint32_t kA = kC * kRow, kSize = kRow > kStride * 4 ? kRow : kStride * 4, kT = kA + kC * kSize;
-  static constexpr uint32_t kVec = kT + kC * kStride * 4;
+  static constexpr uint32_t kLow = kT + kC * kStride * 4;
+  static constexpr uint32_t kVec = kLow + (kParts<T> == 2 ? 2 * kC * kRow : 0);
   static constexpr uint32_t kTotal = kVec + 7 * kC * 4 + 64;
 };
 
-template <int N>
-__global__ void __launch_bounds__(kPrepThreads, 4) delta_prepare_kernel(DeltaParams p, DeltaChunks s) {
-  using M = PrepSmem<N>;
+template <typename T, int N>
+__global__ void __launch_bounds__(kPrepThreads, kParts<T> == 1 ? 4 : 2) delta_prepare_kernel(DeltaParams p, DeltaChunks s) {
+  using M = PrepSmem<T, N>;
+  constexpr int kP = kParts<T>;
   extern __shared__ __align__(16) uint8_t smem[];
   float* s_A = reinterpret_cast<float*>(smem + M::kA);
   float* s_T = reinterpret_cast<float*>(smem + M::kT);
@@ -145,21 +149,26 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prepare_kernel(DeltaPar
   const int per = p.H / p.G, g = h / per;
 
   // rows of K, then of Q; rows behind the sequence are 0
-  constexpr int kRowLanes = N / 8, kPer = 32 / kRowLanes, kLoads = 16 / kPer;
-  const __nv_bfloat16* from[2] = {static_cast<const __nv_bfloat16*>(p.Bm) + b * p.B_batch + t0 * p.B_token + static_cast<int64_t>(g) * N,
-                                  static_cast<const __nv_bfloat16*>(p.Cm) + b * p.C_batch + t0 * p.C_token + static_cast<int64_t>(g) * N};
-  uint4 raw[kLoads];
+  constexpr int kRowLanes = N / 8, kPer = 32 / kRowLanes, kLoads = 16 / kPer;  // a lane has 8 of a row
+  const T* from[2] = {static_cast<const T*>(p.Bm) + b * p.B_batch + t0 * p.B_token + static_cast<int64_t>(g) * N,
+                      static_cast<const T*>(p.Cm) + b * p.C_batch + t0 * p.C_token + static_cast<int64_t>(g) * N};
+  struct Eight {
+    uint4 raw[kP];
+  };
+  Eight eight[kLoads];
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
     const int r = warp * 16 + i * kPer + lane / kRowLanes, t = r & 63;
-    raw[i] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int e = 0; e < kP; ++e) eight[i].raw[e] = make_uint4(0, 0, 0, 0);
     if (t < n) {
-      const __nv_bfloat16* row = (r < kC ? from[0] + t * p.B_token : from[1] + t * p.C_token) + lane % kRowLanes * 8;
+      const T* row = (r < kC ? from[0] + t * p.B_token : from[1] + t * p.C_token) + lane % kRowLanes * 8;
       if (s.vectors) {
-        raw[i] = *reinterpret_cast<const uint4*>(row);
+#pragma unroll
+        for (int e = 0; e < kP; ++e) eight[i].raw[e] = reinterpret_cast<const uint4*>(row)[e];
       } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) reinterpret_cast<__nv_bfloat16*>(&raw[i])[e] = row[e];
+        for (int e = 0; e < 8; ++e) reinterpret_cast<T*>(eight[i].raw)[e] = row[e];
       }
     }
   }
@@ -167,7 +176,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prepare_kernel(DeltaPar
   // 32-bit numbers, the first of few enough bits that differences of it are exact
   if (tid < kC) {
     float d = 0.f, beta = 0.f;
-    if (tid < n) d = delta_log_decay<__nv_bfloat16>(p, b, t0 + tid, h) * kLog2e, beta = delta_beta<__nv_bfloat16>(p, b, t0 + tid, h);
+    if (tid < n) d = delta_log_decay<T>(p, b, t0 + tid, h) * kLog2e, beta = delta_beta<T>(p, b, t0 + tid, h);
     if (!(d == d)) beta = d;  // a NaN goes on through beta
     int64_t G = __float2ll_rn(fminf(fmaxf(d, -1000.f), 1000.f) * 4294967296.f);
 #pragma unroll
@@ -183,34 +192,41 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prepare_kernel(DeltaPar
     s_beta[tid] = beta;
   }
   // in fp16, times a power of two
-  uint8_t* rows_out = h == g * per ? s.rows + ((b * p.G + g) * s.count + blockIdx.x) * static_cast<int64_t>(rows_bytes(N)) : nullptr;
+  uint8_t* rows_out = h == g * per ? s.rows + ((b * p.G + g) * s.count + blockIdx.x) * static_cast<int64_t>(rows_bytes(N, kP)) : nullptr;
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
     const int r = warp * 16 + i * kPer + lane / kRowLanes;
-    const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-    float squares = 0.f;
-    uint32_t largest = 0;
+    float v[8], squares = 0.f, largest = 0.f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      squares = fmaf(bf16_lo(w[e]), bf16_lo(w[e]), fmaf(bf16_hi(w[e]), bf16_hi(w[e]), squares));
-      largest = __vmaxu2(largest, w[e] & 0x7FFF7FFFu);  // (positive numbers of a type are in the order of their bits)
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t w = (&eight[i].raw[0].x)[kP == 1 ? e / 2 : e];
+      v[e] = kP == 2 ? __uint_as_float(w) : e & 1 ? bf16_hi(w) : bf16_lo(w);
+      squares = fmaf(v[e], v[e], squares), largest = fmaxf(largest, fabsf(v[e]));
     }
 #pragma unroll
     for (int o = kRowLanes / 2; o; o /= 2) {
       squares += __shfl_xor_sync(0xffffffffu, squares, o);
-      largest = __vmaxu2(largest, __shfl_xor_sync(0xffffffffu, largest, o));
+      largest = fmaxf(largest, __shfl_xor_sync(0xffffffffu, largest, o));
     }
-    const Scale scale = scale_for(max(largest & 0xFFFF0000u, largest << 16));
-    uint4 half;
+    const Scale scale = scale_for(__float_as_uint(largest));
+    uint4 half[kP];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const __half2 v = __floats2half2_rn(bf16_lo(w[e]) * scale.up, bf16_hi(w[e]) * scale.up);
-      (&half.x)[e] = *reinterpret_cast<const uint32_t*>(&v);
+      const float lo = v[2 * e] * scale.up, hi = v[2 * e + 1] * scale.up;
+      if constexpr (kP == 1) {
+        const __half2 pair = __floats2half2_rn(lo, hi);
+        (&half[0].x)[e] = *reinterpret_cast<const uint32_t*>(&pair);
+      } else {
+        split(lo, hi, (&half[0].x)[e], (&half[kP - 1].x)[e]);
+      }
     }
     const int col = lane % kRowLanes;
-    *reinterpret_cast<uint4*>(smem + r * M::kRow + col * 16) = half;
-    if (rows_out)
-      *reinterpret_cast<uint4*>(rows_out + (col >> 3) * 2 * kSlab + r * 128 + (((col & 7) ^ (r & 7)) << 4)) = half;
+#pragma unroll
+    for (int e = 0; e < kP; ++e) {
+      *reinterpret_cast<uint4*>(smem + (e ? M::kLow : 0) + r * M::kRow + col * 16) = half[e];
+      if (rows_out)
+        *reinterpret_cast<uint4*>(rows_out + e * rows_bytes(N, 1) + (col >> 3) * 2 * kSlab + r * 128 + (((col & 7) ^ (r & 7)) << 4)) = half[e];
+    }
     if (col == 0) s_squares[r] = make_float2(squares, scale.down);
   }
   __syncthreads();
@@ -235,13 +251,20 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prepare_kernel(DeltaPar
     const uint32_t bt = rows + ((lane & 7) + (lane >> 4) * 8) * M::kRow + ((lane >> 3) & 1) * 16;
 #pragma unroll
     for (int k = 0; k < N / 16; ++k) {
-      uint32_t a[4];
+      uint32_t a[4], al[4];
       ldmatrix4(a, at + k * 32);
+      if (kP == 2) ldmatrix4(al, at + M::kLow + k * 32);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if (j > mt) break;
         uint32_t v[4];
         ldmatrix4(v, bt + j * 16 * M::kRow + k * 32);
+        if constexpr (kP == 2) {
+          uint32_t l[4];
+          ldmatrix4(l, bt + M::kLow + j * 16 * M::kRow + k * 32);
+          mma_f16(acc[2 * j], al, v[0], v[1]), mma_f16(acc[2 * j + 1], al, v[2], v[3]);
+          mma_f16(acc[2 * j], a, l[0], l[1]), mma_f16(acc[2 * j + 1], a, l[2], l[3]);
+        }
         mma_f16(acc[2 * j], a, v[0], v[1]);
         mma_f16(acc[2 * j + 1], a, v[2], v[3]);
       }
@@ -382,14 +405,20 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prepare_kernel(DeltaPar
     const int at_row = 16 * mt + (lane >> 3 & 1) * 8 + (lane & 7);
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
-      uint32_t v[4];
+      uint32_t v[4], l[4] = {};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float* from = &o[j + (e >> 1)][e & 1 ? 2 : 0];
-        const __half2 pair = __floats2half2_rn(from[0] * kTScale, from[1] * kTScale);
-        v[e] = *reinterpret_cast<const uint32_t*>(&pair);
+        const float* from_o = &o[j + (e >> 1)][e & 1 ? 2 : 0];
+        if constexpr (kP == 1) {
+          const __half2 pair = __floats2half2_rn(from_o[0] * kTScale, from_o[1] * kTScale);
+          v[e] = *reinterpret_cast<const uint32_t*>(&pair);
+        } else {
+          split(from_o[0] * kTScale, from_o[1] * kTScale, v[e], l[e]);
+        }
       }
-      stmatrix4(rows + M::kA + at_row * 128 + (((j + (lane >> 4)) ^ (at_row & 7)) << 4), v[0], v[1], v[2], v[3]);
+      const uint32_t to = rows + at_row * 128 + (((j + (lane >> 4)) ^ (at_row & 7)) << 4);
+      stmatrix4(to + M::kA, v[0], v[1], v[2], v[3]);
+      if (kP == 2) stmatrix4(to + M::kLow + kC * M::kRow, l[0], l[1], l[2], l[3]);  // (where Q's second part was)
     }
   }
 
@@ -419,6 +448,11 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prepare_kernel(DeltaPar
     for (int m = 0; m < kTiles; ++m) {
       uint32_t a[4];
       ldmatrix4_t(a, kt + k * 16 * M::kRow + m * 32);
+      if constexpr (kP == 2) {
+        uint32_t al[4];
+        ldmatrix4_t(al, kt + M::kLow + k * 16 * M::kRow + m * 32);
+        mma_f16(w[m], al, bh[k][0], bh[k][1]);
+      }
       mma_f16(w[m], a, bl[k][0], bl[k][1]);
       mma_f16(w[m], a, bh[k][0], bh[k][1]);
     }
@@ -446,9 +480,9 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prepare_kernel(DeltaPar
   }
   fence_proxy_async_smem();
   __syncthreads();
-  uint8_t* out = s.records + ((b * p.H + h) * s.count + blockIdx.x) * static_cast<int64_t>(record_bytes(N));
+  uint8_t* out = s.records + ((b * p.H + h) * s.count + blockIdx.x) * static_cast<int64_t>(record_bytes(N, kP));
   if (tid < kC) {
-    float* factors = reinterpret_cast<float*>(out + tile_bytes(N));
+    float* factors = reinterpret_cast<float*>(out + tile_bytes(N, kP));
     const float since = exp2f(s_hi[tid] + s_lo[tid]), qn = p.scale * s_qn[tid];
     factors[kBeta * kC + tid] = s_beta[tid];
     factors[kFromState * kC + tid] = s_beta[tid] * s_kn[tid] * since;
@@ -465,6 +499,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prepare_kernel(DeltaPar
     bulk_store(out, rows, N * 128);
     bulk_store(out + N * 128, rows + M::kT, N * 128);
     bulk_store(out + 2 * N * 128, rows + M::kA, kSlab);
+    if (kP == 2) bulk_store(out + 2 * N * 128 + kSlab, rows + M::kLow + kC * M::kRow, kSlab);
     tma_store_commit();
     tma_store_wait_all();
   }
@@ -475,20 +510,21 @@ __global__ void __launch_bounds__(kPrepThreads, 4) delta_prepare_kernel(DeltaPar
 
 // kPT: columns of the state (values of a head) that a block has; kGroups: warpgroups that share them;
 // kStages: buffers of rows and of [T; P T].
-template <int N, int kPT, int kGroups, int kStages>
+template <typename T, int N, int kPT, int kGroups, int kStages>
 struct Walk {
+  static constexpr int kP = kParts<T>;
   static constexpr int kWorkers = 4 * kGroups;             // warps with the state
   static constexpr int kThreads = 32 * (kWorkers + 2);     // and one that loads, one that issues the products
   static constexpr int kCols = kPT / kGroups;              // of a thread
   static constexpr int kSlabs = (2 * kPT + 63) / 64;       // 64 columns each of the two parts side by side
   static constexpr uint32_t kSlabS = N * 128;
-  static constexpr uint32_t kRows = 0, kTile = kRows + kStages * rows_bytes(N), kS = kTile + kStages * tile_bytes(N);
+  static constexpr uint32_t kRows = 0, kTile = kRows + kStages * rows_bytes(N, kP), kS = kTile + kStages * tile_bytes(N, kP);
   static constexpr bool kOwnR = kStages > 1;               // r has a place of its own, or the state's
   static constexpr uint32_t kR = kS + (kOwnR ? kSlabs * kSlabS : 0);
   static constexpr uint32_t kEnd = kS + kSlabs * kSlabS + (kOwnR ? kSlabs * kSlab : 0);
   static constexpr uint32_t kLargest = kEnd + 18 * 8 + 4 * 4, kF = kLargest + 4 * kWorkers * 4;
   static constexpr uint32_t kX = kF + kStages * kFactorBytes;  // a chunk's x, every thread's where it put it
-  static constexpr uint32_t kTotal = kX + kC * kPT * 2;
+  static constexpr uint32_t kTotal = kX + kC * kPT * sizeof(T);
   static constexpr uint32_t kTmem = 4 * kPT;               // columns of tensor memory
 };
 
@@ -508,10 +544,10 @@ __device__ __forceinline__ void tmem_ld8(uint32_t at, uint32_t (&r)[8]) {
                : "r"(at));
 }
 
-template <int N, int kPT, int kGroups, int kStages, int kBlocks>
-__global__ void __launch_bounds__(Walk<N, kPT, kGroups, kStages>::kThreads, kBlocks) delta_walk_kernel(DeltaParams p, DeltaChunks s) {
-  using M = Walk<N, kPT, kGroups, kStages>;
-  constexpr int kCols = M::kCols, kWorkers = M::kWorkers;
+template <typename T, int N, int kPT, int kGroups, int kStages, int kBlocks>
+__global__ void __launch_bounds__(Walk<T, N, kPT, kGroups, kStages>::kThreads, kBlocks) delta_walk_kernel(DeltaParams p, DeltaChunks s) {
+  using M = Walk<T, N, kPT, kGroups, kStages>;
+  constexpr int kP = M::kP, kCols = M::kCols, kWorkers = M::kWorkers, kVecs = kCols * static_cast<int>(sizeof(T)) / 16;
   constexpr uint32_t kColD1 = 0, kColD3 = 2 * kPT;  // W r goes where [K; Q] h was
   extern __shared__ __align__(1024) uint8_t walk_smem[];
   uint8_t* smem = walk_smem;
@@ -544,8 +580,8 @@ __global__ void __launch_bounds__(Walk<N, kPT, kGroups, kStages>::kThreads, kBlo
   const int64_t length = seq.row < 0 || seq.length < begin ? begin : seq.length < end ? seq.length : end;
   const int chunks = static_cast<int>((length - begin + kC - 1) / kC);
   const int g = h / (p.H / p.G);
-  const uint8_t* records = s.records + (b * p.H + h) * s.count * static_cast<int64_t>(record_bytes(N));
-  const uint8_t* rows = s.rows + (b * p.G + g) * s.count * static_cast<int64_t>(rows_bytes(N));
+  const uint8_t* records = s.records + (b * p.H + h) * s.count * static_cast<int64_t>(record_bytes(N, kP));
+  const uint8_t* rows = s.rows + (b * p.G + g) * s.count * static_cast<int64_t>(rows_bytes(N, kP));
   auto wait = [&](int bar, int phase) {
     if (mbar_try_wait_short(&bars[bar], phase & 1)) return true;
     const uint64_t t0 = globaltimer_ns();
@@ -577,15 +613,15 @@ __global__ void __launch_bounds__(Walk<N, kPT, kGroups, kStages>::kThreads, kBlo
         // has been filled twice)
         ok = ok && (turn == 0 || wait(kFactorsRead + st, turn - 1));
         if (!ok) break;
-        mbar_arrive_expect_tx(&bars[kRowsFull + st], rows_bytes(N) + kFactorBytes);
-        bulk_load(smem + M::kRows + st * rows_bytes(N), rows + c * static_cast<int64_t>(rows_bytes(N)), rows_bytes(N), &bars[kRowsFull + st]);
-        bulk_load(smem + M::kF + c % kStages * kFactorBytes, records + c * static_cast<int64_t>(record_bytes(N)) + tile_bytes(N), kFactorBytes,
+        mbar_arrive_expect_tx(&bars[kRowsFull + st], rows_bytes(N, kP) + kFactorBytes);
+        bulk_load(smem + M::kRows + st * rows_bytes(N, kP), rows + c * static_cast<int64_t>(rows_bytes(N, kP)), rows_bytes(N, kP), &bars[kRowsFull + st]);
+        bulk_load(smem + M::kF + c % kStages * kFactorBytes, records + c * static_cast<int64_t>(record_bytes(N, kP)) + tile_bytes(N, kP), kFactorBytes,
                   &bars[kRowsFull + st]);
         ++c;
         ok = turn == 0 || wait(kTileEmpty + st, turn - 1);
         if (!ok) break;
-        mbar_arrive_expect_tx(&bars[kTileFull + st], tile_bytes(N));
-        bulk_load(smem + M::kTile + st * tile_bytes(N), records + t * static_cast<int64_t>(record_bytes(N)), tile_bytes(N), &bars[kTileFull + st]);
+        mbar_arrive_expect_tx(&bars[kTileFull + st], tile_bytes(N, kP));
+        bulk_load(smem + M::kTile + st * tile_bytes(N, kP), records + t * static_cast<int64_t>(record_bytes(N, kP)), tile_bytes(N, kP), &bars[kTileFull + st]);
         ++t;
       }
       if (!ok) {  // nothing is in flight when the block ends
@@ -601,18 +637,23 @@ __global__ void __launch_bounds__(Walk<N, kPT, kGroups, kStages>::kThreads, kBlo
       const uint64_t dS = sdesc_sw128(base + M::kS, M::kSlabS, 1024), dR = sdesc_sw128(base + M::kR, kSlab, 1024);
       for (int c = 0; c < chunks; ++c) {
         const int st = c % kStages, turn = c / kStages;
-        const uint32_t kq = base + M::kRows + st * rows_bytes(N);
+        const uint32_t kq = base + M::kRows + st * rows_bytes(N, kP);
         if (!wait(kRowsFull + st, turn) || !spin(kStateReady, c)) break;
         tc_fence_after();
         const uint64_t kq_rows = sdesc_sw128(kq, 16, 1024);
 #pragma unroll
         for (int k = 0; k < N / 16; ++k)
           mma_ss<false>(tmem + kColD1, kq_rows + (((k >> 2) * 2 * kSlab + (k & 3) * 32) >> 4), dS + (k * 2048 >> 4), id_two, k != 0);
+        if constexpr (kP == 2) {
+#pragma unroll
+          for (int k = 0; k < N / 16; ++k)
+            mma_ss<false>(tmem + kColD1, kq_rows + ((rows_bytes(N, 1) + (k >> 2) * 2 * kSlab + (k & 3) * 32) >> 4), dS + (k * 2048 >> 4), id_one, 1);
+        }
         mma_commit(&bars[kFromStateDone]);
         mma_commit(&bars[kRowsEmpty + st]);
         if (!wait(kTileFull + st, turn) || !spin(kRestReady, c)) break;
         tc_fence_after();
-        const uint32_t tile = base + M::kTile + st * tile_bytes(N);
+        const uint32_t tile = base + M::kTile + st * tile_bytes(N, kP);
         const uint64_t w = sdesc_sw128(tile, 16, 1024);
 #pragma unroll
         for (int k = 0; k < kC / 16; ++k) {  // both first parts, and the second of either with the first of the other
@@ -623,7 +664,10 @@ __global__ void __launch_bounds__(Walk<N, kPT, kGroups, kStages>::kThreads, kBlo
         // P T's 64 rows go to the lanes of Q: they are the second half of 128 that begin in what lies before them
         const uint64_t pt = sdesc_sw128(tile + (2 * (N / 64) - 1) * kSlab, 16, 1024);
 #pragma unroll
-        for (int k = 0; k < kC / 16; ++k) mma_ss<false>(tmem + kColD3, pt + (k * 32 >> 4), dR + (k * 2048 >> 4), id_two, k != 0);
+        for (int k = 0; k < kC / 16; ++k) {
+          mma_ss<false>(tmem + kColD3, pt + (k * 32 >> 4), dR + (k * 2048 >> 4), id_two, k != 0);
+          if constexpr (kP == 2) mma_ss<false>(tmem + kColD3, pt + ((kSlab + k * 32) >> 4), dR + (k * 2048 >> 4), id_one, 1);
+        }
         mma_commit(&bars[kRestDone]);
         mma_commit(&bars[kTileEmpty + st]);
       }
@@ -639,8 +683,8 @@ __global__ void __launch_bounds__(Walk<N, kPT, kGroups, kStages>::kThreads, kBlo
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + group * kCols;
     const int col0 = p0 + group * kCols;  // the thread's values of the head
     const int64_t y_token = static_cast<int64_t>(p.H) * p.P;
-    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + b * p.seqlen * y_token + static_cast<int64_t>(h) * p.P + col0;
-    const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x) + b * p.x_batch + static_cast<int64_t>(h) * p.P + col0;
+    T* y = static_cast<T*>(p.y) + b * p.seqlen * y_token + static_cast<int64_t>(h) * p.P + col0;
+    const T* x = static_cast<const T*>(p.x) + b * p.x_batch + static_cast<int64_t>(h) * p.P + col0;
 
     // kCols values of a row, scaled, as two parts side by side: rows of 128 bytes in slabs of 64 columns
     auto put = [&](uint32_t tile, uint32_t slab, int at_row, const float (&v)[kCols], float up) {
@@ -720,16 +764,17 @@ __global__ void __launch_bounds__(Walk<N, kPT, kGroups, kStages>::kThreads, kBlo
     auto ask = [&](int c) {
       const int64_t t = begin + static_cast<int64_t>(c) * kC + token;
 #pragma unroll
-      for (int i = 0; i < kCols / 8; ++i) {
+      for (int i = 0; i < kVecs; ++i) {
+        constexpr int kE = 16 / sizeof(T);
         uint4* to = s_x + i * kStrideX;
-        const __nv_bfloat16* from = x + t * p.x_token + 8 * i;
-        if (t >= length || col0 + 8 * i >= p.P) {
+        const T* from = x + t * p.x_token + kE * i;
+        if (t >= length || col0 + kE * i >= p.P) {
           *to = make_uint4(0, 0, 0, 0);
         } else if (s.vectors) {
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(__cvta_generic_to_global(from)) : "memory");
         } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) reinterpret_cast<__nv_bfloat16*>(to)[e] = from[e];
+          for (int e = 0; e < kE; ++e) reinterpret_cast<T*>(to)[e] = from[e];
         }
       }
     };
@@ -751,7 +796,7 @@ __global__ void __launch_bounds__(Walk<N, kPT, kGroups, kStages>::kThreads, kBlo
     for (int c = 0; c < chunks; ++c) {
       const int64_t t = begin + static_cast<int64_t>(c) * kC + token;
       const bool live = t < length;
-      const float* out_factors = reinterpret_cast<const float*>(records + c * static_cast<int64_t>(record_bytes(N)) + tile_bytes(N));
+      const float* out_factors = reinterpret_cast<const float*>(records + c * static_cast<int64_t>(record_bytes(N, kP)) + tile_bytes(N, kP));
       float fa, fb;
       if (!is_token) fa = out_factors[kOutState * kC + token], fb = out_factors[kOutRest * kC + token];
       ok = ok && all_wait(kRowsFull + c % kStages, c / kStages);
@@ -763,12 +808,15 @@ __global__ void __launch_bounds__(Walk<N, kPT, kGroups, kStages>::kThreads, kBlo
         fa = factors[kBeta * kC + token], fb = factors[kFromState * kC + token];
         asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll
-        for (int i = 0; i < kCols / 8; ++i) {
+        for (int i = 0; i < kVecs; ++i) {
           const uint4 xs = s_x[i * kStrideX];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const uint32_t w = (&xs.x)[e];
-            bx[8 * i + 2 * e] = fa * bf16_lo(w), bx[8 * i + 2 * e + 1] = fa * bf16_hi(w);
+            if constexpr (kP == 1)
+              bx[8 * i + 2 * e] = fa * bf16_lo(w), bx[8 * i + 2 * e + 1] = fa * bf16_hi(w);
+            else
+              bx[4 * i + e] = fa * __uint_as_float(w);
           }
         }
         if (c + 1 < chunks) ask(c + 1);
@@ -824,19 +872,19 @@ __global__ void __launch_bounds__(Walk<N, kPT, kGroups, kStages>::kThreads, kBlo
         // y: the state's part, and P T r
         const float from_rest = fb * rest.down;
 #pragma unroll
-        for (int i = 0; i < kCols / 8; ++i) {
-          if (col0 + 8 * i >= p.P) break;
+        for (int i = 0; i < kCols; ++i) v[i] = fmaf(from_rest, v[i], bx[i]);
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+          constexpr int kE = 16 / sizeof(T);
+          if (col0 + kE * i >= p.P) break;
           uint4 w;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int at = 8 * i + 2 * e;
-            (&w.x)[e] = pack_bf16x2(fmaf(from_rest, v[at], bx[at]), fmaf(from_rest, v[at + 1], bx[at + 1]));
-          }
+          for (int e = 0; e < 4; ++e) (&w.x)[e] = kP == 1 ? pack_bf16x2(v[kE * i + 2 * e % kE], v[kE * i + 2 * e % kE + 1]) : __float_as_uint(v[kE * i + e]);
           if (s.vectors) {
-            *reinterpret_cast<uint4*>(y + t * y_token + 8 * i) = w;
+            *reinterpret_cast<uint4*>(y + t * y_token + kE * i) = w;
           } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[t * y_token + 8 * i + e] = reinterpret_cast<const __nv_bfloat16*>(&w)[e];
+            for (int e = 0; e < kE; ++e) y[t * y_token + kE * i + e] = reinterpret_cast<const T*>(&w)[e];
           }
         }
       }
@@ -852,13 +900,19 @@ __global__ void __launch_bounds__(Walk<N, kPT, kGroups, kStages>::kThreads, kBlo
         if (col0 + i < p.P) to[(static_cast<int64_t>(h) * p.P + col0 + i) * N + row] = S[i];
     }
     // rows of y behind the sequence are 0; a wait that ran out leaves NaN
-    const uint32_t rest = ok ? 0u : 0x7FC07FC0u;
+    const uint32_t rest = ok ? 0u : 0x7FC07FC0u;  // (a NaN in both types)
     for (int64_t t = (ok ? length : begin) + row; t < end; t += 128)
       for (int i = 0; i < kCols && col0 + i < p.P; i += 8) {
         if (s.vectors) {
-          *reinterpret_cast<uint4*>(y + t * y_token + i) = make_uint4(rest, rest, rest, rest);
+#pragma unroll
+          for (int e = 0; e < kP; ++e) reinterpret_cast<uint4*>(y + t * y_token + i)[e] = make_uint4(rest, rest, rest, rest);
         } else {
-          for (int e = 0; e < 8; ++e) y[t * y_token + i + e] = __ushort_as_bfloat16(static_cast<unsigned short>(rest));
+          for (int e = 0; e < 8; ++e) {
+            if constexpr (kP == 1)
+              y[t * y_token + i + e] = __ushort_as_bfloat16(static_cast<unsigned short>(rest));
+            else
+              y[t * y_token + i + e] = __uint_as_float(rest);
+          }
         }
       }
   }
@@ -870,33 +924,37 @@ __global__ void __launch_bounds__(Walk<N, kPT, kGroups, kStages>::kThreads, kBlo
   }
 }
 
-template <int N, int kPT, int kGroups, int kStages, int kBlocks>
+template <typename T, int N, int kPT, int kGroups, int kStages, int kBlocks>
 cudaError_t launch_walk(const DeltaParams& p, const DeltaChunks& s, cudaStream_t stream) {
-  using M = Walk<N, kPT, kGroups, kStages>;
+  using M = Walk<T, N, kPT, kGroups, kStages>;
   constexpr int bytes = static_cast<int>(M::kTotal);
   static_assert(kBlocks * (bytes + 1024) <= 228 * 1024 && kBlocks * M::kTmem <= 512, "shared or tensor memory");
-  auto kernel = delta_walk_kernel<N, kPT, kGroups, kStages, kBlocks>;
+  auto kernel = delta_walk_kernel<T, N, kPT, kGroups, kStages, kBlocks>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
   return launch_k(kernel, dim3(static_cast<unsigned>(ceil_div(p.P, kPT)), static_cast<unsigned>(p.H), static_cast<unsigned>(p.batch)),
                   dim3(M::kThreads), bytes, stream, true, p, s);
 }
 
-template <int N>
+template <typename T, int N>
 cudaError_t launch_chunks(const DeltaParams& p, const DeltaChunks& s, cudaStream_t stream) {
-  constexpr int bytes = static_cast<int>(PrepSmem<N>::kTotal);
-  cudaError_t e = cudaFuncSetAttribute(delta_prepare_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  constexpr int bytes = static_cast<int>(PrepSmem<T, N>::kTotal);
+  cudaError_t e = cudaFuncSetAttribute(delta_prepare_kernel<T, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess)
-    e = launch_k(delta_prepare_kernel<N>, dim3(static_cast<unsigned>(s.count), static_cast<unsigned>(p.H), static_cast<unsigned>(p.batch)),
+    e = launch_k(delta_prepare_kernel<T, N>, dim3(static_cast<unsigned>(s.count), static_cast<unsigned>(p.H), static_cast<unsigned>(p.batch)),
                  dim3(kPrepThreads), bytes, stream, true, p, s);
   if (e != cudaSuccess) return e;
   // Columns of a block: as few as leave every block a multiprocessor of its own (the chain is the shorter, and what is
   // loaded for it the same), 32 where there are more, two blocks on each.  16 heads of 128 x 128, 16384 tokens:
   // 16 columns 379 us, 32 482; 128 heads, 4096 tokens: 32 columns 479 and, two blocks each, 360, 16 491.
   const int64_t heads = p.batch * p.H, sms = layer_sm_count();
-  return heads * ceil_div(p.P, 16) <= sms ? launch_walk<N, 16, 2, 2, 1>(p, s, stream)
-         : heads * ceil_div(p.P, 32) <= sms ? launch_walk<N, 32, 2, 2, 1>(p, s, stream)
-                                            : launch_walk<N, 32, 2, 1, 2>(p, s, stream);
+  // 32-bit rows take twice the shared memory: one buffer, and one block on each.
+  if constexpr (sizeof(T) == 4)
+    return heads * ceil_div(p.P, 16) <= sms ? launch_walk<T, N, 16, 2, 1, 1>(p, s, stream) : launch_walk<T, N, 32, 2, 1, 1>(p, s, stream);
+  else
+    return heads * ceil_div(p.P, 16) <= sms ? launch_walk<T, N, 16, 2, 2, 1>(p, s, stream)
+           : heads * ceil_div(p.P, 32) <= sms ? launch_walk<T, N, 32, 2, 2, 1>(p, s, stream)
+                                              : launch_walk<T, N, 32, 2, 1, 2>(p, s, stream);
 }
 
 // Chunks of a pair of launches.  Pairs overlap, the first launch of one with the walk of the one before, and what
@@ -905,7 +963,7 @@ cudaError_t launch_chunks(const DeltaParams& p, const DeltaChunks& s, cudaStream
 // 24 MB 549, one pair 568; 128 heads, 4096 tokens: one pair 651, 48 MB 675.
 constexpr int64_t kPairBytes = int64_t(48) << 20, kPairBytesFull = int64_t(512) << 20;
 
-int64_t bytes_of_chunk(const DeltaParams& p) { return p.batch * (int64_t(record_bytes(p.N)) * p.H + int64_t(rows_bytes(p.N)) * p.G); }
+int64_t bytes_of_chunk(const DeltaParams& p) { return p.batch * (int64_t(record_bytes(p.N, p.parts)) * p.H + int64_t(rows_bytes(p.N, p.parts)) * p.G); }
 int64_t chunks_at_once(const DeltaParams& p) {
   const int64_t all = ceil_div(p.seqlen, kC), fit = (p.batch * p.H * ceil_div(p.P, 16) <= layer_sm_count() ? kPairBytes : kPairBytesFull) / bytes_of_chunk(p);
   return ceil_div(all, ceil_div(all, fit < 16 ? 16 : fit));
@@ -914,7 +972,8 @@ int64_t chunks_at_once(const DeltaParams& p) {
 }  // namespace
 
 bool delta_chunked(int dtype, int64_t seqlen, int dstate) {
-  return dtype == SSD_BF16 && (dstate == 64 || dstate == 128) && seqlen >= kMinTokens;
+  (void)dtype;
+  return (dstate == 64 || dstate == 128) && seqlen >= kMinTokens;
 }
 
 size_t delta_chunks_workspace(const DeltaParams& p) {
@@ -931,16 +990,17 @@ ssd_status launch_delta_chunks(const DeltaParams& p, void* workspace, cudaStream
   s.limit_ns = spin_limit_ns();
   s.vectors = 1;
   for (const void* t : {p.x, p.Bm, p.Cm, (const void*)p.y}) s.vectors &= aligned_to(t, 16);
-  for (int64_t stride : {p.x_batch, p.x_token, p.B_batch, p.B_token, p.C_batch, p.C_token}) s.vectors &= stride % 8 == 0;
+  for (int64_t stride : {p.x_batch, p.x_token, p.B_batch, p.B_token, p.C_batch, p.C_token}) s.vectors &= stride * (p.parts == 1 ? 2 : 4) % 16 == 0;
   // Each launch is a dependent of the one before it in the stream and may begin beside it.  A walk waits for the
   // first launch of its pair, which ends after the walk before; a first launch writes a buffer whose last walk
   // ended before the present one began.
   for (int64_t first = 0, pair = 0; first < all; first += most, ++pair) {
     s.records = pairs + (pair & 1) * most * bytes_of_chunk(p);
-    s.rows = s.records + p.batch * p.H * most * record_bytes(p.N);
+    s.rows = s.records + p.batch * p.H * most * record_bytes(p.N, p.parts);
     s.first = static_cast<int>(first), s.count = static_cast<int>(all - first < most ? all - first : most);
     s.last = first + most >= all;
-    const cudaError_t e = p.N == 64 ? launch_chunks<64>(p, s, stream) : launch_chunks<128>(p, s, stream);
+    const cudaError_t e = p.parts == 1 ? (p.N == 64 ? launch_chunks<__nv_bfloat16, 64>(p, s, stream) : launch_chunks<__nv_bfloat16, 128>(p, s, stream))
+                                       : (p.N == 64 ? launch_chunks<float, 64>(p, s, stream) : launch_chunks<float, 128>(p, s, stream));
     if (e != cudaSuccess) return SSD_ERR_CUDA;
   }
   return SSD_OK;

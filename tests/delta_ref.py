@@ -13,7 +13,7 @@ system whose inverse has entries of at most m^C beta |k|^2: an error of one
 token's value reaches the C - 1 after it, each by that much, so `spread` is 1 + C
 there.  An output is off by |scale| |q| times the state's error and EPS of the
 state's norm; in chunks, where it is the entering state's part plus
-sum_j (P T)_tj r_j, also by P T's rounding to 11 bits, 2^-12 |(P T)_tj| |r_j|.
+sum_j (P T)_tj r_j, also by P T's rounding to 11 bits (bf16) or 22, pt |(P T)_tj| |r_j|.
 (P T)_tj is scale q_t.z_j, z_j being k_j carried through the tokens after j."""
 import torch
 
@@ -21,7 +21,7 @@ from layer_ref import EPS, HALF_BF16, d64, softplus
 
 
 def delta(x, dt, A, Bm, Cm, beta, scale=None, dt_bias=None, dt_softplus=False, beta_sigmoid=False, norm_eps=None,
-          init_state=None, slots=None, positions=None, lengths=None, final_state=None, spread=1.0, eps=EPS):
+          init_state=None, slots=None, positions=None, lengths=None, final_state=None, spread=1.0, eps=EPS, pt=2.0 ** -12):
     """(y, its bound, final state, its bound); rows of final_state that no
     sequence has are those of ``final_state`` (0)."""
     x, dt, A, Bm, Cm, beta = (d64(v) for v in (x, dt, A, Bm, Cm, beta))
@@ -69,7 +69,7 @@ def delta(x, dt, A, Bm, Cm, beta, scale=None, dt_bias=None, dt_softplus=False, b
             h = h + (w[:, None] * (x[b, t] - (h * k[:, None]).sum(-1)))[..., None] * k[:, None]
             y[b, t] = scale * (h * q[:, None]).sum(-1)
             for z, r in zip(carried, rests):
-                ybound[b, t] += 2.0 ** -12 * abs(scale) * (q * z).sum(-1).abs()[:, None] * r.abs()
+                ybound[b, t] += pt * abs(scale) * (q * z).sum(-1).abs()[:, None] * r.abs()
             ybound[b, t] += abs(scale) * q.norm(dim=-1)[:, None] * (e + eps * h.norm(dim=-1))
         out[row], err[row] = h, e[..., None].expand(H, P, N)
     return y, ybound, out, err + 2.0 ** -23 * out.abs() + 1e-30

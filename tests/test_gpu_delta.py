@@ -38,7 +38,8 @@ def to(d, dev="cuda"):
 def run(ssd, a, o, spread=1.0, **more):
     y, final = ssd.ssd_delta_fwd(**to(a), **to({**o, **more}))
     torch.cuda.synchronize()
-    ry, by, rf, bf = ref.delta(**a, **{k: v for k, v in {**o, **more}.items() if k not in ("want_final_state", "y")}, spread=spread)
+    ry, by, rf, bf = ref.delta(**a, **{k: v for k, v in {**o, **more}.items() if k not in ("want_final_state", "y")}, spread=spread,
+                               pt=2.0 ** (-12 if a["x"].dtype == torch.bfloat16 else -22))
     check("y", y, ry, store(ry, by, a["x"].dtype))
     if final is not None:
         check("final", final, rf, bf)
@@ -71,24 +72,24 @@ def near(name, got, want, bound):
     assert err <= bound, (name, err)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("B,L,H,G,P,N", [
     (1, 64, 1, 1, 64, 64), (1, 64, 2, 1, 128, 128), (2, 65, 2, 2, 32, 128), (1, 127, 4, 2, 16, 64), (2, 128, 3, 1, 48, 128),
-    (1, 129, 2, 2, 80, 64), (1, 321, 6, 3, 128, 128), (3, 200, 2, 1, 144, 128), (40, 70, 4, 4, 128, 64), (1, 700, 2, 2, 128, 128),
-    (20, 192, 8, 4, 64, 128)])
-def test_prompts(ssd, B, L, H, G, P, N):
-    """Whole prompts in bf16.  Over all rows the roundings are independent: 2^-19 of the state (three products a
-    chunk, a few 2^-22 each), and y is rounded once more."""
-    a, o = inputs(B, L, H, G, P, N, torch.bfloat16, seed=L + P)
+    (1, 129, 2, 2, 80, 64), (1, 321, 6, 3, 128, 128), (3, 200, 2, 1, 144, 128), (40, 70, 4, 4, 64, 64), (20, 64, 8, 4, 48, 128)])
+def test_prompts(ssd, B, L, H, G, P, N, dtype):
+    """Whole prompts.  Over all rows the roundings are independent: 2^-19 of the state (three products a chunk, a
+    few 2^-22 each), of y as well, and y is rounded once more."""
+    a, o = inputs(B, L, H, G, P, N, dtype, seed=L + P)
     y, final = run(ssd, a, o, spread=65.0)
     ry, _, rf, _ = ref.delta(**a, **o)
     near("final", final, rf, 2.0 ** -19)
-    near("y", y, ry, 2.0 ** -8)
+    near("y", y, ry, 2.0 ** -19 if dtype == torch.float32 else 2.0 ** -8)
 
 
-@pytest.mark.parametrize("N", [64, 128])
-@pytest.mark.parametrize("L", [64, 150, 513])
-def test_prompts_in_a_cache(ssd, L, N):
-    a, o = inputs(6, L, 4, 2, 64, N, torch.bfloat16, cached=True, seed=3)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("L,N", [(64, 128), (150, 64), (257, 128)])
+def test_prompts_in_a_cache(ssd, L, N, dtype):
+    a, o = inputs(6, L, 4, 2, 64, N, dtype, cached=True, seed=3)
     o["lengths"] = torch.tensor([L, 0, L - 1, 63, L + 9, 1], dtype=torch.int32)
     o["positions"] = torch.tensor([4, 2, 0, 0, 1, 7], dtype=torch.int32)
     y, final = run(ssd, a, o, spread=65.0)
@@ -97,9 +98,10 @@ def test_prompts_in_a_cache(ssd, L, N):
     assert not y2[0].any() and not y2[4].any() and torch.equal(y[[1, 2, 3, 5]], y2[[1, 2, 3, 5]])
 
 
-def test_prompt_is_its_tokens(ssd):
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_prompt_is_its_tokens(ssd, dtype):
     """A prompt, and the same one resumed in pieces and token by token."""
-    a, o = inputs(2, 200, 4, 2, 128, 128, torch.bfloat16, seed=12)
+    a, o = inputs(2, 200, 4, 2, 128, 128, dtype, seed=12)
     y, final = ssd.ssd_delta_fwd(**to(a), **to(o))
     state, ys = None, []
     for lo, hi in ((0, 100), (100, 170), (170, 171), (171, 180), (180, 200)):
@@ -107,7 +109,25 @@ def test_prompt_is_its_tokens(ssd):
         yp, state = ssd.ssd_delta_fwd(**part, **to(o), init_state=state)
         ys.append(yp)
     near("final", state, final.double().cpu(), 2.0 ** -18)
-    near("y", torch.cat(ys, 1), y.double().cpu(), 2.0 ** -7)
+    near("y", torch.cat(ys, 1), y.double().cpu(), 2.0 ** (-18 if dtype == torch.float32 else -7))
+
+
+def test_many_chunks_in_pairs_of_launches(ssd):
+    """So many heads and chunks that a call makes several pairs of launches, which overlap."""
+    for H, L in ((16, 4500), (160, 3400)):
+        a, o = inputs(1, L, H, H, 64, 64, torch.bfloat16, seed=H)
+        A, O = to(a), to(o)
+        y, final = ssd.ssd_delta_fwd(**A, **O)
+        state, ys = None, []
+        for lo in range(0, L, 640):
+            part = {k: v[:, lo:lo + 640] if v.dim() > 1 else v for k, v in A.items()}
+            yp, state = ssd.ssd_delta_fwd(**part, **O, init_state=state)
+            ys.append(yp)
+        near("final", state, final.double().cpu(), 2.0 ** -18)
+        near("y", torch.cat(ys, 1), y.double().cpu(), 2.0 ** -7)
+        for _ in range(20):
+            y2, final2 = ssd.ssd_delta_fwd(**A, **O)
+            assert torch.equal(y, y2) and torch.equal(final, final2)
 
 
 def test_strong_and_weak_decay(ssd):
@@ -149,12 +169,13 @@ def test_plain_arguments(ssd):
     run(ssd, a, dict(scale=-0.75))
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("L", [21, 90])
-def test_strides(ssd, L):
+def test_strides(ssd, L, dtype):
     B, H, G, P, N = 2, 4, 2, 64, 128
-    a, o = inputs(B, L, H, G, P, N, torch.bfloat16, seed=2)
+    a, o = inputs(B, L, H, G, P, N, dtype, seed=2)
     for pad in (0, 8, 3):  # 16-byte rows and others
-        wide = torch.zeros(B, L, H * P + 2 * G * N + 2 * H + pad, dtype=torch.bfloat16)
+        wide = torch.zeros(B, L, H * P + 2 * G * N + 2 * H + pad, dtype=dtype)
         parts = [H * P, G * N, G * N, H, H]
         views = [v.unflatten(2, s) if s else v for v, s in zip(wide[:, :, pad:].split(parts, 2), [(H, P), (G, N), (G, N), None, None])]
         for v, k in zip(views, ("x", "Bm", "Cm", "dt", "beta")):
