@@ -174,10 +174,17 @@ cudaError_t launch_scan(const DeltaParams& p, cudaStream_t stream) {
                   dim3(32 * kWarps), 0, stream, true, p, tiles);
 }
 
+template <typename T, int N>
+cudaError_t launch_rows(const DeltaParams& p, cudaStream_t stream) {
+  // rows a lane: four, whose sums are joined together, or two while four leave multiprocessors without a block
+  // (31 tokens of 16 heads 18.5 us with two, 21.4 with four, one and more warps 16.7; single tokens 5 us with any)
+  const bool few = p.batch * p.H * ceil_div(p.P, 4 * 2048 / N) < 2 * static_cast<int64_t>(layer_sm_count());
+  return few ? launch_scan<T, N, 2, 4>(p, stream) : launch_scan<T, N, 4, 4>(p, stream);
+}
+
 template <typename T>
 cudaError_t launch_delta(const DeltaParams& p, cudaStream_t stream) {
-  return p.N == 64 ? launch_scan<T, 64, 4, 4>(p, stream) : p.N == 128 ? launch_scan<T, 128, 4, 4>(p, stream)
-                                                                      : launch_scan<T, 256, 4, 4>(p, stream);
+  return p.N == 64 ? launch_rows<T, 64>(p, stream) : p.N == 128 ? launch_rows<T, 128>(p, stream) : launch_rows<T, 256>(p, stream);
 }
 
 ssd_status check_delta(const ssd_delta_args* a) {
