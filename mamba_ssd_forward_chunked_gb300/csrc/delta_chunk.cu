@@ -152,27 +152,29 @@ __global__ void __launch_bounds__(kPrepThreads, kParts<T> == 1 ? 4 : 2) delta_pr
   const int n = seq.length - t0 < kC ? static_cast<int>(seq.length - t0) : kC;
   const int per = p.H / p.G, g = h / per;
 
-  // rows of K, then of Q; rows behind the sequence are 0
+  // rows of K (four warps, 16 each), of Q (four more); rows behind the sequence are 0
   constexpr int kRowLanes = N / 8, kPer = 32 / kRowLanes, kLoads = 16 / kPer;  // a lane has 8 of a row
-  const T* from[2] = {static_cast<const T*>(p.Bm) + b * p.B_batch + t0 * p.B_token + static_cast<int64_t>(g) * N,
-                      static_cast<const T*>(p.Cm) + b * p.C_batch + t0 * p.C_token + static_cast<int64_t>(g) * N};
+  const bool is_q = warp >= 4;
+  const int row0 = 16 * warp + lane / kRowLanes, token0 = row0 & 63, col = lane % kRowLanes;
   struct Eight {
     uint4 raw[kP];
   };
   Eight eight[kLoads];
+  {
+    const int64_t step = is_q ? p.C_token : p.B_token;
+    const T* from = static_cast<const T*>(is_q ? p.Cm : p.Bm) + b * (is_q ? p.C_batch : p.B_batch) + (t0 + token0) * step +
+                    static_cast<int64_t>(g) * N + col * 8;
 #pragma unroll
-  for (int i = 0; i < kLoads; ++i) {
-    const int r = warp * 16 + i * kPer + lane / kRowLanes, t = r & 63;
+    for (int i = 0; i < kLoads; ++i, from += kPer * step) {
 #pragma unroll
-    for (int e = 0; e < kP; ++e) eight[i].raw[e] = make_uint4(0, 0, 0, 0);
-    if (t < n) {
-      const T* row = (r < kC ? from[0] + t * p.B_token : from[1] + t * p.C_token) + lane % kRowLanes * 8;
+      for (int e = 0; e < kP; ++e) eight[i].raw[e] = make_uint4(0, 0, 0, 0);
+      if (token0 + i * kPer >= n) continue;
       if (s.vectors) {
 #pragma unroll
-        for (int e = 0; e < kP; ++e) eight[i].raw[e] = reinterpret_cast<const uint4*>(row)[e];
+        for (int e = 0; e < kP; ++e) eight[i].raw[e] = reinterpret_cast<const uint4*>(from)[e];
       } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) reinterpret_cast<T*>(eight[i].raw)[e] = row[e];
+        for (int e = 0; e < 8; ++e) reinterpret_cast<T*>(eight[i].raw)[e] = from[e];
       }
     }
   }
@@ -196,10 +198,12 @@ __global__ void __launch_bounds__(kPrepThreads, kParts<T> == 1 ? 4 : 2) delta_pr
     s_beta[tid] = beta;
   }
   // in fp16, times a power of two
-  uint8_t* rows_out = h == g * per ? s.rows + ((b * p.G + g) * s.count + blockIdx.x) * static_cast<int64_t>(rows_bytes(N, kP)) : nullptr;
+  uint8_t* rows_out = h == g * per ? s.rows + ((b * p.G + g) * s.count + blockIdx.x) * static_cast<int64_t>(rows_bytes(N, kP)) +
+                                         (col >> 3) * 2 * kSlab + row0 * 128
+                                   : nullptr;
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
-    const int r = warp * 16 + i * kPer + lane / kRowLanes;
+    const int r = row0 + i * kPer;
     float v[8], squares = 0.f, largest = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -224,12 +228,10 @@ __global__ void __launch_bounds__(kPrepThreads, kParts<T> == 1 ? 4 : 2) delta_pr
         split(lo, hi, (&half[0].x)[e], (&half[kP - 1].x)[e]);
       }
     }
-    const int col = lane % kRowLanes;
 #pragma unroll
     for (int e = 0; e < kP; ++e) {
       *reinterpret_cast<uint4*>(smem + (e ? M::kLow : 0) + r * M::kRow + col * 16) = half[e];
-      if (rows_out)
-        *reinterpret_cast<uint4*>(rows_out + e * rows_bytes(N, 1) + (col >> 3) * 2 * kSlab + r * 128 + (((col & 7) ^ (r & 7)) << 4)) = half[e];
+      if (rows_out) *reinterpret_cast<uint4*>(rows_out + e * rows_bytes(N, 1) + i * kPer * 128 + (((col & 7) ^ (r & 7)) << 4)) = half[e];
     }
     if (col == 0) s_squares[r] = make_float2(squares, scale.down);
   }
@@ -242,7 +244,6 @@ __global__ void __launch_bounds__(kPrepThreads, kParts<T> == 1 ? 4 : 2) delta_pr
   }
 
   // K K^T (four warps, 16 rows each) and Q K^T (four more)
-  const bool is_q = warp >= 4;
   const int mt = is_q ? 7 - warp : warp;  // (beside a warp of few columns one of many)
   const uint32_t rows = smem_u32(smem);
   float acc[8][4];
