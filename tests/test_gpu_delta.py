@@ -114,7 +114,7 @@ def test_prompt_is_its_tokens(ssd, dtype):
 
 
 def test_many_chunks_in_pairs_of_launches(ssd):
-    """So many heads and chunks that a call makes several pairs of launches, which overlap."""
+    """So many heads and chunks that a call makes several pairs of launches, which overlap (also when replayed)."""
     for H, L in ((16, 4500), (160, 3400)):
         a, o = inputs(1, L, H, H, 64, 64, torch.bfloat16, seed=H)
         A, O = to(a), to(o)
@@ -129,6 +129,14 @@ def test_many_chunks_in_pairs_of_launches(ssd):
         for _ in range(20):
             y2, final2 = ssd.ssd_delta_fwd(**A, **O)
             assert torch.equal(y, y2) and torch.equal(final, final2)
+        side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.graph(graph, stream=side):
+            y3, final3 = ssd.ssd_delta_fwd(**A, **O)
+        for _ in range(10):
+            y3.fill_(float("nan"))
+            graph.replay()
+            assert torch.equal(y, y3) and torch.equal(final, final3)
 
 
 def test_strong_and_weak_decay(ssd):
@@ -136,6 +144,10 @@ def test_strong_and_weak_decay(ssd):
         a, o = inputs(1, 300, 2, 1, 64, 128, torch.bfloat16, seed=13)
         o["dt_bias"] = torch.full((2,), shift)
         run(ssd, a, o)
+    a["A"] = a["A"].abs() * 0.1  # (growth)
+    o["dt_bias"] = torch.full((2,), -3.0)
+    run(ssd, a, o)
+    a["A"], o["dt_bias"] = -a["A"] * 10, torch.full((2,), 4.0)
     a["dt"][0, 50:60] = 300.0  # forgets everything, several times
     a["dt"][0, 130] = 300.0
     run(ssd, a, o)
