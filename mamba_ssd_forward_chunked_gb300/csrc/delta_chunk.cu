@@ -549,6 +549,15 @@ __device__ __forceinline__ void tmem_ld8(uint32_t at, uint32_t (&r)[8]) {
                : "r"(at));
 }
 
+// One thread of a warp that is together, always the same one.  What the others compute beside it is known to be the
+// same in all, so that descriptors stay in uniform registers: a product is issued every 41 cycles (M 128, N 32), under
+// a plain test of the lane every 60.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 template <typename T, int N, int kPT, int kGroups, int kStages, int kBlocks>
 __global__ void __launch_bounds__(Walk<T, N, kPT, kGroups, kStages>::kThreads, kBlocks) delta_walk_kernel(DeltaParams p, DeltaChunks s) {
   using M = Walk<T, N, kPT, kGroups, kStages>;
@@ -635,17 +644,17 @@ __global__ void __launch_bounds__(Walk<T, N, kPT, kGroups, kStages>::kThreads, k
       }
     }
   } else if (warp == kWorkers + 1) {
-    // products
-    if (lane == 0) {
-      constexpr uint32_t id_two = idesc_f32acc(0, 128, 2 * kPT, 0, 1), id_one = idesc_f32acc(0, 128, kPT, 0, 1);
-      const uint32_t base = smem_u32(smem);
-      const uint64_t dS = sdesc_sw128(base + M::kS, M::kSlabS, 1024), dR = sdesc_sw128(base + M::kR, kSlab, 1024);
-      for (int c = 0; c < chunks; ++c) {
-        const int st = c % kStages, turn = c / kStages;
-        const uint32_t kq = base + M::kRows + st * rows_bytes(N, kP);
-        if (!wait(kRowsFull + st, turn) || !spin(kStateReady, c)) break;
-        tc_fence_after();
-        const uint64_t kq_rows = sdesc_sw128(kq, 16, 1024);
+    // products: the warp stays together and one thread issues (see elect_one)
+    constexpr uint32_t id_two = idesc_f32acc(0, 128, 2 * kPT, 0, 1), id_one = idesc_f32acc(0, 128, kPT, 0, 1);
+    const uint32_t base = smem_u32(smem);
+    const uint64_t dS = sdesc_sw128(base + M::kS, M::kSlabS, 1024), dR = sdesc_sw128(base + M::kR, kSlab, 1024);
+    for (int c = 0; c < chunks; ++c) {
+      const int st = c % kStages, turn = c / kStages;
+      const uint32_t kq = base + M::kRows + st * rows_bytes(N, kP);
+      if (!__all_sync(0xffffffffu, wait(kRowsFull + st, turn) && spin(kStateReady, c))) break;
+      tc_fence_after();
+      const uint64_t kq_rows = sdesc_sw128(kq, 16, 1024);
+      if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < N / 16; ++k)
           mma_ss<false>(tmem + kColD1, kq_rows + (((k >> 2) * 2 * kSlab + (k & 3) * 32) >> 4), dS + (k * 2048 >> 4), id_two, k != 0);
@@ -656,18 +665,21 @@ __global__ void __launch_bounds__(Walk<T, N, kPT, kGroups, kStages>::kThreads, k
         }
         mma_commit(&bars[kFromStateDone]);
         mma_commit(&bars[kRowsEmpty + st]);
-        if (!wait(kTileFull + st, turn) || !spin(kRestReady, c)) break;
-        tc_fence_after();
-        const uint32_t tile = base + M::kTile + st * tile_bytes(N, kP);
-        const uint64_t w = sdesc_sw128(tile, 16, 1024);
+      }
+      __syncwarp();
+      if (!__all_sync(0xffffffffu, wait(kTileFull + st, turn) && spin(kRestReady, c))) break;
+      tc_fence_after();
+      const uint32_t tile = base + M::kTile + st * tile_bytes(N, kP);
+      const uint64_t w = sdesc_sw128(tile, 16, 1024);
+      // P T's 64 rows go to the lanes of Q: they are the second half of 128 that begin in what lies before them
+      const uint64_t pt = sdesc_sw128(tile + (2 * (N / 64) - 1) * kSlab, 16, 1024);
+      if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < kC / 16; ++k) {  // both first parts, and the second of either with the first of the other
           mma_ss<false>(tmem + kColD1, w + (k * 32 >> 4), dR + (k * 2048 >> 4), id_two, k != 0);
           mma_ss<false>(tmem + kColD1, w + ((N / 64 * kSlab + k * 32) >> 4), dR + (k * 2048 >> 4), id_one, 1);
         }  // (N 64: the upper lanes' product is nobody's)
         mma_commit(&bars[kUpdateDone]);
-        // P T's 64 rows go to the lanes of Q: they are the second half of 128 that begin in what lies before them
-        const uint64_t pt = sdesc_sw128(tile + (2 * (N / 64) - 1) * kSlab, 16, 1024);
 #pragma unroll
         for (int k = 0; k < kC / 16; ++k) {
           mma_ss<false>(tmem + kColD3, pt + (k * 32 >> 4), dR + (k * 2048 >> 4), id_two, k != 0);
@@ -676,6 +688,9 @@ __global__ void __launch_bounds__(Walk<T, N, kPT, kGroups, kStages>::kThreads, k
         mma_commit(&bars[kRestDone]);
         mma_commit(&bars[kTileEmpty + st]);
       }
+      __syncwarp();
+    }
+    if (elect_one()) {
       mma_commit(&bars[kDrained]);
       mbar_wait(&bars[kDrained], 0, s.limit_ns);
     }
@@ -863,16 +878,13 @@ __global__ void __launch_bounds__(Walk<T, N, kPT, kGroups, kStages>::kThreads, k
       }
       state = next;
       const bool more = c + 1 < chunks;
-      if constexpr (M::kOwnR) {
-        if (more && has_state && ok) put(M::kS, M::kSlabS, row, S, state.up);
-        if (!is_token) ok = ok && all_wait(kRestDone, c);
-      } else {
-        ok = ok && all_wait(kRestDone, c);  // P T has read r, whose place the state takes
-        if (more && has_state && ok) put(M::kS, M::kSlabS, row, S, state.up);
-      }
+      if constexpr (!M::kOwnR) ok = ok && all_wait(kRestDone, c);  // P T has read r, whose place the state takes
+      if (more && has_state && ok) put(M::kS, M::kSlabS, row, S, state.up);
+      if (more && ok) arrive(kStateReady);
+      // (the next P T r waits for these warps' next arrival, which comes after this)
+      if (M::kOwnR && !is_token) ok = ok && all_wait(kRestDone, c);
       tc_fence_after();
       if (!is_token && ok) take(kColD3, v);
-      if (more && ok) arrive(kStateReady);
       if (!is_token && live && ok) {
         // y: the state's part, and P T r
         const float from_rest = fb * rest.down;
