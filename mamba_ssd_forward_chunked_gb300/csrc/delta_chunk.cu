@@ -32,8 +32,8 @@ constexpr int64_t kMinTokens = 32;
 // chunk of a head: two parts of W (N rows), P T (64 rows; for bf16 one part, as it goes into y alone, which has
 // 8 bits), and the tokens' factors.  Of a chunk of a group, for every part and 64 of N: 64 rows of K, then of Q.
 constexpr uint32_t kSlab = 8192;  // 64 rows of 128 bytes
-enum { kBeta, kFromState, kScalars, kOutState, kOutRest, kFactors };
-constexpr uint32_t kFactorBytes = 2 * kC * 4 + 16;  // those that the second launch keeps in shared memory: up to the scalars
+enum { kBeta, kFromState, kOutState, kOutRest, kScalars, kFactors };
+constexpr uint32_t kFactorBytes = 4 * kC * 4 + 16;  // with the four scalars
 enum { kDecay, kUpdate, kReach, kSpread };  // the scalars: e^{G_64}; what undoes W's scale; see the bounds of delta_walk_kernel
 template <typename T>
 constexpr int kParts = sizeof(T) == 2 ? 1 : 2;  // of K, Q and P T
@@ -524,9 +524,8 @@ struct Walk {
   static constexpr int kSlabs = (2 * kPT + 63) / 64;       // 64 columns each of the two parts side by side
   static constexpr uint32_t kSlabS = N * 128;
   static constexpr uint32_t kRows = 0, kTile = kRows + kStages * rows_bytes(N, kP), kS = kTile + kStages * tile_bytes(N, kP);
-  static constexpr bool kOwnR = kStages > 1;               // r has a place of its own, or the state's
-  static constexpr uint32_t kR = kS + (kOwnR ? kSlabs * kSlabS : 0);
-  static constexpr uint32_t kEnd = kS + kSlabs * kSlabS + (kOwnR ? kSlabs * kSlab : 0);
+  static constexpr uint32_t kR = kS + kSlabs * kSlabS;
+  static constexpr uint32_t kEnd = kR + kSlabs * kSlab;
   static constexpr uint32_t kLargest = kEnd + 18 * 8 + 4 * 4, kF = kLargest + 4 * kWorkers * 4;
   static constexpr uint32_t kX = kF + kStages * kFactorBytes;  // a chunk's x, every thread's where it put it
   static constexpr uint32_t kTotal = kX + kC * kPT * sizeof(T);
@@ -816,16 +815,13 @@ __global__ void __launch_bounds__(Walk<T, N, kPT, kGroups, kStages>::kThreads, k
     for (int c = 0; c < chunks; ++c) {
       const int64_t t = begin + static_cast<int64_t>(c) * kC + token;
       const bool live = t < length;
-      const float* out_factors = reinterpret_cast<const float*>(records + c * static_cast<int64_t>(record_bytes(N, kP)) + tile_bytes(N, kP));
-      float fa, fb;
-      if (!is_token) fa = out_factors[kOutState * kC + token], fb = out_factors[kOutRest * kC + token];
       ok = ok && all_wait(kRowsFull + c % kStages, c / kStages);
       const float* factors = reinterpret_cast<const float*>(smem + M::kF + c % kStages * kFactorBytes);
       const float4 scalars = *reinterpret_cast<const float4*>(factors + kScalars * kC);
       const float decay = scalars.x, update = scalars.y;
+      const float fa = factors[(is_token ? kBeta : kOutState) * kC + token], fb = factors[(is_token ? kFromState : kOutRest) * kC + token];
       float bx[kCols];
       if (is_token) {
-        fa = factors[kBeta * kC + token], fb = factors[kFromState * kC + token];
         asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
@@ -878,11 +874,10 @@ __global__ void __launch_bounds__(Walk<T, N, kPT, kGroups, kStages>::kThreads, k
       }
       state = next;
       const bool more = c + 1 < chunks;
-      if constexpr (!M::kOwnR) ok = ok && all_wait(kRestDone, c);  // P T has read r, whose place the state takes
       if (more && has_state && ok) put(M::kS, M::kSlabS, row, S, state.up);
       if (more && ok) arrive(kStateReady);
       // (the next P T r waits for these warps' next arrival, which comes after this)
-      if (M::kOwnR && !is_token) ok = ok && all_wait(kRestDone, c);
+      if (!is_token) ok = ok && all_wait(kRestDone, c);
       tc_fence_after();
       if (!is_token && ok) take(kColD3, v);
       if (!is_token && live && ok) {
