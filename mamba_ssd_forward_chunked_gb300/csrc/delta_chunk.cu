@@ -527,8 +527,9 @@ struct Walk {
   static constexpr uint32_t kR = kS + kSlabs * kSlabS;
   static constexpr uint32_t kEnd = kR + kSlabs * kSlab;
   static constexpr uint32_t kLargest = kEnd + 18 * 8 + 4 * 4, kF = kLargest + 4 * kWorkers * 4;
-  static constexpr uint32_t kX = kF + kStages * kFactorBytes;  // a chunk's x, every thread's where it put it
-  static constexpr uint32_t kTotal = kX + kC * kPT * sizeof(T);
+  static constexpr uint32_t kX = kF + kStages * kFactorBytes;      // x, a token's row after the other
+  static constexpr uint32_t kXRow = kPT * sizeof(T) + 16;          // (so that eight rows lie in different banks)
+  static constexpr uint32_t kTotal = kX + kStages * kC * kXRow;
   static constexpr uint32_t kTmem = 4 * kPT;               // columns of tensor memory
 };
 
@@ -572,7 +573,10 @@ __global__ void __launch_bounds__(Walk<T, N, kPT, kGroups, kStages>::kThreads, k
   const int64_t b = blockIdx.z;
   const int h = blockIdx.y, p0 = blockIdx.x * kPT;
   if (tid == 0) {
-    for (int i = 0; i < kBarriers; ++i) mbar_init(&bars[i], i == kStateReady || i == kRestReady || i == kFactorsRead || i == kFactorsRead1 ? kWorkers : 1);
+    for (int i = 0; i < kBarriers; ++i)
+      mbar_init(&bars[i], i == kStateReady || i == kRestReady || i == kFactorsRead || i == kFactorsRead1 ? kWorkers
+                          : i == kRowsFull || i == kRowsFull1                                             ? 33
+                                                                                                          : 1);
     fence_mbar_init();
     *failed = 0;
     for (int i = 0; i < 4 * kWorkers; ++i) s_largest[i] = 0;
@@ -615,32 +619,47 @@ __global__ void __launch_bounds__(Walk<T, N, kPT, kGroups, kStages>::kThreads, k
   };
 
   if (warp == kWorkers) {
-    // loads
-    if (lane == 0) {
-      int c = 0, t = 0;  // chunks whose rows, and whose tiles, are on their way
-      bool ok = true;
-      while (t < chunks) {
-        const int st = t % kStages, turn = t / kStages;
-        ok = turn == 0 || wait(kRowsEmpty + st, turn - 1);
-        // (the rows' product does not wait for those who read the factors, nor would they notice that the stage
-        // has been filled twice)
-        ok = ok && (turn == 0 || wait(kFactorsRead + st, turn - 1));
-        if (!ok) break;
-        mbar_arrive_expect_tx(&bars[kRowsFull + st], rows_bytes(N, kP) + kFactorBytes);
-        bulk_load(smem + M::kRows + st * rows_bytes(N, kP), rows + c * static_cast<int64_t>(rows_bytes(N, kP)), rows_bytes(N, kP), &bars[kRowsFull + st]);
-        bulk_load(smem + M::kF + c % kStages * kFactorBytes, records + c * static_cast<int64_t>(record_bytes(N, kP)) + tile_bytes(N, kP), kFactorBytes,
-                  &bars[kRowsFull + st]);
-        ++c;
-        ok = turn == 0 || wait(kTileEmpty + st, turn - 1);
-        if (!ok) break;
+    // loads: x by all lanes, the rest by one
+    int c = 0, t = 0;  // chunks whose rows, and whose tiles, are on their way
+    bool ok = true;
+    const uint32_t x_bytes = (p.P - p0 < kPT ? p.P - p0 : kPT) * static_cast<uint32_t>(sizeof(T));
+    const T* x = static_cast<const T*>(p.x) + b * p.x_batch + static_cast<int64_t>(h) * p.P + p0;
+    while (t < chunks) {
+      const int st = t % kStages, turn = t / kStages;
+      // (the rows' product does not wait for those who read the factors and x, nor would they notice that the stage
+      // has been filled twice)
+      ok = __all_sync(0xffffffffu, turn == 0 || (wait(kRowsEmpty + st, turn - 1) && wait(kFactorsRead + st, turn - 1)));
+      if (!ok) break;
+      uint64_t* full = &bars[kRowsFull + st];
+      const int64_t t0 = begin + static_cast<int64_t>(c) * kC;
+      const uint32_t tokens = !s.vectors ? 0 : length - t0 < kC ? static_cast<uint32_t>(length - t0) : kC;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(full, rows_bytes(N, kP) + kFactorBytes);
+        bulk_load(smem + M::kRows + st * rows_bytes(N, kP), rows + c * static_cast<int64_t>(rows_bytes(N, kP)), rows_bytes(N, kP), full);
+        bulk_load(smem + M::kF + st * kFactorBytes, records + c * static_cast<int64_t>(record_bytes(N, kP)) + tile_bytes(N, kP), kFactorBytes, full);
+      }
+      constexpr uint32_t kPer = kPT * sizeof(T) / 16;  // pieces of a row, side by side in neighbouring lanes
+#pragma unroll
+      for (uint32_t i = lane; i < kC * kPer; i += 32) {
+        const uint32_t token = i / kPer, at = i % kPer * 16;
+        if (token >= tokens || at >= x_bytes) continue;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem + M::kX + (st * kC + token) * M::kXRow + at)),
+                     "l"(__cvta_generic_to_global(reinterpret_cast<const uint8_t*>(x + (t0 + token) * p.x_token) + at))
+                     : "memory");
+      }
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(full)) : "memory");
+      ++c;
+      ok = __all_sync(0xffffffffu, turn == 0 || wait(kTileEmpty + st, turn - 1));
+      if (!ok) break;
+      if (lane == 0) {
         mbar_arrive_expect_tx(&bars[kTileFull + st], tile_bytes(N, kP));
         bulk_load(smem + M::kTile + st * tile_bytes(N, kP), records + t * static_cast<int64_t>(record_bytes(N, kP)), tile_bytes(N, kP), &bars[kTileFull + st]);
-        ++t;
       }
-      if (!ok) {  // nothing is in flight when the block ends
-        for (int i = c > kStages ? c - kStages : 0; i < c; ++i) mbar_wait(&bars[kRowsFull + i % kStages], (i / kStages) & 1, s.limit_ns);
-        for (int i = t > kStages ? t - kStages : 0; i < t; ++i) mbar_wait(&bars[kTileFull + i % kStages], (i / kStages) & 1, s.limit_ns);
-      }
+      ++t;
+    }
+    if (!ok) {  // nothing is in flight when the block ends
+      for (int i = c > kStages ? c - kStages : 0; i < c; ++i) mbar_wait(&bars[kRowsFull + i % kStages], (i / kStages) & 1, s.limit_ns);
+      for (int i = t > kStages ? t - kStages : 0; i < t; ++i) mbar_wait(&bars[kTileFull + i % kStages], (i / kStages) & 1, s.limit_ns);
     }
   } else if (warp == kWorkers + 1) {
     // products: the warp stays together and one thread issues (see elect_one)
@@ -777,28 +796,6 @@ __global__ void __launch_bounds__(Walk<T, N, kPT, kGroups, kStages>::kThreads, k
       for (int i = 0; i < kCols; ++i)
         S[i] = from && has_state && col0 + i < p.P ? from[(static_cast<int64_t>(h) * p.P + col0 + i) * N + row] : 0.f;
     }
-    // x is asked for a chunk ahead, into shared memory
-    uint4* s_x = reinterpret_cast<uint4*>(smem + M::kX) + (2 * group + quarter) * 32 + lane;  // (of tokens)
-    constexpr int kStrideX = 16 * kWorkers;
-    auto ask = [&](int c) {
-      const int64_t t = begin + static_cast<int64_t>(c) * kC + token;
-#pragma unroll
-      for (int i = 0; i < kVecs; ++i) {
-        constexpr int kE = 16 / sizeof(T);
-        uint4* to = s_x + i * kStrideX;
-        const T* from = x + t * p.x_token + kE * i;
-        if (t >= length || col0 + kE * i >= p.P) {
-          *to = make_uint4(0, 0, 0, 0);
-        } else if (s.vectors) {
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(__cvta_generic_to_global(from)) : "memory");
-        } else {
-#pragma unroll
-          for (int e = 0; e < kE; ++e) reinterpret_cast<T*>(to)[e] = from[e];
-        }
-      }
-    };
-    if (is_token) ask(0);
-
     // Scales go by bounds that are known while the products run, not by what comes out of them, so that nobody
     // waits for the others in the chain: with s the largest of the state
     //     |r| <= max |beta x| + s max_j beta e^{G_j} |k_j|_1,    |state after| <= e^{G_64} s + 64 max |W| max |r|.
@@ -822,10 +819,19 @@ __global__ void __launch_bounds__(Walk<T, N, kPT, kGroups, kStages>::kThreads, k
       const float fa = factors[(is_token ? kBeta : kOutState) * kC + token], fb = factors[(is_token ? kFromState : kOutRest) * kC + token];
       float bx[kCols];
       if (is_token) {
-        asm volatile("cp.async.wait_all;" ::: "memory");
+        const uint8_t* s_x = smem + M::kX + (c % kStages * kC + token) * M::kXRow + group * kCols * sizeof(T);
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
-          const uint4 xs = s_x[i * kStrideX];
+          constexpr int kE = 16 / sizeof(T);
+          uint4 xs = make_uint4(0, 0, 0, 0);
+          if (live && col0 + kE * i < p.P) {
+            if (s.vectors) {
+              xs = *reinterpret_cast<const uint4*>(s_x + 16 * i);
+            } else {
+#pragma unroll
+              for (int e = 0; e < kE; ++e) reinterpret_cast<T*>(&xs)[e] = x[t * p.x_token + kE * i + e];
+            }
+          }
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const uint32_t w = (&xs.x)[e];
@@ -835,7 +841,6 @@ __global__ void __launch_bounds__(Walk<T, N, kPT, kGroups, kStages>::kThreads, k
               bx[4 * i + e] = fa * __uint_as_float(w);
           }
         }
-        if (c + 1 < chunks) ask(c + 1);
         leave(1, c, magnitude(bx), 2 * group + quarter);
       }
       __syncwarp();
