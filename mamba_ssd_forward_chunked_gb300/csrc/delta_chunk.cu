@@ -527,13 +527,13 @@ struct Walk {
   static constexpr uint32_t kR = kS + kSlabs * kSlabS;
   static constexpr uint32_t kEnd = kR + kSlabs * kSlab;
   static constexpr uint32_t kLargest = kEnd + 18 * 8 + 4 * 4, kF = kLargest + 4 * kWorkers * 4;
-  static constexpr uint32_t kX = kF + kStages * kFactorBytes;      // x, a token's row after the other
+  static constexpr uint32_t kX = kF + 2 * kFactorBytes;            // x, a token's row after the other
   static constexpr uint32_t kXRow = kPT * sizeof(T) + 16;          // (so that eight rows lie in different banks)
-  static constexpr uint32_t kTotal = kX + kStages * kC * kXRow;
+  static constexpr uint32_t kTotal = kX + 2 * kC * kXRow;
   static constexpr uint32_t kTmem = 4 * kPT;               // columns of tensor memory
 };
 
-enum { kRowsFull, kRowsFull1, kRowsEmpty, kRowsEmpty1, kFactorsRead, kFactorsRead1, kTileFull, kTileFull1, kTileEmpty, kTileEmpty1, kStateReady, kFromStateDone,
+enum { kRowsFull, kRowsFull1, kRowsEmpty, kRowsEmpty1, kSideFull, kSideFull1, kSideEmpty, kSideEmpty1, kTileFull, kTileFull1, kTileEmpty, kTileEmpty1, kStateReady, kFromStateDone,
        kRestReady, kUpdateDone, kRestDone, kDrained, kBarriers };
 
 // cp.async.bulk: bytes from global to shared memory, counted by the barrier.
@@ -574,9 +574,7 @@ __global__ void __launch_bounds__(Walk<T, N, kPT, kGroups, kStages>::kThreads, k
   const int h = blockIdx.y, p0 = blockIdx.x * kPT;
   if (tid == 0) {
     for (int i = 0; i < kBarriers; ++i)
-      mbar_init(&bars[i], i == kStateReady || i == kRestReady || i == kFactorsRead || i == kFactorsRead1 ? kWorkers
-                          : i == kRowsFull || i == kRowsFull1                                             ? 33
-                                                                                                          : 1);
+      mbar_init(&bars[i], i == kStateReady || i == kRestReady || i == kSideEmpty || i == kSideEmpty1 ? kWorkers : i == kSideFull || i == kSideFull1 ? 33 : 1);
     fence_mbar_init();
     *failed = 0;
     for (int i = 0; i < 4 * kWorkers; ++i) s_largest[i] = 0;
@@ -619,26 +617,22 @@ __global__ void __launch_bounds__(Walk<T, N, kPT, kGroups, kStages>::kThreads, k
   };
 
   if (warp == kWorkers) {
-    // loads: x by all lanes, the rest by one
-    int c = 0, t = 0;  // chunks whose rows, and whose tiles, are on their way
+    // loads
     bool ok = true;
     const uint32_t x_bytes = (p.P - p0 < kPT ? p.P - p0 : kPT) * static_cast<uint32_t>(sizeof(T));
     const T* x = static_cast<const T*>(p.x) + b * p.x_batch + static_cast<int64_t>(h) * p.P + p0;
-    while (t < chunks) {
-      const int st = t % kStages, turn = t / kStages;
-      // (the rows' product does not wait for those who read the factors and x, nor would they notice that the stage
-      // has been filled twice)
-      ok = __all_sync(0xffffffffu, turn == 0 || (wait(kRowsEmpty + st, turn - 1) && wait(kFactorsRead + st, turn - 1)));
-      if (!ok) break;
-      uint64_t* full = &bars[kRowsFull + st];
+    // what the threads read themselves, the factors and x (of that, by all lanes, neighbours on a row)
+    auto load_side = [&](int c) {
+      const int st = c & 1, turn = c >> 1;
+      if (!__all_sync(0xffffffffu, turn == 0 || wait(kSideEmpty + st, turn - 1))) return false;
       const int64_t t0 = begin + static_cast<int64_t>(c) * kC;
       const uint32_t tokens = !s.vectors ? 0 : length - t0 < kC ? static_cast<uint32_t>(length - t0) : kC;
+      uint64_t* full = &bars[kSideFull + st];
       if (lane == 0) {
-        mbar_arrive_expect_tx(full, rows_bytes(N, kP) + kFactorBytes);
-        bulk_load(smem + M::kRows + st * rows_bytes(N, kP), rows + c * static_cast<int64_t>(rows_bytes(N, kP)), rows_bytes(N, kP), full);
+        mbar_arrive_expect_tx(full, kFactorBytes);
         bulk_load(smem + M::kF + st * kFactorBytes, records + c * static_cast<int64_t>(record_bytes(N, kP)) + tile_bytes(N, kP), kFactorBytes, full);
       }
-      constexpr uint32_t kPer = kPT * sizeof(T) / 16;  // pieces of a row, side by side in neighbouring lanes
+      constexpr uint32_t kPer = kPT * sizeof(T) / 16;
 #pragma unroll
       for (uint32_t i = lane; i < kC * kPer; i += 32) {
         const uint32_t token = i / kPer, at = i % kPer * 16;
@@ -648,6 +642,23 @@ __global__ void __launch_bounds__(Walk<T, N, kPT, kGroups, kStages>::kThreads, k
                      : "memory");
       }
       asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(full)) : "memory");
+      return true;
+    };
+    int sides = 0, c = 0, t = 0;  // chunks whose factors, rows and tiles are on their way
+    if (chunks > 0) load_side(sides++);
+    while (t < chunks) {
+      const int st = t % kStages, turn = t / kStages;
+      if (sides < chunks) {
+        ok = load_side(sides);
+        if (!ok) break;
+        ++sides;
+      }
+      ok = __all_sync(0xffffffffu, turn == 0 || wait(kRowsEmpty + st, turn - 1));
+      if (!ok) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&bars[kRowsFull + st], rows_bytes(N, kP));
+        bulk_load(smem + M::kRows + st * rows_bytes(N, kP), rows + c * static_cast<int64_t>(rows_bytes(N, kP)), rows_bytes(N, kP), &bars[kRowsFull + st]);
+      }
       ++c;
       ok = __all_sync(0xffffffffu, turn == 0 || wait(kTileEmpty + st, turn - 1));
       if (!ok) break;
@@ -658,6 +669,7 @@ __global__ void __launch_bounds__(Walk<T, N, kPT, kGroups, kStages>::kThreads, k
       ++t;
     }
     if (!ok) {  // nothing is in flight when the block ends
+      for (int i = sides > 2 ? sides - 2 : 0; i < sides; ++i) mbar_wait(&bars[kSideFull + (i & 1)], (i >> 1) & 1, s.limit_ns);
       for (int i = c > kStages ? c - kStages : 0; i < c; ++i) mbar_wait(&bars[kRowsFull + i % kStages], (i / kStages) & 1, s.limit_ns);
       for (int i = t > kStages ? t - kStages : 0; i < t; ++i) mbar_wait(&bars[kTileFull + i % kStages], (i / kStages) & 1, s.limit_ns);
     }
@@ -802,29 +814,21 @@ __global__ void __launch_bounds__(Walk<T, N, kPT, kGroups, kStages>::kThreads, k
     // They can be a thousand times too large (the sums' signs); two parts have 2^17 to spare.
     Scale state{1.f, 1.f};
     bool ok = true;
-    if (chunks > 0) {
-      leave(0, 1, magnitude(S), warp);
-      named_bar_sync(1, 32 * kWorkers);
-      state = scale_for(__float_as_uint(largest_of(0, 1, kWorkers)));
-      if (has_state) put(M::kS, M::kSlabS, row, S, state.up);
-      arrive(kStateReady);
-    }
-    for (int c = 0; c < chunks; ++c) {
-      const int64_t t = begin + static_cast<int64_t>(c) * kC + token;
-      const bool live = t < length;
-      ok = ok && all_wait(kRowsFull + c % kStages, c / kStages);
-      const float* factors = reinterpret_cast<const float*>(smem + M::kF + c % kStages * kFactorBytes);
-      const float4 scalars = *reinterpret_cast<const float4*>(factors + kScalars * kC);
-      const float decay = scalars.x, update = scalars.y;
-      const float fa = factors[(is_token ? kBeta : kOutState) * kC + token], fb = factors[(is_token ? kFromState : kOutRest) * kC + token];
-      float bx[kCols];
+    float bx[kCols], fa, fb;  // beta x of tokens, and then the state's part of y of the others; the row's factors
+    float4 scalars;
+    auto ahead = [&](int c) {
+      if (!all_wait(kSideFull + (c & 1), c >> 1)) return false;
+      const float* factors = reinterpret_cast<const float*>(smem + M::kF + (c & 1) * kFactorBytes);
+      scalars = *reinterpret_cast<const float4*>(factors + kScalars * kC);
+      fa = factors[(is_token ? kBeta : kOutState) * kC + token], fb = factors[(is_token ? kFromState : kOutRest) * kC + token];
       if (is_token) {
-        const uint8_t* s_x = smem + M::kX + (c % kStages * kC + token) * M::kXRow + group * kCols * sizeof(T);
+        const uint8_t* s_x = smem + M::kX + ((c & 1) * kC + token) * M::kXRow + group * kCols * sizeof(T);
+        const int64_t t = begin + static_cast<int64_t>(c) * kC + token;
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
           constexpr int kE = 16 / sizeof(T);
           uint4 xs = make_uint4(0, 0, 0, 0);
-          if (live && col0 + kE * i < p.P) {
+          if (t < length && col0 + kE * i < p.P) {
             if (s.vectors) {
               xs = *reinterpret_cast<const uint4*>(s_x + 16 * i);
             } else {
@@ -844,11 +848,25 @@ __global__ void __launch_bounds__(Walk<T, N, kPT, kGroups, kStages>::kThreads, k
         leave(1, c, magnitude(bx), 2 * group + quarter);
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[kFactorsRead + c % kStages]);
+      if (lane == 0) mbar_arrive(&bars[kSideEmpty + (c & 1)]);
+      return true;
+    };
+    if (chunks > 0) {
+      ok = ahead(0);
+      leave(0, 1, magnitude(S), warp);
+      named_bar_sync(1, 32 * kWorkers);
+      state = scale_for(__float_as_uint(largest_of(0, 1, kWorkers)));
+      if (has_state) put(M::kS, M::kSlabS, row, S, state.up);
+      if (ok) arrive(kStateReady);
+    }
+    for (int c = 0; c < chunks; ++c) {
+      const int64_t t = begin + static_cast<int64_t>(c) * kC + token;
+      const bool live = t < length;
       leave(0, c, magnitude(S), warp);
       ok = !named_bar_or(1, 32 * kWorkers, !ok);  // (whoever has given up takes the others along)
       if (!ok) break;
       const float largest = largest_of(0, c, kWorkers);
+      const float decay = scalars.x, update = scalars.y;
       const float rest_bound = largest_of(1, c, kWorkers / 2) + scalars.z * largest;
       const Scale rest = scale_for(__float_as_uint(rest_bound));
       const Scale next = scale_for(__float_as_uint(fmaf(decay, largest, scalars.w * rest_bound)));
@@ -868,6 +886,8 @@ __global__ void __launch_bounds__(Walk<T, N, kPT, kGroups, kStages>::kThreads, k
         for (int i = 0; i < kCols; ++i) bx[i] = from_state * v[i];  // the state's part of y
       }
       if (ok) arrive(kRestReady);
+      const float out_rest = fb * rest.down;
+      if (c + 1 < chunks) ok = ok && ahead(c + 1);  // while the products run
       // the state
       ok = ok && all_wait(kUpdateDone, c);
       tc_fence_after();
@@ -887,9 +907,8 @@ __global__ void __launch_bounds__(Walk<T, N, kPT, kGroups, kStages>::kThreads, k
       if (!is_token && ok) take(kColD3, v);
       if (!is_token && live && ok) {
         // y: the state's part, and P T r
-        const float from_rest = fb * rest.down;
 #pragma unroll
-        for (int i = 0; i < kCols; ++i) v[i] = fmaf(from_rest, v[i], bx[i]);
+        for (int i = 0; i < kCols; ++i) v[i] = fmaf(out_rest, v[i], bx[i]);
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
           constexpr int kE = 16 / sizeof(T);
