@@ -533,7 +533,7 @@ struct Walk {
   static constexpr uint32_t kTmem = 4 * kPT;               // columns of tensor memory
 };
 
-enum { kRowsFull, kRowsFull1, kRowsEmpty, kRowsEmpty1, kSideFull, kSideFull1, kSideEmpty, kSideEmpty1, kTileFull, kTileFull1, kTileEmpty, kTileEmpty1, kStateReady, kFromStateDone,
+enum { kRowsFull, kRowsFull1, kRowsEmpty, kRowsEmpty1, kSideFull, kSideFull1, kSideEmpty, kSideEmpty1, kTileFull, kTileFull1, kTileEmpty, kTileEmpty1, kStateReady, kLargestReady, kFromStateDone,
        kRestReady, kUpdateDone, kRestDone, kDrained, kBarriers };
 
 // cp.async.bulk: bytes from global to shared memory, counted by the barrier.
@@ -574,7 +574,7 @@ __global__ void __launch_bounds__(Walk<T, N, kPT, kGroups, kStages>::kThreads, k
   const int h = blockIdx.y, p0 = blockIdx.x * kPT;
   if (tid == 0) {
     for (int i = 0; i < kBarriers; ++i)
-      mbar_init(&bars[i], i == kStateReady || i == kRestReady || i == kSideEmpty || i == kSideEmpty1 ? kWorkers : i == kSideFull || i == kSideFull1 ? 33 : 1);
+      mbar_init(&bars[i], i == kStateReady || i == kLargestReady || i == kRestReady || i == kSideEmpty || i == kSideEmpty1 ? kWorkers : i == kSideFull || i == kSideFull1 ? 33 : 1);
     fence_mbar_init();
     *failed = 0;
     for (int i = 0; i < 4 * kWorkers; ++i) s_largest[i] = 0;
@@ -851,6 +851,10 @@ __global__ void __launch_bounds__(Walk<T, N, kPT, kGroups, kStages>::kThreads, k
       if (lane == 0) mbar_arrive(&bars[kSideEmpty + (c & 1)]);
       return true;
     };
+    auto leave_state = [&](int c) {
+      leave(0, c, magnitude(S), warp);
+      if (lane == 0) mbar_arrive(&bars[kLargestReady]);
+    };
     if (chunks > 0) {
       ok = ahead(0);
       leave(0, 1, magnitude(S), warp);
@@ -858,12 +862,12 @@ __global__ void __launch_bounds__(Walk<T, N, kPT, kGroups, kStages>::kThreads, k
       state = scale_for(__float_as_uint(largest_of(0, 1, kWorkers)));
       if (has_state) put(M::kS, M::kSlabS, row, S, state.up);
       if (ok) arrive(kStateReady);
+      leave_state(0);
     }
     for (int c = 0; c < chunks; ++c) {
       const int64_t t = begin + static_cast<int64_t>(c) * kC + token;
       const bool live = t < length;
-      leave(0, c, magnitude(S), warp);
-      ok = !named_bar_or(1, 32 * kWorkers, !ok);  // (whoever has given up takes the others along)
+      ok = ok && all_wait(kLargestReady, c);
       if (!ok) break;
       const float largest = largest_of(0, c, kWorkers);
       const float decay = scalars.x, update = scalars.y;
@@ -900,7 +904,7 @@ __global__ void __launch_bounds__(Walk<T, N, kPT, kGroups, kStages>::kThreads, k
       state = next;
       const bool more = c + 1 < chunks;
       if (more && has_state && ok) put(M::kS, M::kSlabS, row, S, state.up);
-      if (more && ok) arrive(kStateReady);
+      if (more && ok) arrive(kStateReady), leave_state(c + 1);
       // (the next P T r waits for these warps' next arrival, which comes after this)
       if (!is_token) ok = ok && all_wait(kRestDone, c);
       tc_fence_after();
