@@ -997,11 +997,11 @@ cudaError_t launch_chunks(const DeltaParams& p, const DeltaChunks& s, cudaStream
                                               : launch_walk<T, N, 32, 2, 1, 2>(p, s, stream);
 }
 
-// Chunks of a pair of launches.  Pairs overlap, the first launch of one with the walk of the one before, and what
-// the one leaves for the other stays in the L2; but every walk begins and ends once more.  Where the walk leaves
-// no room (more blocks than multiprocessors) pairs only limit the workspace.  16 heads, 16384 tokens: 48 MB 538 us,
-// 24 MB 549, one pair 568; 128 heads, 4096 tokens: one pair 651, 48 MB 675.
-constexpr int64_t kPairBytes = int64_t(48) << 20, kPairBytesFull = int64_t(512) << 20;
+// Chunks of a pair of launches.  Pairs overlap, the first launch of one with the walk of the one before, but every
+// walk begins and ends once more.  Where the walk leaves no room (more blocks than multiprocessors) pairs only limit
+// the workspace.  16 heads, 16384 tokens: 48 MB 465 us, 64 MB 442, 128 MB 436, one pair 443; 128 heads, 4096 tokens:
+// one pair 651, 48 MB 675 (both before the walk was as fast as now).
+constexpr int64_t kPairBytes = int64_t(128) << 20, kPairBytesFull = int64_t(512) << 20;
 
 int64_t bytes_of_chunk(const DeltaParams& p) { return p.batch * (int64_t(record_bytes(p.N, p.parts)) * p.H + int64_t(rows_bytes(p.N, p.parts)) * p.G); }
 int64_t chunks_at_once(const DeltaParams& p) {

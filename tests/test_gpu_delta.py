@@ -115,7 +115,7 @@ def test_prompt_is_its_tokens(ssd, dtype):
 
 def test_many_chunks_in_pairs_of_launches(ssd):
     """So many heads and chunks that a call makes several pairs of launches, which overlap (also when replayed)."""
-    for H, L in ((16, 4500), (160, 3400)):
+    for H, L in ((16, 4500), (16, 25000), (160, 3400)):
         a, o = inputs(1, L, H, H, 64, 64, torch.bfloat16, seed=H)
         A, O = to(a), to(o)
         y, final = ssd.ssd_delta_fwd(**A, **O)
