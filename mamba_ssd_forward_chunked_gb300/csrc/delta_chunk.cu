@@ -15,7 +15,17 @@
 // each, and with a power of two that brings a tile's largest value to 2^14 the second part's last place is
 // at most 2^-22 of a value or 2^-38 of the largest.  (Three bf16 parts need no scale, but half as much again
 // of shared memory, stores and products.)  A row of bf16 K or Q times a power of two is fp16; 32-bit ones have
-// two parts as well, and so has P T then.  Parts lie side by side along the product's columns, and the threads add up what comes out.
+// two parts as well, and so has P T then.  Parts lie side by side along the product's columns, and the threads
+// add up what comes out.
+//
+// What it takes, of 128 x 128 states in bf16: 4 x 4096 tokens of 32 heads 562 us (61 for the bytes alone), the first
+// launch 254 and the walk 321; 16384 tokens of 16 heads 436 (40), a walk's chunk 1.17.  The first launch is bound by
+// shared memory and its barriers (60 % of the wavefronts, 49 % of the issue slots, 29 % of the DRAM), the walk by its
+// chain: one block an SM, 16 columns, passes a chunk in 2,250 cycles, two products of 570 each, r and the state 550
+// each on their way through the threads and their barriers.  So nothing else is in the chain: x and the factors of
+// the next chunk are read while W r runs, the largest values are agreed on while y is written, and y is written while
+// the next product runs.  Chunks of 64 tokens: W and P T are one operand of a product each, and 128 tokens would
+// need twice the columns of tensor memory and four times the first launch's work per chunk, for half the chain.
 #include <cuda_fp16.h>
 
 #include "delta_chunk.cuh"
@@ -513,6 +523,14 @@ __global__ void __launch_bounds__(kPrepThreads, kParts<T> == 1 ? 4 : 2) delta_pr
 
 // ------------------------------------------------------------------ second launch
 
+enum {
+  kRowsFull, kRowsFull1, kRowsEmpty, kRowsEmpty1,  // K and Q
+  kSideFull, kSideFull1, kSideEmpty, kSideEmpty1,  // the factors and x
+  kTileFull, kTileFull1, kTileEmpty, kTileEmpty1,  // W and P T
+  kStateReady, kFromStateDone, kRestReady, kUpdateDone, kRestDone,  // the chain
+  kLargestReady, kDrained, kBarriers
+};
+
 // kPT: columns of the state (values of a head) that a block has; kGroups: warpgroups that share them;
 // kStages: buffers of rows and of [T; P T].
 template <typename T, int N, int kPT, int kGroups, int kStages>
@@ -526,15 +544,12 @@ struct Walk {
   static constexpr uint32_t kRows = 0, kTile = kRows + kStages * rows_bytes(N, kP), kS = kTile + kStages * tile_bytes(N, kP);
   static constexpr uint32_t kR = kS + kSlabs * kSlabS;
   static constexpr uint32_t kEnd = kR + kSlabs * kSlab;
-  static constexpr uint32_t kLargest = kEnd + 18 * 8 + 4 * 4, kF = kLargest + 4 * kWorkers * 4;
+  static constexpr uint32_t kLargest = kEnd + (kBarriers * 8 + 2 * 4 + 15) / 16 * 16, kF = kLargest + 4 * kWorkers * 4;
   static constexpr uint32_t kX = kF + 2 * kFactorBytes;            // x, a token's row after the other
   static constexpr uint32_t kXRow = kPT * sizeof(T) + 16;          // (so that eight rows lie in different banks)
   static constexpr uint32_t kTotal = kX + 2 * kC * kXRow;
   static constexpr uint32_t kTmem = 4 * kPT;               // columns of tensor memory
 };
-
-enum { kRowsFull, kRowsFull1, kRowsEmpty, kRowsEmpty1, kSideFull, kSideFull1, kSideEmpty, kSideEmpty1, kTileFull, kTileFull1, kTileEmpty, kTileEmpty1, kStateReady, kLargestReady, kFromStateDone,
-       kRestReady, kUpdateDone, kRestDone, kDrained, kBarriers };
 
 // cp.async.bulk: bytes from global to shared memory, counted by the barrier.
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -668,11 +683,10 @@ __global__ void __launch_bounds__(Walk<T, N, kPT, kGroups, kStages>::kThreads, k
       }
       ++t;
     }
-    if (!ok) {  // nothing is in flight when the block ends
-      for (int i = sides > 2 ? sides - 2 : 0; i < sides; ++i) mbar_wait(&bars[kSideFull + (i & 1)], (i >> 1) & 1, s.limit_ns);
-      for (int i = c > kStages ? c - kStages : 0; i < c; ++i) mbar_wait(&bars[kRowsFull + i % kStages], (i / kStages) & 1, s.limit_ns);
-      for (int i = t > kStages ? t - kStages : 0; i < t; ++i) mbar_wait(&bars[kTileFull + i % kStages], (i / kStages) & 1, s.limit_ns);
-    }
+    // nothing is in flight when the block ends, whoever has given up
+    for (int i = sides > 2 ? sides - 2 : 0; i < sides; ++i) mbar_wait(&bars[kSideFull + (i & 1)], (i >> 1) & 1, s.limit_ns);
+    for (int i = c > kStages ? c - kStages : 0; i < c; ++i) mbar_wait(&bars[kRowsFull + i % kStages], (i / kStages) & 1, s.limit_ns);
+    for (int i = t > kStages ? t - kStages : 0; i < t; ++i) mbar_wait(&bars[kTileFull + i % kStages], (i / kStages) & 1, s.limit_ns);
   } else if (warp == kWorkers + 1) {
     // products: the warp stays together and one thread issues (see elect_one)
     constexpr uint32_t id_two = idesc_f32acc(0, 128, 2 * kPT, 0, 1), id_one = idesc_f32acc(0, 128, kPT, 0, 1);
@@ -986,8 +1000,10 @@ cudaError_t launch_chunks(const DeltaParams& p, const DeltaChunks& s, cudaStream
   if (e != cudaSuccess) return e;
   // Columns of a block: as few as leave every block a multiprocessor of its own (the chain is the shorter, and what is
   // loaded for it the same), 32 where there are more, two blocks on each.  16 heads of 128 x 128, 16384 tokens:
-  // 16 columns 379 us, 32 482; 128 heads, 4096 tokens: 32 columns 479 and, two blocks each, 360, 16 491.
+  // 16 columns 379 us, 32 482; 128 heads, 4096 tokens: 32 columns 479 and, two blocks each, 360, 16 491 (all of an
+  // earlier form; now 300 and 321 for the first and the last choice).
   const int64_t heads = p.batch * p.H, sms = layer_sm_count();
+  // (64 columns, one block an SM: the walk of the last 385 us, when 32 had 355.)
   // 32-bit rows take twice the shared memory: one buffer, and one block on each.
   if constexpr (sizeof(T) == 4)
     return heads * ceil_div(p.P, 16) <= sms ? launch_walk<T, N, 16, 2, 1, 1>(p, s, stream) : launch_walk<T, N, 32, 2, 1, 1>(p, s, stream);
