@@ -518,10 +518,10 @@ typedef struct {
   size_t workspace_bytes;
 } ssd_delta_args;
 
-/* Bytes of workspace on the current device: for bf16 prompts (0 otherwise, or
- * where the sizes are refused); the sizes and dtype are read, no tensor.  A
- * wait in these prompts' kernels that runs out (see above) leaves NaN in the
- * outputs of its head. */
+/* Bytes of workspace on the current device: for calls that run in chunks (0
+ * otherwise, or where the sizes are refused); the sizes and dtype are read, no
+ * tensor.  A wait in these calls' kernels that runs out (see above) leaves NaN
+ * in the outputs of its head. */
 size_t ssd_delta_workspace_size(const ssd_delta_args* args);
 ssd_status ssd_delta_fwd(const ssd_delta_args* args, ssd_stream_t stream);
 

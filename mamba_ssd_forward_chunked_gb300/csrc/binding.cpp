@@ -593,14 +593,14 @@ PyObject* select_workspace(PyObject* const* p) {
   return PyLong_FromSize_t(ssd_beam_select_workspace_size(&a));
 }
 
-// batch, seqlen, nheads, headdim, dstate, bf16
+// batch, seqlen, nheads, headdim, ngroups, dstate, bf16
 PyObject* delta_workspace(PyObject* const* p) {
   ssd_delta_args a{};
   a.size = sizeof(a);
   a.batch = whole(p[0], "batch"), a.seqlen = whole(p[1], "seqlen"), a.nslots = a.batch;
   a.nheads = small(whole(p[2], "nheads"), "nheads"), a.headdim = small(whole(p[3], "headdim"), "headdim");
-  a.ngroups = 1, a.dstate = small(whole(p[4], "dstate"), "dstate");
-  a.dtype = a.gate_dtype = truth(p[5]) ? SSD_BF16 : SSD_F32;
+  a.ngroups = small(whole(p[4], "ngroups"), "ngroups"), a.dstate = small(whole(p[5], "dstate"), "dstate");
+  a.dtype = a.gate_dtype = truth(p[6]) ? SSD_BF16 : SSD_F32;
   return PyLong_FromSize_t(ssd_delta_workspace_size(&a));
 }
 
@@ -661,7 +661,7 @@ PyMODINIT_FUNC PyInit__layer_binding() {
       method<draft_verify, 7>("draft_verify"),
       method<scan_workspace, 5>("scan_workspace"),
       method<select_workspace, 4>("select_workspace"),
-      method<delta_workspace, 6>("delta_workspace"),
+      method<delta_workspace, 7>("delta_workspace"),
       method<verify_workspace, 5>("verify_workspace"),
       {nullptr, nullptr, 0, nullptr},
   };

@@ -232,7 +232,6 @@ extern "C" size_t ssd_delta_workspace_size(const ssd_delta_args* a) {
   return delta_chunks_workspace(params_of(a));
 }
 
-
 extern "C" ssd_status ssd_delta_fwd(const ssd_delta_args* a, ssd_stream_t stream) {
   using namespace ssd;
   const ssd_status st = check_delta(a);

@@ -1,4 +1,4 @@
-// The chunked form of the gated delta rule (delta_chunk.cu), for whole bf16 prompts.
+// The chunked form of the gated delta rule (delta_chunk.cu), for whole prompts.
 #pragma once
 #include "delta.cuh"
 

@@ -140,10 +140,11 @@ def ssd_step(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, D: torch.Tensor
 
 # ------------------------------------------------------------------ delta rule
 
-def ssd_delta_workspace_size(batch: int, seqlen: int, nheads: int, headdim: int, dstate: int, dtype: torch.dtype) -> int:
+def ssd_delta_workspace_size(batch: int, seqlen: int, nheads: int, headdim: int, dstate: int, dtype: torch.dtype,
+                             ngroups: int = 1) -> int:
     """Bytes of workspace ssd_delta_fwd needs for these sizes on the current
     device (0: none)."""
-    return _binding.delta_workspace(batch, seqlen, nheads, headdim, dstate, dtype == torch.bfloat16)
+    return _binding.delta_workspace(batch, seqlen, nheads, headdim, ngroups, dstate, dtype == torch.bfloat16)
 
 
 def ssd_delta_fwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, Bm: torch.Tensor, Cm: torch.Tensor,

@@ -161,6 +161,22 @@ def test_given_workspaces(ssd):
         ssd.ssd_draft_verify(*v, workspace=torch.empty(n - 1, dtype=torch.uint8, device="cuda"))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("L,H,G,N", [(100, 4, 4, 64), (70, 6, 2, 128), (16000, 8, 2, 64), (33, 3, 3, 128)])
+def test_workspaces_of_several_groups(ssd, dtype, L, H, G, N):
+    """What the function says is enough for the groups it was told of, and not more than that."""
+    a, o = inputs(1, L, H, G, 16, N, dtype)
+    A, O = to(a), to(o)
+    n = ssd.ssd_delta_workspace_size(1, L, H, 16, N, dtype, G)
+    want = ssd.ssd_delta_fwd(**A, **O)
+    space = torch.empty(n + 64, dtype=torch.uint8, device="cuda").fill_(0xA5)
+    got = ssd.ssd_delta_fwd(**A, **O, workspace=space[:n])
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert bool((space[n:] == 0xA5).all())
+    with pytest.raises(ssd.SSDError):
+        ssd.ssd_delta_fwd(**A, **O, workspace=space[:n - 16])
+
+
 def test_arguments_are_refused(ssd):
     a, o = inputs(2, 3, 4, 2, 64, 64, torch.bfloat16, cached=True)
     A, O = to(a), to(o)
