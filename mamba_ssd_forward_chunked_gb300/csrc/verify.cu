@@ -40,7 +40,7 @@ constexpr int kMaxDrafts = 64;
 constexpr int kMaxCluster = 8;
 constexpr int kDrawThreads = 512;
 constexpr int kDrawWarps = kDrawThreads / 32;
-constexpr int kMaxVocab = 1 << 19;  // sums of weights stay below 2^63
+constexpr int kMaxVocab = 1 << 19;  // sums of weights are 2^63 at most, that of as many equal logits
 constexpr float kLog2eLow = 1.925963e-8f;  // log2(e) - kLog2e
 
 struct VerifyParams {
@@ -296,7 +296,7 @@ __device__ __forceinline__ uint64_t warp_scan(uint64_t v, int lane) {
 }
 
 // A probability in units of 2^-61: weights over the sum of all (Z), multiplied by 2^125 / (Z 2^shift),
-// where Z 2^shift is at least 2^62.
+// where Z 2^shift is at least 2^62 and at most 2^63.
 struct Share {
   uint64_t inv;
   int shift;
@@ -305,7 +305,7 @@ struct Share {
 __device__ __forceinline__ Share share_of(uint64_t all) {
   Share s{0, 0};
   if (all == 0) return s;
-  s.shift = __clzll(static_cast<long long>(all)) - 1;  // (the sum is below 2^63)
+  s.shift = max(__clzll(static_cast<long long>(all)) - 1, 0);
   s.inv = static_cast<uint64_t>(0x1p125 / static_cast<double>(all << s.shift));
   return s;
 }
@@ -533,6 +533,9 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(VerifyPara
     }
     const Share share = share_of(lane == 0 ? sum[kAllP] : sum[kAllQ]);
     if (lane < 2) s_share[lane] = share;
+    // (the maximum alone weighs 2^44, so the sum is above 0 and one lane finds its run below; the search stays in
+    // bounds without that)
+    if (lane == 0) s_which = 0, s_below = 0, s_plain = true;
     __syncwarp();
     const Share share_p = s_share[0], share_q = s_share[1];
     // p itself where (next to) nothing is left of p - q: 2^-49, which the runs' roundings cannot use up

@@ -1,0 +1,32 @@
+"""The verification of drafted tokens at the ends of its ranges, against the same
+loop in 64 bits as in test_gpu_verify (its docstring has the tolerances)."""
+import pytest
+import torch
+
+from test_gpu_verify import run, ssd  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [2 ** 19, 2 ** 19 - 1])
+def test_largest_vocabulary_of_equal_logits(ssd, V, dtype):  # noqa: F811
+    """The sum of all weights is the largest there is (2^63 of their units for 2^19 equal logits).  The random
+    numbers are odd multiples of 2^-24 (a token has 32 of 2^19), so that none falls on a token's border."""
+    flat = torch.full((1, 1, V), 1.5, dtype=dtype)
+    u = torch.tensor([0.0, 1 - 2.0 ** -24, 2.0 ** -24, 0.5 + 2.0 ** -24, 0.3 * 2 ** 24 // 2 * 2.0 ** -23 + 2.0 ** -24])
+    got = run(ssd, dict(logits=flat.expand(5, 1, V), draft=torch.zeros(5, 0, dtype=torch.int32), uniforms=u[:, None]))
+    assert got[0].flatten().tolist() == [int(v * V) for v in u.double()]
+    # a draft's row of equal logits too: accepted, or outside the vocabulary, with nothing left of p - q
+    draft = torch.tensor([[V - 1], [-1], [7]], dtype=torch.int32)
+    uniforms = torch.stack([torch.tensor([0.75, 0.25, 0.0]), u[2:]], 1)
+    got = run(ssd, dict(logits=flat.expand(3, 2, V), draft=draft, draft_logits=flat.expand(3, 1, V), uniforms=uniforms))
+    assert got[1].tolist() == [1, 0, 1]
+    # the draft's row flat, the target's not, and the other way round
+    g = torch.Generator().manual_seed(V)
+    steep = (torch.randn(1, 1, V, generator=g) * 2).to(dtype)
+    draft[:, 0] = torch.tensor([int((steep < 0)[0, 0].long().argmax()), 5, 11])  # an unlikely one
+    uniforms[:, 0] = 1 - 2.0 ** -24
+    run(ssd, dict(logits=steep.expand(3, 2, V), draft=draft, draft_logits=flat.expand(3, 1, V), uniforms=uniforms))
+    run(ssd, dict(logits=flat.expand(3, 2, V), draft=draft, draft_logits=steep.expand(3, 1, V), uniforms=uniforms))
+    run(ssd, dict(logits=flat.expand(3, 2, V), draft=draft, uniforms=uniforms))
