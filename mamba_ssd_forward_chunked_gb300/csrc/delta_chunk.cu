@@ -249,7 +249,8 @@ __global__ void __launch_bounds__(kPrepThreads, kParts<T> == 1 ? 4 : 2) delta_pr
   if (tid < 2 * kC) {
     const float2 v = s_squares[tid];
     const float norm = delta_norm(p, v.x);
-    (tid < kC ? s_kn : s_qn)[tid & 63] = norm * v.y;  // undoes the power of two and normalises
+    // undoes the power of two and normalises; a row of zeros has factor 0 whatever norm it is given
+    (tid < kC ? s_kn : s_qn)[tid & 63] = v.y > 0x1p-126f ? norm * v.y : 0.f;
     if (tid < kC) s_len[tid] = norm * sqrtf(v.x);
   }
 
@@ -324,7 +325,8 @@ __global__ void __launch_bounds__(kPrepThreads, kParts<T> == 1 ? 4 : 2) delta_pr
       v[e] = i < n ? s_kn[i] * exp2f((s_hi[kC - 1] - s_hi[i]) + (s_lo[kC - 1] - s_lo[i])) : 0.f;
     }
     const float most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(v[0], v[1]))));
-    const float f = most > 0.f ? kTScale / most : 0.f;
+    // (keys of zeros, or keys that the chunk's end has forgotten to 2^-120: nothing is written into the state)
+    const float f = most > 0x1p-120f ? kTScale / most : 0.f;
     s_to[lane] = v[0] * f, s_to[lane + 32] = v[1] * f;
     reach = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(reach)));
     if (lane == 0) *s_most = most, *s_reach = reach;
