@@ -321,7 +321,8 @@ __global__ void __launch_bounds__(kPrepThreads, kParts<T> == 1 ? 4 : 2) delta_pr
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int i = lane + 32 * e;
-      reach = fmaxf(reach, fabsf(s_beta[i]) * exp2f(s_hi[i] + s_lo[i]) * s_len[i]);
+      const float own = fabsf(s_beta[i]) * exp2f(s_hi[i] + s_lo[i]) * s_len[i];
+      reach = fmaxf(reach, own < INFINITY ? own : 0.f);
       v[e] = i < n ? s_kn[i] * exp2f((s_hi[kC - 1] - s_hi[i]) + (s_lo[kC - 1] - s_lo[i])) : 0.f;
     }
     const float most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(v[0], v[1]))));
@@ -793,10 +794,16 @@ __global__ void __launch_bounds__(Walk<T, N, kPT, kGroups, kStages>::kThreads, k
       if (lane == 0) mbar_arrive(&bars[bar]);
     };
     auto all_wait = [&](int bar, int phase) { return __all_sync(0xffffffffu, wait(bar, phase)) != 0; };
-    // Largest magnitudes that the warps have left, [state, beta x][chunk mod 2][warp].
-    auto leave = [&](int which, int c, float v, int place) {
-      const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(v));
-      if (lane == 0) s_largest[(2 * which + (c & 1)) * kWorkers + place] = bits;
+    // Largest finite magnitudes that the warps have left, [state, beta x][chunk mod 2][warp].  Columns are independent of
+    // each other, so an infinity, which is NaN in its parts whatever the scale, must not set that of its neighbours:
+    // twice the bits plus 2^24 wraps around to less than 2^24, that of 0, for infinities and NaN.
+    auto leave = [&](int which, int c, const float (&v)[kCols], int place) {
+      constexpr uint32_t kZero = 0x01000000u;
+      uint32_t top = kZero;
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) top = max(top, 2 * __float_as_uint(v[i]) + kZero);
+      top = __reduce_max_sync(0xffffffffu, top);
+      if (lane == 0) s_largest[(2 * which + (c & 1)) * kWorkers + place] = (top - kZero) >> 1;
     };
     auto largest_of = [&](int which, int c, int warps) {
       const uint4* at = reinterpret_cast<const uint4*>(s_largest + (2 * which + (c & 1)) * kWorkers);
@@ -808,12 +815,6 @@ __global__ void __launch_bounds__(Walk<T, N, kPT, kGroups, kStages>::kThreads, k
         top = max(max(top, max(v.x, v.y)), max(v.z, v.w));
       }
       return __uint_as_float(top);
-    };
-    auto magnitude = [&](const float (&v)[kCols]) {
-      float top = 0.f;
-#pragma unroll
-      for (int i = 0; i < kCols; ++i) top = fmaxf(top, fabsf(v[i]));
-      return top;
     };
 
     float S[kCols];
@@ -827,7 +828,8 @@ __global__ void __launch_bounds__(Walk<T, N, kPT, kGroups, kStages>::kThreads, k
     // Scales go by bounds that are known while the products run, not by what comes out of them, so that nobody
     // waits for the others in the chain: with s the largest of the state
     //     |r| <= max |beta x| + s max_j beta e^{G_j} |k_j|_1,    |state after| <= e^{G_64} s + 64 max |W| max |r|.
-    // They can be a thousand times too large (the sums' signs); two parts have 2^17 to spare.
+    // They can be a thousand times too large (the sums' signs); two parts have 2^17 to spare.  One past 32 bits is
+    // infinite, which scale_for takes for 2^128.
     Scale state{1.f, 1.f};
     bool ok = true;
     float bx[kCols], fa, fb;  // beta x of tokens, and then the state's part of y of the others; the row's factors
@@ -861,19 +863,19 @@ __global__ void __launch_bounds__(Walk<T, N, kPT, kGroups, kStages>::kThreads, k
               bx[4 * i + e] = fa * __uint_as_float(w);
           }
         }
-        leave(1, c, magnitude(bx), 2 * group + quarter);
+        leave(1, c, bx, 2 * group + quarter);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[kSideEmpty + (c & 1)]);
       return true;
     };
     auto leave_state = [&](int c) {
-      leave(0, c, magnitude(S), warp);
+      leave(0, c, S, warp);
       if (lane == 0) mbar_arrive(&bars[kLargestReady]);
     };
     if (chunks > 0) {
       ok = ahead(0);
-      leave(0, 1, magnitude(S), warp);
+      leave(0, 1, S, warp);
       named_bar_sync(1, 32 * kWorkers);
       state = scale_for(__float_as_uint(largest_of(0, 1, kWorkers)));
       if (has_state) put(M::kS, M::kSlabS, row, S, state.up);

@@ -3,7 +3,9 @@ recurrence in 64 bits (bounds: delta_ref)."""
 import pytest
 import torch
 
-from test_gpu_delta import inputs, run, ssd  # noqa: F401
+import delta_ref as ref
+from layer_ref import check, store
+from test_gpu_delta import inputs, near, run, ssd, to  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -34,3 +36,50 @@ def test_keys_of_zeros(ssd, L, N, eps, dtype):  # noqa: F811
     y, final = run(ssd, a, {**o, "norm_eps": eps})
     o["lengths"] = torch.tensor([L - 1, 33], dtype=torch.int32)
     run(ssd, a, {**o, "norm_eps": eps})
+
+
+def bounds(a, o):
+    return ref.delta(**a, **o, spread=65.0, pt=2.0 ** (-12 if a["x"].dtype == torch.bfloat16 else -22))
+
+
+@BOTH
+@pytest.mark.parametrize("value", [float("inf"), -float("inf"), float("nan")])
+@pytest.mark.parametrize("H,P,N", [(2, 48, 128), (2, 32, 64), (80, 32, 64), (160, 16, 128)])  # every form of the walk
+def test_values_that_are_not_finite_stay_in_their_channel(ssd, H, P, N, value, dtype):  # noqa: F811
+    """One in x, in the second of four chunks, and one in a row of a state: the other channels are those of the
+    recurrence without it, its own is not finite from there on and as it was before."""
+    a, o = inputs(1, 200, H, H, P, N, dtype, seed=P)
+    o["init_state"] = torch.randn(1, H, P, N, generator=torch.Generator().manual_seed(P)) * 0.3
+    ry, by, rf, bf = bounds(a, o)
+    by = store(ry, by, dtype)
+    for where in ("x", "init_state"):
+        bad = dict(a, **o)
+        bad[where] = bad[where].clone()
+        first = 64 if where == "x" else 0
+        if where == "x":
+            bad["x"][0, 100, 1, 5] = value
+        else:
+            bad["init_state"][0, 1, 5, 9] = value
+        y, final = (v.cpu() for v in ssd.ssd_delta_fwd(**to(bad)))
+        others = torch.ones(H, P, dtype=torch.bool)
+        others[1, 5] = False
+        check(where + ": y", y[:, :, others], ry[:, :, others], by[:, :, others])
+        check(where + ": final", final[:, others], rf[:, others], bf[:, others])
+        check(where + ": y before", y[:, :first, 1, 5], ry[:, :first, 1, 5], by[:, :first, 1, 5])
+        assert not torch.isfinite(y[0, max(first, 101):, 1, 5]).any() and not torch.isfinite(final[0, 1, 5]).any()
+
+
+@BOTH
+@pytest.mark.parametrize("H,P,N", [(2, 48, 128), (80, 32, 64), (160, 16, 128)])
+def test_bounds_past_32_bits(ssd, H, P, N, dtype):  # noqa: F811
+    """Values so large that 64 times them is no number: a channel of them keeps its digits, and so does a state."""
+    a, o = inputs(1, 200, H, H, P, N, dtype, seed=P)
+    a["x"][0, :, 1, 5] = a["x"][0, :, 1, 5] * 2.0 ** 123
+    o["init_state"] = torch.randn(1, H, P, N, generator=torch.Generator().manual_seed(P))
+    o["init_state"][0, 0, 3] *= 2.0 ** 124
+    y, final = ssd.ssd_delta_fwd(**to(a), **to(o))
+    ry, _, rf, _ = ref.delta(**a, **o)
+    for h, p in ((1, 5), (0, 3)):
+        near("final", final[0, h, p], rf[0, h, p], 2.0 ** -19)
+        near("y", y[0, :, h, p], ry[0, :, h, p], 2.0 ** -19 if dtype == torch.float32 else 2.0 ** -8)
+    assert torch.isfinite(y).all() and torch.isfinite(final).all()
