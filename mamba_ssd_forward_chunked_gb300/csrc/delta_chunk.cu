@@ -547,7 +547,8 @@ struct Walk {
   static constexpr uint32_t kRows = 0, kTile = kRows + kStages * rows_bytes(N, kP), kS = kTile + kStages * tile_bytes(N, kP);
   static constexpr uint32_t kR = kS + kSlabs * kSlabS;
   static constexpr uint32_t kEnd = kR + kSlabs * kSlab;
-  static constexpr uint32_t kLargest = kEnd + (kBarriers * 8 + 2 * 4 + 15) / 16 * 16, kF = kLargest + 4 * kWorkers * 4;
+  static constexpr uint32_t kLargest = kEnd + (kBarriers * 8 + 2 * 4 + 15) / 16 * 16, kSeen = kLargest + 4 * kWorkers * 4;
+  static constexpr uint32_t kF = kSeen + kWorkers * 4;
   static constexpr uint32_t kX = kF + 2 * kFactorBytes;            // x, a token's row after the other
   static constexpr uint32_t kXRow = kPT * sizeof(T) + 16;          // (so that eight rows lie in different banks)
   static constexpr uint32_t kTotal = kX + 2 * kC * kXRow;
@@ -865,8 +866,15 @@ __global__ void __launch_bounds__(Walk<T, N, kPT, kGroups, kStages>::kThreads, k
         }
         leave(1, c, bx, 2 * group + quarter);
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[kSideEmpty + (c & 1)]);
+      // The loads have to be over before the buffer is given back, and a load that is only under way does not hold up an
+      // arrival (it may wait for hundreds of cycles while copies fill the shared memory): what all lanes have read goes
+      // into a word that nobody wants, whose store lies before the arrival.
+      const uint32_t seen = __reduce_or_sync(0xffffffffu, __float_as_uint(fa) | __float_as_uint(fb) | __float_as_uint(scalars.x) |
+                                                              __float_as_uint(scalars.y) | __float_as_uint(scalars.z) | __float_as_uint(scalars.w));
+      if (lane == 0) {
+        asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(smem_u32(smem + M::kSeen + 4 * warp)), "r"(seen) : "memory");
+        mbar_arrive(&bars[kSideEmpty + (c & 1)]);
+      }
       return true;
     };
     auto leave_state = [&](int c) {

@@ -83,3 +83,16 @@ def test_bounds_past_32_bits(ssd, H, P, N, dtype):  # noqa: F811
         near("final", final[0, h, p], rf[0, h, p], 2.0 ** -19)
         near("y", y[0, :, h, p], ry[0, :, h, p], 2.0 ** -19 if dtype == torch.float32 else 2.0 ** -8)
     assert torch.isfinite(y).all() and torch.isfinite(final).all()
+
+
+@pytest.mark.parametrize("B,L,H,G,P,N", [(1, 25000, 16, 16, 64, 64), (4, 4096, 32, 16, 128, 128)])
+def test_repeated_calls_give_the_same(ssd, B, L, H, G, P, N):  # noqa: F811
+    """Factors that a warp had not read yet were replaced by those of two chunks later, in one call of some 400."""
+    a, o = inputs(B, L, H, G, P, N, torch.bfloat16, seed=1)
+    A, O = to(a), to(o)
+    y, final = ssd.ssd_delta_fwd(**A, **O)
+    other = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(2500):
+        y2, final2 = ssd.ssd_delta_fwd(**A, **O)
+        other += (y2 != y).any().long() + (final2 != final).any().long()
+    assert int(other) == 0 and torch.isfinite(y.float()).all() and torch.isfinite(final).all()
