@@ -51,8 +51,6 @@ __host__ __device__ constexpr uint32_t tile_bytes(int N, int parts) { return (2 
 __host__ __device__ constexpr uint32_t record_bytes(int N, int parts) { return tile_bytes(N, parts) + kFactors * kC * 4; }
 __host__ __device__ constexpr uint32_t rows_bytes(int N, int parts) { return N / 64 * 2 * kSlab * parts; }
 
-constexpr float kTScale = 16.f;  // of T and P T: T's diagonal is 1, so second parts' last places are 2^-29 of that
-
 // The power of two that brings numbers up to `largest` (its bits) below 2^15, and its inverse.
 struct Scale {
   float up, down;
@@ -127,7 +125,7 @@ struct PrepSmem {
   static constexpr uint32_t kA = kC * kRow, kSize = kRow > kStride * 4 ? kRow : kStride * 4, kT = kA + kC * kSize;
   static constexpr uint32_t kLow = kT + kC * kStride * 4;
   static constexpr uint32_t kVec = kLow + (kParts<T> == 2 ? 2 * kC * kRow : 0);
-  static constexpr uint32_t kTotal = kVec + 7 * kC * 4 + 64;
+  static constexpr uint32_t kTotal = kVec + 9 * kC * 4 + 64;
 };
 
 template <typename T, int N>
@@ -138,8 +136,9 @@ __global__ void __launch_bounds__(kPrepThreads, kParts<T> == 1 ? 4 : 2) delta_pr
   float* s_A = reinterpret_cast<float*>(smem + M::kA);
   float* s_T = reinterpret_cast<float*>(smem + M::kT);
   float* s_hi = reinterpret_cast<float*>(smem + M::kVec);
-  float *s_lo = s_hi + kC, *s_beta = s_lo + kC, *s_kn = s_beta + kC, *s_qn = s_kn + kC, *s_to = s_qn + kC, *s_len = s_to + kC;
-  int64_t* s_half = reinterpret_cast<int64_t*>(s_len + kC);
+  float *s_lo = s_hi + kC, *s_beta = s_lo + kC, *s_kn = s_beta + kC, *s_qn = s_kn + kC, *s_to = s_qn + kC, *s_len = s_to + kC,
+        *s_bx = s_len + kC, *s_down = s_bx + kC;
+  int64_t* s_half = reinterpret_cast<int64_t*>(s_down + kC);
   uint32_t* s_largest = reinterpret_cast<uint32_t*>(s_half + 1);  // of every warp
   float *s_most = reinterpret_cast<float*>(s_largest + 8), *s_reach = s_most + 1;
   float2* s_squares = reinterpret_cast<float2*>(smem + M::kT);  // of a row, and what undoes its scale (T comes later)
@@ -246,14 +245,6 @@ __global__ void __launch_bounds__(kPrepThreads, kParts<T> == 1 ? 4 : 2) delta_pr
     if (col == 0) s_squares[r] = make_float2(squares, scale.down);
   }
   __syncthreads();
-  if (tid < 2 * kC) {
-    const float2 v = s_squares[tid];
-    const float norm = delta_norm(p, v.x);
-    // undoes the power of two and normalises; a row of zeros has factor 0 whatever norm it is given
-    (tid < kC ? s_kn : s_qn)[tid & 63] = v.y > 0x1p-126f ? norm * v.y : 0.f;
-    if (tid < kC) s_len[tid] = norm * sqrtf(v.x);
-  }
-
   // K K^T (four warps, 16 rows each) and Q K^T (four more)
   const int mt = is_q ? 7 - warp : warp;  // (beside a warp of few columns one of many)
   const uint32_t rows = smem_u32(smem);
@@ -284,6 +275,40 @@ __global__ void __launch_bounds__(kPrepThreads, kParts<T> == 1 ? 4 : 2) delta_pr
         mma_f16(acc[2 * j], a, v[0], v[1]);
         mma_f16(acc[2 * j + 1], a, v[2], v[3]);
       }
+    }
+  }
+  // What makes of a row, times its power of two, the row that counts: of K by the first two warps, of Q by the last, who
+  // had the fewest columns.
+  if (tid < kC || tid >= 3 * kC) {
+    const int at = tid < kC ? tid : tid - 2 * kC, token = tid & 63;
+    const float2 v = s_squares[at];
+    const float up = __int_as_float(0x7F000000 - __float_as_int(v.y));
+    float norm = v.y, squares = v.x * up * up;  // (of the row times its power of two: below 2^38)
+    if (!(v.x > 0x1p-80f && v.x < 0x1p120f) && token < n) {  // squares that 32 bits may not have held
+      squares = 0.f;
+#pragma unroll 1
+      for (int i = 0; i < N; ++i) {
+        const __half* from = reinterpret_cast<const __half*>(smem + at * M::kRow);
+        float e = __half2float(from[i]);
+        if (kP == 2) e += __half2float(from[M::kLow / 2 + i]);
+        squares = fmaf(e, e, squares);
+      }
+    }
+    if (p.norm_eps >= 0.f) {
+      const float e = p.norm_eps * up * up;
+      norm = e < 0x1p80f ? rsqrtf(squares + e) : v.y * rsqrtf(p.norm_eps);
+    }
+    if (squares == 0.f || token >= n) norm = 0.f;
+    if (tid >= kC) {
+      s_qn[token] = norm;
+    } else {
+      // A key times 2^-e, x times 2^-e and beta times 2^2e are the same rule: with lengths between 0.7 and 1.4 the keys'
+      // own sizes set none of the scales below, whether they are normalised or as they are.
+      const float length = norm * sqrtf(squares);
+      const int e = min(max((__float_as_int(length * 1.41421356f) >> 23 & 0xFF) - 127, -126), 126);
+      const float longer = __int_as_float((127 + e) << 23), shorter = __int_as_float((127 - e) << 23);
+      const float bx = s_beta[token] * longer;
+      s_kn[token] = norm * shorter, s_len[token] = length * shorter, s_bx[token] = bx, s_beta[token] = bx * longer;
     }
   }
   __syncthreads();  // Q's rows have been read
@@ -327,7 +352,7 @@ __global__ void __launch_bounds__(kPrepThreads, kParts<T> == 1 ? 4 : 2) delta_pr
     }
     const float most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(v[0], v[1]))));
     // (keys of zeros, or keys that the chunk's end has forgotten to 2^-120: nothing is written into the state)
-    const float f = most > 0x1p-120f ? kTScale / most : 0.f;
+    const float f = most > 0x1p-120f ? 1.f / most : 0.f;
     s_to[lane] = v[0] * f, s_to[lane + 32] = v[1] * f;
     reach = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(reach)));
     if (lane == 0) *s_most = most, *s_reach = reach;
@@ -419,7 +444,21 @@ __global__ void __launch_bounds__(kPrepThreads, kParts<T> == 1 ? 4 : 2) delta_pr
 #pragma unroll
       for (int j = 0; j <= k; ++j) mma_tf32_parts(o[j], a, t[8 * k * kStride + 8 * j], t[(8 * k + 1) * kStride + 8 * j]);
     }
-    // as the second launch reads it, where A was; blocks above the diagonal are 0
+    // as the second launch reads it, where A was; blocks above the diagonal are 0.  A row has a power of two of its own,
+    // which its factor undoes: rows behind strong decays keep their digits.
+    float top = 0.f, top8 = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      top = fmaxf(fmaxf(top, fabsf(o[j][0])), fabsf(o[j][1]));
+      top8 = fmaxf(fmaxf(top8, fabsf(o[j][2])), fabsf(o[j][3]));
+    }
+#pragma unroll
+    for (int e = 1; e < 4; e *= 2) {
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, e));
+      top8 = fmaxf(top8, __shfl_xor_sync(0xffffffffu, top8, e));
+    }
+    const Scale of = scale_for(__float_as_uint(top)), of8 = scale_for(__float_as_uint(top8));
+    if ((lane & 3) == 0) s_down[16 * mt + (lane >> 2)] = of.down, s_down[16 * mt + (lane >> 2) + 8] = of8.down;
     const int at_row = 16 * mt + (lane >> 3 & 1) * 8 + (lane & 7);
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
@@ -427,11 +466,12 @@ __global__ void __launch_bounds__(kPrepThreads, kParts<T> == 1 ? 4 : 2) delta_pr
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float* from_o = &o[j + (e >> 1)][e & 1 ? 2 : 0];
+        const float up = e & 1 ? of8.up : of.up;
         if constexpr (kP == 1) {
-          const __half2 pair = __floats2half2_rn(from_o[0] * kTScale, from_o[1] * kTScale);
+          const __half2 pair = __floats2half2_rn(from_o[0] * up, from_o[1] * up);
           v[e] = *reinterpret_cast<const uint32_t*>(&pair);
         } else {
-          split(from_o[0] * kTScale, from_o[1] * kTScale, v[e], l[e]);
+          split(from_o[0] * up, from_o[1] * up, v[e], l[e]);
         }
       }
       const uint32_t to = rows + at_row * 128 + (((j + (lane >> 4)) ^ (at_row & 7)) << 4);
@@ -440,10 +480,11 @@ __global__ void __launch_bounds__(kPrepThreads, kParts<T> == 1 ? 4 : 2) delta_pr
     }
   }
 
-  // W = K^T T', T's rows times their factors in two fp16 parts (K is one): 8 columns a warp
+  // W = K^T T', T's rows times their factors in two fp16 parts (K is one): 8 columns a warp, with a power of two
   constexpr int kTiles = N / 16;
   float w[kTiles][4];
   uint32_t bh[4][2], bl[4][2];
+  float factored[4][2][2], top = 0.f;
 #pragma unroll
   for (int m = 0; m < kTiles; ++m)
 #pragma unroll
@@ -455,8 +496,16 @@ __global__ void __launch_bounds__(kPrepThreads, kParts<T> == 1 ? 4 : 2) delta_pr
     for (int e = 0; e < 2; ++e) {
       const int i = 16 * k + 8 * e + (lane & 3) * 2;
       const float* t = &s_T[i * kStride + 8 * warp + (lane >> 2)];
-      split(t[0] * s_to[i], t[kStride] * s_to[i + 1], bh[k][e], bl[k][e]);
+      factored[k][e][0] = t[0] * s_to[i], factored[k][e][1] = t[kStride] * s_to[i + 1];
+      top = fmaxf(fmaxf(top, fabsf(factored[k][e][0])), fabsf(factored[k][e][1]));
     }
+  }
+  const Scale own = scale_for(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (k < warp >> 1) continue;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) split(factored[k][e][0] * own.up, factored[k][e][1] * own.up, bh[k][e], bl[k][e]);
   }
   const uint32_t kt = rows + ((lane & 7) + (lane >> 4) * 8) * M::kRow + ((lane >> 3) & 1) * 16;
 #pragma unroll
@@ -475,11 +524,11 @@ __global__ void __launch_bounds__(kPrepThreads, kParts<T> == 1 ? 4 : 2) delta_pr
       mma_f16(w[m], a, bh[k][0], bh[k][1]);
     }
   }
-  float top = 0.f;
+  top = 0.f;
 #pragma unroll
   for (int m = 0; m < kTiles; ++m)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(w[m][e]));
+    for (int e = 0; e < 4; ++e) w[m][e] *= own.down, top = fmaxf(top, fabsf(w[m][e]));
   const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
   if (lane == 0) s_largest[warp] = bits;
   __syncthreads();
@@ -502,13 +551,13 @@ __global__ void __launch_bounds__(kPrepThreads, kParts<T> == 1 ? 4 : 2) delta_pr
   if (tid < kC) {
     float* factors = reinterpret_cast<float*>(out + tile_bytes(N, kP));
     const float since = exp2f(s_hi[tid] + s_lo[tid]), qn = p.scale * s_qn[tid];
-    factors[kBeta * kC + tid] = s_beta[tid];
+    factors[kBeta * kC + tid] = s_bx[tid];
     factors[kFromState * kC + tid] = s_beta[tid] * s_kn[tid] * since;
     factors[kOutState * kC + tid] = qn * since;
-    factors[kOutRest * kC + tid] = qn * (0x1p14f / kTScale);
+    factors[kOutRest * kC + tid] = qn * 0x1p14f * s_down[tid];
     if (tid == kC - 1) {
       float* scalars = factors + kScalars * kC;
-      scalars[kDecay] = since, scalars[kUpdate] = scale.down * *s_most / kTScale;
+      scalars[kDecay] = since, scalars[kUpdate] = scale.down * *s_most;
       scalars[kReach] = *s_reach * (N == 64 ? 8.f : 11.5f);  // (a row's sum of magnitudes is sqrt(N) of its length at most)
       scalars[kSpread] = kC * 32768.f * scalars[kUpdate];    // (W's largest is below 2^15 of its unit)
     }

@@ -96,3 +96,61 @@ def test_repeated_calls_give_the_same(ssd, B, L, H, G, P, N):  # noqa: F811
         y2, final2 = ssd.ssd_delta_fwd(**A, **O)
         other += (y2 != y).any().long() + (final2 != final).any().long()
     assert int(other) == 0 and torch.isfinite(y.float()).all() and torch.isfinite(final).all()
+
+@BOTH
+@pytest.mark.parametrize("eps", [None, 1e-6])
+def test_the_last_key_alone_and_forgotten_ones(ssd, eps, dtype):  # noqa: F811
+    """A chunk whose only token with a key is its first, forgotten by 2^-100 and more at its end."""
+    a, o = inputs(1, 128, 3, 1, 48, 128, dtype, seed=4)
+    short(a)
+    a["Bm"][0, 1:64] = 0
+    for gate in (1.0, 5.0, 50.0):  # times 63 tokens
+        a["dt"] = torch.full_like(a["dt"], gate)
+        a["A"] = torch.tensor([-0.5, -1.0, -3.0])
+        run(ssd, a, dict(beta_sigmoid=True, norm_eps=eps))
+
+
+@BOTH
+@pytest.mark.parametrize("L,N", [(90, 64), (90, 128), (200, 64), (200, 128)])
+def test_plain_arguments(ssd, L, N, dtype):  # noqa: F811
+    """No norms, no activations, a scale of its own, 32-bit gates beside bf16."""
+    a, o = inputs(2, L, 2, 2, 64, N, dtype, gates=torch.float32, seed=9)
+    a["Bm"], a["Cm"] = a["Bm"] * N ** -0.5, a["Cm"] * 0.5
+    a["dt"], a["beta"] = a["dt"].abs() * 0.1, torch.rand(2, L, 2, generator=torch.Generator().manual_seed(L)) * 2
+    run(ssd, a, dict(scale=-0.75))
+
+
+@BOTH
+@pytest.mark.parametrize("N", [64, 128])
+@pytest.mark.parametrize("length", [1e-17, 1e-7, 1e-3, 1.0, 30.0, 1000.0, 1e17, "mixed"])
+def test_keys_of_any_length(ssd, length, N, dtype):  # noqa: F811
+    """Keys as they are, beta |k|^2 between 0.3 and 1: the same digits whatever their length, also where every token
+    has another.  (Over all values as in test_prompts.)"""
+    g = torch.Generator().manual_seed(N)
+    a, _ = inputs(2, 150, 4, 2, 48, N, dtype, gates=torch.float32, seed=5)
+    size = torch.full((2, 150, 2, 1), length) if length != "mixed" else 10.0 ** (torch.rand(2, 150, 2, 1, generator=g) * 6 - 3)
+    a["Bm"] = (a["Bm"].float() / a["Bm"].float().norm(dim=-1, keepdim=True) * size).to(dtype)
+    a["Cm"] = (a["Cm"].float() * 10.0 ** (torch.rand(2, 150, 2, 1, generator=g) * 20 - 10)).to(dtype)
+    a["dt"] = a["dt"].abs() * 0.1
+    share = 0.3 + 0.7 * torch.rand(2, 150, 4, generator=g)
+    a["beta"] = (share.double() / size.double().square().repeat_interleave(2, 2)[..., 0]).float()
+    o = dict(init_state=torch.randn(2, 4, 48, N, generator=g) / size[:, :1, :1, :, None].mean())
+    y, final = run(ssd, a, o)
+    ry, _, rf, _ = ref.delta(**a, **o)
+    near("final", final, rf, 2.0 ** -19)
+    near("y", y, ry, 2.0 ** -19 if dtype == torch.float32 else 2.0 ** -8)
+
+
+@BOTH
+@pytest.mark.parametrize("L,N", [(100, 64), (180, 128)])
+def test_rules_that_grow(ssd, L, N, dtype):  # noqa: F811
+    """One key for all tokens and beta |k|^2 = 2.25: a value becomes -1.25 times itself a token, 10^6 times a chunk.
+    What a product loses grows as the values do, so it stays 2^-22 of them: 2^-17 for all of a state's chunks."""
+    a, o = inputs(1, L, 2, 1, 32, N, dtype, gates=torch.float32, seed=6)
+    a["Bm"] = torch.full((1, L, 1, N), (1.0 / N) ** 0.5 if N == 64 else 0.125 * 0.5).to(dtype)  # (exact; |k|^2 is 1, or 0.5)
+    a["dt"][:] = 0.0
+    a["beta"][:] = 2.25 if N == 64 else 4.5
+    y, final = run(ssd, a, {})
+    ry, _, rf, _ = ref.delta(**a)
+    near("final", final, rf, 2.0 ** -17)
+    near("y", y, ry, 2.0 ** -17 if dtype == torch.float32 else 2.0 ** -8)
