@@ -490,11 +490,12 @@ ssd_status ssd_beam_reorder(const ssd_beam_reorder_args* args, ssd_stream_t stre
  * whatever its row holds.  Rows of final_state that no sequence of the call has
  * stay as they are; outputs must not overlap the inputs otherwise.
  * Calls of 32 tokens or more with a dstate of 64 or 128 run in chunks of 64
- * tokens on the tensor cores, whose products keep 22 bits of every factor (8
- * more than y has in bf16): the state is off by 5e-7 of its norm.  There a value
- * of x or init_state that is not finite makes its own channel NaN, from the first
- * of its 64 tokens on, and no other; one of Bm, Cm, dt or beta may do so to all of
- * a head that reads it.  Fewer tokens, and a dstate of 256, go one by one. */
+ * tokens on the tensor cores.  Their products keep 22 bits of every factor (11
+ * where only a bf16 y takes them), or 2^-38 of the largest of a chunk's tokens in
+ * 32 channels: the state is off by 5e-7 of its norm.  There a value of x or
+ * init_state that is not finite makes its own channel NaN, from the first of its
+ * 64 tokens on, and no other; one of Bm, Cm, dt or beta may do so to all of a
+ * head that reads it.  Fewer tokens, and a dstate of 256, go one by one. */
 typedef struct {
   int64_t size;
   int64_t batch, seqlen;    /* batch <= 65535, seqlen <= 2^30 */

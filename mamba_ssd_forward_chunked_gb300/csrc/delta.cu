@@ -48,6 +48,25 @@ __device__ __forceinline__ constexpr int lane_of_row(int i) {
   return R == 4 ? (i >> 1) | (i & 1) << 1 : i;
 }
 
+// For a row whose squares may not have stayed in 32 bits: a power of two, and the factor of the row times that (1 and
+// what it was given where the row is 0 or not finite).  A call of its own, so that it costs the others nothing.
+template <typename T, int N>
+__device__ __noinline__ float2 norm_by_power(float eps, const T* row, float factor) {
+  const int lane = threadIdx.x & 31;
+  float largest = 0.f, squares = 0.f;
+  for (int i = lane; i < N; i += 32) largest = fmaxf(largest, fabsf(to_f32(row[i])));
+  largest = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(largest)));
+  if (!(largest > 0.f && largest < INFINITY)) return make_float2(1.f, factor);
+  const float up = exp2f(static_cast<float>(-max(ilogbf(largest), -126)));
+  for (int i = lane; i < N; i += 32) {
+    const float v = to_f32(row[i]) * up;
+    squares = fmaf(v, v, squares);
+  }
+  for (int o = 16; o; o /= 2) squares += __shfl_xor_sync(0xffffffffu, squares, o);
+  const float e = eps * up * up;
+  return make_float2(up, e < 0x1p80f ? 1.f / sqrtf(squares + e) : 1.f / (sqrtf(eps) * up));
+}
+
 template <typename T, int N, int R, int kWarps>
 __global__ void __launch_bounds__(32 * kWarps) delta_scan_kernel(DeltaParams p, int tiles) {
   constexpr int kLanes = N / 16;
@@ -96,7 +115,14 @@ __global__ void __launch_bounds__(32 * kWarps) delta_scan_kernel(DeltaParams p, 
       for (int i = 0; i < N / 32; ++i) v[i] = to_f32(from[lane + 32 * i]), squares = fmaf(v[i], v[i], squares);
 #pragma unroll
       for (int o = 16; o; o /= 2) squares += __shfl_xor_sync(0xffffffffu, squares, o);
-      const float f = delta_norm(p, squares) * (j & 1 ? p.scale : 1.f);
+      float f = delta_norm(p, squares);
+      if (p.norm_eps >= 0.f && !(squares > 0x1p-80f && squares < 0x1p120f)) {  // squares that 32 bits may not have held
+        const float2 scaled = norm_by_power<T, N>(p.norm_eps, from, f);
+        f = scaled.y;
+#pragma unroll
+        for (int i = 0; i < N / 32; ++i) v[i] *= scaled.x;
+      }
+      f *= j & 1 ? p.scale : 1.f;
       float* to = j & 1 ? s_q[j >> 1] : s_k[j >> 1];
 #pragma unroll
       for (int i = 0; i < N / 32; ++i) to[lane + 32 * i] = v[i] * f;

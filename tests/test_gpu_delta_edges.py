@@ -154,3 +154,35 @@ def test_rules_that_grow(ssd, L, N, dtype):  # noqa: F811
     ry, _, rf, _ = ref.delta(**a)
     near("final", final, rf, 2.0 ** -17)
     near("y", y, ry, 2.0 ** -17 if dtype == torch.float32 else 2.0 ** -8)
+
+
+@BOTH
+@pytest.mark.parametrize("L,N", [(9, 64), (9, 256), (70, 64), (70, 128)])
+@pytest.mark.parametrize("eps", [0.0, 1e-6])
+def test_norms_of_rows_whose_squares_leave_32_bits(ssd, L, N, eps, dtype):  # noqa: F811
+    """Rows of 10^-30 to 10^30, a single small value, and zeros.  In chunks the values to be written, r, of 64 tokens have
+    one power of two: their second parts end at 2^-25 of a unit, and the bound that sets it, max |x| + sqrt(N) max |h|
+    at most (beta and decays are below 1), is below 2^15 units and above 2^14, so each is off by 2^-39 of that bound
+    whatever its own size.  A token's y has 64 of them at most, times |scale q| and a key of length below 1.42."""
+    a, o = inputs(1, L, 2, 2, 32, N, dtype, seed=N)
+    g = torch.Generator().manual_seed(L)
+    for k in ("Bm", "Cm"):
+        a[k] = (a[k].float() * 10.0 ** torch.randint(-30, 31, (1, L, 2, 1), generator=g)).to(dtype)
+        a[k][0, 4] = 0
+        a[k][0, 5, 0] = 0
+        a[k][0, 5, 0, 7] = 1e-35
+    o["norm_eps"] = eps
+    y, final = ssd.ssd_delta_fwd(**to(a), **to(o))
+    ry, by, rf, bf = ref.delta(**a, **o, spread=65.0 if L >= 32 else 1.0, pt=2.0 ** (-12 if dtype == torch.bfloat16 else -22))
+    if L >= 32:
+        h = 0.0
+        for t in range(L + 1):
+            h = max(h, float(ref.delta(**{k: v[:, :t] if v.dim() > 1 else v for k, v in a.items()}, **o)[2].abs().max()))
+        floor = 2.0 ** -39 * 64 * 1.42 * (float(a["x"].abs().max()) + N ** 0.5 * h)
+        q = a["Cm"].double()
+        size = q.square().sum(-1) + eps
+        length = torch.where(size > 0, q.norm(dim=-1) * size.rsqrt(), 0.0)
+        by += floor * N ** -0.5 * length[..., None]
+        bf += floor
+    check("y", y, ry, store(ry, by, dtype))
+    check("final", final, rf, bf)
