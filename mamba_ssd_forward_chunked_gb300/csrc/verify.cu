@@ -423,20 +423,21 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(VerifyPara
     bool taken = false;
     if (tid < count) {
       const float2 t = s_row[tid];
-      float ep = 0.f, eq = 0.f, zq = 1.f;
-      if (d >= 0 && d < p.V) {
-        if (t.y > 0.f) {
-          const float z = scale * (plain_logit(logit) - t.x);
-          ep = expf(z), logp = z - logf(t.y);
-        }
-        eq = 1.f;
+      if (d >= 0 && d < p.V && t.y > 0.f) {
+        const float z = scale * (plain_logit(logit) - t.x);
+        logp = z - logf(t.y);
+        float zq = 0.f, sum_q = 1.f;
         if (probs) {
           const float2 r = s_row[p.T + 1 + tid];
-          eq = 0.f;
-          if (r.y > 0.f) eq = expf(scale * (plain_logit(logit_q) - r.x)), zq = r.y;
+          zq = -INFINITY;
+          if (r.y > 0.f) zq = scale * (plain_logit(logit_q) - r.x), sum_q = r.y;
         }
+        // from the larger of the two, so that neither is lost where both are small; and p itself is above 0 where its
+        // exponential is not
+        const float top = fmaxf(z, zq);
+        if (top > -INFINITY) taken = number * expf(zq - top) * t.y < expf(z - top) * sum_q;
+        if (number == 0.f) taken = z > -INFINITY;
       }
-      taken = number * eq * t.y < ep * zq;
     }
     const uint32_t mask = __ballot_sync(0xffffffffu, taken);
     if (lane == 0) s_taken[warp] = mask;

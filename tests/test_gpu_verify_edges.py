@@ -30,3 +30,23 @@ def test_largest_vocabulary_of_equal_logits(ssd, V, dtype):  # noqa: F811
     run(ssd, dict(logits=steep.expand(3, 2, V), draft=draft, draft_logits=flat.expand(3, 1, V), uniforms=uniforms))
     run(ssd, dict(logits=flat.expand(3, 2, V), draft=draft, draft_logits=steep.expand(3, 1, V), uniforms=uniforms))
     run(ssd, dict(logits=flat.expand(3, 2, V), draft=draft, uniforms=uniforms))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_drafts_that_hardly_have_a_weight(ssd, dtype):  # noqa: F811
+    """Shares of e^-200 of a drafted token under both: their ratio decides, as for any other; 0 accepts what has any."""
+    V = 300
+    g = torch.Generator().manual_seed(9)
+    target, near = torch.randn(V, generator=g).to(dtype), torch.randn(V, generator=g).to(dtype)
+    for i, (p, q) in enumerate(((-200, -199), (-199, -200), (-150, -80), (-80, -150), (-120, -120.5))):
+        target[10 * i], near[10 * i] = p, q
+    target[60] = -float("inf")
+    draft = torch.tensor([0, 0, 10, 20, 30, 40, 40, 20, 60, 0])
+    u = torch.tensor([0.2, 0.6, 0.9, 0.0, 0.9, 0.5, 0.99, 0.5, 0.0, 0.0])
+    a = dict(logits=target.expand(10, 2, V), draft=draft.int()[:, None], draft_logits=near.expand(10, 1, V),
+             uniforms=torch.stack([u, torch.rand(10, generator=g)], 1))
+    got = run(ssd, a)
+    assert len(set(got[1].tolist())) == 2
+    got = run(ssd, {**a, "draft_logits": None})
+    assert got[1].tolist() == [0, 0, 0, 1, 0, 0, 0, 0, 0, 1]
+    run(ssd, {**a, "scale": torch.full((10,), 3.0)})
