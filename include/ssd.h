@@ -538,6 +538,12 @@ ssd_status ssd_delta_fwd(const ssd_delta_args* args, ssd_stream_t stream);
  * accepted[b] = n; logprobs = log p of each token, 0 beside a -1.  n + 1 is the
  * number of tokens to commit where the model has run on the last token and the
  * drafts: the `lengths` of ssd_conv_fwd, ssd_selective_scan and ssd_delta_fwd.
+ * The drawn token is that of 64-bit arithmetic, up to numbers within 2^-34 of a
+ * token's border.  Drafts are accepted in 32 bits: a number within 2^-20 of the
+ * border p_i / q_i, relatively (and 2^-24 of the scaled logits' distances from
+ * their rows' largest, if that is more), may fall either way, and what is left of
+ * p_n - q_n counts as nothing where it may be below 2^-20 in all.  Log-probabilities
+ * are off by 2^-20, relatively or absolutely.
  * A NaN logit counts as -infinity; a row with +infinity is shared by its
  * infinities.  A drafted token outside the vocabulary is not accepted, and
  * nothing is taken off p for it.  Where the target's row allows no token, or

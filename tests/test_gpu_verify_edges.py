@@ -50,3 +50,38 @@ def test_drafts_that_hardly_have_a_weight(ssd, dtype):  # noqa: F811
     got = run(ssd, {**a, "draft_logits": None})
     assert got[1].tolist() == [0, 0, 0, 1, 0, 0, 0, 0, 0, 1]
     run(ssd, {**a, "scale": torch.full((10,), 3.0)})
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("kind", ["noise", "one token", "two tokens exchanged", "a part"])
+def test_drafts_almost_like_the_target(ssd, kind, dtype):  # noqa: F811
+    """p and q are equal to 10^-5 or so, which 32-bit sums cannot tell for all tokens: what is drawn after a refusal is
+    the 64-bit loop's.  (Weights are good to 2^-38 and p - q to 2^-38 10^5 of itself: no number is that near a
+    token's border.)"""
+    V, B = 3001, 48
+    g = torch.Generator().manual_seed(5)
+    target = torch.randn(V, generator=g).mul(2).to(dtype).float()
+    near = target.clone()
+    if kind == "noise":
+        near = near + torch.randn(V, generator=g) * (1e-5 if dtype == torch.float32 else 0.0)
+        if dtype == torch.bfloat16:  # (a last place, of a few tokens)
+            i = torch.randperm(V, generator=g)[:9]
+            near[i] = near[i] * (1 + 2.0 ** -7)
+    elif kind == "one token":
+        near[17] += 2.0 ** -7 * near[17].abs()
+    elif kind == "two tokens exchanged":
+        near[5], near[2900] = float(target[2900]), float(target[5])
+    else:
+        near[1500:] -= 1e-4 if dtype == torch.float32 else 2.0 ** -7 * near[1500:].abs()
+    p, q = target.double().softmax(0), near.to(dtype).double().softmax(0)
+    refused = int((p / q).argmin())
+    assert float(p[refused] / q[refused]) < 1 - 2.0 ** -18
+    u = torch.rand(B, 2, generator=g)
+    u[:, 0] = 1 - 2.0 ** -24
+    a = dict(logits=target.to(dtype).expand(B, 2, V), draft_logits=near.to(dtype).expand(B, 1, V),
+             draft=torch.full((B, 1), refused, dtype=torch.int32), uniforms=u)
+    rest = (p - q).clamp(min=0)
+    border = (rest.cumsum(0) / rest.sum())[:, None] - u[:, 1].double()
+    assert float(border.abs().min()) > 2.0 ** -38 / float(rest.sum()), "a number at a border"
+    got = run(ssd, a)
+    assert not got[1].any() and len(set(got[0][:, 0].tolist())) > (0 if kind == "two tokens exchanged" else 9)
