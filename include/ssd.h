@@ -522,7 +522,9 @@ typedef struct {
 
 /* Bytes of workspace on the current device: for calls that run in chunks (0
  * otherwise, or where the sizes are refused); the sizes and dtype are read, no
- * tensor.  A wait in these calls' kernels that runs out (see above) leaves NaN
+ * tensor.  1 GiB at most, and the states of the sequences that fit in that (with
+ * thousands of heads two chunks of all of one sequence's, some 50 KB a head each
+ * in bf16, 115 in fp32).  A wait in these calls' kernels that runs out (see above) leaves NaN
  * in the outputs of its head. */
 size_t ssd_delta_workspace_size(const ssd_delta_args* args);
 ssd_status ssd_delta_fwd(const ssd_delta_args* args, ssd_stream_t stream);

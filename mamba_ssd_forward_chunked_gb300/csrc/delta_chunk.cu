@@ -144,11 +144,11 @@ __global__ void __launch_bounds__(kPrepThreads, kParts<T> == 1 ? 4 : 2) delta_pr
   float2* s_squares = reinterpret_cast<float2*>(smem + M::kT);  // of a row, and what undoes its scale (T comes later)
   // A pair of launches before this one may still walk its chunks, from the other buffer: only the end of this
   // launch waits for it, in one block, so that the next walk finds both complete (see launch_delta_chunks).
-  if (s.first == 0)
+  if (!s.follows)
     begin_kernel();
   else
     grid_dep_launch();
-  const bool holds_on = s.first > 0 && blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1 && blockIdx.z == gridDim.z - 1;
+  const bool holds_on = s.follows && blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1 && blockIdx.z == gridDim.z - 1;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t b = blockIdx.z;
   const int h = blockIdx.y, chunk = s.first + blockIdx.x;
@@ -1079,11 +1079,49 @@ cudaError_t launch_chunks(const DeltaParams& p, const DeltaChunks& s, cudaStream
 // the workspace.  16 heads, 16384 tokens: 48 MB 465 us, 64 MB 442, 128 MB 436, one pair 443; 128 heads, 4096 tokens:
 // one pair 651, 48 MB 675 (both before the walk was as fast as now).
 constexpr int64_t kPairBytes = int64_t(128) << 20, kPairBytesFull = int64_t(512) << 20;
+// Sequences that would leave a pair fewer chunks than 16 are taken in parts, one after the other, so that a call's
+// workspace is twice kPairBytesFull and a part's states at most (two chunks of all heads of one sequence, where that is
+// more).  32 heads, 2048 tokens: 256 sequences at once 16.96 ms with 15.9 GB; in pairs of 8 chunks 18.1 with 8.2, of
+// one 28.2 with 1.5; in parts of 16 sequences 17.1 with 1.0.
+constexpr int64_t kPairChunks = 16;
 
 int64_t bytes_of_chunk(const DeltaParams& p) { return p.batch * (int64_t(record_bytes(p.N, p.parts)) * p.H + int64_t(rows_bytes(p.N, p.parts)) * p.G); }
+int64_t chunks_of(const DeltaParams& p) { return ceil_div(p.seqlen, kC); }
+// Blocks of 16 columns leave multiprocessors without one: pairs that overlap pay.
+bool few_blocks(const DeltaParams& p) { return p.batch * p.H * ceil_div(p.P, 16) <= layer_sm_count(); }
+// All at once, in the place of two pairs.
+bool one_pair(const DeltaParams& p) { return !few_blocks(p) && chunks_of(p) <= 2 * kPairBytesFull / bytes_of_chunk(p); }
+// Sequences of a part, as even as they come.
+int64_t sequences_at_once(const DeltaParams& p) {
+  const int64_t chunks = chunks_of(p) < kPairChunks ? chunks_of(p) : kPairChunks, fit = kPairBytesFull / (chunks * (bytes_of_chunk(p) / p.batch));
+  return one_pair(p) || fit >= p.batch ? p.batch : fit < 1 ? 1 : ceil_div(p.batch, ceil_div(p.batch, fit));
+}
+// Chunks of a pair, p.batch being a part's sequences.
 int64_t chunks_at_once(const DeltaParams& p) {
-  const int64_t all = ceil_div(p.seqlen, kC), fit = (p.batch * p.H * ceil_div(p.P, 16) <= layer_sm_count() ? kPairBytes : kPairBytesFull) / bytes_of_chunk(p);
-  return ceil_div(all, ceil_div(all, fit < 16 ? 16 : fit));
+  if (one_pair(p)) return chunks_of(p);
+  const int64_t fit = (few_blocks(p) ? kPairBytes : kPairBytesFull) / bytes_of_chunk(p);
+  return ceil_div(chunks_of(p), ceil_div(chunks_of(p), fit < 1 ? 1 : fit));
+}
+// A part of the sequences as a call of its own.
+DeltaParams part_of(const DeltaParams& p, int64_t first, int64_t count) {
+  DeltaParams q = p;
+  const int64_t es = p.parts == 1 ? 2 : 4, gs = p.gate_f32 ? 4 : 2;
+  auto on = [](const void* at, int64_t bytes) { return static_cast<const void*>(static_cast<const uint8_t*>(at) + bytes); };
+  q.batch = count;
+  q.x = on(p.x, first * p.x_batch * es), q.Bm = on(p.Bm, first * p.B_batch * es), q.Cm = on(p.Cm, first * p.C_batch * es);
+  q.dt = on(p.dt, first * p.dt_batch * gs), q.beta = on(p.beta, first * p.beta_batch * gs);
+  q.y = static_cast<uint8_t*>(p.y) + first * p.seqlen * p.H * p.P * es;
+  if (p.slots) {
+    q.slots = p.slots + first;
+  } else {  // row b is sequence b's
+    const int64_t state = first * p.H * p.P * p.N;
+    q.nslots = p.nslots - first;
+    if (p.init_state) q.init_state = p.init_state + state;
+    if (p.final_state) q.final_state = p.final_state + state;
+  }
+  if (p.positions) q.positions = p.positions + first;
+  if (p.lengths) q.lengths = p.lengths + first;
+  return q;
 }
 
 }  // namespace
@@ -1093,32 +1131,41 @@ bool delta_chunked(int dtype, int64_t seqlen, int dstate) {
   return (dstate == 64 || dstate == 128) && seqlen >= kMinTokens;
 }
 
-size_t delta_chunks_workspace(const DeltaParams& p) {
+size_t delta_chunks_workspace(const DeltaParams& call) {
+  DeltaParams p = call;
+  p.batch = sequences_at_once(call);
   const int64_t count = chunks_at_once(p);
   const size_t pair = static_cast<size_t>(count * bytes_of_chunk(p));
   return count * kC >= p.seqlen ? pair : 2 * pair + static_cast<size_t>(p.batch) * p.H * p.P * p.N * sizeof(float);
 }
 
-ssd_status launch_delta_chunks(const DeltaParams& p, void* workspace, cudaStream_t stream) {
-  const int64_t all = ceil_div(p.seqlen, kC), most = chunks_at_once(p);
+ssd_status launch_delta_chunks(const DeltaParams& call, void* workspace, cudaStream_t stream) {
   DeltaChunks s{};
-  uint8_t* pairs = static_cast<uint8_t*>(workspace);  // two, used in turn
-  s.carry = reinterpret_cast<float*>(pairs + 2 * most * bytes_of_chunk(p));
   s.limit_ns = spin_limit_ns();
   s.vectors = 1;
-  for (const void* t : {p.x, p.Bm, p.Cm, (const void*)p.y}) s.vectors &= aligned_to(t, 16);
-  for (int64_t stride : {p.x_batch, p.x_token, p.B_batch, p.B_token, p.C_batch, p.C_token}) s.vectors &= stride * (p.parts == 1 ? 2 : 4) % 16 == 0;
-  // Each launch is a dependent of the one before it in the stream and may begin beside it.  A walk waits for the
-  // first launch of its pair, which ends after the walk before; a first launch writes a buffer whose last walk
-  // ended before the present one began.
-  for (int64_t first = 0, pair = 0; first < all; first += most, ++pair) {
-    s.records = pairs + (pair & 1) * most * bytes_of_chunk(p);
-    s.rows = s.records + p.batch * p.H * most * record_bytes(p.N, p.parts);
-    s.first = static_cast<int>(first), s.count = static_cast<int>(all - first < most ? all - first : most);
-    s.last = first + most >= all;
-    const cudaError_t e = p.parts == 1 ? (p.N == 64 ? launch_chunks<__nv_bfloat16, 64>(p, s, stream) : launch_chunks<__nv_bfloat16, 128>(p, s, stream))
-                                       : (p.N == 64 ? launch_chunks<float, 64>(p, s, stream) : launch_chunks<float, 128>(p, s, stream));
-    if (e != cudaSuccess) return SSD_ERR_CUDA;
+  for (const void* t : {call.x, call.Bm, call.Cm, (const void*)call.y}) s.vectors &= aligned_to(t, 16);
+  for (int64_t stride : {call.x_batch, call.x_token, call.B_batch, call.B_token, call.C_batch, call.C_token}) s.vectors &= stride * (call.parts == 1 ? 2 : 4) % 16 == 0;
+  const int64_t at_once = sequences_at_once(call);
+  int64_t pair = 0;
+  for (int64_t b = 0; b < call.batch; b += at_once) {
+    DeltaParams p = part_of(call, b, at_once);  // (a full part's sizes give the buffers)
+    const int64_t all = chunks_of(p), most = chunks_at_once(p), bytes = most * bytes_of_chunk(p);
+    uint8_t* pairs = static_cast<uint8_t*>(workspace);  // two, used in turn
+    s.carry = reinterpret_cast<float*>(pairs + 2 * bytes);
+    if (call.batch - b < at_once) p.batch = call.batch - b;
+    // Each launch is a dependent of the one before it in the stream and may begin beside it.  A walk waits for the
+    // first launch of its pair, which ends after the walk before; a first launch writes a buffer whose last walk
+    // ended before the present one began.
+    for (int64_t first = 0; first < all; first += most, ++pair) {
+      s.follows = pair > 0 && most < all;
+      s.records = pairs + (most < all ? (pair & 1) * bytes : 0);
+      s.rows = s.records + p.batch * p.H * most * record_bytes(p.N, p.parts);
+      s.first = static_cast<int>(first), s.count = static_cast<int>(all - first < most ? all - first : most);
+      s.last = first + most >= all;
+      const cudaError_t e = p.parts == 1 ? (p.N == 64 ? launch_chunks<__nv_bfloat16, 64>(p, s, stream) : launch_chunks<__nv_bfloat16, 128>(p, s, stream))
+                                         : (p.N == 64 ? launch_chunks<float, 64>(p, s, stream) : launch_chunks<float, 128>(p, s, stream));
+      if (e != cudaSuccess) return SSD_ERR_CUDA;
+    }
   }
   return SSD_OK;
 }

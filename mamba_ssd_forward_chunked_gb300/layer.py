@@ -143,7 +143,7 @@ def ssd_step(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, D: torch.Tensor
 def ssd_delta_workspace_size(batch: int, seqlen: int, nheads: int, headdim: int, dstate: int, dtype: torch.dtype,
                              ngroups: int = 1) -> int:
     """Bytes of workspace ssd_delta_fwd needs for these sizes on the current
-    device (0: none)."""
+    device (0: none; about 1 GB at most, however large the batch)."""
     return _binding.delta_workspace(batch, seqlen, nheads, headdim, ngroups, dstate, dtype == torch.bfloat16)
 
 

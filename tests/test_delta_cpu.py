@@ -105,3 +105,13 @@ def test_tensors_are_checked():
         ssd.ssd_draft_verify(torch.zeros(1, 2, 5), torch.zeros(1, 1, dtype=torch.int32), torch.zeros(1, 2))
     with pytest.raises(ssd.SSDError, match="3-D"):
         ssd.ssd_draft_verify(torch.zeros(2, 5), torch.zeros(1, 1, dtype=torch.int32), torch.zeros(1, 2))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("B,L,H,G,P,N", [(256, 2048, 32, 16, 128, 128), (65535, 4096, 32, 32, 128, 128), (7, 100000, 64, 1, 64, 64),
+                                         (2, 10 ** 6, 256, 256, 1024, 128), (1, 2 ** 30, 8, 8, 64, 128)])
+def test_delta_workspace_is_bounded(B, L, H, G, P, N, dtype):
+    """2 x 512 MiB, and the states of as many sequences as have 16 chunks in 512 MiB, or of one."""
+    record = (2 * (N // 64) + (1 if dtype == torch.bfloat16 else 2)) * 8192 * H
+    states = max(1, (512 << 20) // (16 * record)) * H * P * N * 4
+    assert 0 < ssd.ssd_delta_workspace_size(B, L, H, P, N, dtype, G) <= 2 * (512 << 20) + states
