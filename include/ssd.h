@@ -495,7 +495,8 @@ ssd_status ssd_beam_reorder(const ssd_beam_reorder_args* args, ssd_stream_t stre
  * 32 channels: the state is off by 5e-7 of its norm.  There a value of x or
  * init_state that is not finite makes its own channel NaN, from the first of its
  * 64 tokens on, and no other; one of Bm, Cm, dt or beta may do so to all of a
- * head that reads it.  Fewer tokens, and a dstate of 256, go one by one. */
+ * head that reads it; and with dt A above 0 its sums over 64 tokens must not pass
+ * 88, where exp leaves 32 bits.  Fewer tokens, and a dstate of 256, go one by one. */
 typedef struct {
   int64_t size;
   int64_t batch, seqlen;    /* batch <= 65535, seqlen <= 2^30 */

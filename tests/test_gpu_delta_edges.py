@@ -186,3 +186,30 @@ def test_norms_of_rows_whose_squares_leave_32_bits(ssd, L, N, eps, dtype):  # no
         bf += floor
     check("y", y, ry, store(ry, by, dtype))
     check("final", final, rf, bf)
+
+
+@BOTH
+@pytest.mark.parametrize("N", [64, 128])
+@pytest.mark.parametrize("of", ["channels", "tokens", "heads"])
+def test_values_of_different_sizes(ssd, of, N, dtype):  # noqa: F811
+    """x of sizes from 1 to 10^4 by channel, by token (every 13th large) or by head, the smallest ones' digits.  The
+    large ones set the powers of two of a block's columns: with X their largest, the bound of the state is up to
+    64 1.42 (1 + sqrt(N)) X = 2^11 X, and its second parts end at 2^-39 of that, 2^-28 X, or 2^-13 for X = 4 10^4 beside
+    values of 1: 2^-12 of the small channels' states over all values.  A head has bounds of its own: 2^-19."""
+    a, o = inputs(1, 260, 4, 4, 32, N, torch.float32, seed=8)
+    size = torch.ones(1, 260, 4, 32)
+    if of == "channels":
+        size *= 10.0 ** torch.arange(32).remainder(5)
+    elif of == "tokens":
+        size[:, ::13] *= 1e4
+    else:
+        size[:, :, 1::2] *= 1e4
+    a["x"] = (a["x"] * size).to(dtype)
+    for k in ("Bm", "Cm", "dt", "beta"):
+        a[k] = a[k].to(dtype)
+    y, final = run(ssd, a, o)
+    ry, _, rf, _ = ref.delta(**a, **o)
+    small = {"channels": (slice(None), slice(0, 32, 5)), "tokens": (slice(None), slice(None)), "heads": (slice(0, 4, 2), slice(None))}[of]
+    loss = 2.0 ** -12 if of == "channels" else 2.0 ** -19
+    near("final", final[:, small[0], small[1]], rf[:, small[0], small[1]], loss)
+    near("y", y[:, :, small[0], small[1]], ry[:, :, small[0], small[1]], loss if dtype == torch.float32 else 2.0 ** -8)
