@@ -8,7 +8,7 @@
 // time: k and q with their norms, x, the gates.
 //
 // The state's bytes bound it: it is read and written once, 64 KB of a head of 128 x 128 for each token or handful
-// of tokens.  256 single tokens of 32 heads 169 us, 94 % of a copy's rate; 32 times 5 drafted tokens 28 us (floor
+// of tokens.  256 single tokens of 32 heads 170 us, 94 % of a copy's rate; 32 times 5 drafted tokens 28 us (floor
 // 20: a block loads, computes and stores one after the other); one token 4.1 us, a launch's latency.  16 values a
 // lane, so that a row's sum takes two or three shuffles; four rows a lane share them (join_rows), two where there
 // are too few blocks.

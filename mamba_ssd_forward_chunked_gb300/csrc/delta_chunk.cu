@@ -16,11 +16,12 @@
 // at most 2^-22 of a value or 2^-38 of the largest.  (Three bf16 parts need no scale, but half as much again
 // of shared memory, stores and products.)  A row of bf16 K or Q times a power of two is fp16; 32-bit ones have
 // two parts as well, and so has P T then.  Parts lie side by side along the product's columns, and the threads
-// add up what comes out.
+// add up what comes out.  Keys enter with lengths near 1 whatever they are (their own powers of two go into beta and x),
+// a row of P T and eight columns of T with powers of two of their own.
 //
-// What it takes, of 128 x 128 states in bf16: 4 x 4096 tokens of 32 heads 562 us (61 for the bytes alone), the first
-// launch 254 and the walk 321; 16384 tokens of 16 heads 436 (40), a walk's chunk 1.17.  The first launch is bound by
-// shared memory and its barriers (60 % of the wavefronts, 49 % of the issue slots, 29 % of the DRAM), the walk by its
+// What it takes, of 128 x 128 states in bf16: 4 x 4096 tokens of 32 heads 570 us (61 for the bytes alone), the first
+// launch 261 and the walk 329 (each alone, cold); 16384 tokens of 16 heads 440 (40), a walk's chunk 1.19.  The first launch is
+// bound by shared memory and its barriers (58 % of the wavefronts, 51 % of the issue slots, 29 % of the DRAM), the walk by its
 // chain: one block an SM, 16 columns, passes a chunk in 2,250 cycles, two products of 570 each, r and the state 550
 // each on their way through the threads and their barriers.  So nothing else is in the chain: x and the factors of
 // the next chunk are read while W r runs, the largest values are agreed on while y is written, and y is written while
@@ -1062,7 +1063,7 @@ cudaError_t launch_chunks(const DeltaParams& p, const DeltaChunks& s, cudaStream
   // Columns of a block: as few as leave every block a multiprocessor of its own (the chain is the shorter, and what is
   // loaded for it the same), 32 where there are more, two blocks on each.  16 heads of 128 x 128, 16384 tokens:
   // 16 columns 379 us, 32 482; 128 heads, 4096 tokens: 32 columns 479 and, two blocks each, 360, 16 491 (all of an
-  // earlier form; now 300 and 321 for the first and the last choice).
+  // earlier form; now 307 and 329 for the first and the last choice).
   const int64_t heads = p.batch * p.H, sms = layer_sm_count();
   // (64 columns, one block an SM: the walk of the last 385 us, when 32 had 355.)
   // 32-bit rows take twice the shared memory: one buffer, and one block on each.

@@ -8,7 +8,7 @@ namespace ssd {
 struct DeltaChunks {
   int first, count, last;  // chunks of 64 tokens from `first` on; last: the sequences end with them
   int vectors;             // x, Bm, Cm and y are rows of 16-byte vectors
-  int follows;             // a pair of the same call came before
+  int follows;             // a pair of the same call came before, in the other buffer
   uint8_t* records;        // [batch][nheads][count]: what the first launch leaves for the second
   uint8_t* rows;           // [batch][ngroups][count]: and K and Q of the group
   float* carry;            // [batch][nheads][headdim][dstate]: states between pairs of launches

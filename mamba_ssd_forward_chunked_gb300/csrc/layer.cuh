@@ -108,8 +108,8 @@ __device__ __forceinline__ uint64_t load_l2(const uint64_t* p) {
 //    next kernel to be set up; that kernel's own wait is for this one's completion all the same;
 //  - w4_kernel behind columns_kernel reads its codes before it waits: columns_kernel signals after its own
 //    wait, so by then nobody writes them;
-//  - delta_prepare_kernel, from a call's second pair of launches on, reads nothing that the call's kernels write and
-//    writes a buffer whose last reader ended earlier: it begins beside the walk in front, and only its last block
+//  - delta_prepare_kernel, behind a pair of launches of the same call that uses the other buffer, reads nothing that the
+//    call's kernels write and writes a buffer whose last reader ended earlier: it begins beside the walk in front, and only its last block
 //    waits, at its end, so that the walk behind it does not begin before that walk has ended.
 // What the kernel in front may write is read by ordinary or volatile loads, never through the read-only
 // path, which wants data that stay unchanged for as long as the kernel is resident.
