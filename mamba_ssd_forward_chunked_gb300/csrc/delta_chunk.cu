@@ -20,13 +20,14 @@
 // a row of P T and eight columns of T with powers of two of their own.
 //
 // What it takes, of 128 x 128 states in bf16: 4 x 4096 tokens of 32 heads 570 us (61 for the bytes alone), the first
-// launch 261 and the walk 329 (each alone, cold); 16384 tokens of 16 heads 440 (40), a walk's chunk 1.19.  The first launch is
-// bound by shared memory and its barriers (58 % of the wavefronts, 51 % of the issue slots, 29 % of the DRAM), the walk by its
-// chain: one block an SM, 16 columns, passes a chunk in 2,250 cycles, two products of 570 each, r and the state 550
-// each on their way through the threads and their barriers.  So nothing else is in the chain: x and the factors of
-// the next chunk are read while W r runs, the largest values are agreed on while y is written, and y is written while
-// the next product runs.  Chunks of 64 tokens: W and P T are one operand of a product each, and 128 tokens would
-// need twice the columns of tensor memory and four times the first launch's work per chunk, for half the chain.
+// launch 261 and the walk 329 (each alone, cold); 16384 tokens of 16 heads 440 (40), a walk's chunk 1.19.  The first
+// launch is bound by shared memory and its barriers (58 % of the wavefronts, 51 % of the issue slots, 29 % of the
+// DRAM), the walk by its chain: one block an SM, 16 columns, passes a chunk in 2,250 cycles, two products of 570 each,
+// r and the state 550 each on their way through the threads and their barriers.  So nothing else is in the chain: x and
+// the factors of the next chunk are read while W r runs, the largest values are agreed on while y is written, and y is
+// written while the next product runs.  Chunks of 64 tokens: W and P T are one operand of a product each, and 128
+// tokens would need twice the columns of tensor memory and four times the first launch's work per chunk, for half the
+// chain.
 #include <cuda_fp16.h>
 
 #include "delta_chunk.cuh"
@@ -246,6 +247,7 @@ __global__ void __launch_bounds__(kPrepThreads, kParts<T> == 1 ? 4 : 2) delta_pr
     if (col == 0) s_squares[r] = make_float2(squares, scale.down);
   }
   __syncthreads();
+
   // K K^T (four warps, 16 rows each) and Q K^T (four more)
   const int mt = is_q ? 7 - warp : warp;  // (beside a warp of few columns one of many)
   const uint32_t rows = smem_u32(smem);
